@@ -316,6 +316,78 @@ cr_status cr_mlp_w4a4(const void* x_bf16, int M, int K, const void* wg_packed, c
                       const float* wd_scale, int N, void* y_bf16, void* ws, size_t ws_bytes,
                       hipStream_t stream);
 
+/* ---- 4-bit weights with group scales (weight-only) ---------------------
+ * The form a decoder's weights take while it generates: 16-bit activations,
+ * used as they are (no rotation, no activation codes), and
+ *   W[n,k] = s[n, k/group] * (q[n,k] - z[n, k/group]),
+ * q in 0..15, z in 0..15 (8 for every group of a weight without zero points),
+ * group = 32, 64 or 128 consecutive k (any other value, or a K that is no
+ * multiple of it -> CR_ERR_GROUP).  `dtype` names the 16-bit type of the
+ * activations, scales, bias and outputs of a call: CR_BF16 or CR_FP16
+ * (CR_ERR_KIND otherwise).  Products are exact and sums are held in float32,
+ * group by group, each multiplied by its scale there; the only rounding to
+ * 16 bits is the output's.  An x row with an infinity or a NaN gives NaN in
+ * its own row of y and touches no other; so does a row whose group sums of
+ * |x| leave float32's range. */
+#define CR_BF16 0
+#define CR_FP16 1
+
+/* Bytes of one packed weight [N,K] (0 on bad args), a multiple of 256;
+ * `zeros` nonzero: with zero points. */
+size_t cr_w4g_packed_bytes(int group, int zeros, int N, int K);
+
+/* Encoder: a finite 16-bit weight [N,K] to its stored form, nearest codes
+ * group by group (float32, IEEE divisions, rint half to even):
+ *   zeros NULL  s = T(absmax / 7), q = clamp(rint(w / s), -8, 7) + 8
+ *               (8 where s = 0);
+ *   otherwise   lo = min(0, min w), hi = max(0, max w), s = T((hi - lo) / 15),
+ *               z = clamp(rint(-lo / s), 0, 15),
+ *               q = clamp(rint(w / s) + z, 0, 15) (both 0 where s = 0).
+ *   codes  [N,K/2] uint8, two to a byte, low nibble = even k   (out)
+ *   scales [N,K/group] of the weight's type                     (out)
+ *   zeros  [N,K/group] uint8 or NULL                            (out)
+ * At most 2^34 weights.  Stacked weights [E,N,K] are one weight [E*N,K]. */
+cr_status cr_encode_w4g(int dtype, const void* w, int N, int K, int group, void* codes, void* scales, void* zeros,
+                        hipStream_t stream);
+
+/* Lays `count` stored weights [N,K] (each as cr_encode_w4g writes it, one
+ * after the other; other encoders' codes do as well) out for the kernels,
+ * cr_w4g_packed_bytes() apart.  The low four bits of a zero point count.
+ *   w_packed count * cr_w4g_packed_bytes(group, zeros != NULL, N, K) (out) */
+cr_status cr_pack_weight_w4g(const void* codes, const void* scales, const void* zeros, int count, int N, int K,
+                             int group, void* w_packed, hipStream_t stream);
+
+/* y[m,n] = T(sum_k x[m,k] W[n,k] + bias[n]); x [M,K], y [M,N], bias [N] or
+ * NULL; group and zeros as the weight was packed.  No workspace.  M = 0 is a
+ * no-op. */
+cr_status cr_linear_w4g(int dtype, const void* x, int M, int K, const void* w_packed, int group, int zeros, int N,
+                        const void* bias, void* y, hipStream_t stream);
+
+/* Mixture-of-experts layer on such weights, for a few tokens (more go in
+ * passes of 64): for each row of x [M,K]
+ *   l[e] = sum_k x[k] router[e,k] in float64 (router [E,K]);
+ *   the topk largest, in descending order, equal ones by their index (a NaN
+ *   counts as larger than any number);
+ *   p[e] = exp(l[e] - max l), c[r] = p[e_r] / sum of p over the chosen
+ *   (norm nonzero) or over all experts;
+ *   h[r] = T(c[r] * silu(Wg_e x) * (Wu_e x)), Wg, Wu [F,K]  (e = e_r)
+ *   y = T(sum_r Wd_e h[r]), Wd [K,F].
+ * h is held in the 16-bit type: it is the operand of the down product, and
+ * rounding it costs what rounding y does.
+ *   wg/wu/wd_packed  E packed weights each (cr_pack_weight_w4g, count = E)
+ *   y [M,K] (out); ids [M,topk] int32 and weights [M,topk] float: the chosen
+ *   experts and c (out, each may be NULL)
+ *   ws / ws_bytes: at least cr_moe_w4g_workspace_bytes(M,K,F,E,topk,group).
+ * K and F must be multiples of group.  1 <= E <= CR_MOE_MAX_EXPERTS,
+ * 1 <= topk <= min(E, CR_MOE_MAX_TOPK) (CR_ERR_SHAPE). */
+#define CR_MOE_MAX_EXPERTS 1024
+#define CR_MOE_MAX_TOPK 16
+size_t cr_moe_w4g_workspace_bytes(int M, int K, int F, int E, int topk, int group);
+
+cr_status cr_moe_w4g(int dtype, const void* x, int M, int K, const void* router, int E, int topk, int norm,
+                     const void* wg_packed, const void* wu_packed, const void* wd_packed, int F, int group, int zeros,
+                     void* y, int32_t* ids, float* weights, void* ws, size_t ws_bytes, hipStream_t stream);
+
 /* ---- status ----------------------------------------------------------- */
 const char* cr_status_str(cr_status s);
 const char* cr_last_error(void);   /* thread-local detail of the last failure */

@@ -14,6 +14,9 @@ Formats (model cards cited by title and section):
     where the kernel demands it": used for layers whose K is not a multiple
     of 256.
   * asym W4A8 codebook - [REB] "What's inside a file".
+  * W4G - weight-only: 16-bit activations (bf16 or fp16), 4-bit weights with
+    a scale, and optionally a zero point, per group of 32, 64 or 128 along K;
+    linears and a mixture-of-experts layer.
 """
 from __future__ import annotations
 
@@ -37,9 +40,14 @@ __all__ = [
     "linear_w4a4_noalloc", "NOALLOC_SCRATCH_BYTES",
     "encode_w4a8", "encode_w4a8_workspace_bytes", "dbg_e4m3_encode",
     "dbg_fused_config", "dbg_fused_timeouts", "dbg_big_plan", "dbg_small_plan",
+    "W4G", "w4g_packed_bytes", "encode_w4g", "pack_weight_w4g", "linear_w4g",
+    "moe_w4g_workspace_bytes", "moe_w4g", "PackedExperts", "pack_experts", "moe",
 ]
 
 W4A4, INT8TW, W4A8, INT8ROT, W4A4_G64, W4A4_G16, W4A4_RH = 0, 1, 2, 3, 4, 5, 6
+# Group-scaled 4-bit weights: a kind of PackedWeight, with calls of its own
+# (the generic calls that take a kind refuse it)
+W4G = 7
 # W4A4 kind of each rotation group size
 W4_GROUP_KIND = {256: W4A4, 64: W4A4_G64, 16: W4A4_G16}
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libconvrot.so")
@@ -62,6 +70,8 @@ EXPORTS = [
     "cr_linear_w4a4_noalloc",
     "cr_encode_w4a8_workspace_bytes", "cr_encode_w4a8", "cr_dbg_e4m3_encode",
     "cr_dbg_fused_config", "cr_dbg_fused_timeouts", "cr_dbg_big_plan", "cr_dbg_small_plan",
+    "cr_w4g_packed_bytes", "cr_encode_w4g", "cr_pack_weight_w4g", "cr_linear_w4g",
+    "cr_moe_w4g_workspace_bytes", "cr_moe_w4g",
 ]
 
 
@@ -117,6 +127,12 @@ def lib() -> ctypes.CDLL:
         "cr_dbg_linear_acc": (i, [i, vp, i, i, vp, i, vp, vp, sz, vp]),
         "cr_quantize_activations": (i, [i, vp, i, i, vp, sz, vp]),
         "cr_gemm_quantized": (i, [i, i, i, vp, vp, i, vp, vp, vp, sz, vp]),
+        "cr_w4g_packed_bytes": (sz, [i, i, i, i]),
+        "cr_encode_w4g": (i, [i, vp, i, i, i, vp, vp, vp, vp]),
+        "cr_pack_weight_w4g": (i, [vp, vp, vp, i, i, i, i, vp, vp]),
+        "cr_linear_w4g": (i, [i, vp, i, i, vp, i, i, i, vp, vp, vp]),
+        "cr_moe_w4g_workspace_bytes": (sz, [i, i, i, i, i, i]),
+        "cr_moe_w4g": (i, [i, vp, i, i, vp, i, i, i, vp, vp, vp, i, i, i, vp, vp, vp, vp, sz, vp]),
         "cr_probe_mfma_i8": (i, [i, i, vp, vp, vp]),
         "cr_probe_read": (i, [vp, sz, vp, vp]),
         "cr_probe_copy": (i, [vp, vp, sz, vp]),
@@ -493,6 +509,170 @@ def dbg_silu_mul(g: torch.Tensor, u: torch.Tensor) -> torch.Tensor:
 
 
 # ---------------------------------------------------------------------------
+# 4-bit weights with group scales (weight-only)
+# ---------------------------------------------------------------------------
+
+_MAX_DIM = 1 << 20            # CR_MAX_DIM
+_W4G_MAX_WEIGHTS = 1 << 34    # weights one call takes
+_W4G_DTYPE = {torch.bfloat16: 0, torch.float16: 1}
+
+
+def _dtype16(t: torch.Tensor, name: str) -> int:
+    code = _W4G_DTYPE.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name} must be torch.bfloat16 or torch.float16, got {t.dtype}")
+    return code
+
+
+def _call_on(device, fn, *args):
+    """fn(*args, stream) with ``device`` current and on its current stream,
+    whichever device is current outside."""
+    if device.index == torch.cuda.current_device():
+        return _check(fn(*args, _stream()))
+    with torch.cuda.device(device):
+        return _check(fn(*args, _stream()))
+
+
+def w4g_packed_bytes(group: int, zeros: bool, N: int, K: int) -> int:
+    return int(lib().cr_w4g_packed_bytes(group, int(zeros), N, K))
+
+
+def encode_w4g(w: torch.Tensor, group: int = 128, zeros: bool = False):
+    """16-bit [..., N, K] -> the stored form of 4-bit weights with group
+    scales: (codes uint8 [..., N, K/2], low nibble = even k; scales
+    [..., N, K/group] of w's type; zero points uint8 [..., N, K/group], or
+    None without ``zeros``: the codes then stand for q - 8)."""
+    code = _dtype16(w, "w")
+    _dev(w, "w")
+    if w.dim() < 2:
+        raise ValueError("w must be [..., N, K]")
+    K = w.shape[-1]
+    if group not in (32, 64, 128) or K == 0 or K % group:
+        raise ConvRotError(3, f"K={K}, scale group {group}: the group must be 32, 64 or 128 and divide K")
+    lead = tuple(w.shape[:-1])
+    codes = torch.empty((*lead, K // 2), dtype=torch.uint8, device=w.device)
+    scales = torch.empty((*lead, K // group), dtype=w.dtype, device=w.device)
+    z = torch.empty((*lead, K // group), dtype=torch.uint8, device=w.device) if zeros else None
+    # rows are independent: as many a call as the library takes
+    rows = w.numel() // K
+    step = max(1, min(_MAX_DIM, _W4G_MAX_WEIGHTS // K) & ~127)   # keeps every pointer aligned
+    for r in range(0, rows, step):
+        n, g = min(step, rows - r), K // group
+        _call_on(w.device, lib().cr_encode_w4g, code, w.data_ptr() + 2 * r * K, n, K, group,
+                 codes.data_ptr() + r * (K // 2), scales.data_ptr() + 2 * r * g,
+                 None if z is None else z.data_ptr() + r * g)
+    return codes, scales, z
+
+
+def pack_weight_w4g(codes: torch.Tensor, scales: torch.Tensor, zeros: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Stored codes [N, K/2], scales [N, K/group] and zero points (as
+    :func:`encode_w4g` gives them, or another encoder) -> packed uint8; with a
+    leading dimension E, the weights of E experts, packed [E, bytes].  The
+    scales' type is the type the activations must have."""
+    _dev(codes, "codes", torch.uint8)
+    _dtype16(scales, "scales")
+    _dev(scales, "scales")
+    if codes.dim() not in (2, 3) or scales.dim() != codes.dim() or scales.shape[:-1] != codes.shape[:-1]:
+        raise ValueError("codes and scales must be [N, K/2] and [N, K/group], or both with a leading dimension E")
+    if zeros is not None:
+        _dev(zeros, "zeros", torch.uint8)
+        if zeros.shape != scales.shape:
+            raise ValueError("zeros must have the shape of scales")
+    _same_device(codes, scales=scales, zeros=zeros)
+    N, K = codes.shape[-2], 2 * codes.shape[-1]
+    count = codes.shape[0] if codes.dim() == 3 else 1
+    group = K // scales.shape[-1] if scales.shape[-1] and K % scales.shape[-1] == 0 else 0
+    nb = w4g_packed_bytes(group, zeros is not None, N, K)
+    if nb == 0 or count == 0:
+        _check(lib().cr_pack_weight_w4g(None, None, None, count, N, K, group, None, None) or 2)
+    out = torch.empty((count, nb), dtype=torch.uint8, device=codes.device)
+    _call_on(codes.device, lib().cr_pack_weight_w4g, _ptr(codes), _ptr(scales), _ptr(zeros), count, N, K, group,
+             _ptr(out))
+    return out if codes.dim() == 3 else out[0]
+
+
+def _check_w4g(packed, name: str, count: int, N: int, K: int, group: int, zeros: bool):
+    """Refuse packed weights smaller than their layout (the kernels would
+    read past their end); sizes the library rejects give 0 bytes here and are
+    left to its own error."""
+    _dev(packed, name, torch.uint8)
+    need = count * w4g_packed_bytes(group, zeros, N, K)
+    if packed.numel() < need:
+        raise ValueError(f"{name} has {packed.numel()} bytes, {count} x N={N} K={K} group={group} needs {need}")
+
+
+def linear_w4g(x, packed, N, group, zeros=False, bias=None, out=None):
+    """y = x W^T (+ bias) with a weight from :func:`pack_weight_w4g`: x bf16 or
+    fp16 [M, K] of the scales' type, y of the same type; ``group`` and
+    ``zeros`` as the weight was packed."""
+    code = _dtype16(x, "x")
+    _dev(x, "x")
+    if x.dim() != 2:
+        raise ValueError("x must be [M, K]")
+    M, K = x.shape
+    _check_w4g(packed, "packed", 1, N, K, group, zeros)
+    if bias is not None:
+        _dev(bias, "bias", x.dtype)
+        if bias.numel() != N:
+            raise ValueError("bias must have N elements")
+    if out is None:
+        out = torch.empty((M, max(N, 0)), dtype=x.dtype, device=x.device)
+    else:
+        _dev(out, "out", x.dtype)
+        if tuple(out.shape) != (M, N):
+            raise ValueError("out must be [M, N]")
+    _same_device(x, packed=packed, bias=bias, out=out)
+    _call_on(x.device, lib().cr_linear_w4g, code, _ptr(x), M, K, _ptr(packed), group, int(zeros), N, _ptr(bias),
+             _ptr(out))
+    return out
+
+
+def moe_w4g_workspace_bytes(M: int, K: int, F: int, E: int, topk: int, group: int) -> int:
+    return int(lib().cr_moe_w4g_workspace_bytes(M, K, F, E, topk, group))
+
+
+def moe_w4g(x, router, gate, up, down, F, group, topk, zeros=False, norm=True, out=None, workspace=None,
+            routing=False):
+    """Mixture-of-experts layer: router logits, top-k and softmax, the chosen
+    experts' silu(gate(x)) * up(x) and down, and their weighted sum.
+
+    x [M, K] and router [E, K] of one 16-bit type; gate, up (E weights
+    [F, K]) and down (E weights [K, F]) from :func:`pack_weight_w4g`;
+    ``norm``: the chosen experts' weights sum to one, otherwise they are the
+    softmax over all experts.  Returns y [M, K], with ``routing`` also the
+    chosen experts (int32 [M, topk], by descending logit, equal ones by
+    index) and their weights (float32 [M, topk])."""
+    code = _dtype16(x, "x")
+    _dev(x, "x")
+    _dev(router, "router", x.dtype)
+    if x.dim() != 2 or router.dim() != 2 or router.shape[1] != x.shape[1]:
+        raise ValueError("x must be [M, K] and router [E, K]")
+    M, K = x.shape
+    E = router.shape[0]
+    for t, name, n, k in ((gate, "gate", F, K), (up, "up", F, K), (down, "down", K, F)):
+        _check_w4g(t, name, E, n, k, group, zeros)
+    if out is None:
+        out = torch.empty_like(x)
+    else:
+        _dev(out, "out", x.dtype)
+        if out.shape != x.shape:
+            raise ValueError("out must be [M, K]")
+    ids = weights = None
+    if routing:
+        ids = torch.empty((M, max(topk, 0)), dtype=torch.int32, device=x.device)
+        weights = torch.empty((M, max(topk, 0)), dtype=torch.float32, device=x.device)
+    if workspace is None:
+        workspace = _empty_u8(max(moe_w4g_workspace_bytes(M, K, F, E, topk, group), 256), x.device)
+    else:
+        _dev(workspace, "workspace", torch.uint8)
+    _same_device(x, router=router, gate=gate, up=up, down=down, out=out, workspace=workspace)
+    _call_on(x.device, lib().cr_moe_w4g, code, _ptr(x), M, K, _ptr(router), E, topk, int(norm), _ptr(gate), _ptr(up),
+             _ptr(down), F, group, int(zeros), _ptr(out), _ptr(ids), _ptr(weights), _ptr(workspace),
+             workspace.numel())
+    return (out, ids, weights) if routing else out
+
+
+# ---------------------------------------------------------------------------
 # Two-phase form: quantise x once, run GEMMs against one or more weights
 # ---------------------------------------------------------------------------
 
@@ -576,19 +756,28 @@ class PackedWeight:
     N: int
     K: int
     packed: torch.Tensor
-    scale: torch.Tensor              # tensor scale (W4A4, int8tw), s_channel (W4A8), row scales (INT8ROT)
+    scale: Optional[torch.Tensor]    # tensor scale (W4A4, int8tw), s_channel (W4A8), row scales (INT8ROT)
     bias: Optional[torch.Tensor] = None
+    # W4G only (its scales are in `packed`): scale group, zero points, type of x
+    w4g: int = 0
+    zeros: bool = False
+    dtype: Optional[torch.dtype] = None
 
 
 def pack_linear(w: torch.Tensor, bias: Optional[torch.Tensor] = None, int8: bool = False,
-                group: int = 256, regular: bool = False) -> PackedWeight:
+                group: int = 256, regular: bool = False, w4g: int = 0, zeros: bool = False) -> PackedWeight:
     """Pack a bf16 [N,K] weight: W4A4 ConvRot when K % 256 == 0 (ConvRot INT8
     row-scaled instead with ``int8=True``, the format [Q3N] gives attention
     projections; ``group`` picks the W4A4 rotation group: 256, 64 or 16, and
     ``regular=True`` the group-256 regular Hadamard),
     otherwise int8_tensorwise ([REB] "Mixed formats where the
-    kernel demands it")."""
+    kernel demands it").  ``w4g`` = 32, 64 or 128 packs a bf16 or fp16 weight
+    weight-only instead, 4-bit with a scale per group of that many k (and
+    zero points with ``zeros``); K must be a multiple of it."""
     N, K = w.shape
+    if w4g:
+        p = pack_weight_w4g(*encode_w4g(w, w4g, zeros))
+        return PackedWeight(W4G, N, K, p, None, bias, w4g, zeros, w.dtype)
     if K % 256 == 0 and int8:
         p, s = pack_weight_int8rot(w)
         return PackedWeight(INT8ROT, N, K, p, s, bias)
@@ -603,12 +792,53 @@ def pack_linear(w: torch.Tensor, bias: Optional[torch.Tensor] = None, int8: bool
 
 
 def linear(x: torch.Tensor, pw: PackedWeight, out=None, workspace=None) -> torch.Tensor:
+    if pw.kind == W4G:   # needs no workspace
+        if x.dtype != pw.dtype:
+            raise ValueError(f"x must be {pw.dtype}, the type of the weight's scales, got {x.dtype}")
+        return linear_w4g(x, pw.packed, pw.N, pw.w4g, pw.zeros, pw.bias, out)
     if pw.kind in (W4A4_G64, W4A4_G16):
         group = 64 if pw.kind == W4A4_G64 else 16
         return linear_w4a4(x, pw.packed, pw.scale, pw.N, pw.bias, out, workspace, group=group)
     fn = {W4A4: linear_w4a4, INT8TW: linear_int8tw, W4A8: linear_w4a8, INT8ROT: linear_int8rot,
           W4A4_RH: linear_w4a4_regular}[pw.kind]
     return fn(x, pw.packed, pw.scale, pw.N, pw.bias, out, workspace)
+
+
+@dataclasses.dataclass
+class PackedExperts:
+    """The packed experts of a mixture-of-experts layer."""
+    E: int
+    K: int
+    F: int
+    group: int
+    zeros: bool
+    dtype: torch.dtype
+    gate: torch.Tensor
+    up: torch.Tensor
+    down: torch.Tensor
+
+
+def pack_experts(gate: torch.Tensor, up: torch.Tensor, down: torch.Tensor, group: int = 128,
+                 zeros: bool = False) -> PackedExperts:
+    """Pack the experts' 16-bit weights: gate and up [E, F, K], down [E, K, F]."""
+    if gate.dim() != 3 or up.shape != gate.shape or down.shape != (gate.shape[0], gate.shape[2], gate.shape[1]):
+        raise ValueError("gate and up must be [E, F, K] and down [E, K, F]")
+    if up.dtype != gate.dtype or down.dtype != gate.dtype:
+        raise ValueError("gate, up and down must have one type")
+    E, F, K = gate.shape
+    return PackedExperts(E, K, F, group, zeros, gate.dtype,
+                         *(pack_weight_w4g(*encode_w4g(w, group, zeros)) for w in (gate, up, down)))
+
+
+def moe(x: torch.Tensor, router: torch.Tensor, experts: PackedExperts, topk: int, norm: bool = True, out=None,
+        workspace=None, routing: bool = False):
+    """:func:`moe_w4g` with experts from :func:`pack_experts`."""
+    if x.dtype != experts.dtype:
+        raise ValueError(f"x must be {experts.dtype}, the type of the experts' scales, got {x.dtype}")
+    if tuple(router.shape) != (experts.E, experts.K):
+        raise ValueError(f"router must be [{experts.E}, {experts.K}]")
+    return moe_w4g(x, router, experts.gate, experts.up, experts.down, experts.F, experts.group, topk,
+                   experts.zeros, norm, out, workspace, routing)
 
 
 # ---------------------------------------------------------------------------

@@ -343,6 +343,36 @@ cr_status check_mlp_shape(int M, int K, int F, int N) {
     return check_nk(CR_W4A4, N, F);
 }
 
+// ---- 4-bit weights with group scales --------------------------------------
+cr_status check_dtype(int dtype) {
+    if (dtype != CR_BF16 && dtype != CR_FP16) return fail(CR_ERR_KIND, "unknown dtype %d", dtype);
+    return CR_OK;
+}
+
+cr_status check_w4g_shape(int N, int K, int group) {
+    if (N < 1 || K < 1 || N > CR_MAX_DIM || K > CR_MAX_DIM)
+        return fail(CR_ERR_SHAPE, "bad shape N=%d K=%d (need 1..%d)", N, K, CR_MAX_DIM);
+    if (group != 32 && group != 64 && group != 128)
+        return fail(CR_ERR_GROUP, "scale group %d is not 32, 64 or 128", group);
+    if (K % group != 0) return fail(CR_ERR_GROUP, "K=%d is not a multiple of the scale group %d", K, group);
+    return CR_OK;
+}
+
+// Weights one call takes: what a launch's grid covers (2^31 threads of 8).
+constexpr size_t kW4gMaxWeights = (size_t)1 << 34;
+
+cr_status check_moe_shape(int M, int K, int F, int E, int topk, int group) {
+    cr_status s;
+    if ((s = check_m(M)) != CR_OK) return s;
+    if ((s = check_w4g_shape(F, K, group)) != CR_OK) return s;
+    if ((s = check_w4g_shape(K, F, group)) != CR_OK) return s;
+    if (E < 1 || E > CR_MOE_MAX_EXPERTS) return fail(CR_ERR_SHAPE, "E=%d experts (need 1..%d)", E, CR_MOE_MAX_EXPERTS);
+    if (topk < 1 || topk > CR_MOE_MAX_TOPK || topk > E)
+        return fail(CR_ERR_SHAPE, "topk=%d (need 1..%d, at most E=%d)", topk, CR_MOE_MAX_TOPK, E);
+    return CR_OK;
+}
+static_assert(cr::kMoeMaxExperts == CR_MOE_MAX_EXPERTS && cr::kMoeMaxTopk == CR_MOE_MAX_TOPK, "header and library agree");
+
 }  // namespace
 
 extern "C" {
@@ -715,6 +745,94 @@ cr_status cr_dbg_fused_timeouts(uint32_t* count) {
     cr_status s;
     if ((s = check_device()) != CR_OK) return s;
     return launch_err(cr::fused_timeouts(count), "reading the fused linear's timeout counter");
+}
+
+size_t cr_w4g_packed_bytes(int group, int zeros, int N, int K) {
+    if (check_w4g_shape(N, K, group) != CR_OK) return 0;
+    return cr::w4g_packed_bytes(group, zeros != 0, N, K);
+}
+
+cr_status cr_encode_w4g(int dtype, const void* w, int N, int K, int group, void* codes, void* scales, void* zeros,
+                        hipStream_t stream) {
+    cr_status s;
+    if ((s = check_dtype(dtype)) != CR_OK) return s;
+    if ((s = check_w4g_shape(N, K, group)) != CR_OK) return s;
+    if ((size_t)N * K > kW4gMaxWeights) return fail(CR_ERR_SHAPE, "N=%d K=%d: more than 2^34 weights", N, K);
+    if (!w || !codes || !scales) return fail(CR_ERR_NULL, "w, codes or scales is NULL");
+    if (!aligned16(w) || !aligned16(codes) || !aligned16(scales) || !aligned16(zeros))
+        return fail(CR_ERR_ALIGN, "a pointer is not 16-byte aligned");
+    if ((s = check_device()) != CR_OK) return s;
+    return launch_err(cr::launch_w4g_encode(dtype == CR_FP16, static_cast<const uint16_t*>(w), N, K, group,
+                                            static_cast<uint8_t*>(codes), static_cast<uint16_t*>(scales),
+                                            static_cast<uint8_t*>(zeros), stream),
+                      "group encoder");
+}
+
+cr_status cr_pack_weight_w4g(const void* codes, const void* scales, const void* zeros, int count, int N, int K,
+                             int group, void* w_packed, hipStream_t stream) {
+    cr_status s;
+    if ((s = check_w4g_shape(N, K, group)) != CR_OK) return s;
+    if (count < 1 || count > CR_MAX_DIM) return fail(CR_ERR_SHAPE, "bad count=%d", count);
+    const size_t padded = (size_t)cr::round_up(N, 16) * cr::round_up(K, 128);
+    if (padded > kW4gMaxWeights / count) return fail(CR_ERR_SHAPE, "%d x N=%d K=%d: more than 2^34 weights", count, N, K);
+    if (!codes || !scales || !w_packed) return fail(CR_ERR_NULL, "codes, scales or packed weight is NULL");
+    if (!aligned16(codes) || !aligned16(scales) || !aligned16(zeros) || !aligned16(w_packed))
+        return fail(CR_ERR_ALIGN, "a pointer is not 16-byte aligned");
+    if ((s = check_device()) != CR_OK) return s;
+    return launch_err(cr::launch_w4g_pack(static_cast<const uint8_t*>(codes), static_cast<const uint16_t*>(scales),
+                                          static_cast<const uint8_t*>(zeros), count, N, K, group,
+                                          static_cast<uint8_t*>(w_packed), stream),
+                      "group weight packing");
+}
+
+cr_status cr_linear_w4g(int dtype, const void* x, int M, int K, const void* w_packed, int group, int zeros, int N,
+                        const void* bias, void* y, hipStream_t stream) {
+    cr_status s;
+    if ((s = check_dtype(dtype)) != CR_OK) return s;
+    if ((s = check_m(M)) != CR_OK) return s;
+    if ((s = check_w4g_shape(N, K, group)) != CR_OK) return s;
+    if (!w_packed) return fail(CR_ERR_NULL, "packed weight is NULL");
+    if (!aligned16(w_packed) || !aligned16(bias)) return fail(CR_ERR_ALIGN, "packed weight or bias not 16-byte aligned");
+    if (M == 0) return ok();
+    if (!x || !y) return fail(CR_ERR_NULL, "x or y is NULL");
+    if (!aligned16(x) || !aligned16(y)) return fail(CR_ERR_ALIGN, "x or y not 16-byte aligned");
+    if ((s = check_device()) != CR_OK) return s;
+    return launch_err(cr::launch_w4g_linear(dtype == CR_FP16, static_cast<const uint16_t*>(x), M, K,
+                                            static_cast<const uint8_t*>(w_packed), group, zeros != 0, N,
+                                            static_cast<const uint16_t*>(bias), static_cast<uint16_t*>(y), stream),
+                      "group-scaled linear");
+}
+
+size_t cr_moe_w4g_workspace_bytes(int M, int K, int F, int E, int topk, int group) {
+    if (check_moe_shape(M, K, F, E, topk, group) != CR_OK) return 0;
+    const size_t n = cr::moe_workspace(M, F, E, topk);
+    return n < 256 ? 256 : n;
+}
+
+cr_status cr_moe_w4g(int dtype, const void* x, int M, int K, const void* router, int E, int topk, int norm,
+                     const void* wg_packed, const void* wu_packed, const void* wd_packed, int F, int group, int zeros,
+                     void* y, int32_t* ids, float* weights, void* ws, size_t ws_bytes, hipStream_t stream) {
+    cr_status s;
+    if ((s = check_dtype(dtype)) != CR_OK) return s;
+    if ((s = check_moe_shape(M, K, F, E, topk, group)) != CR_OK) return s;
+    if (!router || !wg_packed || !wu_packed || !wd_packed) return fail(CR_ERR_NULL, "router or a packed weight is NULL");
+    if (!aligned16(router) || !aligned16(wg_packed) || !aligned16(wu_packed) || !aligned16(wd_packed))
+        return fail(CR_ERR_ALIGN, "router or a packed weight not 16-byte aligned");
+    if (M == 0) return ok();
+    if (!x || !y || !ws) return fail(CR_ERR_NULL, "x, y or workspace is NULL");
+    if (!aligned16(x) || !aligned16(y) || !aligned16(ws) || !aligned16(ids) || !aligned16(weights))
+        return fail(CR_ERR_ALIGN, "x, y, ids, weights or workspace not 16-byte aligned");
+    const size_t need = cr_moe_w4g_workspace_bytes(M, K, F, E, topk, group);
+    if (ws_bytes < need) return fail(CR_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", ws_bytes, need);
+    if ((s = check_device()) != CR_OK) return s;
+    cr::MoeArgs a{};
+    a.fp16 = dtype == CR_FP16; a.zeros = zeros != 0; a.norm = norm != 0;
+    a.x = static_cast<const uint16_t*>(x); a.router = static_cast<const uint16_t*>(router);
+    a.wg = static_cast<const uint8_t*>(wg_packed); a.wu = static_cast<const uint8_t*>(wu_packed);
+    a.wd = static_cast<const uint8_t*>(wd_packed);
+    a.M = M; a.K = K; a.F = F; a.E = E; a.topk = topk; a.group = group;
+    a.y = static_cast<uint16_t*>(y); a.ids = ids; a.weights = weights; a.ws = ws;
+    return launch_err(cr::launch_moe(a, stream), "mixture-of-experts layer");
 }
 
 }  // extern "C"

@@ -107,6 +107,35 @@ hipError_t launch_encode_w4a8(const uint16_t* w, int N, int K, int iters, uint8_
 // E4M3FN codes (nearest, ties to the even code) of n non-negative floats <= 448.
 hipError_t launch_e4m3_encode(const float* v, size_t n, uint8_t* out, hipStream_t st);
 
+// 4-bit weights with group scales (cr_w4g.hip; layout in cr_w4g.h): packed
+// size, the encoder, packing of `count` stacked weights, the linear.  The
+// 16-bit type is bf16, or fp16 where `fp16` is set; group is 32, 64 or 128.
+size_t w4g_packed_bytes(int group, bool zeros, int N, int K);
+hipError_t launch_w4g_encode(bool fp16, const uint16_t* w, int N, int K, int group, uint8_t* codes, uint16_t* scales,
+                             uint8_t* zeros, hipStream_t st);
+hipError_t launch_w4g_pack(const uint8_t* codes, const uint16_t* scales, const uint8_t* zeros, int count, int N,
+                           int K, int group, uint8_t* out, hipStream_t st);
+hipError_t launch_w4g_linear(bool fp16, const uint16_t* x, int M, int K, const uint8_t* w, int group, bool zeros,
+                             int N, const uint16_t* bias, uint16_t* y, hipStream_t st);
+
+// Mixture-of-experts layer on such weights (cr_moe.hip), kMoeChunk tokens a
+// pass.
+constexpr int kMoeChunk = 64, kMoeMaxExperts = 1024, kMoeMaxTopk = 16;
+struct MoeArgs {
+    bool fp16, zeros, norm;
+    const uint16_t* x;         // [M, K]
+    const uint16_t* router;    // [E, K]
+    const uint8_t *wg, *wu;    // E packed [F, K] each
+    const uint8_t* wd;         // E packed [K, F]
+    int M, K, F, E, topk, group;
+    uint16_t* y;               // [M, K]
+    int32_t* ids;              // [M, topk] or null
+    float* weights;            // [M, topk] or null
+    void* ws;                  // moe_workspace(M, F, E, topk) bytes
+};
+size_t moe_workspace(int M, int F, int E, int topk);
+hipError_t launch_moe(const MoeArgs& a, hipStream_t st);
+
 struct GemmArgs {
     int kind;              // WKind
     const int8_t* qx;      // [M, Kp]
