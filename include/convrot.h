@@ -326,9 +326,8 @@ cr_status cr_mlp_w4a4(const void* x_bf16, int M, int K, const void* wg_packed, c
  * activations, scales, bias and outputs of a call: CR_BF16 or CR_FP16
  * (CR_ERR_KIND otherwise).  Products are exact and sums are held in float32,
  * group by group, each multiplied by its scale there; the only rounding to
- * 16 bits is the output's.  An x row with an infinity or a NaN gives NaN in
- * its own row of y and touches no other; so does a row whose group sums of
- * |x| leave float32's range. */
+ * 16 bits is the output's.  An x row with an infinity or a NaN gives
+ * infinities and NaN in its own row of y and touches no other. */
 #define CR_BF16 0
 #define CR_FP16 1
 
@@ -378,10 +377,11 @@ cr_status cr_linear_w4g(int dtype, const void* x, int M, int K, const void* w_pa
  *   y [M,K] (out); ids [M,topk] int32 and weights [M,topk] float: the chosen
  *   experts and c (out, each may be NULL)
  *   ws / ws_bytes: at least cr_moe_w4g_workspace_bytes(M,K,F,E,topk,group).
- * K and F must be multiples of group.  1 <= E <= CR_MOE_MAX_EXPERTS,
+ * K and F must be multiples of group, at most CR_MOE_MAX_DIM.  1 <= E <= CR_MOE_MAX_EXPERTS,
  * 1 <= topk <= min(E, CR_MOE_MAX_TOPK) (CR_ERR_SHAPE). */
 #define CR_MOE_MAX_EXPERTS 1024
 #define CR_MOE_MAX_TOPK 16
+#define CR_MOE_MAX_DIM 65536
 size_t cr_moe_w4g_workspace_bytes(int M, int K, int F, int E, int topk, int group);
 
 cr_status cr_moe_w4g(int dtype, const void* x, int M, int K, const void* router, int E, int topk, int norm,

@@ -366,6 +366,8 @@ cr_status check_moe_shape(int M, int K, int F, int E, int topk, int group) {
     if ((s = check_m(M)) != CR_OK) return s;
     if ((s = check_w4g_shape(F, K, group)) != CR_OK) return s;
     if ((s = check_w4g_shape(K, F, group)) != CR_OK) return s;
+    if (K > CR_MOE_MAX_DIM || F > CR_MOE_MAX_DIM)
+        return fail(CR_ERR_SHAPE, "K=%d F=%d exceed %d for a mixture of experts", K, F, CR_MOE_MAX_DIM);
     if (E < 1 || E > CR_MOE_MAX_EXPERTS) return fail(CR_ERR_SHAPE, "E=%d experts (need 1..%d)", E, CR_MOE_MAX_EXPERTS);
     if (topk < 1 || topk > CR_MOE_MAX_TOPK || topk > E)
         return fail(CR_ERR_SHAPE, "topk=%d (need 1..%d, at most E=%d)", topk, CR_MOE_MAX_TOPK, E);

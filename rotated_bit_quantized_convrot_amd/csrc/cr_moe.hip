@@ -220,7 +220,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void k_moe_route(const double* __
 constexpr int kWaves = 4;
 
 template <class T, int GPU, bool ZP>
-__global__ __launch_bounds__(64 * kWaves) void k_moe_gate_up(const uint16_t* __restrict__ x, int K, int F,
+__global__ __launch_bounds__(64 * kWaves) void k_moe_gate_up(const uint16_t* __restrict__ x, int M, int K, int F,
                                                              const uint8_t* __restrict__ wg,
                                                              const uint8_t* __restrict__ wu, int topk, int slots,
                                                              int32_t* lists, const float* __restrict__ weights,
@@ -235,17 +235,22 @@ __global__ __launch_bounds__(64 * kWaves) void k_moe_gate_up(const uint16_t* __r
     wu += (size_t)e * l.total;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const size_t tile = blockIdx.x;
+    const buf_t xb = w4g_buf(x, M, K);
     for (int p0 = begin; p0 < end; p0 += 16) {
         const int mine = p0 + (lane & 15);
-        const uint16_t* row = mine < end ? x + (size_t)(ml.pair[mine] / topk) * K : nullptr;
+        const uint32_t row = mine < end ? (uint32_t)(ml.pair[mine] / topk) * (2u * K) : kNoRow;
         f32x4 acc[1][2] = {{f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}}};
         for (int u = wave; u < l.units; u += kWaves) {
             const W4gUnit<GPU> w[2] = {w4g_load<GPU, ZP>(wg, l, tile * l.units + u, lane),
                                        w4g_load<GPU, ZP>(wu, l, tile * l.units + u, lane)};
-            u32x4 a[1][4];
 #pragma unroll
-            for (int d = 0; d < 4; ++d) a[0][d] = w4g_x(row, u * 128 + d * 32 + (lane >> 4) * 8, K);
-            w4g_mac<T, GPU, ZP, 1, 2>(w, a, acc);
+            for (int g = 0; g < GPU; ++g) {
+                u32x4 a[1][4 / GPU];
+#pragma unroll
+                for (int s = 0; s < 4 / GPU; ++s)
+                    a[0][s] = w4g_x(xb, row, u * 128 + (g * (4 / GPU) + s) * 32 + (lane >> 4) * 8, K);
+                w4g_mac<T, GPU, ZP, 1, 2>(g, w, a, acc);
+            }
         }
         part[wave][0][lane] = acc[0][0];
         part[wave][1][lane] = acc[0][1];
@@ -271,7 +276,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_moe_gate_up(const uint16_t* __r
 // so the experts' sums add up in the same accumulators.
 // ---------------------------------------------------------------------------
 template <class T, int GPU, bool ZP, int MT>
-__global__ __launch_bounds__(64 * kWaves) void k_moe_down(const uint16_t* __restrict__ h, int M, int F, int N,
+__global__ __launch_bounds__(64 * kWaves) void k_moe_down(const uint16_t* __restrict__ h, int M, int F, int N, int topk,
                                                           const uint8_t* __restrict__ wd, int slots, int32_t* lists,
                                                           const int16_t* __restrict__ slot_pair,
                                                           uint16_t* __restrict__ y) {
@@ -281,6 +286,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_moe_down(const uint16_t* __rest
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const size_t tile = blockIdx.x;
     const int total = ml.active[0] * l.units;
+    const buf_t hb = w4g_buf(h, M * topk, F);
     f32x4 acc[MT][1];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) acc[mt][0] = f32x4{0, 0, 0, 0};
@@ -288,15 +294,22 @@ __global__ __launch_bounds__(64 * kWaves) void k_moe_down(const uint16_t* __rest
         const int slot = i / l.units, u = i - slot * l.units;
         const W4gUnit<GPU> w[1] = {
             w4g_load<GPU, ZP>(wd + (size_t)ml.expert[slot] * l.total, l, tile * l.units + u, lane)};
-        u32x4 a[MT][4];
+        uint32_t row[MT];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
             const int p = slot_pair[(size_t)slot * kChunk + mt * 16 + (lane & 15)];
-            const uint16_t* row = p >= 0 ? h + (size_t)p * F : nullptr;
-#pragma unroll
-            for (int d = 0; d < 4; ++d) a[mt][d] = w4g_x(row, u * 128 + d * 32 + (lane >> 4) * 8, F);
+            row[mt] = p >= 0 ? (uint32_t)p * (2u * F) : kNoRow;
         }
-        w4g_mac<T, GPU, ZP, MT, 1>(w, a, acc);
+#pragma unroll
+        for (int g = 0; g < GPU; ++g) {
+            u32x4 a[MT][4 / GPU];
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int s = 0; s < 4 / GPU; ++s)
+                    a[mt][s] = w4g_x(hb, row[mt], u * 128 + (g * (4 / GPU) + s) * 32 + (lane >> 4) * 8, F);
+            w4g_mac<T, GPU, ZP, MT, 1>(g, w, a, acc);
+        }
     }
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) part[wave][mt][lane] = acc[mt][0];
@@ -326,15 +339,15 @@ hipError_t moe_t(const MoeArgs& a, const MoeWs& l, int M, const uint16_t* x, uin
     k_moe_logits<T><<<dim3((a.E + 3) / 4, M), 256, 0, st>>>(x, M, a.K, a.router, a.E, logits);
     k_moe_route<<<1, 64 * kRouteWaves, 0, st>>>(logits, M, a.E, a.topk, a.norm, slots, ids_ws, weights_ws, lists,
                                                 slot_pair, ids, weights);
-    k_moe_gate_up<T, GPU, ZP><<<dim3(a.F / 16, slots), 64 * kWaves, 0, st>>>(x, a.K, a.F, a.wg, a.wu, a.topk, slots,
+    k_moe_gate_up<T, GPU, ZP><<<dim3(a.F / 16, slots), 64 * kWaves, 0, st>>>(x, M, a.K, a.F, a.wg, a.wu, a.topk, slots,
                                                                             lists, weights_ws, h);
     const dim3 dg((a.K + 15) / 16), db(64 * kWaves);
     if (M <= 16)
-        k_moe_down<T, GPU, ZP, 1><<<dg, db, 0, st>>>(h, M, a.F, a.K, a.wd, slots, lists, slot_pair, y);
+        k_moe_down<T, GPU, ZP, 1><<<dg, db, 0, st>>>(h, M, a.F, a.K, a.topk, a.wd, slots, lists, slot_pair, y);
     else if (M <= 32)
-        k_moe_down<T, GPU, ZP, 2><<<dg, db, 0, st>>>(h, M, a.F, a.K, a.wd, slots, lists, slot_pair, y);
+        k_moe_down<T, GPU, ZP, 2><<<dg, db, 0, st>>>(h, M, a.F, a.K, a.topk, a.wd, slots, lists, slot_pair, y);
     else
-        k_moe_down<T, GPU, ZP, 4><<<dg, db, 0, st>>>(h, M, a.F, a.K, a.wd, slots, lists, slot_pair, y);
+        k_moe_down<T, GPU, ZP, 4><<<dg, db, 0, st>>>(h, M, a.F, a.K, a.topk, a.wd, slots, lists, slot_pair, y);
     return hipGetLastError();
 }
 

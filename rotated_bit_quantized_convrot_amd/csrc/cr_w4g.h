@@ -9,13 +9,12 @@
 //   codes   1 KiB tiles (16 rows x 128 k), tile (t, u) at (t U + u) * 1024;
 //           lane l of the wave that reads it owns the 16 bytes at 16 l: row
 //           16 t + l % 16, dword d holding k = 128 u + 32 d + 8 (l / 16) + 0..7,
-//           k + 2 j in bits 4 j and k + 2 j + 1 in bits 16 + 4 j: the order in
-//           which one shift and one AND-OR make an operand register of two
-//           codes, and 4 dwords are the B operands of 4 MFMA 16x16x32.
+//           the B operand of one MFMA 16x16x32: q ^ 8 of k + 2 j in bits 4 j,
+//           of k + 2 j + 1 in bits 16 + 4 j (below, the 16-bit types)
 //   scales  16-bit, [t][u][row % 16][128 / g]
 //   zeros   (weights with zero points) [t][u][row % 16][max(1, 64 / g)]
 //           bytes, group i of the unit in bits 4 (i % 2) of byte i / 2
-// Rows past N and k past K hold code 0 and scale 0.
+// Rows past N and k past K hold zeros.
 #pragma once
 #include "cr_device.h"
 
@@ -25,25 +24,45 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 
-// The 16-bit types.  An operand register of two codes is (1 + q / 16) twice:
-// the code in the top mantissa bits of 1.0, so making it takes no
-// conversion, and 16 sum x (1 + q/16) - (16 + z) sum x = sum x (q - z).
-// 1 + q/16 is exact in both types; the offset costs the float32 sums ~2 bits
-// against sums of x (q - z), of which a 16-bit result keeps 8 or 11.
+// The 16-bit types: the MFMA, conversions, and an MFMA operand of 8 codes.
+// The operand holds (q - z) / 16, exact in both types; the factor 16 goes
+// into the group's scale.
+//   fp16  (1 + q / 16) is the code put into the top mantissa bits of 1.0, and
+//         one packed add takes 1 + z / 16 off.
+//   bf16  has no packed add; v_cvt_off_f32_i4 turns a two's-complement nibble
+//         c into c / 16 as float32, whose upper half is that value in bf16.
+//         The packed codes are therefore stored as q ^ 8 = q - 8; where a
+//         weight has zero points the operand stays (q - 8) / 16 and the
+//         sums start from (8 - z) / 16 sum x.
 struct Bf16 {
-    static constexpr uint32_t kMask = 0x00780078u, kOne = 0x3F803F80u;
-    static constexpr int kShift = 3;
+    static constexpr uint32_t kMinusOne = 0xBF80BF80u;
+    static constexpr bool kZeroInOperand = false;
     static __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b),
                                                        c, 0, 0, 0);
     }
     static __device__ __forceinline__ float to_f32(uint32_t v) { return __uint_as_float(v << 16); }
     static __device__ __forceinline__ uint16_t from_f32(float v) { return (uint16_t)f32_to_bf16_rne(v); }
+    static __device__ __forceinline__ u32x4 operand(uint32_t c, uint32_t) {
+        // the low nibbles of c's bytes are k 0, 4, 1, 5, those of c >> 4 are k 2, 6, 3, 7
+        uint32_t h = c >> 4;
+        asm("" : "+v"(h));   // kept as it is: the conversions then take its bytes with no shift of their own
+        u32x4 b;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t v = (j & 1) ? h : c;
+            const float lo = __builtin_amdgcn_cvt_off_f32_i4((v >> (4 * (j & 2))) & 0xFFu);
+            const float hi = __builtin_amdgcn_cvt_off_f32_i4((v >> (16 + 4 * (j & 2))) & 0xFFu);
+            b[j] = __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u);
+        }
+        return b;
+    }
 };
 struct Fp16 {
-    static constexpr uint32_t kMask = 0x03C003C0u, kOne = 0x3C003C00u;
-    static constexpr int kShift = 6;
+    static constexpr uint32_t kMinusOne = 0xBC00BC00u;
+    static constexpr bool kZeroInOperand = true;
     static __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c,
                                                       0, 0, 0);
@@ -53,6 +72,18 @@ struct Fp16 {
     }
     static __device__ __forceinline__ uint16_t from_f32(float v) {
         return __builtin_bit_cast(uint16_t, (_Float16)v);
+    }
+    // `off`: -(1 + z / 16) twice; the XOR sets 1.0 and flips the code's top bit back
+    static __device__ __forceinline__ u32x4 operand(uint32_t c, uint32_t off) {
+        u32x4 b;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int sh = 6 - 4 * j;
+            const uint32_t v = sh >= 0 ? c << (sh >= 0 ? sh : 0) : c >> (sh < 0 ? -sh : 0);
+            const uint32_t p = (v & 0x03C003C0u) ^ 0x3E003E00u;
+            b[j] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, p) + __builtin_bit_cast(f16x2, off));
+        }
+        return b;
     }
 };
 
@@ -108,68 +139,97 @@ __device__ __forceinline__ W4gUnit<GPU> w4g_load(const uint8_t* w, const W4gLayo
     return r;
 }
 
-// Eight codes -> the MFMA operand (1 + q / 16) x 8.
-template <class T>
-__device__ __forceinline__ u32x4 w4g_operand(uint32_t c) {
-    u32x4 b;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int sh = T::kShift - 4 * j;
-        const uint32_t v = sh >= 0 ? c << (sh >= 0 ? sh : 0) : c >> (sh < 0 ? -sh : 0);
-        b[j] = (v & T::kMask) | T::kOne;
-    }
-    return b;
-}
-
-// acc[mt][nt] += x W^T over one unit.  a[mt][d]: x rows 16 mt + lane % 16 at
-// k = 32 d + 8 (lane / 16) + 0..7 of the unit (zero where there is no such
-// row or k); acc in the MFMA's C layout: column n = lane % 16, rows
-// m = 4 (lane / 16) + i.  Every group's sum is held in float32 and scaled
-// there; sum x comes from one more MFMA against ones, which leaves it in the
-// lanes that need it and is shared by the NT weight tiles.
+// acc[mt][nt] += x W^T over group g of a unit.  a[mt][s]: x rows
+// 16 mt + lane % 16 at k = 32 (g SPG + s) + 8 (lane / 16) + 0..7 of the unit
+// (zero where there is no such k; rows do not mix, so what a row that does
+// not exist holds is no matter); acc in the MFMA's C layout: column
+// n = lane % 16, rows m = 4 (lane / 16) + i.  The group's sum is held in
+// float32 and scaled there.
 template <class T, int GPU, bool ZP, int MT, int NT>
-__device__ __forceinline__ void w4g_mac(const W4gUnit<GPU> (&w)[NT], const u32x4 (&a)[MT][4], f32x4 (&acc)[MT][NT]) {
+__device__ __forceinline__ void w4g_mac(int g, const W4gUnit<GPU> (&w)[NT], const u32x4 (&a)[MT][4 / GPU],
+                                        f32x4 (&acc)[MT][NT]) {
     constexpr int SPG = 4 / GPU;   // MFMA steps per group
-    const u32x4 ones = {T::kOne, T::kOne, T::kOne, T::kOne};
+    u32x4 b[NT][SPG];
+    float s16[NT];
 #pragma unroll
-    for (int g = 0; g < GPU; ++g) {
-        f32x4 xs[MT], t[MT][NT];
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-            xs[mt] = f32x4{0, 0, 0, 0};
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) t[mt][nt] = f32x4{0, 0, 0, 0};
-        }
-#pragma unroll
-        for (int s = 0; s < SPG; ++s) {
-            const int d = g * SPG + s;
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) xs[mt] = T::mfma(a[mt][d], ones, xs[mt]);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const u32x4 b = w4g_operand<T>(w[nt].codes[d]);
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt) t[mt][nt] = T::mfma(a[mt][d], b, t[mt][nt]);
-            }
-        }
+    for (int nt = 0; nt < NT; ++nt) s16[nt] = 16.0f * T::to_f32((w[nt].scale[g / 2] >> (16 * (g % 2))) & 0xFFFFu);
+    if constexpr (ZP && !T::kZeroInOperand) {
+        // -sum x of the group comes from one more MFMA, against -1, in the lanes that need it; the
+        // operands are made first, so that one row tile's sums are alive at a time
+        const u32x4 minus = {T::kMinusOne, T::kMinusOne, T::kMinusOne, T::kMinusOne};
+        float z[NT];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const float s = T::to_f32((w[nt].scale[g / 2] >> (16 * (g % 2))) & 0xFFFFu);
-            const float z = ZP ? (float)((w[nt].zero >> (4 * g)) & 15u) : 8.0f;
-            const float s16 = 16.0f * s, sz = -s * (16.0f + z);
+#pragma unroll
+            for (int s = 0; s < SPG; ++s) b[nt][s] = T::operand(w[nt].codes[g * SPG + s], 0);
+            z[nt] = 0.0625f * (float)((int)((w[nt].zero >> (4 * g)) & 15u) - 8);
+        }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            f32x4 xs = {0, 0, 0, 0};
+#pragma unroll
+            for (int s = 0; s < SPG; ++s) xs = T::mfma(a[mt][s], minus, xs);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                f32x4 t = {0, 0, 0, 0};
+#pragma unroll
+                for (int s = 0; s < SPG; ++s) t = T::mfma(a[mt][s], b[nt][s], t);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    acc[mt][nt][i] = __builtin_fmaf(s16[nt], __builtin_fmaf(xs[i], z[nt], t[i]), acc[mt][nt][i]);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const uint32_t z = ZP ? (w[nt].zero >> (4 * g)) & 15u : 8u;
+            f32x4 t[MT];
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) t[mt] = f32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int s = 0; s < SPG; ++s) {
+                b[nt][s] = T::operand(w[nt].codes[g * SPG + s], 0xBC00BC00u + z * 0x00400040u);
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) t[mt] = T::mfma(a[mt][s], b[nt][s], t[mt]);
+            }
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    acc[mt][nt][i] = __builtin_fmaf(s16, t[mt][nt][i], __builtin_fmaf(sz, xs[mt][i], acc[mt][nt][i]));
+                for (int i = 0; i < 4; ++i) acc[mt][nt][i] = __builtin_fmaf(s16[nt], t[mt][i], acc[mt][nt][i]);
         }
     }
 }
 
-// 8 values of x row `row` (nullptr: none) at k, zero past K.
-__device__ __forceinline__ u32x4 w4g_x(const uint16_t* row, int k, int K) {
-    if (row == nullptr || k >= K) return u32x4{0, 0, 0, 0};
-    return *reinterpret_cast<const u32x4*>(row + k);
+// Rows of x behind a buffer descriptor: a load past its end gives zeros, so
+// rows and k that do not exist take no branch.  The rows of one tile only:
+// offsets stay in 32 bits whatever the matrix.
+__device__ __forceinline__ v4i w4g_rows(const uint16_t* x, int rows, int K) {
+    const uint64_t a = (uint64_t)(uintptr_t)x;
+    v4i r;
+    r.x = __builtin_amdgcn_readfirstlane((int)(uint32_t)a);
+    r.y = __builtin_amdgcn_readfirstlane((int)((uint32_t)(a >> 32) & 0xFFFFu));
+    r.z = __builtin_amdgcn_readfirstlane(rows * K * 2);
+    r.w = 0x00020000;
+    return r;
 }
+typedef __amdgpu_buffer_rsrc_t buf_t;
+__device__ __forceinline__ buf_t w4g_buf(const uint16_t* x, int rows, int K) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(x), 0, rows * K * 2, 0x00020000);
+}
+constexpr uint32_t kNoRow = 0x80000000u;   // + 2 k stays past any tile
+// 8 values at byte offset `row` (kNoRow: none) + 2 k, zeros past K.
+__device__ __forceinline__ u32x4 w4g_x(buf_t x, uint32_t row, int k, int K) {
+    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(x, k < K ? row + 2u * (uint32_t)k : kNoRow, 0, 0));
+}
+
+// Lane i's 16 bytes at byte offset `off` of the rows go to LDS address
+// lds + 16 i (wave-uniform); the caller waits (w4g_wait) before a barrier
+// that publishes them.  Every offset has to lie inside the rows.
+__device__ __forceinline__ void w4g_x_to_lds(v4i x, uint32_t off, uint32_t lds) {
+    asm volatile("buffer_load_dwordx4 %0, %1, 0 offen lds" : : "v"(off), "s"(x), "{m0}"(lds) : "memory");
+}
+// Every load of this wave has arrived.
+__device__ __forceinline__ void w4g_wait() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+__device__ __forceinline__ void w4g_barrier() { asm volatile("s_barrier" ::: "memory"); }
 
 }  // namespace cr

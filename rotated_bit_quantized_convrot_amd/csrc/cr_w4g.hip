@@ -83,7 +83,7 @@ __global__ __launch_bounds__(256) void k_w4g_pack(const uint8_t* __restrict__ co
             uint32_t e = w & 0x0F0F0F0Fu, o = (w >> 4) & 0x0F0F0F0Fu;
             e = (e | (e >> 4)) & 0x00FF00FFu;
             o = (o | (o >> 4)) & 0x00FF00FFu;
-            v[d] = ((e | (e >> 8)) & 0xFFFFu) | ((o | (o >> 8)) << 16);
+            v[d] = (((e | (e >> 8)) & 0xFFFFu) | ((o | (o >> 8)) << 16)) ^ 0x88888888u;
         }
     }
     *reinterpret_cast<u32x4*>(out + tu * 1024 + lane * 16) = v;
@@ -105,76 +105,186 @@ __global__ __launch_bounds__(256) void k_w4g_pack(const uint8_t* __restrict__ co
 }
 
 // ---------------------------------------------------------------------------
-// Linear.  A block owns 16 weight rows and 16 MT rows of x; its waves take
-// the units of K in turn and their sums meet in LDS, added in the order of
-// the waves (no atomics: results do not change between runs).
+// Linear.  Block tile BM = 16 MT WM rows of x by BN = 16 NT WN weight rows,
+// by WM x WN waves for each of KG groups of waves that take the units of K
+// in turn; the groups' sums meet in LDS and are added in their order (no
+// atomics: results do not change between runs).  A group's x tile (BM rows
+// x 128 k) goes straight to LDS, one unit ahead; weights go straight to
+// registers, one unit ahead, and are made operands there.  A group of one
+// wave needs no barrier: it waits for its own loads.
+// LDS rows of 256 bytes, 16-byte chunk c of row r at slot c ^ (r % 16): the
+// 16 rows of an operand read hit 16 different slots.
 // ---------------------------------------------------------------------------
-constexpr int kWaves = 4;
+template <int MT, int NT, int WM, int WN, int KG>
+struct Tile {
+    static constexpr int kThreads = 64 * WM * WN * KG;
+    static constexpr int kBM = 16 * MT * WM, kBN = 16 * NT * WN;
+    static constexpr int kTile = kBM * 256, kStage = KG * kTile;
+    static constexpr int kSums = KG * kBM * kBN * 4;
+    static constexpr int kLds = 2 * kStage > kSums ? 2 * kStage : kSums;
+    static_assert(kLds <= 160 * 1024 && kThreads <= 1024, "a block fits a CU");
+    static_assert(kBM / 4 % (WM * WN) == 0, "the group's waves share the staging evenly");
+};
 
-template <class T, int GPU, bool ZP, int MT>
-__global__ __launch_bounds__(64 * kWaves) void k_w4g_linear(const uint16_t* __restrict__ x, int M, int K,
-                                                            const uint8_t* __restrict__ w, int N,
-                                                            const uint16_t* __restrict__ bias,
-                                                            uint16_t* __restrict__ y) {
-    __shared__ f32x4 part[kWaves][MT][64];
+template <class T, int GPU, bool ZP, int MT, int NT, int WM, int WN, int KG>
+__global__ __launch_bounds__(64 * WM * WN * KG) void k_w4g_linear(const uint16_t* __restrict__ x, int M, int K,
+                                                                  const uint8_t* __restrict__ w, int N,
+                                                                  const uint16_t* __restrict__ bias,
+                                                                  uint16_t* __restrict__ y) {
+    using C = Tile<MT, NT, WM, WN, KG>;
+    extern __shared__ __attribute__((aligned(16))) char lds[];
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds;
     const W4gLayout l = w4g_layout(128 / GPU, ZP, N, K);
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const size_t tile = blockIdx.x;
-    const int m0 = blockIdx.y * (16 * MT);
-    const uint16_t* rows[MT];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int kg = wave / (WM * WN), r = wave % (WM * WN), wm = r % WM, wn = r / WM;
+    const int m0 = blockIdx.y * C::kBM, rows = M - m0 < C::kBM ? M - m0 : C::kBM;
+    const int tile0 = blockIdx.x * (NT * WN) + wn * NT;
+    const v4i xb = w4g_rows(x + (size_t)m0 * K, rows, K);
+
+    // x of unit u into stage s: 4 rows an instruction.  Rows and k that do
+    // not exist read ones that do: their results are not stored, their
+    // weights' scales are 0.
+    auto stage = [&](int u, int s) {
+        u = u < l.units ? u : l.units - 1;
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-        const int m = m0 + mt * 16 + (lane & 15);
-        rows[mt] = m < M ? x + (size_t)m * K : nullptr;
+        for (int i = 0; i < C::kBM / 4 / (WM * WN); ++i) {
+            const int row4 = (i * (WM * WN) + r) * 4, row = row4 + (lane >> 4);
+            const uint32_t rb = (uint32_t)(row < rows ? row : rows - 1) * (2u * K);
+            const uint32_t kb = u * 256u + (((uint32_t)lane & 15u) ^ ((uint32_t)row & 15u)) * 16u;
+            w4g_x_to_lds(xb, rb + (kb < 2u * K ? kb : 2u * K - 16u), lds0 + s * C::kStage + kg * C::kTile + row4 * 256);
+        }
+    };
+    auto weights = [&](int u, W4gUnit<GPU> (&wu)[NT]) {
+        u = u < l.units ? u : l.units - 1;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int t = tile0 + nt < l.tiles ? tile0 + nt : l.tiles - 1;
+            wu[nt] = w4g_load<GPU, ZP>(w, l, (size_t)t * l.units + u, lane);
+        }
+    };
+
+    f32x4 acc[MT][NT];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) acc[mt][nt] = f32x4{0, 0, 0, 0};
+    const int iters = (l.units + KG - 1) / KG;
+    W4gUnit<GPU> wu[NT];
+    weights(kg, wu);
+    stage(kg, 0);
+    for (int it = 0; it < iters; ++it) {
+        const int u = it * KG + kg;
+        w4g_wait();
+        // this unit's x is there, and the other stage has been read by all
+        if constexpr (WM * WN > 1) w4g_barrier();
+        W4gUnit<GPU> next[NT];
+        if (it + 1 < iters) {
+            weights(u + KG, next);
+            stage(u + KG, (it + 1) & 1);
+        }
+        const char* xt = lds + (it & 1) * C::kStage + kg * C::kTile + (wm * MT * 16 + (lane & 15)) * 256;
+        if (u < l.units) {
+#pragma unroll
+            for (int g = 0; g < GPU; ++g) {
+                u32x4 a[MT][4 / GPU];
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int s = 0; s < 4 / GPU; ++s) {
+                        const int c = (g * (4 / GPU) + s) * 4 + (lane >> 4);
+                        a[mt][s] = *reinterpret_cast<const u32x4*>(xt + mt * 4096 + ((c ^ (lane & 15)) * 16));
+                    }
+                w4g_mac<T, GPU, ZP, MT, NT>(g, wu, a, acc);
+            }
+        }
+        if (it + 1 < iters) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) wu[nt] = next[nt];
+        }
     }
-    f32x4 acc[MT][1];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) acc[mt][0] = f32x4{0, 0, 0, 0};
-    for (int u = wave; u < l.units; u += kWaves) {
-        W4gUnit<GPU> wu[1] = {w4g_load<GPU, ZP>(w, l, tile * l.units + u, lane)};
-        u32x4 a[MT][4];
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int d = 0; d < 4; ++d) a[mt][d] = w4g_x(rows[mt], u * 128 + d * 32 + (lane >> 4) * 8, K);
-        w4g_mac<T, GPU, ZP, MT, 1>(wu, a, acc);
-    }
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) part[wave][mt][lane] = acc[mt][0];
     __syncthreads();
-    // thread -> (row m of the tile, column n): 16 neighbours write 32 bytes
-    for (int i = threadIdx.x; i < 256 * MT; i += 64 * kWaves) {
-        const int m = i >> 4, n = i & 15;
-        const int gm = m0 + m;
-        const size_t gn = tile * 16 + n;
-        if (gm >= M || gn >= (size_t)N) continue;
+    f32x4* part = reinterpret_cast<f32x4*>(lds);   // [KG][WN NT][WM MT][64]
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+            part[((kg * (WN * NT) + wn * NT + nt) * (WM * MT) + wm * MT + mt) * 64 + lane] = acc[mt][nt];
+    __syncthreads();
+    for (int i = threadIdx.x; i < rows * C::kBN; i += C::kThreads) {
+        const int m = i / C::kBN, n = i % C::kBN;
+        const size_t gn = (size_t)blockIdx.x * C::kBN + n;
+        if (gn >= (size_t)N) continue;
         float v = 0.0f;
 #pragma unroll
-        for (int wv = 0; wv < kWaves; ++wv) v += part[wv][m >> 4][((m & 15) >> 2) * 16 + n][m & 3];
+        for (int g = 0; g < KG; ++g)
+            v += part[((g * (WN * NT) + (n >> 4)) * (WM * MT) + (m >> 4)) * 64 + ((m & 15) >> 2) * 16 + (n & 15)][m & 3];
         if (bias != nullptr) v += T::to_f32(bias[gn]);
-        y[(size_t)gm * N + gn] = T::from_f32(v);
+        y[(size_t)(m0 + m) * N + gn] = T::from_f32(v);
     }
 }
 
-template <class T, int GPU, bool ZP>
-hipError_t linear_t(const uint16_t* x, int M, int K, const uint8_t* w, int N, const uint16_t* bias, uint16_t* y,
-                    hipStream_t st) {
-    const dim3 block(64 * kWaves);
-    const unsigned tiles = (unsigned)((N + 15) / 16);
-    if (M <= 16)
-        k_w4g_linear<T, GPU, ZP, 1><<<dim3(tiles, 1), block, 0, st>>>(x, M, K, w, N, bias, y);
-    else
-        k_w4g_linear<T, GPU, ZP, 4><<<dim3(tiles, (M + 63) / 64), block, 0, st>>>(x, M, K, w, N, bias, y);
+struct LinearArgs {
+    const uint16_t* x;
+    int M, K;
+    const uint8_t* w;
+    int N;
+    const uint16_t* bias;
+    uint16_t* y;
+};
+
+template <class T, int GPU, bool ZP, int MT, int NT, int WM, int WN, int KG>
+hipError_t tile(const LinearArgs& a, hipStream_t st) {
+    using C = Tile<MT, NT, WM, WN, KG>;
+    static std::atomic<uint64_t> done{0};
+    const auto kernel = k_w4g_linear<T, GPU, ZP, MT, NT, WM, WN, KG>;
+    const hipError_t e = opt_in_lds(reinterpret_cast<const void*>(kernel), C::kLds, done);
+    if (e != hipSuccess) return e;
+    kernel<<<dim3((a.N + C::kBN - 1) / C::kBN, (a.M + C::kBM - 1) / C::kBM), C::kThreads, C::kLds, st>>>(
+        a.x, a.M, a.K, a.w, a.N, a.bias, a.y);
     return hipGetLastError();
 }
 
+// Tile choice.  Fewer, wider blocks read x less often and share its operand
+// reads; narrow ones put more CUs to work.  The wide tile is taken where its
+// blocks fill half the chip (256 CUs).  Measured, us, bf16, groups of 128,
+// K x N = 2560 x 9728 / 9728 x 2560 / 2560 x 2560 (weights cold):
+//   M = 8     one tile, 4 K groups 6.6 / 14.0 / 4.3, 10 groups 7.2 / 8.1 / 3.6,
+//             16 groups 9.5 / 7.3 / 3.8
+//   M = 32    wide 10.2 / 19.1 / 5.9, narrow 13.0 / 12.9 / 4.5
+//   M = 48    wide 12.3 / 35.5 / 10.3, narrow 16.8 / 16.5 / 5.6
+//   M = 76    wide 15.1 / 42.1 / 12.7, narrow 24.7 / 24.2 / 8.4
+//   M = 1220  128 x 128 86.7 / 95.1, 80 x 64 112.7 / 120.9; M = 300 at
+//             2560 x 2560 (60 blocks of 128 x 128) 26.9 and 13.2
+template <class T, int GPU, bool ZP>
+hipError_t linear_t(const LinearArgs& a, hipStream_t st) {
+    constexpr long kHalf = 128;
+    const long tiles = (a.N + 15) / 16;
+    const int units = (a.K + 127) / 128;
+    if (a.M <= 16) {
+        if (tiles > 2 * 256) return tile<T, GPU, ZP, 1, 1, 1, 1, 4>(a, st);
+        if (units > 40) return tile<T, GPU, ZP, 1, 1, 1, 1, 16>(a, st);
+        return tile<T, GPU, ZP, 1, 1, 1, 1, 10>(a, st);
+    }
+    if (a.M <= 32) {
+        if ((tiles + 1) / 2 >= kHalf) return tile<T, GPU, ZP, 2, 1, 1, 2, 4>(a, st);
+        return tile<T, GPU, ZP, 2, 1, 1, 1, 8>(a, st);
+    }
+    if (a.M <= 48) {
+        if ((tiles + 3) / 4 >= kHalf) return tile<T, GPU, ZP, 3, 2, 1, 2, 4>(a, st);
+        return tile<T, GPU, ZP, 3, 1, 1, 1, 6>(a, st);
+    }
+    if (a.M > 80 && (long)((a.M + 127) / 128) * ((a.N + 127) / 128) >= kHalf)
+        return tile<T, GPU, ZP, 8, 2, 1, 4, 2>(a, st);
+    if ((a.M + 79) / 80 * ((tiles + 3) / 4) >= kHalf) return tile<T, GPU, ZP, 5, 2, 1, 2, 4>(a, st);
+    return tile<T, GPU, ZP, 5, 1, 1, 1, 4>(a, st);
+}
+
 template <class T>
-hipError_t linear_g(const uint16_t* x, int M, int K, const uint8_t* w, int group, bool zeros, int N,
-                    const uint16_t* bias, uint16_t* y, hipStream_t st) {
+hipError_t linear_g(const LinearArgs& a, int group, bool zeros, hipStream_t st) {
     switch (group) {
-        case 32: return zeros ? linear_t<T, 4, true>(x, M, K, w, N, bias, y, st) : linear_t<T, 4, false>(x, M, K, w, N, bias, y, st);
-        case 64: return zeros ? linear_t<T, 2, true>(x, M, K, w, N, bias, y, st) : linear_t<T, 2, false>(x, M, K, w, N, bias, y, st);
-        default: return zeros ? linear_t<T, 1, true>(x, M, K, w, N, bias, y, st) : linear_t<T, 1, false>(x, M, K, w, N, bias, y, st);
+        case 32: return zeros ? linear_t<T, 4, true>(a, st) : linear_t<T, 4, false>(a, st);
+        case 64: return zeros ? linear_t<T, 2, true>(a, st) : linear_t<T, 2, false>(a, st);
+        default: return zeros ? linear_t<T, 1, true>(a, st) : linear_t<T, 1, false>(a, st);
     }
 }
 
@@ -218,8 +328,8 @@ hipError_t launch_w4g_pack(const uint8_t* codes, const uint16_t* scales, const u
 
 hipError_t launch_w4g_linear(bool fp16, const uint16_t* x, int M, int K, const uint8_t* w, int group, bool zeros,
                              int N, const uint16_t* bias, uint16_t* y, hipStream_t st) {
-    if (fp16) return linear_g<Fp16>(x, M, K, w, group, zeros, N, bias, y, st);
-    return linear_g<Bf16>(x, M, K, w, group, zeros, N, bias, y, st);
+    const LinearArgs a = {x, M, K, w, N, bias, y};
+    return fp16 ? linear_g<Fp16>(a, group, zeros, st) : linear_g<Bf16>(a, group, zeros, st);
 }
 
 }  // namespace cr

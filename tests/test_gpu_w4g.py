@@ -124,7 +124,8 @@ def test_linear_layers(M, N, K, group, dtype):
 
 def test_linear_rows_do_not_depend_on_each_other():
     """A row's result is the same bits whatever the other rows hold, and a NaN
-    or an infinity in one stays in it."""
+    or an infinity in one stays in it (an infinity times a code at its zero
+    point is a NaN, as in the definition)."""
     w = R.stored((100,), 384, 64, torch.bfloat16, False, 3)
     packed = crp.pack_weight_w4g(*map(dev, w))
     for M in (16, 70, 300):
@@ -134,7 +135,7 @@ def test_linear_rows_do_not_depend_on_each_other():
         x2[M // 2, 7] = float("nan")
         x2[M // 3, 100] = float("inf")
         y2 = crp.linear_w4g(x2, packed, 100, 64)
-        assert torch.isnan(y2[M // 2]).all() and torch.isnan(y2[M // 3]).all()
+        assert torch.isnan(y2[M // 2]).all() and not torch.isfinite(y2[M // 3]).any()
         keep = [m for m in range(M) if m not in (M // 2, M // 3)]
         assert torch.equal(y[keep], y2[keep])
         assert torch.equal(y, crp.linear_w4g(x, packed, 100, 64))

@@ -87,6 +87,7 @@ def test_moe_refusals(L):
     assert call(E=0) == SHAPE and call(E=1025) == SHAPE
     assert call(topk=0) == SHAPE and call(topk=9) == SHAPE and call(E=64, topk=17) == SHAPE
     assert call(K=200) == GROUP and call(F=100) == GROUP and call(group=256) == GROUP
+    assert call(K=65536 + 128) == SHAPE and call(F=65536 + 128) == SHAPE
     for k in ("router", "wg", "wu", "wd", "x", "y", "ws"):
         assert call(**{k: None}) == NULL, k
     for k in ("router", "wg", "wu", "wd", "x", "y", "ws", "ids", "weights"):
