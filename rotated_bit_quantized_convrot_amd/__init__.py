@@ -22,6 +22,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import functools
 import os
 from typing import Optional
 
@@ -524,15 +525,25 @@ def _dtype16(t: torch.Tensor, name: str) -> int:
     return code
 
 
+def _stream_of(index: int) -> int:
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+# The same handle without building a Stream object (2.5 us of a call whose
+# launch costs 4), where this torch has it.
+_stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", _stream_of)
+
+
 def _call_on(device, fn, *args):
     """fn(*args, stream) with ``device`` current and on its current stream,
     whichever device is current outside."""
     if device.index == torch.cuda.current_device():
-        return _check(fn(*args, _stream()))
+        return _check(fn(*args, _stream_of(device.index)))
     with torch.cuda.device(device):
-        return _check(fn(*args, _stream()))
+        return _check(fn(*args, _stream_of(device.index)))
 
 
+@functools.lru_cache(maxsize=4096)
 def w4g_packed_bytes(group: int, zeros: bool, N: int, K: int) -> int:
     return int(lib().cr_w4g_packed_bytes(group, int(zeros), N, K))
 
@@ -616,7 +627,7 @@ def linear_w4g(x, packed, N, group, zeros=False, bias=None, out=None):
         if bias.numel() != N:
             raise ValueError("bias must have N elements")
     if out is None:
-        out = torch.empty((M, max(N, 0)), dtype=x.dtype, device=x.device)
+        out = x.new_empty((M, max(N, 0)))
     else:
         _dev(out, "out", x.dtype)
         if tuple(out.shape) != (M, N):
@@ -627,6 +638,7 @@ def linear_w4g(x, packed, N, group, zeros=False, bias=None, out=None):
     return out
 
 
+@functools.lru_cache(maxsize=4096)
 def moe_w4g_workspace_bytes(M: int, K: int, F: int, E: int, topk: int, group: int) -> int:
     return int(lib().cr_moe_w4g_workspace_bytes(M, K, F, E, topk, group))
 

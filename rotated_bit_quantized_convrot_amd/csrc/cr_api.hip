@@ -807,7 +807,7 @@ cr_status cr_linear_w4g(int dtype, const void* x, int M, int K, const void* w_pa
 
 size_t cr_moe_w4g_workspace_bytes(int M, int K, int F, int E, int topk, int group) {
     if (check_moe_shape(M, K, F, E, topk, group) != CR_OK) return 0;
-    const size_t n = cr::moe_workspace(M, F, E, topk);
+    const size_t n = cr::moe_workspace(M, K, F, E, topk);
     return n < 256 ? 256 : n;
 }
 

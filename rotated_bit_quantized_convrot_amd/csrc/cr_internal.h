@@ -131,9 +131,9 @@ struct MoeArgs {
     uint16_t* y;               // [M, K]
     int32_t* ids;              // [M, topk] or null
     float* weights;            // [M, topk] or null
-    void* ws;                  // moe_workspace(M, F, E, topk) bytes
+    void* ws;                  // moe_workspace(M, K, F, E, topk) bytes
 };
-size_t moe_workspace(int M, int F, int E, int topk);
+size_t moe_workspace(int M, int K, int F, int E, int topk);
 hipError_t launch_moe(const MoeArgs& a, hipStream_t st);
 
 struct GemmArgs {

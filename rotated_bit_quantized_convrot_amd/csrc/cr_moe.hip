@@ -1,16 +1,26 @@
 // Mixture-of-experts layer on 4-bit weights with group scales, for a few
 // tokens: router logits, top-k and softmax, the chosen experts' gated MLPs
-// and their weighted sum.
+// and their weighted sum, in three launches.
 //
 //   l[m,e] = sum_k x[m,k] r[e,k];  e_0..e_{k-1} the largest, ties to the lower e
 //   p = exp(l - max l),  c[m,r] = p[e_r] / (sum over the chosen, or over all)
-//   h[m,r] = T(c[m,r] silu(Wg_e x[m]) (Wu_e x[m]))        (T: the 16-bit type)
-//   y[m]   = T(sum_r Wd_{e_r} h[m,r])
+//   h[m,r] = silu(Wg_e x[m]) (Wu_e x[m])
+//   y[m]   = T(sum_r c[m,r] Wd_{e_r} h[m,r])       (T: the 16-bit type)
 //
-// A pass is bound by the chosen experts' weights, each read once: the gate /
-// up kernel takes an expert's tokens together, and the down kernel gives
-// every 16 output columns to one block, which walks all chosen experts and
-// sums in a fixed order (no atomics on results).
+// A pass is bound by the chosen experts' weights, each read once, and for a
+// single token by the launches and the loads that wait for each other.  So
+// there is no launch for the choice: whether expert e is chosen by token m is
+// a count of the logits above l[m,e], which every block of the gate / up
+// kernel makes for itself; the down kernel reads the chosen ids.
+// h goes to the down product as two bf16 values (the rounded one and what is
+// left of it, 16 bits of significand together, in bf16's range for either T),
+// in neighbouring rows of one 16-row operand: eight tokens' h cost no more
+// MFMAs than one 16-bit rounding of it would, and y's rounding stays the only
+// one that counts.
+// Both products bring 16 operand rows a wave to its own piece of LDS, by as
+// many 4-row instructions as it has rows (an expert of a few tokens has 1 to
+// 3, so most of a 16-row load by registers would be for nothing), and
+// take them to registers before the next unit's are brought to the same place.
 #include "cr_w4g.h"
 
 namespace cr {
@@ -18,51 +28,54 @@ namespace {
 
 constexpr int kChunk = kMoeChunk;   // tokens per pass
 
-// Workspace of one pass over `m` tokens (byte offsets, 256-byte regions).
-struct MoeWs {
-    size_t logits, ids, weights, lists, slot_pair, h, total;
-};
-inline size_t up256(size_t v) { return (v + 255) / 256 * 256; }
-MoeWs moe_ws(int M, int F, int E, int topk) {
-    const size_t m = M < kChunk ? M : kChunk, pairs = m * topk;
-    const size_t slots = pairs < (size_t)E ? pairs : (size_t)E;
-    MoeWs l;
-    l.logits = 0;
-    l.ids = l.logits + up256(m * E * 8);
-    l.weights = l.ids + up256(pairs * 4);
-    l.lists = l.weights + up256(pairs * 4);
-    l.slot_pair = l.lists + up256((1 + 2 * slots + 1 + pairs) * 4);
-    l.h = l.slot_pair + up256(slots * kChunk * 2);
-    l.total = l.h + up256(pairs * F * 2);
-    return l;
+// The down product's blocks on the passes of one output tile: enough to fill
+// the chip's CUs twice, each wave with at least two (expert, unit) items.
+constexpr int kDownWaves = 8;
+int down_splits(int M, int F, int N, int E, int topk) {
+    const long pairs = (long)M * topk, items = (pairs < E ? pairs : E) * ((F + 127) / 128);
+    long s = 512 / ((N + 15) / 16);
+    if (s > items / (2 * kDownWaves)) s = items / (2 * kDownWaves);
+    return s < 1 ? 1 : (s > 8 ? 8 : (int)s);
 }
 
-// lists: [0] active experts A; [1 + s] expert of slot s; then offsets
-// [slots + 1] into the pair list; then the pairs (m * topk + r) by slot.
-struct MoeLists {
-    int32_t* active;
-    int32_t* expert;
-    int32_t* offset;
-    int32_t* pair;
+// Workspace of one pass (byte offsets, 256-byte regions).
+struct MoeWs {
+    size_t logits, ids, h, arrived, parts, total;
 };
-__host__ __device__ inline MoeLists moe_lists(int32_t* base, int slots) {
-    return {base, base + 1, base + 1 + slots, base + 2 + 2 * slots};
+inline size_t up256(size_t v) { return (v + 255) / 256 * 256; }
+MoeWs moe_ws(int M, int K, int F, int E, int topk) {
+    const size_t m = M < kChunk ? M : kChunk, pairs = m * topk;
+    // neither the splits nor the tokens of a last, smaller pass are more
+    const size_t splits = m ? down_splits((int)m, F, K, E, topk) : 1, parts = splits > 1 ? splits * m : 0;
+    MoeWs l;
+    l.logits = 0;                                        // double [m][E]
+    l.ids = l.logits + up256(m * E * 8);                 // int32 [m][topk]
+    l.h = l.ids + up256(pairs * 4);                      // bf16 [m topk][2][F]
+    l.arrived = l.h + up256(pairs * F * 4);              // uint32 [K / 16]
+    l.parts = l.arrived + up256((size_t)(K / 16) * 4);   // float [splits][m][K]
+    l.total = l.parts + up256(parts * K * 4);
+    return l;
 }
 
 // ---------------------------------------------------------------------------
 // Router logits in float64: which expert is chosen hangs on the order of
 // values that can be close, and the sums then do not depend on their order.
-// A wave per expert, tokens in turn.
+// A wave per expert and token (the router's row comes from the caches again for each token: 4
+// tokens a wave took 9.7 us at 16 tokens, 128 experts, K = 2048, this 4.7).
 // ---------------------------------------------------------------------------
 template <class T>
-__global__ __launch_bounds__(256) void k_moe_logits(const uint16_t* __restrict__ x, int M, int K,
+__global__ __launch_bounds__(256) void k_moe_logits(const uint16_t* __restrict__ x, int K,
                                                     const uint16_t* __restrict__ r, int E,
-                                                    double* __restrict__ logits) {
+                                                    double* __restrict__ logits, uint32_t* __restrict__ arrived,
+                                                    int counters) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int e = blockIdx.x * 4 + wave;
-    const int m = blockIdx.y;
+    const int e = blockIdx.x * 4 + wave, m = blockIdx.y;
+    // the down kernel's arrival counters start at 0
+    if (m == 0)
+        for (int i = blockIdx.x * 256 + threadIdx.x; i < counters; i += gridDim.x * 256) arrived[i] = 0;
     if (e >= E) return;
     double s = 0.0;
+#pragma unroll 4
     for (int k = lane * 8; k < K; k += 512) {
         const u32x4 a = *reinterpret_cast<const u32x4*>(x + (size_t)m * K + k);
         const u32x4 b = *reinterpret_cast<const u32x4*>(r + (size_t)e * K + k);
@@ -79,249 +92,387 @@ __global__ __launch_bounds__(256) void k_moe_logits(const uint16_t* __restrict__
 
 // Total order of float64 values as unsigned integers: -0 as +0, NaN above
 // everything, so that the ranks of a row are always a permutation.
-__device__ __forceinline__ unsigned long long order_key(double v) {
+typedef unsigned long long u64;
+__device__ __forceinline__ u64 order_key(double v) {
     if (v != v) return ~0ull;
-    unsigned long long u = __builtin_bit_cast(unsigned long long, v + 0.0);
+    const u64 u = __builtin_bit_cast(u64, v + 0.0);
     return (u >> 63) ? ~u : (u | (1ull << 63));
 }
 
 // ---------------------------------------------------------------------------
-// Top-k, softmax and the lists of the chosen experts: one block of 16 waves,
-// a wave per token.
+// Gate and up.  blockIdx.y is a (token, rank) pair where there are fewer
+// pairs than experts, else an expert.  The block finds its expert and the
+// tokens that chose it; a block whose expert no token chose, or whose expert
+// an earlier token's pair already stands for, ends.  `ks` of its waves share
+// a tile of 16 rows of the expert's gate and up weights and take the units of
+// K in turn, each loading one unit ahead of its products; tokens go 16 at a
+// time.  With ks = 1 nothing is waited for but a wave's own loads.
 // ---------------------------------------------------------------------------
-constexpr int kRouteWaves = 16;
-
-__global__ __launch_bounds__(64 * kRouteWaves) void k_moe_route(const double* __restrict__ logits, int M, int E,
-                                                                int topk, int norm, int slots, int32_t* ids_ws,
-                                                                float* weights_ws, int32_t* lists,
-                                                                int16_t* slot_pair, int32_t* ids_out,
-                                                                float* weights_out) {
-    __shared__ int count[kMoeMaxExperts], slot_of[kMoeMaxExperts];
-    __shared__ int wave_sum[2][kRouteWaves];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    for (int e = tid; e < E; e += 64 * kRouteWaves) count[e] = 0;
-    for (int i = tid; i < slots * kChunk; i += 64 * kRouteWaves) slot_pair[i] = -1;
-    __syncthreads();
-    for (int m = wave; m < M; m += kRouteWaves) {
-        const double* row = logits + (size_t)m * E;
-        double v[kMoeMaxExperts / 64];
-        unsigned long long key[kMoeMaxExperts / 64];
-        double top = 0.0;
-#pragma unroll
-        for (int i = 0; i < kMoeMaxExperts / 64; ++i) {
-            const int e = i * 64 + lane;
-            key[i] = 0;   // below every value's key (-inf maps to 0x000F..F)
-            v[i] = 0.0;
-            if (e < E) {
-                v[i] = row[e];
-                key[i] = order_key(v[i]);
-            }
-        }
-        int mine_id = 0;
-        float mine_p = 0.0f, chosen = 0.0f;
-        for (int r = 0; r < topk; ++r) {
-            unsigned long long best = 0;
-            int at = kMoeMaxExperts;
-#pragma unroll
-            for (int i = 0; i < kMoeMaxExperts / 64; ++i)
-                if (key[i] > best) {
-                    best = key[i];
-                    at = i * 64 + lane;
-                }
-#pragma unroll
-            for (int o = 1; o < 64; o *= 2) {
-                const unsigned long long b = __shfl_xor(best, o);
-                const int a = __shfl_xor(at, o);
-                if (b > best || (b == best && a < at)) {
-                    best = b;
-                    at = a;
-                }
-            }
-            double val = 0.0;
-#pragma unroll
-            for (int i = 0; i < kMoeMaxExperts / 64; ++i)
-                if (at == i * 64 + lane) {
-                    key[i] = 0;
-                    val = v[i];
-                }
-            val = __shfl(val, at & 63);
-            if (r == 0) top = val;
-            const float p = expf((float)(val - top));
-            chosen += p;
-            if (lane == r) {
-                mine_id = at;
-                mine_p = p;
-            }
-        }
-        float sum = chosen;
-        if (!norm) {
-            sum = 0.0f;
-#pragma unroll
-            for (int i = 0; i < kMoeMaxExperts / 64; ++i)
-                if (i * 64 + lane < E) sum += expf((float)(v[i] - top));
-#pragma unroll
-            for (int o = 1; o < 64; o *= 2) sum += __shfl_xor(sum, o);
-        }
-        if (lane < topk) {
-            const int p = m * topk + lane;
-            const float c = mine_p / sum;
-            ids_ws[p] = mine_id;
-            weights_ws[p] = c;
-            if (ids_out) ids_out[p] = mine_id;
-            if (weights_out) weights_out[p] = c;
-            atomicAdd(&count[mine_id], 1);
-        }
-    }
-    __syncthreads();
-    // slots of the chosen experts in the order of their index, and where
-    // each one's pairs begin: a scan over the experts (E <= 1024 threads)
-    const MoeLists l = moe_lists(lists, slots);
-    const int n = tid < E ? count[tid] : 0;
-    int a = n > 0 ? 1 : 0, b = n;
-#pragma unroll
-    for (int o = 1; o < 64; o *= 2) {
-        const int pa = __shfl_up(a, o), pb = __shfl_up(b, o);
-        if (lane >= o) {
-            a += pa;
-            b += pb;
-        }
-    }
-    if (lane == 63) {
-        wave_sum[0][wave] = a;
-        wave_sum[1][wave] = b;
-    }
-    __syncthreads();
-    for (int i = 0; i < wave; ++i) {
-        a += wave_sum[0][i];
-        b += wave_sum[1][i];
-    }
-    if (n > 0) {
-        l.expert[a - 1] = tid;
-        l.offset[a - 1] = b - n;
-        slot_of[tid] = a - 1;
-        count[tid] = b - n;   // next free place of its pairs
-    }
-    if (tid == 64 * kRouteWaves - 1) {
-        l.active[0] = a;
-        l.offset[a] = b;
-    }
-    __syncthreads();
-    for (int p = tid; p < M * topk; p += 64 * kRouteWaves) {
-        const int e = ids_ws[p], s = slot_of[e];
-        l.pair[atomicAdd(&count[e], 1)] = p;   // the order inside a slot moves columns, not sums
-        slot_pair[(size_t)s * kChunk + p / topk] = (int16_t)p;
-    }
-}
-
-// ---------------------------------------------------------------------------
-// Gate and up: a block owns 16 rows of one chosen expert's gate and up
-// weights; its waves split K, the tokens of the expert go 16 at a time.
-// ---------------------------------------------------------------------------
-constexpr int kWaves = 4;
+constexpr int kUpWaves = 8;
 
 template <class T, int GPU, bool ZP>
-__global__ __launch_bounds__(64 * kWaves) void k_moe_gate_up(const uint16_t* __restrict__ x, int M, int K, int F,
-                                                             const uint8_t* __restrict__ wg,
-                                                             const uint8_t* __restrict__ wu, int topk, int slots,
-                                                             int32_t* lists, const float* __restrict__ weights,
-                                                             uint16_t* __restrict__ h) {
-    __shared__ f32x4 part[kWaves][2][64];
-    const MoeLists ml = moe_lists(lists, slots);
-    const int slot = blockIdx.y;
-    if (slot >= ml.active[0]) return;
-    const int e = ml.expert[slot], begin = ml.offset[slot], end = ml.offset[slot + 1];
+__global__ __launch_bounds__(64 * kUpWaves) void k_moe_gate_up(const uint16_t* __restrict__ x, int M, int K, int F,
+                                                               const uint8_t* __restrict__ wg,
+                                                               const uint8_t* __restrict__ wu, int E, int topk,
+                                                               int by_pair, int ks,
+                                                               const double* __restrict__ logits,
+                                                               int32_t* __restrict__ ids, uint16_t* __restrict__ h) {
+    __shared__ f32x4 part[kUpWaves][2][64];
+    __shared__ __attribute__((aligned(16))) char rows_lds[kUpWaves][4096];
+    __shared__ u64 key[kMoeMaxExperts];
+    __shared__ int above[kMoeMaxExperts];
+    __shared__ int16_t rank_of[kChunk], list[kChunk];
+    __shared__ int found, chosen;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    constexpr int kThreads = 64 * kUpWaves;
+    int e = blockIdx.y, first = 0;
+    if (by_pair) {
+        // the expert of this rank: every expert counts the logits above its
+        // own, the counting split over the threads that are left
+        first = blockIdx.y / topk;
+        const int want = blockIdx.y - first * topk;
+        const double* row = logits + (size_t)first * E;
+        for (int j = tid; j < E; j += kThreads) {
+            key[j] = order_key(row[j]);
+            above[j] = 0;
+        }
+        __syncthreads();
+        const int parts = E < kThreads ? kThreads / E : 1, span = (E + parts - 1) / parts;
+        for (int i = tid; i < E * parts; i += kThreads) {
+            const int mine = i % E, j0 = i / E * span, j1 = j0 + span < E ? j0 + span : E;
+            const u64 k = key[mine];
+            int n = 0;
+            for (int j = j0; j < j1; ++j) n += key[j] > k || (key[j] == k && j < mine);
+            if (n) atomicAdd(&above[mine], n);
+        }
+        __syncthreads();
+        for (int j = tid; j < E; j += kThreads)
+            if (above[j] == want) found = j;   // ranks are a permutation: one thread
+        __syncthreads();
+        e = found;
+        if (M == 1 && tid == 0) rank_of[0] = (int16_t)want;
+    }
+    if (!(by_pair && M == 1)) {
+        for (int m = wave; m < M; m += kUpWaves) {
+            const double* row = logits + (size_t)m * E;
+            const u64 k = order_key(row[e]);
+            int n = 0;
+            for (int j0 = 0; j0 < E; j0 += 64) {
+                const int j = j0 + lane;
+                const u64 o = j < E ? order_key(row[j]) : 0;
+                n += __popcll(__ballot(j < E && (o > k || (o == k && j < e))));
+            }
+            if (lane == 0) rank_of[m] = (int16_t)(n < topk ? n : -1);
+        }
+    }
+    __syncthreads();
+    if (wave == 0) {
+        const bool mine = lane < M && rank_of[lane] >= 0;
+        const u64 all = __ballot(mine);
+        if (mine) {
+            list[__popcll(all & ((1ull << lane) - 1))] = (int16_t)lane;
+            if (blockIdx.x == 0) ids[lane * topk + rank_of[lane]] = e;
+        }
+        if (lane == 0) chosen = (all & ((1ull << first) - 1)) ? 0 : __popcll(all);
+    }
+    __syncthreads();
+    const int n_tok = __builtin_amdgcn_readfirstlane(chosen);
+    if (n_tok == 0) return;
+
     const W4gLayout l = w4g_layout(128 / GPU, ZP, F, K);
     wg += (size_t)e * l.total;
     wu += (size_t)e * l.total;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const size_t tile = blockIdx.x;
-    const buf_t xb = w4g_buf(x, M, K);
-    for (int p0 = begin; p0 < end; p0 += 16) {
-        const int mine = p0 + (lane & 15);
-        const uint32_t row = mine < end ? (uint32_t)(ml.pair[mine] / topk) * (2u * K) : kNoRow;
+    const v4i xb = w4g_rows(x, M, K);
+    const int part_k = wave % ks, tile = blockIdx.x * (kUpWaves / ks) + wave / ks;
+    const bool work = tile < l.tiles;
+    const char* my_rows = rows_lds[wave];
+    const uint32_t my_lds = lds_address(my_rows);
+    for (int p0 = 0; p0 < n_tok; p0 += 16) {
+        const int n = n_tok - p0 < 16 ? n_tok - p0 : 16, fills = (n + 3) >> 2;
+        uint32_t row[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int m = 4 * j + (lane >> 4);
+            row[j] = (uint32_t)list[p0 + (m < n ? m : n - 1)] * (2u * K);
+        }
         f32x4 acc[1][2] = {{f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}}};
-        for (int u = wave; u < l.units; u += kWaves) {
-            const W4gUnit<GPU> w[2] = {w4g_load<GPU, ZP>(wg, l, tile * l.units + u, lane),
-                                       w4g_load<GPU, ZP>(wu, l, tile * l.units + u, lane)};
+        W4gUnit<GPU> next[2];
+        auto load = [&](int u) {
+            next[0] = w4g_load<GPU, ZP>(wg, l, (size_t)tile * l.units + u, lane);
+            next[1] = w4g_load<GPU, ZP>(wu, l, (size_t)tile * l.units + u, lane);
 #pragma unroll
-            for (int g = 0; g < GPU; ++g) {
-                u32x4 a[1][4 / GPU];
+            for (int j = 0; j < 4; ++j)
+                if (j < fills) w4g_x_to_lds(xb, row[j] + w4g_chunk(4 * j, u, K, lane), my_lds + j * 1024);
+        };
+        if (work && part_k < l.units) {
+            load(part_k);
+            for (int u = part_k; u < l.units; u += ks) {
+                w4g_wait();
+                const W4gUnit<GPU> w[2] = {next[0], next[1]};
+                u32x4 a[GPU][1][4 / GPU];
 #pragma unroll
-                for (int s = 0; s < 4 / GPU; ++s)
-                    a[0][s] = w4g_x(xb, row, u * 128 + (g * (4 / GPU) + s) * 32 + (lane >> 4) * 8, K);
-                w4g_mac<T, GPU, ZP, 1, 2>(g, w, a, acc);
+                for (int d = 0; d < 4; ++d) a[d / (4 / GPU)][0][d % (4 / GPU)] = w4g_operand_rows(my_rows, d, lane);
+                w4g_wait_lds();
+                if (u + ks < l.units) load(u + ks);
+#pragma unroll
+                for (int g = 0; g < GPU; ++g) w4g_mac<T, GPU, ZP, 1, 2>(g, w, a[g], acc);
             }
+        }
+        auto store = [&](int m, int n, float g, float u) {
+            const float v = g / (1.0f + expf(-g)) * u;
+            const int t = list[p0 + m];
+            uint16_t* to = h + (size_t)(t * topk + rank_of[t]) * 2 * F + n;
+            const uint16_t hi = Bf16::from_f32(v);
+            to[0] = hi;
+            to[F] = Bf16::from_f32(v - Bf16::to_f32(hi));
+        };
+        if (ks == 1) {
+            if (work) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int m = (lane >> 4) * 4 + i;
+                    if (p0 + m < n_tok) store(m, tile * 16 + (lane & 15), acc[0][0][i], acc[0][1][i]);
+                }
+            }
+            continue;
         }
         part[wave][0][lane] = acc[0][0];
         part[wave][1][lane] = acc[0][1];
         __syncthreads();
-        const int m = threadIdx.x >> 4, n = threadIdx.x & 15;
-        if (p0 + m < end) {
+        for (int i = tid; i < 256 * (kUpWaves / ks); i += kThreads) {
+            const int m = (i >> 4) & 15, n = i & 15, w0 = (i >> 8) * ks, t = blockIdx.x * (kUpWaves / ks) + (i >> 8);
+            if (p0 + m >= n_tok || t >= l.tiles) continue;
             float g = 0.0f, u = 0.0f;
-#pragma unroll
-            for (int wv = 0; wv < kWaves; ++wv) {
+            for (int wv = w0; wv < w0 + ks; ++wv) {
                 g += part[wv][0][(m >> 2) * 16 + n][m & 3];
                 u += part[wv][1][(m >> 2) * 16 + n][m & 3];
             }
-            const int p = ml.pair[p0 + m];
-            h[(size_t)p * F + tile * 16 + n] = T::from_f32(g / (1.0f + expf(-g)) * u * weights[p]);
+            store(m, t * 16 + n, g, u);
         }
         __syncthreads();
     }
 }
 
 // ---------------------------------------------------------------------------
-// Down and combination: a block owns 16 columns of y for every token and
-// walks the units of all chosen experts; h already holds the routing weight,
-// so the experts' sums add up in the same accumulators.
+// Down and combination.  gridDim.y blocks share 16 columns of y for every
+// token.  The pairs are sorted by expert and cut into passes of up to 8
+// tokens (operand row 2 t holds token t's h, row 2 t + 1 what is left of it);
+// the (pass, unit) items are shared out to the blocks' waves in contiguous
+// runs.  At the end of a pass a wave adds c times its sums into its own rows
+// of LDS; the waves' rows are added in their order, and so are the blocks',
+// by the one that arrives last: the order of every sum is fixed.  The blocks'
+// sums go through device-scope stores and loads, waited for before the
+// arrival is counted; no fence of the caches is needed.
 // ---------------------------------------------------------------------------
-template <class T, int GPU, bool ZP, int MT>
-__global__ __launch_bounds__(64 * kWaves) void k_moe_down(const uint16_t* __restrict__ h, int M, int F, int N, int topk,
-                                                          const uint8_t* __restrict__ wd, int slots, int32_t* lists,
-                                                          const int16_t* __restrict__ slot_pair,
-                                                          uint16_t* __restrict__ y) {
-    __shared__ f32x4 part[kWaves][MT][64];
-    const MoeLists ml = moe_lists(lists, slots);
-    const W4gLayout l = w4g_layout(128 / GPU, ZP, N, F);
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const size_t tile = blockIdx.x;
-    const int total = ml.active[0] * l.units;
-    const buf_t hb = w4g_buf(h, M * topk, F);
-    f32x4 acc[MT][1];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) acc[mt][0] = f32x4{0, 0, 0, 0};
-    for (int i = wave; i < total; i += kWaves) {
-        const int slot = i / l.units, u = i - slot * l.units;
-        const W4gUnit<GPU> w[1] = {
-            w4g_load<GPU, ZP>(wd + (size_t)ml.expert[slot] * l.total, l, tile * l.units + u, lane)};
-        uint32_t row[MT];
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-            const int p = slot_pair[(size_t)slot * kChunk + mt * 16 + (lane & 15)];
-            row[mt] = p >= 0 ? (uint32_t)p * (2u * F) : kNoRow;
+template <class T, int GPU, bool ZP>
+__global__ __launch_bounds__(64 * kDownWaves) void k_moe_down(const uint16_t* __restrict__ h, int M, int F, int N,
+                                                              const uint8_t* __restrict__ wd, int E, int topk,
+                                                              int norm, const double* __restrict__ logits,
+                                                              const int32_t* __restrict__ ids,
+                                                              uint32_t* __restrict__ arrived,
+                                                              float* __restrict__ parts, uint16_t* __restrict__ y,
+                                                              int32_t* __restrict__ ids_out,
+                                                              float* __restrict__ weights_out) {
+    constexpr int kThreads = 64 * kDownWaves;
+    constexpr int kPairs = kChunk * kMoeMaxTopk;
+    static_assert(kMoeMaxExperts <= 2 * kThreads, "two experts a thread");
+    extern __shared__ __attribute__((aligned(16))) float sums[];   // [waves][M][16]
+    __shared__ u64 tokens[kMoeMaxExperts];                          // bit m: token m chose the expert
+    __shared__ int16_t pairs_at[kMoeMaxExperts];                    // where its pairs begin
+    __shared__ int16_t pair_of[kPairs];                             // pairs by expert, then by token
+    __shared__ int16_t pass_e[kPairs], pass_at[kPairs], pass_n[kPairs];
+    __shared__ float prob[kPairs], total[kChunk];
+    __shared__ int scan[2][kDownWaves];
+    __shared__ __attribute__((aligned(16))) char rows_lds[kDownWaves][4096];
+    __shared__ uint32_t before;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int pairs = M * topk;
+    int passes = topk;
+    if (M == 1) {
+        if (tid < topk) {
+            pair_of[tid] = (int16_t)tid;
+            pass_e[tid] = (int16_t)ids[tid];
+            pass_at[tid] = (int16_t)tid;
+            pass_n[tid] = 1;
         }
+    } else {
+        for (int e = tid; e < E; e += kThreads) tokens[e] = 0;
+        __syncthreads();
+        for (int p = tid; p < pairs; p += kThreads) atomicOr(&tokens[ids[p]], 1ull << (p / topk));
+        __syncthreads();
+        // a thread's experts 2 tid, 2 tid + 1: their pairs and passes, and those before them
+        const int e0 = 2 * tid;
+        const int n0 = e0 < E ? __popcll(tokens[e0]) : 0, n1 = e0 + 1 < E ? __popcll(tokens[e0 + 1]) : 0;
+        int a = n0 + n1, b = ((n0 + 7) >> 3) + ((n1 + 7) >> 3);
+        const int own_a = a, own_b = b;
 #pragma unroll
-        for (int g = 0; g < GPU; ++g) {
-            u32x4 a[MT][4 / GPU];
+        for (int o = 1; o < 64; o *= 2) {
+            const int pa = __shfl_up(a, o), pb = __shfl_up(b, o);
+            if (lane >= o) {
+                a += pa;
+                b += pb;
+            }
+        }
+        if (lane == 63) {
+            scan[0][wave] = a;
+            scan[1][wave] = b;
+        }
+        __syncthreads();
+        a -= own_a;
+        b -= own_b;
+        passes = 0;
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                for (int s = 0; s < 4 / GPU; ++s)
-                    a[mt][s] = w4g_x(hb, row[mt], u * 128 + (g * (4 / GPU) + s) * 32 + (lane >> 4) * 8, F);
-            w4g_mac<T, GPU, ZP, MT, 1>(g, w, a, acc);
+        for (int i = 0; i < kDownWaves; ++i) {
+            if (i < wave) {
+                a += scan[0][i];
+                b += scan[1][i];
+            }
+            passes += scan[1][i];
+        }
+        for (int i = 0; i < 2; ++i) {
+            const int n = i ? n1 : n0;
+            if (n > 0) pairs_at[e0 + i] = (int16_t)a;
+            for (int q = 0; q < n; q += 8) {
+                pass_e[b] = (int16_t)(e0 + i);
+                pass_at[b] = (int16_t)(a + q);
+                pass_n[b] = (int16_t)(n - q < 8 ? n - q : 8);
+                ++b;
+            }
+            a += n;
+        }
+        __syncthreads();
+        for (int p = tid; p < pairs; p += kThreads) {
+            const int e = ids[p];
+            pair_of[pairs_at[e] + __popcll(tokens[e] & ((1ull << (p / topk)) - 1))] = (int16_t)p;
         }
     }
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) part[wave][mt][lane] = acc[mt][0];
+    for (int i = tid; i < kDownWaves * M * 16; i += kThreads) sums[i] = 0.0f;
     __syncthreads();
-    for (int i = threadIdx.x; i < 256 * MT; i += 64 * kWaves) {
-        const int m = i >> 4, n = i & 15;
-        const size_t gn = tile * 16 + n;
-        if (m >= M || gn >= (size_t)N) continue;
+
+    const W4gLayout l = w4g_layout(128 / GPU, ZP, N, F);
+    const int tile = blockIdx.x, split = blockIdx.y, splits = gridDim.y;
+    const v4i hb = w4g_rows(h, 2 * pairs, F);
+    const int items = passes * l.units, run = (items + kDownWaves * splits - 1) / (kDownWaves * splits);
+    const int begin = (split * kDownWaves + wave) * run, end = begin + run < items ? begin + run : items;
+    const char* my_rows = rows_lds[wave];
+    const uint32_t my_lds = lds_address(my_rows);
+    // the next item to load: its pass, its unit, and what changes with the pass
+    int pass = begin / l.units, u = begin % l.units, fills = 0;
+    const uint8_t* we = wd;
+    uint32_t row[4];
+    W4gUnit<GPU> next[1];
+    auto turn = [&]() {
+        const int n = __builtin_amdgcn_readfirstlane(pass_n[pass]), at = pass_at[pass];
+        we = wd + (size_t)__builtin_amdgcn_readfirstlane(pass_e[pass]) * l.total;
+        fills = (n + 1) >> 1;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int r = 4 * j + (lane >> 4), t = (r >> 1) < n ? r >> 1 : n - 1;
+            row[j] = (uint32_t)(2 * pair_of[at + t] + (r & 1)) * (2u * F);
+        }
+    };
+    auto load = [&]() {
+        next[0] = w4g_load<GPU, ZP>(we, l, (size_t)tile * l.units + u, lane);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (j < fills) w4g_x_to_lds(hb, row[j] + w4g_chunk(4 * j, u, F, lane), my_lds + j * 1024);
+    };
+    if (begin < end) {
+        turn();
+        load();
+    }
+
+    // while the first loads are under way: the softmax's numerators, the
+    // tokens' denominators, the weights of the pairs
+    for (int p = tid; p < pairs; p += kThreads) {
+        const double* of = logits + (size_t)(p / topk) * E;
+        prob[p] = expf((float)(of[ids[p]] - of[ids[p / topk * topk]]));
+    }
+    if (!norm) {
+        for (int m = wave; m < M; m += kDownWaves) {
+            const double* of = logits + (size_t)m * E;
+            const double top = of[ids[m * topk]];
+            float s = 0.0f;
+            for (int j = lane; j < E; j += 64) s += expf((float)(of[j] - top));
+#pragma unroll
+            for (int o = 1; o < 64; o *= 2) s += __shfl_xor(s, o);
+            if (lane == 0) total[m] = s;
+        }
+    }
+    __syncthreads();
+    if (norm && tid < M) {
+        float s = 0.0f;
+        for (int r = 0; r < topk; ++r) s += prob[tid * topk + r];
+        total[tid] = s;
+    }
+    __syncthreads();
+    for (int p = tid; p < pairs; p += kThreads) {
+        const float c = prob[p] / total[p / topk];
+        prob[p] = c;
+        if (tile == 0 && split == 0) {
+            if (ids_out) ids_out[p] = ids[p];
+            if (weights_out) weights_out[p] = c;
+        }
+    }
+    __syncthreads();
+
+    f32x4 acc[1][1] = {{f32x4{0, 0, 0, 0}}};
+    for (int i = begin; i < end; ++i) {
+        w4g_wait();
+        const W4gUnit<GPU> w[1] = {next[0]};
+        u32x4 a[GPU][1][4 / GPU];
+#pragma unroll
+        for (int d = 0; d < 4; ++d) a[d / (4 / GPU)][0][d % (4 / GPU)] = w4g_operand_rows(my_rows, d, lane);
+        w4g_wait_lds();
+        const int done = pass;
+        if (++u == l.units) {
+            u = 0;
+            ++pass;
+        }
+        if (i + 1 < end) {
+            if (pass != done) turn();
+            load();
+        }
+#pragma unroll
+        for (int g = 0; g < GPU; ++g) w4g_mac<DownT<T>, GPU, ZP, 1, 1>(g, w, a[g], acc);
+        if (i + 1 < end && pass == done) continue;
+        const int n = pass_n[done], at = pass_at[done];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int t = (lane >> 4) * 2 + j;
+            if (t < n) {
+                const int p = pair_of[at + t];
+                float& to = sums[(wave * M + p / topk) * 16 + (lane & 15)];
+                to = __builtin_fmaf(prob[p], acc[0][0][2 * j] + acc[0][0][2 * j + 1], to);
+            }
+        }
+        acc[0][0] = f32x4{0, 0, 0, 0};
+    }
+    __syncthreads();
+    for (int i = tid; i < M * 16; i += kThreads) {
+        const size_t gn = (size_t)tile * 16 + (i & 15);   // N is a multiple of 16
         float v = 0.0f;
 #pragma unroll
-        for (int wv = 0; wv < kWaves; ++wv) v += part[wv][m >> 4][((m & 15) >> 2) * 16 + n][m & 3];
-        y[(size_t)m * N + gn] = T::from_f32(v);
+        for (int wv = 0; wv < kDownWaves; ++wv) v += sums[wv * M * 16 + i];
+        if (splits == 1)
+            y[(size_t)(i >> 4) * N + gn] = T::from_f32(v);
+        else
+            __hip_atomic_store(&parts[((size_t)split * M + (i >> 4)) * N + gn], v, __ATOMIC_RELAXED,
+                               __HIP_MEMORY_SCOPE_AGENT);
+    }
+    if (splits == 1) return;
+    w4g_wait();   // this wave's sums are where every block reads them
+    __syncthreads();
+    if (tid == 0) before = __hip_atomic_fetch_add(&arrived[tile], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();
+    if (before + 1 != (uint32_t)splits) return;
+    for (int i = tid; i < M * 16; i += kThreads) {
+        const size_t gn = (size_t)tile * 16 + (i & 15);
+        float v = 0.0f;
+        for (int s = 0; s < splits; ++s)
+            v += __hip_atomic_load(&parts[((size_t)s * M + (i >> 4)) * N + gn], __ATOMIC_RELAXED,
+                                   __HIP_MEMORY_SCOPE_AGENT);
+        y[(size_t)(i >> 4) * N + gn] = T::from_f32(v);
     }
 }
 
@@ -330,24 +481,28 @@ hipError_t moe_t(const MoeArgs& a, const MoeWs& l, int M, const uint16_t* x, uin
                  float* weights, hipStream_t st) {
     char* ws = static_cast<char*>(a.ws);
     double* logits = reinterpret_cast<double*>(ws + l.logits);
-    int32_t* lists = reinterpret_cast<int32_t*>(ws + l.lists);
     int32_t* ids_ws = reinterpret_cast<int32_t*>(ws + l.ids);
-    float* weights_ws = reinterpret_cast<float*>(ws + l.weights);
-    int16_t* slot_pair = reinterpret_cast<int16_t*>(ws + l.slot_pair);
     uint16_t* h = reinterpret_cast<uint16_t*>(ws + l.h);
-    const int pairs = M * a.topk, slots = pairs < a.E ? pairs : a.E;
-    k_moe_logits<T><<<dim3((a.E + 3) / 4, M), 256, 0, st>>>(x, M, a.K, a.router, a.E, logits);
-    k_moe_route<<<1, 64 * kRouteWaves, 0, st>>>(logits, M, a.E, a.topk, a.norm, slots, ids_ws, weights_ws, lists,
-                                                slot_pair, ids, weights);
-    k_moe_gate_up<T, GPU, ZP><<<dim3(a.F / 16, slots), 64 * kWaves, 0, st>>>(x, M, a.K, a.F, a.wg, a.wu, a.topk, slots,
-                                                                            lists, weights_ws, h);
-    const dim3 dg((a.K + 15) / 16), db(64 * kWaves);
-    if (M <= 16)
-        k_moe_down<T, GPU, ZP, 1><<<dg, db, 0, st>>>(h, M, a.F, a.K, a.topk, a.wd, slots, lists, slot_pair, y);
-    else if (M <= 32)
-        k_moe_down<T, GPU, ZP, 2><<<dg, db, 0, st>>>(h, M, a.F, a.K, a.topk, a.wd, slots, lists, slot_pair, y);
-    else
-        k_moe_down<T, GPU, ZP, 4><<<dg, db, 0, st>>>(h, M, a.F, a.K, a.topk, a.wd, slots, lists, slot_pair, y);
+    static std::atomic<uint64_t> done{0};
+    const auto down = k_moe_down<T, GPU, ZP>;
+    const hipError_t err = opt_in_lds(reinterpret_cast<const void*>(down), kDownWaves * kChunk * 64, done);
+    if (err != hipSuccess) return err;
+    uint32_t* arrived = reinterpret_cast<uint32_t*>(ws + l.arrived);
+    float* parts = reinterpret_cast<float*>(ws + l.parts);
+    const int splits = down_splits(M, a.F, a.K, a.E, a.topk), out_tiles = a.K / 16;
+    k_moe_logits<T><<<dim3((a.E + 3) / 4, M), 256, 0, st>>>(x, a.K, a.router, a.E, logits, arrived,
+                                                            splits > 1 ? out_tiles : 0);
+    const int pairs = M * a.topk, by_pair = pairs < a.E, rows = by_pair ? pairs : a.E;
+    // a wave per tile where the chosen experts' tiles fill the chip's 4096
+    // wave slots half, else as many waves on a tile's K as bring them there
+    const int tiles = a.F / 16;
+    int ks = 1;
+    while (ks < kUpWaves && (long)rows * tiles * ks < 2048) ks *= 2;
+    const int per = kUpWaves / ks;
+    k_moe_gate_up<T, GPU, ZP><<<dim3((tiles + per - 1) / per, rows), 64 * kUpWaves, 0, st>>>(
+        x, M, a.K, a.F, a.wg, a.wu, a.E, a.topk, by_pair, ks, logits, ids_ws, h);
+    down<<<dim3(out_tiles, splits), 64 * kDownWaves, kDownWaves * M * 64, st>>>(
+        h, M, a.F, a.K, a.wd, a.E, a.topk, a.norm, logits, ids_ws, arrived, parts, y, ids, weights);
     return hipGetLastError();
 }
 
@@ -363,10 +518,10 @@ hipError_t moe_pass(const MoeArgs& a, const MoeWs& l, int M, const uint16_t* x, 
 
 }  // namespace
 
-size_t moe_workspace(int M, int F, int E, int topk) { return moe_ws(M, F, E, topk).total; }
+size_t moe_workspace(int M, int K, int F, int E, int topk) { return moe_ws(M, K, F, E, topk).total; }
 
 hipError_t launch_moe(const MoeArgs& a, hipStream_t st) {
-    const MoeWs l = moe_ws(a.M, a.F, a.E, a.topk);
+    const MoeWs l = moe_ws(a.M, a.K, a.F, a.E, a.topk);
     for (int m = 0; m < a.M; m += kChunk) {
         const int n = a.M - m < kChunk ? a.M - m : kChunk;
         const uint16_t* x = a.x + (size_t)m * a.K;

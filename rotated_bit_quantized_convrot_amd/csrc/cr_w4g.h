@@ -87,13 +87,19 @@ struct Fp16 {
     }
 };
 
+// bf16 operands against a weight whose scales are of type T.
+template <class T>
+struct DownT : Bf16 {
+    static __device__ __forceinline__ float to_f32(uint32_t v) { return T::to_f32(v); }
+};
+
 // Layout of a packed weight (byte offsets); `gpu` is 128 / g, the groups of
 // a unit.
 struct W4gLayout {
     int tiles, units, gpu;
     size_t scales, zeros, total;
 };
-__host__ __device__ inline int w4g_zero_bytes(int gpu) { return gpu == 4 ? 2 : 1; }
+__host__ __device__ constexpr int w4g_zero_bytes(int gpu) { return gpu == 4 ? 2 : 1; }
 __host__ __device__ inline W4gLayout w4g_layout(int group, bool zeros, int N, int K) {
     W4gLayout l;
     l.tiles = (N + 15) / 16;
@@ -108,35 +114,47 @@ __host__ __device__ inline W4gLayout w4g_layout(int group, bool zeros, int N, in
 }
 
 // A unit's weights of one lane: 4 operand dwords, its row's scales and zero
-// points.
+// points.  Where those are narrower than a dword, the whole dword is loaded
+// and the row's part taken at use: the compiler widens a narrower load's
+// result next to the load, which would make loads ahead wait there.
 template <int GPU>
 struct W4gUnit {
     u32x4 codes;
-    uint32_t scale[(GPU + 1) / 2];   // 16-bit scales, low half first
-    uint32_t zero;                   // nibbles
+    uint32_t scale[(GPU + 1) / 2];   // 16-bit scales, low half first (one: two rows')
+    uint32_t zero;                   // nibbles (4 rows', one group to 2; two rows', 4 groups)
 };
 
 template <int GPU, bool ZP>
 __device__ __forceinline__ W4gUnit<GPU> w4g_load(const uint8_t* w, const W4gLayout& l, size_t tile_unit, int lane) {
     W4gUnit<GPU> r;
     r.codes = *reinterpret_cast<const u32x4*>(w + tile_unit * 1024 + lane * 16);
-    const uint8_t* s = w + l.scales + tile_unit * (32 * GPU) + (lane & 15) * (2 * GPU);
+    const uint8_t* s = w + l.scales + tile_unit * (32 * GPU);
     if constexpr (GPU == 1) {
-        r.scale[0] = *reinterpret_cast<const uint16_t*>(s);
+        r.scale[0] = *reinterpret_cast<const uint32_t*>(s + (lane & 14) * 2);
     } else if constexpr (GPU == 2) {
-        r.scale[0] = *reinterpret_cast<const uint32_t*>(s);
+        r.scale[0] = *reinterpret_cast<const uint32_t*>(s + (lane & 15) * 4);
     } else {
-        const uint2 v = *reinterpret_cast<const uint2*>(s);
+        const uint2 v = *reinterpret_cast<const uint2*>(s + (lane & 15) * 8);
         r.scale[0] = v.x;
         r.scale[1] = v.y;
     }
     r.zero = 0;
     if constexpr (ZP) {
-        const uint8_t* z = w + l.zeros + tile_unit * (16 * w4g_zero_bytes(GPU)) + (lane & 15) * w4g_zero_bytes(GPU);
-        if constexpr (GPU == 4) r.zero = *reinterpret_cast<const uint16_t*>(z);
-        else r.zero = *z;
+        constexpr int b = w4g_zero_bytes(GPU);
+        r.zero = *reinterpret_cast<const uint32_t*>(w + l.zeros + tile_unit * (16 * b) + ((lane & 15) * b & ~3));
     }
     return r;
+}
+// 16 times the scale, and the zero point, of group g.
+template <class T, int GPU>
+__device__ __forceinline__ float w4g_scale16(const W4gUnit<GPU>& w, int g, int lane) {
+    const uint32_t v = GPU == 1 ? w.scale[0] >> (16 * (lane & 1)) : w.scale[g / 2] >> (16 * (g % 2));
+    return 16.0f * T::to_f32(v & 0xFFFFu);
+}
+template <int GPU>
+__device__ __forceinline__ uint32_t w4g_zero(const W4gUnit<GPU>& w, int g, int lane) {
+    const int row = GPU == 4 ? 16 * (lane & 1) : 8 * (lane & 3);
+    return (w.zero >> (row + 4 * g)) & 15u;
 }
 
 // acc[mt][nt] += x W^T over group g of a unit.  a[mt][s]: x rows
@@ -149,10 +167,11 @@ template <class T, int GPU, bool ZP, int MT, int NT>
 __device__ __forceinline__ void w4g_mac(int g, const W4gUnit<GPU> (&w)[NT], const u32x4 (&a)[MT][4 / GPU],
                                         f32x4 (&acc)[MT][NT]) {
     constexpr int SPG = 4 / GPU;   // MFMA steps per group
+    const int lane = threadIdx.x & 63;
     u32x4 b[NT][SPG];
     float s16[NT];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) s16[nt] = 16.0f * T::to_f32((w[nt].scale[g / 2] >> (16 * (g % 2))) & 0xFFFFu);
+    for (int nt = 0; nt < NT; ++nt) s16[nt] = w4g_scale16<T, GPU>(w[nt], g, lane);
     if constexpr (ZP && !T::kZeroInOperand) {
         // -sum x of the group comes from one more MFMA, against -1, in the lanes that need it; the
         // operands are made first, so that one row tile's sums are alive at a time
@@ -162,7 +181,7 @@ __device__ __forceinline__ void w4g_mac(int g, const W4gUnit<GPU> (&w)[NT], cons
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
             for (int s = 0; s < SPG; ++s) b[nt][s] = T::operand(w[nt].codes[g * SPG + s], 0);
-            z[nt] = 0.0625f * (float)((int)((w[nt].zero >> (4 * g)) & 15u) - 8);
+            z[nt] = 0.0625f * (float)((int)w4g_zero<GPU>(w[nt], g, lane) - 8);
         }
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
@@ -182,7 +201,7 @@ __device__ __forceinline__ void w4g_mac(int g, const W4gUnit<GPU> (&w)[NT], cons
     } else {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const uint32_t z = ZP ? (w[nt].zero >> (4 * g)) & 15u : 8u;
+            const uint32_t z = ZP ? w4g_zero<GPU>(w[nt], g, lane) : 8u;
             f32x4 t[MT];
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) t[mt] = f32x4{0, 0, 0, 0};
@@ -200,8 +219,7 @@ __device__ __forceinline__ void w4g_mac(int g, const W4gUnit<GPU> (&w)[NT], cons
     }
 }
 
-// Rows of x behind a buffer descriptor: a load past its end gives zeros, so
-// rows and k that do not exist take no branch.  The rows of one tile only:
+// Rows of x behind a buffer descriptor.  One tile's rows, or one pass's: the
 // offsets stay in 32 bits whatever the matrix.
 __device__ __forceinline__ v4i w4g_rows(const uint16_t* x, int rows, int K) {
     const uint64_t a = (uint64_t)(uintptr_t)x;
@@ -212,24 +230,33 @@ __device__ __forceinline__ v4i w4g_rows(const uint16_t* x, int rows, int K) {
     r.w = 0x00020000;
     return r;
 }
-typedef __amdgpu_buffer_rsrc_t buf_t;
-__device__ __forceinline__ buf_t w4g_buf(const uint16_t* x, int rows, int K) {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(x), 0, rows * K * 2, 0x00020000);
-}
-constexpr uint32_t kNoRow = 0x80000000u;   // + 2 k stays past any tile
-// 8 values at byte offset `row` (kNoRow: none) + 2 k, zeros past K.
-__device__ __forceinline__ u32x4 w4g_x(buf_t x, uint32_t row, int k, int K) {
-    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(x, k < K ? row + 2u * (uint32_t)k : kNoRow, 0, 0));
-}
-
 // Lane i's 16 bytes at byte offset `off` of the rows go to LDS address
-// lds + 16 i (wave-uniform); the caller waits (w4g_wait) before a barrier
-// that publishes them.  Every offset has to lie inside the rows.
+// lds + 16 i (wave-uniform); the caller waits (w4g_wait) before they are
+// read.  Every offset has to lie inside the rows.
 __device__ __forceinline__ void w4g_x_to_lds(v4i x, uint32_t off, uint32_t lds) {
     asm volatile("buffer_load_dwordx4 %0, %1, 0 offen lds" : : "v"(off), "s"(x), "{m0}"(lds) : "memory");
 }
-// Every load of this wave has arrived.
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+    return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char*)p;
+}
+// Every load of this wave has arrived / has been read from LDS.
 __device__ __forceinline__ void w4g_wait() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+__device__ __forceinline__ void w4g_wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 __device__ __forceinline__ void w4g_barrier() { asm volatile("s_barrier" ::: "memory"); }
+
+// Operand rows through LDS: rows of 256 bytes (the 128 k of a unit), 16-byte
+// chunk c of row r at slot c ^ (r % 16), so that the 16 rows of an operand
+// read hit 16 different slots.  w4g_chunk: the byte, from the row's start,
+// that lane i of an instruction filling rows r0..r0 + 3 brings for unit u; a
+// chunk past K (its weights' scales are 0) brings the row's last one.
+__device__ __forceinline__ uint32_t w4g_chunk(int r0, int u, int K, int lane) {
+    const uint32_t row = (uint32_t)(r0 + (lane >> 4));
+    const uint32_t b = u * 256u + (((uint32_t)lane & 15u) ^ (row & 15u)) * 16u;
+    return b < 2u * K ? b : 2u * K - 16u;
+}
+// Step d's operand of the 16 rows at `rows`.
+__device__ __forceinline__ u32x4 w4g_operand_rows(const char* rows, int d, int lane) {
+    return *reinterpret_cast<const u32x4*>(rows + (lane & 15) * 256 + (((d * 4 + (lane >> 4)) ^ (lane & 15)) * 16));
+}
 
 }  // namespace cr

@@ -133,7 +133,7 @@ __global__ __launch_bounds__(64 * WM * WN * KG) void k_w4g_linear(const uint16_t
                                                                   uint16_t* __restrict__ y) {
     using C = Tile<MT, NT, WM, WN, KG>;
     extern __shared__ __attribute__((aligned(16))) char lds[];
-    const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds;
+    const uint32_t lds0 = lds_address(lds);
     const W4gLayout l = w4g_layout(128 / GPU, ZP, N, K);
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int kg = wave / (WM * WN), r = wave % (WM * WN), wm = r % WM, wn = r / WM;
@@ -150,8 +150,7 @@ __global__ __launch_bounds__(64 * WM * WN * KG) void k_w4g_linear(const uint16_t
         for (int i = 0; i < C::kBM / 4 / (WM * WN); ++i) {
             const int row4 = (i * (WM * WN) + r) * 4, row = row4 + (lane >> 4);
             const uint32_t rb = (uint32_t)(row < rows ? row : rows - 1) * (2u * K);
-            const uint32_t kb = u * 256u + (((uint32_t)lane & 15u) ^ ((uint32_t)row & 15u)) * 16u;
-            w4g_x_to_lds(xb, rb + (kb < 2u * K ? kb : 2u * K - 16u), lds0 + s * C::kStage + kg * C::kTile + row4 * 256);
+            w4g_x_to_lds(xb, rb + w4g_chunk(row4, u, K, lane), lds0 + s * C::kStage + kg * C::kTile + row4 * 256);
         }
     };
     auto weights = [&](int u, W4gUnit<GPU> (&wu)[NT]) {
@@ -182,7 +181,7 @@ __global__ __launch_bounds__(64 * WM * WN * KG) void k_w4g_linear(const uint16_t
             weights(u + KG, next);
             stage(u + KG, (it + 1) & 1);
         }
-        const char* xt = lds + (it & 1) * C::kStage + kg * C::kTile + (wm * MT * 16 + (lane & 15)) * 256;
+        const char* xt = lds + (it & 1) * C::kStage + kg * C::kTile + wm * MT * 4096;
         if (u < l.units) {
 #pragma unroll
             for (int g = 0; g < GPU; ++g) {
@@ -190,10 +189,8 @@ __global__ __launch_bounds__(64 * WM * WN * KG) void k_w4g_linear(const uint16_t
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-                    for (int s = 0; s < 4 / GPU; ++s) {
-                        const int c = (g * (4 / GPU) + s) * 4 + (lane >> 4);
-                        a[mt][s] = *reinterpret_cast<const u32x4*>(xt + mt * 4096 + ((c ^ (lane & 15)) * 16));
-                    }
+                    for (int s = 0; s < 4 / GPU; ++s)
+                        a[mt][s] = w4g_operand_rows(xt + mt * 4096, g * (4 / GPU) + s, lane);
                 w4g_mac<T, GPU, ZP, MT, NT>(g, wu, a, acc);
             }
         }
