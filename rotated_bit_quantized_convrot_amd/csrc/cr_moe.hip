@@ -21,6 +21,8 @@
 // many 4-row instructions as it has rows (an expert of a few tokens has 1 to
 // 3, so most of a 16-row load by registers would be for nothing), and
 // take them to registers before the next unit's are brought to the same place.
+#include <type_traits>
+
 #include "cr_w4g.h"
 
 namespace cr {
@@ -110,22 +112,21 @@ __device__ __forceinline__ u64 order_key(double v) {
 // ---------------------------------------------------------------------------
 constexpr int kUpWaves = 8;
 
-template <class T, int GPU, bool ZP>
-__global__ __launch_bounds__(64 * kUpWaves) void k_moe_gate_up(const uint16_t* __restrict__ x, int M, int K, int F,
-                                                               const uint8_t* __restrict__ wg,
-                                                               const uint8_t* __restrict__ wu, int E, int topk,
-                                                               int by_pair, int ks,
-                                                               const double* __restrict__ logits,
-                                                               int32_t* __restrict__ ids, uint16_t* __restrict__ h) {
-    __shared__ f32x4 part[kUpWaves][2][64];
-    __shared__ __attribute__((aligned(16))) char rows_lds[kUpWaves][4096];
-    __shared__ u64 key[kMoeMaxExperts];
-    __shared__ int above[kMoeMaxExperts];
-    __shared__ int16_t rank_of[kChunk], list[kChunk];
-    __shared__ int found, chosen;
+struct Choice {
+    u64 key[kMoeMaxExperts];
+    int above[kMoeMaxExperts];
+    int16_t rank_of[kChunk], list[kChunk];   // of the block's expert: rank by token, tokens
+    int found, chosen;
+};
+// The block's expert and its tokens (c.list, c.rank_of); returns their number,
+// 0 where the block has nothing to do, the expert in e.
+template <int WAVES>
+__device__ __forceinline__ int moe_choice(Choice& c, int M, int E, int topk, int by_pair,
+                                          const double* __restrict__ logits, int32_t* __restrict__ ids, int& e) {
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    constexpr int kThreads = 64 * kUpWaves;
-    int e = blockIdx.y, first = 0;
+    constexpr int kThreads = 64 * WAVES;
+    int first = 0;
+    e = blockIdx.y;
     if (by_pair) {
         // the expert of this rank: every expert counts the logits above its
         // own, the counting split over the threads that are left
@@ -133,27 +134,27 @@ __global__ __launch_bounds__(64 * kUpWaves) void k_moe_gate_up(const uint16_t* _
         const int want = blockIdx.y - first * topk;
         const double* row = logits + (size_t)first * E;
         for (int j = tid; j < E; j += kThreads) {
-            key[j] = order_key(row[j]);
-            above[j] = 0;
+            c.key[j] = order_key(row[j]);
+            c.above[j] = 0;
         }
         __syncthreads();
         const int parts = E < kThreads ? kThreads / E : 1, span = (E + parts - 1) / parts;
         for (int i = tid; i < E * parts; i += kThreads) {
             const int mine = i % E, j0 = i / E * span, j1 = j0 + span < E ? j0 + span : E;
-            const u64 k = key[mine];
+            const u64 k = c.key[mine];
             int n = 0;
-            for (int j = j0; j < j1; ++j) n += key[j] > k || (key[j] == k && j < mine);
-            if (n) atomicAdd(&above[mine], n);
+            for (int j = j0; j < j1; ++j) n += c.key[j] > k || (c.key[j] == k && j < mine);
+            if (n) atomicAdd(&c.above[mine], n);
         }
         __syncthreads();
         for (int j = tid; j < E; j += kThreads)
-            if (above[j] == want) found = j;   // ranks are a permutation: one thread
+            if (c.above[j] == want) c.found = j;   // ranks are a permutation: one thread
         __syncthreads();
-        e = found;
-        if (M == 1 && tid == 0) rank_of[0] = (int16_t)want;
+        e = c.found;
+        if (M == 1 && tid == 0) c.rank_of[0] = (int16_t)want;
     }
     if (!(by_pair && M == 1)) {
-        for (int m = wave; m < M; m += kUpWaves) {
+        for (int m = wave; m < M; m += WAVES) {
             const double* row = logits + (size_t)m * E;
             const u64 k = order_key(row[e]);
             int n = 0;
@@ -162,21 +163,47 @@ __global__ __launch_bounds__(64 * kUpWaves) void k_moe_gate_up(const uint16_t* _
                 const u64 o = j < E ? order_key(row[j]) : 0;
                 n += __popcll(__ballot(j < E && (o > k || (o == k && j < e))));
             }
-            if (lane == 0) rank_of[m] = (int16_t)(n < topk ? n : -1);
+            if (lane == 0) c.rank_of[m] = (int16_t)(n < topk ? n : -1);
         }
     }
     __syncthreads();
     if (wave == 0) {
-        const bool mine = lane < M && rank_of[lane] >= 0;
+        const bool mine = lane < M && c.rank_of[lane] >= 0;
         const u64 all = __ballot(mine);
         if (mine) {
-            list[__popcll(all & ((1ull << lane) - 1))] = (int16_t)lane;
-            if (blockIdx.x == 0) ids[lane * topk + rank_of[lane]] = e;
+            c.list[__popcll(all & ((1ull << lane) - 1))] = (int16_t)lane;
+            if (blockIdx.x == 0) ids[lane * topk + c.rank_of[lane]] = e;
         }
-        if (lane == 0) chosen = (all & ((1ull << first) - 1)) ? 0 : __popcll(all);
+        if (lane == 0) c.chosen = (all & ((1ull << first) - 1)) ? 0 : __popcll(all);
     }
     __syncthreads();
-    const int n_tok = __builtin_amdgcn_readfirstlane(chosen);
+    e = __builtin_amdgcn_readfirstlane(e);
+    return __builtin_amdgcn_readfirstlane(c.chosen);
+}
+
+// silu(g) u as two bf16 values, into element n of both rows of pair p's h.
+__device__ __forceinline__ void moe_store_h(uint16_t* h, int p, int F, int n, float g, float u) {
+    const float v = g / (1.0f + expf(-g)) * u;
+    uint16_t* to = h + (size_t)p * 2 * F + n;
+    const uint16_t hi = Bf16::from_f32(v);
+    to[0] = hi;
+    to[F] = Bf16::from_f32(v - Bf16::to_f32(hi));
+}
+
+template <class T, int GPU, bool ZP>
+__global__ __launch_bounds__(64 * kUpWaves, 4) void k_moe_gate_up(const uint16_t* __restrict__ x, int M, int K, int F,
+                                                               const uint8_t* __restrict__ wg,
+                                                               const uint8_t* __restrict__ wu, int E, int topk,
+                                                               int by_pair, int ks,
+                                                               const double* __restrict__ logits,
+                                                               int32_t* __restrict__ ids, uint16_t* __restrict__ h) {
+    __shared__ Choice c;
+    __shared__ __attribute__((aligned(16))) char rows_lds[kUpWaves][4096];
+    __shared__ f32x4 part[kUpWaves][2][64];
+    constexpr int kThreads = 64 * kUpWaves;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    int e;
+    const int n_tok = moe_choice<kUpWaves>(c, M, E, topk, by_pair, logits, ids, e);
     if (n_tok == 0) return;
 
     const W4gLayout l = w4g_layout(128 / GPU, ZP, F, K);
@@ -193,7 +220,7 @@ __global__ __launch_bounds__(64 * kUpWaves) void k_moe_gate_up(const uint16_t* _
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int m = 4 * j + (lane >> 4);
-            row[j] = (uint32_t)list[p0 + (m < n ? m : n - 1)] * (2u * K);
+            row[j] = (uint32_t)c.list[p0 + (m < n ? m : n - 1)] * (2u * K);
         }
         f32x4 acc[1][2] = {{f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}}};
         W4gUnit<GPU> next[2];
@@ -219,12 +246,8 @@ __global__ __launch_bounds__(64 * kUpWaves) void k_moe_gate_up(const uint16_t* _
             }
         }
         auto store = [&](int m, int n, float g, float u) {
-            const float v = g / (1.0f + expf(-g)) * u;
-            const int t = list[p0 + m];
-            uint16_t* to = h + (size_t)(t * topk + rank_of[t]) * 2 * F + n;
-            const uint16_t hi = Bf16::from_f32(v);
-            to[0] = hi;
-            to[F] = Bf16::from_f32(v - Bf16::to_f32(hi));
+            const int t = c.list[p0 + m];
+            moe_store_h(h, t * topk + c.rank_of[t], F, n, g, u);
         };
         if (ks == 1) {
             if (work) {
@@ -250,6 +273,103 @@ __global__ __launch_bounds__(64 * kUpWaves) void k_moe_gate_up(const uint16_t* _
             store(m, t * 16 + n, g, u);
         }
         __syncthreads();
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Gate and up, more tokens: the same, but the block's waves own a tile each
+// and go through K together, so that the rows of x are brought once for all
+// of them, UI units at a time; up to 32 tokens at once, in one 16-row operand
+// or two.
+// ---------------------------------------------------------------------------
+constexpr int kManyWaves = 4;
+template <class T, int GPU, bool ZP>
+__global__ __launch_bounds__(64 * kManyWaves, 4) void k_moe_gate_up_many(
+    const uint16_t* __restrict__ x, int M, int K, int F, const uint8_t* __restrict__ wg,
+    const uint8_t* __restrict__ wu, int E, int topk, int by_pair, const double* __restrict__ logits,
+    int32_t* __restrict__ ids, uint16_t* __restrict__ h) {
+    __shared__ Choice c;
+    constexpr int UI = 1, kStage = UI * 8192;
+    __shared__ __attribute__((aligned(16))) char rows_lds[2 * kStage];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    int e;
+    const int n_tok = moe_choice<kManyWaves>(c, M, E, topk, by_pair, logits, ids, e);
+    if (n_tok == 0) return;
+
+    const W4gLayout l = w4g_layout(128 / GPU, ZP, F, K);
+    wg += (size_t)e * l.total;
+    wu += (size_t)e * l.total;
+    const v4i xb = w4g_rows(x, M, K);
+    const int tile = blockIdx.x * kManyWaves + wave, mine = tile < l.tiles ? tile : l.tiles - 1;
+    const uint32_t lds0 = lds_address(rows_lds);
+    auto run = [&](auto mt_count, int p0) {
+        constexpr int MT = decltype(mt_count)::value;
+        // wave w brings rows 4 w..4 w + 3, and 16 more than that
+        const int n = n_tok - p0 < 16 * MT ? n_tok - p0 : 16 * MT, r0 = 4 * wave;
+        uint32_t row[MT];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            const int m = 16 * mt + r0 + (lane >> 4);
+            row[mt] = (uint32_t)c.list[p0 + (m < n ? m : n - 1)] * (2u * K);
+        }
+        W4gUnit<GPU> next[UI][2];
+        auto load = [&](int u0, int stage) {
+#pragma unroll
+            for (int i = 0; i < UI; ++i) {
+                const int u = u0 + i < l.units ? u0 + i : l.units - 1;
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+                    if (16 * mt + r0 < n)
+                        w4g_x_to_lds(xb, row[mt] + w4g_chunk(r0, u, K, lane), lds0 + stage * kStage + i * 8192 + mt * 4096 + r0 * 256);
+                next[i][0] = w4g_load<GPU, ZP>(wg, l, (size_t)mine * l.units + u, lane);
+                next[i][1] = w4g_load<GPU, ZP>(wu, l, (size_t)mine * l.units + u, lane);
+            }
+        };
+        f32x4 acc[MT][2];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) acc[mt][0] = acc[mt][1] = f32x4{0, 0, 0, 0};
+        load(0, 0);
+        for (int u0 = 0, stage = 0; u0 < l.units; u0 += UI, stage ^= 1) {
+            w4g_wait();
+            w4g_barrier();   // the units' rows are there, the other stage has been read
+            W4gUnit<GPU> w[UI][2];
+#pragma unroll
+            for (int i = 0; i < UI; ++i) {
+                w[i][0] = next[i][0];
+                w[i][1] = next[i][1];
+            }
+            if (u0 + UI < l.units) load(u0 + UI, stage ^ 1);
+#pragma unroll
+            for (int i = 0; i < UI; ++i) {
+                if (u0 + i >= l.units) break;
+#pragma unroll
+                for (int g = 0; g < GPU; ++g) {
+                    u32x4 a[MT][4 / GPU];
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                        for (int s = 0; s < 4 / GPU; ++s)
+                            a[mt][s] = w4g_operand_rows(rows_lds + stage * kStage + i * 8192 + mt * 4096,
+                                                        g * (4 / GPU) + s, lane);
+                    w4g_mac<T, GPU, ZP, MT, 2>(g, w[i], a, acc);
+                }
+            }
+        }
+        w4g_barrier();   // before the next tokens' rows come into the first stage
+        if (tile >= l.tiles) return;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int m = mt * 16 + (lane >> 4) * 4 + i;
+                if (m >= n) continue;
+                const int t = c.list[p0 + m];
+                moe_store_h(h, t * topk + c.rank_of[t], F, tile * 16 + (lane & 15), acc[mt][0][i], acc[mt][1][i]);
+            }
+    };
+    for (int p0 = 0; p0 < n_tok; p0 += 32) {
+        if (n_tok - p0 <= 16) run(std::integral_constant<int, 1>{}, p0);
+        else run(std::integral_constant<int, 2>{}, p0);
     }
 }
 
@@ -499,7 +619,11 @@ hipError_t moe_t(const MoeArgs& a, const MoeWs& l, int M, const uint16_t* x, uin
     int ks = 1;
     while (ks < kUpWaves && (long)rows * tiles * ks < 2048) ks *= 2;
     const int per = kUpWaves / ks;
-    k_moe_gate_up<T, GPU, ZP><<<dim3((tiles + per - 1) / per, rows), 64 * kUpWaves, 0, st>>>(
+    if (M > 16)
+        k_moe_gate_up_many<T, GPU, ZP><<<dim3((tiles + kManyWaves - 1) / kManyWaves, rows), 64 * kManyWaves, 0, st>>>(
+            x, M, a.K, a.F, a.wg, a.wu, a.E, a.topk, by_pair, logits, ids_ws, h);
+    else
+        k_moe_gate_up<T, GPU, ZP><<<dim3((tiles + per - 1) / per, rows), 64 * kUpWaves, 0, st>>>(
         x, M, a.K, a.F, a.wg, a.wu, a.E, a.topk, by_pair, ks, logits, ids_ws, h);
     down<<<dim3(out_tiles, splits), 64 * kDownWaves, kDownWaves * M * 64, st>>>(
         h, M, a.F, a.K, a.wd, a.E, a.topk, a.norm, logits, ids_ws, arrived, parts, y, ids, weights);
