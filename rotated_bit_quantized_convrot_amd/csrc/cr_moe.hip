@@ -30,14 +30,20 @@ namespace {
 
 constexpr int kChunk = kMoeChunk;   // tokens per pass
 
-// The down product's blocks on the passes of one output tile: enough to fill
-// the chip's CUs twice, each wave with at least two (expert, unit) items.
-constexpr int kDownWaves = 8;
-int down_splits(int M, int F, int N, int E, int topk) {
+// The down product: tiles of 16 columns a block, and blocks on the same
+// columns: enough to fill the chip's CUs twice, each wave (up to 16 tokens) or
+// group of waves with at least two (expert, unit) items.
+constexpr int kDownWaves = 8, kManyN = 4, kManyG = 2, kFewTokens = 16;
+struct DownGrid {
+    int columns, splits;
+};
+DownGrid down_grid(int M, int F, int N, int E, int topk) {
+    const int tiles = (N + 15) / 16, columns = M <= kFewTokens ? tiles : (tiles + kManyN - 1) / kManyN;
     const long pairs = (long)M * topk, items = (pairs < E ? pairs : E) * ((F + 127) / 128);
-    long s = 512 / ((N + 15) / 16);
-    if (s > items / (2 * kDownWaves)) s = items / (2 * kDownWaves);
-    return s < 1 ? 1 : (s > 8 ? 8 : (int)s);
+    const long most = items / (2 * (M <= kFewTokens ? kDownWaves : kManyG));
+    long s = 512 / columns;
+    s = s < most ? s : most;
+    return {columns, s < 1 ? 1 : (s > 8 ? 8 : (int)s)};
 }
 
 // Workspace of one pass (byte offsets, 256-byte regions).
@@ -47,8 +53,10 @@ struct MoeWs {
 inline size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 MoeWs moe_ws(int M, int K, int F, int E, int topk) {
     const size_t m = M < kChunk ? M : kChunk, pairs = m * topk;
-    // neither the splits nor the tokens of a last, smaller pass are more
-    const size_t splits = m ? down_splits((int)m, F, K, E, topk) : 1, parts = splits > 1 ? splits * m : 0;
+    // a last, smaller pass has fewer tokens and 8 splits at most
+    const size_t splits = m ? down_grid((int)m, F, K, E, topk).splits : 1, few = m < kFewTokens ? m : kFewTokens;
+    size_t parts = splits > 1 ? splits * m : 0;
+    if (parts < 8 * few && M > kChunk) parts = 8 * few;
     MoeWs l;
     l.logits = 0;                                        // double [m][E]
     l.ids = l.logits + up256(m * E * 8);                 // int32 [m][topk]
@@ -374,104 +382,221 @@ __global__ __launch_bounds__(64 * kManyWaves, 4) void k_moe_gate_up_many(
 }
 
 // ---------------------------------------------------------------------------
-// Down and combination.  gridDim.y blocks share 16 columns of y for every
-// token.  The pairs are sorted by expert and cut into passes of up to 8
-// tokens (operand row 2 t holds token t's h, row 2 t + 1 what is left of it);
-// the (pass, unit) items are shared out to the blocks' waves in contiguous
-// runs.  At the end of a pass a wave adds c times its sums into its own rows
-// of LDS; the waves' rows are added in their order, and so are the blocks',
-// by the one that arrives last: the order of every sum is fixed.  The blocks'
-// sums go through device-scope stores and loads, waited for before the
-// arrival is counted; no fence of the caches is needed.
+// Down and combination.  The pairs are sorted by expert and cut into passes of
+// up to TOK tokens (operand row 2 t holds token t's h, row 2 t + 1 what is
+// left of it); the items (pass, unit of F) are shared out in contiguous runs.
+// At the end of a pass a wave adds c times its sums into its own rows of LDS;
+// the waves' rows are added in their order, and so are those of the gridDim.y
+// blocks on the same columns, by the one that arrives last: the order of
+// every sum is fixed.  The blocks' sums go through device-scope stores and
+// loads, waited for before the arrival is counted; no fence of the caches is
+// needed.
 // ---------------------------------------------------------------------------
-template <class T, int GPU, bool ZP>
-__global__ __launch_bounds__(64 * kDownWaves) void k_moe_down(const uint16_t* __restrict__ h, int M, int F, int N,
-                                                              const uint8_t* __restrict__ wd, int E, int topk,
-                                                              int norm, const double* __restrict__ logits,
-                                                              const int32_t* __restrict__ ids,
-                                                              uint32_t* __restrict__ arrived,
-                                                              float* __restrict__ parts, uint16_t* __restrict__ y,
-                                                              int32_t* __restrict__ ids_out,
-                                                              float* __restrict__ weights_out) {
-    constexpr int kThreads = 64 * kDownWaves;
-    constexpr int kPairs = kChunk * kMoeMaxTopk;
-    static_assert(kMoeMaxExperts <= 2 * kThreads, "two experts a thread");
-    extern __shared__ __attribute__((aligned(16))) float sums[];   // [waves][M][16]
-    __shared__ u64 tokens[kMoeMaxExperts];                          // bit m: token m chose the expert
-    __shared__ int16_t pairs_at[kMoeMaxExperts];                    // where its pairs begin
-    __shared__ int16_t pair_of[kPairs];                             // pairs by expert, then by token
-    __shared__ int16_t pass_e[kPairs], pass_at[kPairs], pass_n[kPairs];
-    __shared__ float prob[kPairs], total[kChunk];
-    __shared__ int scan[2][kDownWaves];
-    __shared__ __attribute__((aligned(16))) char rows_lds[kDownWaves][4096];
-    __shared__ uint32_t before;
+struct Passes {
+    static constexpr int kPairs = kChunk * kMoeMaxTopk;
+    int16_t pair_of[kPairs];                               // pairs by expert, then by token
+    int16_t expert[kPairs], at[kPairs], n[kPairs];         // of a pass
+    float c[kPairs], total[kChunk];                        // of a pair, of a token
+    int scan[2][16];
+    uint32_t before;
+};
+
+// While the passes are made, in the LDS that the rows take later.
+struct ByExpert {
+    u64 tokens[kMoeMaxExperts];         // bit m: token m chose the expert
+    int16_t pairs_at[kMoeMaxExperts];   // where its pairs begin
+};
+
+// Fills the passes; returns their number.
+template <int WAVES, int TOK>
+__device__ __forceinline__ int moe_passes(Passes& s, ByExpert& by, int M, int E, int topk, const int32_t* __restrict__ ids) {
+    constexpr int kThreads = 64 * WAVES, kEach = (kMoeMaxExperts + kThreads - 1) / kThreads;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int pairs = M * topk;
-    int passes = topk;
     if (M == 1) {
         if (tid < topk) {
-            pair_of[tid] = (int16_t)tid;
-            pass_e[tid] = (int16_t)ids[tid];
-            pass_at[tid] = (int16_t)tid;
-            pass_n[tid] = 1;
+            s.pair_of[tid] = s.at[tid] = (int16_t)tid;
+            s.expert[tid] = (int16_t)ids[tid];
+            s.n[tid] = 1;
         }
-    } else {
-        for (int e = tid; e < E; e += kThreads) tokens[e] = 0;
         __syncthreads();
-        for (int p = tid; p < pairs; p += kThreads) atomicOr(&tokens[ids[p]], 1ull << (p / topk));
-        __syncthreads();
-        // a thread's experts 2 tid, 2 tid + 1: their pairs and passes, and those before them
-        const int e0 = 2 * tid;
-        const int n0 = e0 < E ? __popcll(tokens[e0]) : 0, n1 = e0 + 1 < E ? __popcll(tokens[e0 + 1]) : 0;
-        int a = n0 + n1, b = ((n0 + 7) >> 3) + ((n1 + 7) >> 3);
-        const int own_a = a, own_b = b;
+        return topk;
+    }
+    for (int e = tid; e < E; e += kThreads) by.tokens[e] = 0;
+    __syncthreads();
+    for (int p = tid; p < pairs; p += kThreads) atomicOr(&by.tokens[ids[p]], 1ull << (p / topk));
+    __syncthreads();
+    // a thread's kEach experts: their pairs and passes, and those before them
+    int n[kEach], a = 0, b = 0;
 #pragma unroll
-        for (int o = 1; o < 64; o *= 2) {
-            const int pa = __shfl_up(a, o), pb = __shfl_up(b, o);
-            if (lane >= o) {
-                a += pa;
-                b += pb;
-            }
-        }
-        if (lane == 63) {
-            scan[0][wave] = a;
-            scan[1][wave] = b;
-        }
-        __syncthreads();
-        a -= own_a;
-        b -= own_b;
-        passes = 0;
+    for (int i = 0; i < kEach; ++i) {
+        const int e = tid * kEach + i;
+        n[i] = e < E ? __popcll(by.tokens[e]) : 0;
+        a += n[i];
+        b += (n[i] + TOK - 1) / TOK;
+    }
+    const int own_a = a, own_b = b;
 #pragma unroll
-        for (int i = 0; i < kDownWaves; ++i) {
-            if (i < wave) {
-                a += scan[0][i];
-                b += scan[1][i];
-            }
-            passes += scan[1][i];
-        }
-        for (int i = 0; i < 2; ++i) {
-            const int n = i ? n1 : n0;
-            if (n > 0) pairs_at[e0 + i] = (int16_t)a;
-            for (int q = 0; q < n; q += 8) {
-                pass_e[b] = (int16_t)(e0 + i);
-                pass_at[b] = (int16_t)(a + q);
-                pass_n[b] = (int16_t)(n - q < 8 ? n - q : 8);
-                ++b;
-            }
-            a += n;
-        }
-        __syncthreads();
-        for (int p = tid; p < pairs; p += kThreads) {
-            const int e = ids[p];
-            pair_of[pairs_at[e] + __popcll(tokens[e] & ((1ull << (p / topk)) - 1))] = (int16_t)p;
+    for (int o = 1; o < 64; o *= 2) {
+        const int pa = __shfl_up(a, o), pb = __shfl_up(b, o);
+        if (lane >= o) {
+            a += pa;
+            b += pb;
         }
     }
-    for (int i = tid; i < kDownWaves * M * 16; i += kThreads) sums[i] = 0.0f;
+    if (lane == 63) {
+        s.scan[0][wave] = a;
+        s.scan[1][wave] = b;
+    }
     __syncthreads();
+    a -= own_a;
+    b -= own_b;
+    int passes = 0;
+#pragma unroll
+    for (int i = 0; i < WAVES; ++i) {
+        if (i < wave) {
+            a += s.scan[0][i];
+            b += s.scan[1][i];
+        }
+        passes += s.scan[1][i];
+    }
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        if (n[i] > 0) by.pairs_at[tid * kEach + i] = (int16_t)a;
+        for (int q = 0; q < n[i]; q += TOK) {
+            s.expert[b] = (int16_t)(tid * kEach + i);
+            s.at[b] = (int16_t)(a + q);
+            s.n[b] = (int16_t)(n[i] - q < TOK ? n[i] - q : TOK);
+            ++b;
+        }
+        a += n[i];
+    }
+    __syncthreads();
+    for (int p = tid; p < pairs; p += kThreads) {
+        const int e = ids[p];
+        s.pair_of[by.pairs_at[e] + __popcll(by.tokens[e] & ((1ull << (p / topk)) - 1))] = (int16_t)p;
+    }
+    __syncthreads();
+    return __builtin_amdgcn_readfirstlane(passes);
+}
+
+// The pairs' weights: the softmax's numerators over the tokens' denominators;
+// one block writes the choice out.
+template <int WAVES>
+__device__ __forceinline__ void moe_weights(Passes& s, int M, int E, int topk, int norm,
+                                            const double* __restrict__ logits, const int32_t* __restrict__ ids,
+                                            bool write, int32_t* __restrict__ ids_out,
+                                            float* __restrict__ weights_out) {
+    constexpr int kThreads = 64 * WAVES;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int pairs = M * topk;
+    for (int p = tid; p < pairs; p += kThreads) {
+        const double* of = logits + (size_t)(p / topk) * E;
+        s.c[p] = expf((float)(of[ids[p]] - of[ids[p / topk * topk]]));
+    }
+    if (!norm) {
+        for (int m = wave; m < M; m += WAVES) {
+            const double* of = logits + (size_t)m * E;
+            const double top = of[ids[m * topk]];
+            float v = 0.0f;
+            for (int j = lane; j < E; j += 64) v += expf((float)(of[j] - top));
+#pragma unroll
+            for (int o = 1; o < 64; o *= 2) v += __shfl_xor(v, o);
+            if (lane == 0) s.total[m] = v;
+        }
+    }
+    __syncthreads();
+    if (norm && tid < M) {
+        float v = 0.0f;
+        for (int r = 0; r < topk; ++r) v += s.c[tid * topk + r];
+        s.total[tid] = v;
+    }
+    __syncthreads();
+    for (int p = tid; p < pairs; p += kThreads) {
+        const float c = s.c[p] / s.total[p / topk];
+        s.c[p] = c;
+        if (write) {
+            if (ids_out) ids_out[p] = ids[p];
+            if (weights_out) weights_out[p] = c;
+        }
+    }
+    __syncthreads();
+}
+
+// A pass's sums (operand rows 16 mt + ..) times c into the wave's rows [M][16].
+template <int MT>
+__device__ __forceinline__ void moe_scatter(const Passes& s, int pass, int topk, f32x4 (&acc)[MT][1], float* sums) {
+    const int lane = threadIdx.x & 63, n = s.n[pass], at = s.at[pass];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int t = mt * 8 + (lane >> 4) * 2 + j;
+            if (t < n) {
+                const int p = s.pair_of[at + t];
+                float& to = sums[p / topk * 16 + (lane & 15)];
+                to = __builtin_fmaf(s.c[p], acc[mt][0][2 * j] + acc[mt][0][2 * j + 1], to);
+            }
+        }
+        acc[mt][0] = f32x4{0, 0, 0, 0};
+    }
+}
+
+// Columns blockIdx.x C.. of y: this block's sums value(m, column) and, where
+// more blocks share the columns, theirs.
+template <class T, int WAVES, int C, class V>
+__device__ __forceinline__ void moe_finish(Passes& s, int M, int N, uint32_t* arrived, float* parts, uint16_t* y,
+                                           V value) {
+    constexpr int kThreads = 64 * WAVES;
+    const int tid = threadIdx.x, splits = gridDim.y;
+    for (int i = tid; i < M * C; i += kThreads) {
+        const int m = i / C;
+        const size_t n = (size_t)blockIdx.x * C + i % C;
+        if (n >= (size_t)N) continue;
+        if (splits == 1)
+            y[(size_t)m * N + n] = T::from_f32(value(m, i % C));
+        else
+            __hip_atomic_store(&parts[((size_t)blockIdx.y * M + m) * N + n], value(m, i % C), __ATOMIC_RELAXED,
+                               __HIP_MEMORY_SCOPE_AGENT);
+    }
+    if (splits == 1) return;
+    w4g_wait();   // this wave's sums are where every block reads them
+    __syncthreads();
+    if (tid == 0)
+        s.before = __hip_atomic_fetch_add(&arrived[blockIdx.x], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();
+    if (s.before + 1 != (uint32_t)splits) return;
+    for (int i = tid; i < M * C; i += kThreads) {
+        const int m = i / C;
+        const size_t n = (size_t)blockIdx.x * C + i % C;
+        if (n >= (size_t)N) continue;
+        float v = 0.0f;
+        for (int j = 0; j < splits; ++j)
+            v += __hip_atomic_load(&parts[((size_t)j * M + m) * N + n], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        y[(size_t)m * N + n] = T::from_f32(v);
+    }
+}
+
+template <class T, int GPU, bool ZP>
+__global__ __launch_bounds__(64 * kDownWaves, 4) void k_moe_down(
+    const uint16_t* __restrict__ h, int M, int F, int N, const uint8_t* __restrict__ wd, int E, int topk, int norm,
+    const double* __restrict__ logits, const int32_t* __restrict__ ids, uint32_t* __restrict__ arrived,
+    float* __restrict__ parts, uint16_t* __restrict__ y, int32_t* __restrict__ ids_out,
+    float* __restrict__ weights_out) {
+    // one tile of 16 columns a block, the items shared out to its waves, each
+    // with rows of its own
+    constexpr int kThreads = 64 * kDownWaves;
+    extern __shared__ __attribute__((aligned(16))) float sums[];   // [waves][M][16]
+    __shared__ Passes s;
+    __shared__ __attribute__((aligned(16))) char rows_lds[kDownWaves][4096];
+    static_assert(sizeof(ByExpert) <= sizeof(rows_lds), "the rows' place holds it");
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    for (int i = tid; i < kDownWaves * M * 16; i += kThreads) sums[i] = 0.0f;
+    const int passes = moe_passes<kDownWaves, 8>(s, *reinterpret_cast<ByExpert*>(rows_lds), M, E, topk, ids);
 
     const W4gLayout l = w4g_layout(128 / GPU, ZP, N, F);
     const int tile = blockIdx.x, split = blockIdx.y, splits = gridDim.y;
-    const v4i hb = w4g_rows(h, 2 * pairs, F);
+    const v4i hb = w4g_rows(h, 2 * M * topk, F);
     const int items = passes * l.units, run = (items + kDownWaves * splits - 1) / (kDownWaves * splits);
     const int begin = (split * kDownWaves + wave) * run, end = begin + run < items ? begin + run : items;
     const char* my_rows = rows_lds[wave];
@@ -482,13 +607,13 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_moe_down(const uint16_t* __
     uint32_t row[4];
     W4gUnit<GPU> next[1];
     auto turn = [&]() {
-        const int n = __builtin_amdgcn_readfirstlane(pass_n[pass]), at = pass_at[pass];
-        we = wd + (size_t)__builtin_amdgcn_readfirstlane(pass_e[pass]) * l.total;
+        const int n = __builtin_amdgcn_readfirstlane(s.n[pass]), at = s.at[pass];
+        we = wd + (size_t)__builtin_amdgcn_readfirstlane(s.expert[pass]) * l.total;
         fills = (n + 1) >> 1;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int r = 4 * j + (lane >> 4), t = (r >> 1) < n ? r >> 1 : n - 1;
-            row[j] = (uint32_t)(2 * pair_of[at + t] + (r & 1)) * (2u * F);
+            row[j] = (uint32_t)(2 * s.pair_of[at + t] + (r & 1)) * (2u * F);
         }
     };
     auto load = [&]() {
@@ -501,40 +626,8 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_moe_down(const uint16_t* __
         turn();
         load();
     }
-
-    // while the first loads are under way: the softmax's numerators, the
-    // tokens' denominators, the weights of the pairs
-    for (int p = tid; p < pairs; p += kThreads) {
-        const double* of = logits + (size_t)(p / topk) * E;
-        prob[p] = expf((float)(of[ids[p]] - of[ids[p / topk * topk]]));
-    }
-    if (!norm) {
-        for (int m = wave; m < M; m += kDownWaves) {
-            const double* of = logits + (size_t)m * E;
-            const double top = of[ids[m * topk]];
-            float s = 0.0f;
-            for (int j = lane; j < E; j += 64) s += expf((float)(of[j] - top));
-#pragma unroll
-            for (int o = 1; o < 64; o *= 2) s += __shfl_xor(s, o);
-            if (lane == 0) total[m] = s;
-        }
-    }
-    __syncthreads();
-    if (norm && tid < M) {
-        float s = 0.0f;
-        for (int r = 0; r < topk; ++r) s += prob[tid * topk + r];
-        total[tid] = s;
-    }
-    __syncthreads();
-    for (int p = tid; p < pairs; p += kThreads) {
-        const float c = prob[p] / total[p / topk];
-        prob[p] = c;
-        if (tile == 0 && split == 0) {
-            if (ids_out) ids_out[p] = ids[p];
-            if (weights_out) weights_out[p] = c;
-        }
-    }
-    __syncthreads();
+    // while the first loads are under way
+    moe_weights<kDownWaves>(s, M, E, topk, norm, logits, ids, tile == 0 && split == 0, ids_out, weights_out);
 
     f32x4 acc[1][1] = {{f32x4{0, 0, 0, 0}}};
     for (int i = begin; i < end; ++i) {
@@ -555,45 +648,111 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_moe_down(const uint16_t* __
         }
 #pragma unroll
         for (int g = 0; g < GPU; ++g) w4g_mac<DownT<T>, GPU, ZP, 1, 1>(g, w, a[g], acc);
-        if (i + 1 < end && pass == done) continue;
-        const int n = pass_n[done], at = pass_at[done];
+        if (i + 1 == end || pass != done) moe_scatter<1>(s, done, topk, acc, sums + wave * M * 16);
+    }
+    __syncthreads();
+    moe_finish<T, kDownWaves, 16>(s, M, N, arrived, parts, y, [&](int m, int n) {
+        float v = 0.0f;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int t = (lane >> 4) * 2 + j;
-            if (t < n) {
-                const int p = pair_of[at + t];
-                float& to = sums[(wave * M + p / topk) * 16 + (lane & 15)];
-                to = __builtin_fmaf(prob[p], acc[0][0][2 * j] + acc[0][0][2 * j + 1], to);
-            }
+        for (int wv = 0; wv < kDownWaves; ++wv) v += sums[(wv * M + m) * 16 + n];
+        return v;
+    });
+}
+
+// More tokens: kManyN tiles of 16 columns a block, whose waves go through the
+// same items together, so that the rows of h are brought once for all of
+// them; kManyG such groups of waves a block, each with its share of the items.
+template <class T, int GPU, bool ZP>
+__global__ __launch_bounds__(64 * kManyN * kManyG, 4) void k_moe_down_many(
+    const uint16_t* __restrict__ h, int M, int F, int N, const uint8_t* __restrict__ wd, int E, int topk, int norm,
+    const double* __restrict__ logits, const int32_t* __restrict__ ids, uint32_t* __restrict__ arrived,
+    float* __restrict__ parts, uint16_t* __restrict__ y, int32_t* __restrict__ ids_out,
+    float* __restrict__ weights_out) {
+    constexpr int kWaves = kManyN * kManyG, kThreads = 64 * kWaves, MT = 2, kStage = kManyG * MT * 4096;
+    extern __shared__ __attribute__((aligned(16))) float sums[];   // [waves][M][16]
+    __shared__ Passes s;
+    __shared__ __attribute__((aligned(16))) char rows_lds[2 * kStage];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int group = wave / kManyN, wn = wave % kManyN;
+    for (int i = tid; i < kWaves * M * 16; i += kThreads) sums[i] = 0.0f;
+    const int passes = moe_passes<kWaves, 8 * MT>(s, *reinterpret_cast<ByExpert*>(rows_lds), M, E, topk, ids);
+
+    const W4gLayout l = w4g_layout(128 / GPU, ZP, N, F);
+    const int tile = blockIdx.x * kManyN + wn, mine = tile < l.tiles ? tile : l.tiles - 1;
+    const int split = blockIdx.y, splits = gridDim.y;
+    const v4i hb = w4g_rows(h, 2 * M * topk, F);
+    const int items = passes * l.units, run = (items + kManyG * splits - 1) / (kManyG * splits);
+    const int begin = (split * kManyG + group) * run, end = begin + run < items ? begin + run : items;
+    const uint32_t lds0 = lds_address(rows_lds) + group * MT * 4096;
+    int pass = begin / l.units, u = begin % l.units, n = 0;
+    const uint8_t* we = wd;
+    uint32_t row[MT];   // of this wave's instructions: rows 4 wn.. of both operands
+    W4gUnit<GPU> next[1];
+    auto turn = [&]() {
+        n = __builtin_amdgcn_readfirstlane(s.n[pass]);
+        const int at = s.at[pass];
+        we = wd + (size_t)__builtin_amdgcn_readfirstlane(s.expert[pass]) * l.total;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            const int r = 16 * mt + 4 * wn + (lane >> 4), t = (r >> 1) < n ? r >> 1 : n - 1;
+            row[mt] = (uint32_t)(2 * s.pair_of[at + t] + (r & 1)) * (2u * F);
         }
-        acc[0][0] = f32x4{0, 0, 0, 0};
+    };
+    auto load = [&](int stage) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+            if (8 * mt + 2 * wn < n)
+                w4g_x_to_lds(hb, row[mt] + w4g_chunk(4 * wn, u, F, lane), lds0 + stage * kStage + mt * 4096 + wn * 1024);
+        next[0] = w4g_load<GPU, ZP>(we, l, (size_t)mine * l.units + u, lane);
+    };
+    if (begin < end) {
+        turn();
+        load(0);
+    }
+    moe_weights<kWaves>(s, M, E, topk, norm, logits, ids, blockIdx.x == 0 && split == 0, ids_out, weights_out);
+
+    f32x4 acc[MT][1];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) acc[mt][0] = f32x4{0, 0, 0, 0};
+    for (int i = begin; i < begin + run; ++i) {   // as many turns for every wave: they meet in each
+        w4g_wait();
+        w4g_barrier();   // the item's rows are there, the other stage has been read
+        if (i >= end) continue;
+        const int stage = (i - begin) & 1;
+        const W4gUnit<GPU> w[1] = {next[0]};
+        const int done = pass, rows = n;
+        if (++u == l.units) {
+            u = 0;
+            ++pass;
+        }
+        if (i + 1 < end) {
+            if (pass != done) turn();
+            load(stage ^ 1);
+        }
+        const char* at = rows_lds + group * MT * 4096 + stage * kStage;
+        auto use = [&](auto mt_count) {
+            constexpr int C = decltype(mt_count)::value;
+#pragma unroll
+            for (int g = 0; g < GPU; ++g) {
+                u32x4 a[C][4 / GPU];
+#pragma unroll
+                for (int mt = 0; mt < C; ++mt)
+#pragma unroll
+                    for (int d = 0; d < 4 / GPU; ++d) a[mt][d] = w4g_operand_rows(at + mt * 4096, g * (4 / GPU) + d, lane);
+                w4g_mac<DownT<T>, GPU, ZP, C, 1>(g, w, a, reinterpret_cast<f32x4(&)[C][1]>(acc));
+            }
+        };
+        if (rows <= 8) use(std::integral_constant<int, 1>{});
+        else use(std::integral_constant<int, 2>{});
+        if (i + 1 == end || pass != done) moe_scatter<MT>(s, done, topk, acc, sums + wave * M * 16);
     }
     __syncthreads();
-    for (int i = tid; i < M * 16; i += kThreads) {
-        const size_t gn = (size_t)tile * 16 + (i & 15);   // N is a multiple of 16
+    moe_finish<T, kWaves, 16 * kManyN>(s, M, N, arrived, parts, y, [&](int m, int c) {
         float v = 0.0f;
 #pragma unroll
-        for (int wv = 0; wv < kDownWaves; ++wv) v += sums[wv * M * 16 + i];
-        if (splits == 1)
-            y[(size_t)(i >> 4) * N + gn] = T::from_f32(v);
-        else
-            __hip_atomic_store(&parts[((size_t)split * M + (i >> 4)) * N + gn], v, __ATOMIC_RELAXED,
-                               __HIP_MEMORY_SCOPE_AGENT);
-    }
-    if (splits == 1) return;
-    w4g_wait();   // this wave's sums are where every block reads them
-    __syncthreads();
-    if (tid == 0) before = __hip_atomic_fetch_add(&arrived[tile], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    __syncthreads();
-    if (before + 1 != (uint32_t)splits) return;
-    for (int i = tid; i < M * 16; i += kThreads) {
-        const size_t gn = (size_t)tile * 16 + (i & 15);
-        float v = 0.0f;
-        for (int s = 0; s < splits; ++s)
-            v += __hip_atomic_load(&parts[((size_t)s * M + (i >> 4)) * N + gn], __ATOMIC_RELAXED,
-                                   __HIP_MEMORY_SCOPE_AGENT);
-        y[(size_t)(i >> 4) * N + gn] = T::from_f32(v);
-    }
+        for (int g = 0; g < kManyG; ++g) v += sums[((g * kManyN + (c >> 4)) * M + m) * 16 + (c & 15)];
+        return v;
+    });
 }
 
 template <class T, int GPU, bool ZP>
@@ -604,14 +763,17 @@ hipError_t moe_t(const MoeArgs& a, const MoeWs& l, int M, const uint16_t* x, uin
     int32_t* ids_ws = reinterpret_cast<int32_t*>(ws + l.ids);
     uint16_t* h = reinterpret_cast<uint16_t*>(ws + l.h);
     static std::atomic<uint64_t> done{0};
-    const auto down = k_moe_down<T, GPU, ZP>;
-    const hipError_t err = opt_in_lds(reinterpret_cast<const void*>(down), kDownWaves * kChunk * 64, done);
-    if (err != hipSuccess) return err;
+    static_assert(kDownWaves == kManyN * kManyG, "either kernel's waves");
+    const auto down = M <= kFewTokens ? k_moe_down<T, GPU, ZP> : k_moe_down_many<T, GPU, ZP>;
+    if (M > kFewTokens) {
+        const hipError_t err = opt_in_lds(reinterpret_cast<const void*>(down), kDownWaves * kChunk * 64, done);
+        if (err != hipSuccess) return err;
+    }
     uint32_t* arrived = reinterpret_cast<uint32_t*>(ws + l.arrived);
     float* parts = reinterpret_cast<float*>(ws + l.parts);
-    const int splits = down_splits(M, a.F, a.K, a.E, a.topk), out_tiles = a.K / 16;
+    const DownGrid grid = down_grid(M, a.F, a.K, a.E, a.topk);
     k_moe_logits<T><<<dim3((a.E + 3) / 4, M), 256, 0, st>>>(x, a.K, a.router, a.E, logits, arrived,
-                                                            splits > 1 ? out_tiles : 0);
+                                                            grid.splits > 1 ? grid.columns : 0);
     const int pairs = M * a.topk, by_pair = pairs < a.E, rows = by_pair ? pairs : a.E;
     // a wave per tile where the chosen experts' tiles fill the chip's 4096
     // wave slots half, else as many waves on a tile's K as bring them there
@@ -619,13 +781,13 @@ hipError_t moe_t(const MoeArgs& a, const MoeWs& l, int M, const uint16_t* x, uin
     int ks = 1;
     while (ks < kUpWaves && (long)rows * tiles * ks < 2048) ks *= 2;
     const int per = kUpWaves / ks;
-    if (M > 16)
+    if (M > kFewTokens)
         k_moe_gate_up_many<T, GPU, ZP><<<dim3((tiles + kManyWaves - 1) / kManyWaves, rows), 64 * kManyWaves, 0, st>>>(
             x, M, a.K, a.F, a.wg, a.wu, a.E, a.topk, by_pair, logits, ids_ws, h);
     else
         k_moe_gate_up<T, GPU, ZP><<<dim3((tiles + per - 1) / per, rows), 64 * kUpWaves, 0, st>>>(
         x, M, a.K, a.F, a.wg, a.wu, a.E, a.topk, by_pair, ks, logits, ids_ws, h);
-    down<<<dim3(out_tiles, splits), 64 * kDownWaves, kDownWaves * M * 64, st>>>(
+    down<<<dim3(grid.columns, grid.splits), 64 * kDownWaves, kDownWaves * M * 64, st>>>(
         h, M, a.F, a.K, a.wd, a.E, a.topk, a.norm, logits, ids_ws, arrived, parts, y, ids, weights);
     return hipGetLastError();
 }
