@@ -48,7 +48,7 @@ DownGrid down_grid(int M, int F, int N, int E, int topk) {
 
 // Workspace of one pass (byte offsets, 256-byte regions).
 struct MoeWs {
-    size_t logits, ids, h, arrived, parts, total;
+    size_t logits, ids, top, h, arrived, parts, total;
 };
 inline size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 MoeWs moe_ws(int M, int K, int F, int E, int topk) {
@@ -60,7 +60,8 @@ MoeWs moe_ws(int M, int K, int F, int E, int topk) {
     MoeWs l;
     l.logits = 0;                                        // double [m][E]
     l.ids = l.logits + up256(m * E * 8);                 // int32 [m][topk]
-    l.h = l.ids + up256(pairs * 4);                      // bf16 [m topk][2][F]
+    l.top = l.ids + up256(pairs * 4);                    // double [m][topk]: the chosen logits
+    l.h = l.top + up256(pairs * 8);                      // bf16 [m topk][2][F]
     l.arrived = l.h + up256(pairs * F * 4);              // uint32 [K / 16]
     l.parts = l.arrived + up256((size_t)(K / 16) * 4);   // float [splits][m][K]
     l.total = l.parts + up256(parts * K * 4);
@@ -121,58 +122,122 @@ __device__ __forceinline__ u64 order_key(double v) {
 constexpr int kUpWaves = 8;
 
 struct Choice {
-    u64 key[kMoeMaxExperts];
-    int above[kMoeMaxExperts];
-    int16_t rank_of[kChunk], list[kChunk];   // of the block's expert: rank by token, tokens
-    int found, chosen;
+    int16_t rank_of[kChunk], list[kChunk];   // of the block's expert: rank by token (-1: not chosen), tokens
+    int chosen;
 };
+// The largest of the wave's values, by DPP steps (row shifts by 1, 2, 4, 8,
+// then the rows' last lanes broadcast) that end in lane 63.
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+#define CR_MAX_STEP(ctrl, rows)                                                                                        \
+    {                                                                                                                  \
+        const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, ctrl, rows, 0xF, false);              \
+        v = o > v ? o : v;                                                                                             \
+    }
+    CR_MAX_STEP(0x111, 0xF)
+    CR_MAX_STEP(0x112, 0xF)
+    CR_MAX_STEP(0x114, 0xF)
+    CR_MAX_STEP(0x118, 0xF)
+    CR_MAX_STEP(0x142, 0xA)
+    CR_MAX_STEP(0x143, 0xC)
+#undef CR_MAX_STEP
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+// The expert of rank `want` in a row of logits: `want` + 1 times the largest
+// key, equal ones by index, taken out.  Every wave does it for itself: 0.1 us
+// a rank, with no LDS and no barrier, where counting for every expert the
+// logits above it (E^2 comparisons through LDS) took 3 us of 128 experts.
+template <int EACH>   // E <= 64 EACH
+__device__ __forceinline__ int moe_of_rank(const double* __restrict__ row, int E, int want) {
+    const int lane = threadIdx.x & 63;
+    u64 key[EACH];
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) {
+        const int e = i * 64 + lane;
+        const double v = row[e < E ? e : E - 1];
+        key[i] = e < E ? order_key(v) : 0;   // 0 is below every value's key (-inf's is 0x000F..F)
+    }
+    int at = 0;
+    for (int r = 0; r <= want; ++r) {
+        u64 best = key[0];
+        int mine = lane;
+#pragma unroll
+        for (int i = 1; i < EACH; ++i)
+            if (key[i] > best) {   // equal: the earlier one
+                best = key[i];
+                mine = i * 64 + lane;
+            }
+        const uint32_t hi = wave_max((uint32_t)(best >> 32));
+        const uint32_t lo = wave_max((uint32_t)(best >> 32) == hi ? (uint32_t)best : 0u);
+        const bool is = best == (((u64)hi << 32) | lo);
+        at = (int)~wave_max(is ? ~(uint32_t)mine : 0u);
+#pragma unroll
+        for (int i = 0; i < EACH; ++i) key[i] = at == i * 64 + lane ? 0 : key[i];
+    }
+    return at;
+}
+
 // The block's expert and its tokens (c.list, c.rank_of); returns their number,
-// 0 where the block has nothing to do, the expert in e.
+// 0 where the block has nothing to do, the expert in e.  Blocks of the first
+// tile write the choice down: ids and logits by (token, rank).
 template <int WAVES>
 __device__ __forceinline__ int moe_choice(Choice& c, int M, int E, int topk, int by_pair,
-                                          const double* __restrict__ logits, int32_t* __restrict__ ids, int& e) {
+                                          const double* __restrict__ logits, int32_t* __restrict__ ids,
+                                          double* __restrict__ top, int& e) {
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    constexpr int kThreads = 64 * WAVES;
     int first = 0;
     e = blockIdx.y;
     if (by_pair) {
-        // the expert of this rank: every expert counts the logits above its
-        // own, the counting split over the threads that are left
         first = blockIdx.y / topk;
         const int want = blockIdx.y - first * topk;
         const double* row = logits + (size_t)first * E;
-        for (int j = tid; j < E; j += kThreads) {
-            c.key[j] = order_key(row[j]);
-            c.above[j] = 0;
-        }
-        __syncthreads();
-        const int parts = E < kThreads ? kThreads / E : 1, span = (E + parts - 1) / parts;
-        for (int i = tid; i < E * parts; i += kThreads) {
-            const int mine = i % E, j0 = i / E * span, j1 = j0 + span < E ? j0 + span : E;
-            const u64 k = c.key[mine];
-            int n = 0;
-            for (int j = j0; j < j1; ++j) n += c.key[j] > k || (c.key[j] == k && j < mine);
-            if (n) atomicAdd(&c.above[mine], n);
-        }
-        __syncthreads();
-        for (int j = tid; j < E; j += kThreads)
-            if (c.above[j] == want) c.found = j;   // ranks are a permutation: one thread
-        __syncthreads();
-        e = c.found;
-        if (M == 1 && tid == 0) c.rank_of[0] = (int16_t)want;
-    }
-    if (!(by_pair && M == 1)) {
-        for (int m = wave; m < M; m += WAVES) {
-            const double* row = logits + (size_t)m * E;
-            const u64 k = order_key(row[e]);
-            int n = 0;
-            for (int j0 = 0; j0 < E; j0 += 64) {
-                const int j = j0 + lane;
-                const u64 o = j < E ? order_key(row[j]) : 0;
-                n += __popcll(__ballot(j < E && (o > k || (o == k && j < e))));
+        e = E <= 128 ? moe_of_rank<2>(row, E, want) : E <= 256 ? moe_of_rank<4>(row, E, want)
+                                                               : moe_of_rank<kMoeMaxExperts / 64>(row, E, want);
+        if (M == 1) {
+            if (tid == 0) {
+                c.rank_of[0] = (int16_t)want;
+                c.list[0] = 0;
+                if (blockIdx.x == 0) {
+                    ids[want] = e;
+                    top[want] = logits[e];
+                }
             }
-            if (lane == 0) c.rank_of[m] = (int16_t)(n < topk ? n : -1);
+            __syncthreads();
+            return 1;
         }
+    }
+    // the rank of e in every row: the logits above its own, counted by a wave,
+    // two rows and 256 logits under way at a time
+    constexpr int kRows = 2, kCols = 4;
+    for (int m0 = wave; m0 < M; m0 += WAVES * kRows) {
+        u64 mine[kRows];
+        int n[kRows];
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+            const int m = m0 + r * WAVES < M ? m0 + r * WAVES : m0;
+            mine[r] = order_key(logits[(size_t)m * E + e]);
+            n[r] = 0;
+        }
+        for (int j0 = 0; j0 < E; j0 += 64 * kCols) {
+            double v[kRows][kCols];
+#pragma unroll
+            for (int r = 0; r < kRows; ++r)
+#pragma unroll
+                for (int i = 0; i < kCols; ++i) {
+                    const int m = m0 + r * WAVES < M ? m0 + r * WAVES : m0, j = j0 + i * 64 + lane;
+                    v[r][i] = logits[(size_t)m * E + (j < E ? j : E - 1)];
+                }
+#pragma unroll
+            for (int r = 0; r < kRows; ++r)
+#pragma unroll
+                for (int i = 0; i < kCols; ++i) {
+                    const int j = j0 + i * 64 + lane;
+                    const u64 o = order_key(v[r][i]);
+                    n[r] += __popcll(__ballot(j < E && (o > mine[r] || (o == mine[r] && j < e))));
+                }
+        }
+#pragma unroll
+        for (int r = 0; r < kRows; ++r)
+            if (lane == 0 && m0 + r * WAVES < M) c.rank_of[m0 + r * WAVES] = (int16_t)(n[r] < topk ? n[r] : -1);
     }
     __syncthreads();
     if (wave == 0) {
@@ -180,12 +245,14 @@ __device__ __forceinline__ int moe_choice(Choice& c, int M, int E, int topk, int
         const u64 all = __ballot(mine);
         if (mine) {
             c.list[__popcll(all & ((1ull << lane) - 1))] = (int16_t)lane;
-            if (blockIdx.x == 0) ids[lane * topk + c.rank_of[lane]] = e;
+            if (blockIdx.x == 0) {
+                ids[lane * topk + c.rank_of[lane]] = e;
+                top[lane * topk + c.rank_of[lane]] = logits[(size_t)lane * E + e];
+            }
         }
         if (lane == 0) c.chosen = (all & ((1ull << first) - 1)) ? 0 : __popcll(all);
     }
     __syncthreads();
-    e = __builtin_amdgcn_readfirstlane(e);
     return __builtin_amdgcn_readfirstlane(c.chosen);
 }
 
@@ -204,14 +271,15 @@ __global__ __launch_bounds__(64 * kUpWaves, 4) void k_moe_gate_up(const uint16_t
                                                                const uint8_t* __restrict__ wu, int E, int topk,
                                                                int by_pair, int ks,
                                                                const double* __restrict__ logits,
-                                                               int32_t* __restrict__ ids, uint16_t* __restrict__ h) {
+                                                               int32_t* __restrict__ ids, double* __restrict__ top,
+                                                               uint16_t* __restrict__ h) {
     __shared__ Choice c;
     __shared__ __attribute__((aligned(16))) char rows_lds[kUpWaves][4096];
     __shared__ f32x4 part[kUpWaves][2][64];
     constexpr int kThreads = 64 * kUpWaves;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     int e;
-    const int n_tok = moe_choice<kUpWaves>(c, M, E, topk, by_pair, logits, ids, e);
+    const int n_tok = moe_choice<kUpWaves>(c, M, E, topk, by_pair, logits, ids, top, e);
     if (n_tok == 0) return;
 
     const W4gLayout l = w4g_layout(128 / GPU, ZP, F, K);
@@ -295,13 +363,13 @@ template <class T, int GPU, bool ZP>
 __global__ __launch_bounds__(64 * kManyWaves, 4) void k_moe_gate_up_many(
     const uint16_t* __restrict__ x, int M, int K, int F, const uint8_t* __restrict__ wg,
     const uint8_t* __restrict__ wu, int E, int topk, int by_pair, const double* __restrict__ logits,
-    int32_t* __restrict__ ids, uint16_t* __restrict__ h) {
+    int32_t* __restrict__ ids, double* __restrict__ top, uint16_t* __restrict__ h) {
     __shared__ Choice c;
     constexpr int UI = 1, kStage = UI * 8192;
     __shared__ __attribute__((aligned(16))) char rows_lds[2 * kStage];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     int e;
-    const int n_tok = moe_choice<kManyWaves>(c, M, E, topk, by_pair, logits, ids, e);
+    const int n_tok = moe_choice<kManyWaves>(c, M, E, topk, by_pair, logits, ids, top, e);
     if (n_tok == 0) return;
 
     const W4gLayout l = w4g_layout(128 / GPU, ZP, F, K);
@@ -400,109 +468,53 @@ struct Passes {
     int scan[2][16];
     uint32_t before;
 };
-
-// While the passes are made, in the LDS that the rows take later.
+// While those are made, in the LDS that the rows take later.
 struct ByExpert {
     u64 tokens[kMoeMaxExperts];         // bit m: token m chose the expert
-    int16_t pairs_at[kMoeMaxExperts];   // where its pairs begin
+    double top[Passes::kPairs];         // the pairs' logits
+    int16_t pairs_at[kMoeMaxExperts];   // where an expert's pairs begin
+    int16_t expert[Passes::kPairs];     // of a pair
 };
 
-// Fills the passes; returns their number.
+// Fills the passes and the pairs' weights (the softmax's numerators over the
+// tokens' denominators); returns the number of passes.  One block writes the
+// choice out.  The choice is read once, everything else happens in LDS.
 template <int WAVES, int TOK>
-__device__ __forceinline__ int moe_passes(Passes& s, ByExpert& by, int M, int E, int topk, const int32_t* __restrict__ ids) {
+__device__ __forceinline__ int moe_passes(Passes& s, ByExpert& by, int M, int E, int topk, int norm,
+                                          const double* __restrict__ logits, const int32_t* __restrict__ ids,
+                                          const double* __restrict__ top, bool write, int32_t* __restrict__ ids_out,
+                                          float* __restrict__ weights_out) {
     constexpr int kThreads = 64 * WAVES, kEach = (kMoeMaxExperts + kThreads - 1) / kThreads;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int pairs = M * topk;
-    if (M == 1) {
-        if (tid < topk) {
-            s.pair_of[tid] = s.at[tid] = (int16_t)tid;
-            s.expert[tid] = (int16_t)ids[tid];
-            s.n[tid] = 1;
-        }
-        __syncthreads();
-        return topk;
-    }
-    for (int e = tid; e < E; e += kThreads) by.tokens[e] = 0;
-    __syncthreads();
-    for (int p = tid; p < pairs; p += kThreads) atomicOr(&by.tokens[ids[p]], 1ull << (p / topk));
-    __syncthreads();
-    // a thread's kEach experts: their pairs and passes, and those before them
-    int n[kEach], a = 0, b = 0;
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-        const int e = tid * kEach + i;
-        n[i] = e < E ? __popcll(by.tokens[e]) : 0;
-        a += n[i];
-        b += (n[i] + TOK - 1) / TOK;
-    }
-    const int own_a = a, own_b = b;
-#pragma unroll
-    for (int o = 1; o < 64; o *= 2) {
-        const int pa = __shfl_up(a, o), pb = __shfl_up(b, o);
-        if (lane >= o) {
-            a += pa;
-            b += pb;
-        }
-    }
-    if (lane == 63) {
-        s.scan[0][wave] = a;
-        s.scan[1][wave] = b;
-    }
-    __syncthreads();
-    a -= own_a;
-    b -= own_b;
-    int passes = 0;
-#pragma unroll
-    for (int i = 0; i < WAVES; ++i) {
-        if (i < wave) {
-            a += s.scan[0][i];
-            b += s.scan[1][i];
-        }
-        passes += s.scan[1][i];
-    }
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-        if (n[i] > 0) by.pairs_at[tid * kEach + i] = (int16_t)a;
-        for (int q = 0; q < n[i]; q += TOK) {
-            s.expert[b] = (int16_t)(tid * kEach + i);
-            s.at[b] = (int16_t)(a + q);
-            s.n[b] = (int16_t)(n[i] - q < TOK ? n[i] - q : TOK);
-            ++b;
-        }
-        a += n[i];
-    }
-    __syncthreads();
     for (int p = tid; p < pairs; p += kThreads) {
-        const int e = ids[p];
-        s.pair_of[by.pairs_at[e] + __popcll(by.tokens[e] & ((1ull << (p / topk)) - 1))] = (int16_t)p;
+        by.expert[p] = (int16_t)ids[p];
+        by.top[p] = top[p];
     }
-    __syncthreads();
-    return __builtin_amdgcn_readfirstlane(passes);
-}
-
-// The pairs' weights: the softmax's numerators over the tokens' denominators;
-// one block writes the choice out.
-template <int WAVES>
-__device__ __forceinline__ void moe_weights(Passes& s, int M, int E, int topk, int norm,
-                                            const double* __restrict__ logits, const int32_t* __restrict__ ids,
-                                            bool write, int32_t* __restrict__ ids_out,
-                                            float* __restrict__ weights_out) {
-    constexpr int kThreads = 64 * WAVES;
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int pairs = M * topk;
-    for (int p = tid; p < pairs; p += kThreads) {
-        const double* of = logits + (size_t)(p / topk) * E;
-        s.c[p] = expf((float)(of[ids[p]] - of[ids[p / topk * topk]]));
-    }
+    if (M > 1)
+        for (int e = tid; e < E; e += kThreads) by.tokens[e] = 0;
     if (!norm) {
         for (int m = wave; m < M; m += WAVES) {
             const double* of = logits + (size_t)m * E;
-            const double top = of[ids[m * topk]];
+            const double most = top[m * topk];
             float v = 0.0f;
-            for (int j = lane; j < E; j += 64) v += expf((float)(of[j] - top));
+#pragma unroll 4
+            for (int j = lane; j < E; j += 64) v += expf((float)(of[j] - most));
 #pragma unroll
             for (int o = 1; o < 64; o *= 2) v += __shfl_xor(v, o);
             if (lane == 0) s.total[m] = v;
+        }
+    }
+    __syncthreads();
+    for (int p = tid; p < pairs; p += kThreads) {
+        const int m = p / topk;
+        s.c[p] = expf((float)(by.top[p] - by.top[m * topk]));
+        if (M > 1) {
+            atomicOr(&by.tokens[by.expert[p]], 1ull << m);
+        } else {
+            s.pair_of[p] = s.at[p] = (int16_t)p;
+            s.expert[p] = by.expert[p];
+            s.n[p] = 1;
         }
     }
     __syncthreads();
@@ -511,16 +523,67 @@ __device__ __forceinline__ void moe_weights(Passes& s, int M, int E, int topk, i
         for (int r = 0; r < topk; ++r) v += s.c[tid * topk + r];
         s.total[tid] = v;
     }
-    __syncthreads();
-    for (int p = tid; p < pairs; p += kThreads) {
-        const float c = s.c[p] / s.total[p / topk];
-        s.c[p] = c;
-        if (write) {
-            if (ids_out) ids_out[p] = ids[p];
-            if (weights_out) weights_out[p] = c;
+    int passes = topk;
+    if (M > 1) {
+        // a thread's kEach experts: their pairs and passes, and those before them
+        int n[kEach], a = 0, b = 0;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            const int e = tid * kEach + i;
+            n[i] = e < E ? __popcll(by.tokens[e]) : 0;
+            a += n[i];
+            b += (n[i] + TOK - 1) / TOK;
+        }
+        const int own_a = a, own_b = b;
+#pragma unroll
+        for (int o = 1; o < 64; o *= 2) {
+            const int pa = __shfl_up(a, o), pb = __shfl_up(b, o);
+            if (lane >= o) {
+                a += pa;
+                b += pb;
+            }
+        }
+        if (lane == 63) {
+            s.scan[0][wave] = a;
+            s.scan[1][wave] = b;
+        }
+        __syncthreads();
+        a -= own_a;
+        b -= own_b;
+        passes = 0;
+#pragma unroll
+        for (int i = 0; i < WAVES; ++i) {
+            if (i < wave) {
+                a += s.scan[0][i];
+                b += s.scan[1][i];
+            }
+            passes += s.scan[1][i];
+        }
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            if (n[i] > 0) by.pairs_at[tid * kEach + i] = (int16_t)a;
+            for (int q = 0; q < n[i]; q += TOK) {
+                s.expert[b] = (int16_t)(tid * kEach + i);
+                s.at[b] = (int16_t)(a + q);
+                s.n[b] = (int16_t)(n[i] - q < TOK ? n[i] - q : TOK);
+                ++b;
+            }
+            a += n[i];
         }
     }
     __syncthreads();
+    for (int p = tid; p < pairs; p += kThreads) {
+        const int m = p / topk, e = by.expert[p];
+        const float c = s.c[p] / s.total[m];
+        s.c[p] = c;
+        if (write) {
+            if (ids_out) ids_out[p] = e;
+            if (weights_out) weights_out[p] = c;
+        }
+        if (M > 1) s.pair_of[by.pairs_at[e] + __popcll(by.tokens[e] & ((1ull << m) - 1))] = (int16_t)p;
+    }
+    __syncthreads();
+    return __builtin_amdgcn_readfirstlane(passes);
 }
 
 // A pass's sums (operand rows 16 mt + ..) times c into the wave's rows [M][16].
@@ -580,7 +643,8 @@ __device__ __forceinline__ void moe_finish(Passes& s, int M, int N, uint32_t* ar
 template <class T, int GPU, bool ZP>
 __global__ __launch_bounds__(64 * kDownWaves, 4) void k_moe_down(
     const uint16_t* __restrict__ h, int M, int F, int N, const uint8_t* __restrict__ wd, int E, int topk, int norm,
-    const double* __restrict__ logits, const int32_t* __restrict__ ids, uint32_t* __restrict__ arrived,
+    const double* __restrict__ logits, const int32_t* __restrict__ ids, const double* __restrict__ top,
+    uint32_t* __restrict__ arrived,
     float* __restrict__ parts, uint16_t* __restrict__ y, int32_t* __restrict__ ids_out,
     float* __restrict__ weights_out) {
     // one tile of 16 columns a block, the items shared out to its waves, each
@@ -592,7 +656,8 @@ __global__ __launch_bounds__(64 * kDownWaves, 4) void k_moe_down(
     static_assert(sizeof(ByExpert) <= sizeof(rows_lds), "the rows' place holds it");
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     for (int i = tid; i < kDownWaves * M * 16; i += kThreads) sums[i] = 0.0f;
-    const int passes = moe_passes<kDownWaves, 8>(s, *reinterpret_cast<ByExpert*>(rows_lds), M, E, topk, ids);
+    const int passes = moe_passes<kDownWaves, 8>(s, *reinterpret_cast<ByExpert*>(rows_lds), M, E, topk, norm, logits, ids,
+                                                 top, blockIdx.x == 0 && blockIdx.y == 0, ids_out, weights_out);
 
     const W4gLayout l = w4g_layout(128 / GPU, ZP, N, F);
     const int tile = blockIdx.x, split = blockIdx.y, splits = gridDim.y;
@@ -626,8 +691,6 @@ __global__ __launch_bounds__(64 * kDownWaves, 4) void k_moe_down(
         turn();
         load();
     }
-    // while the first loads are under way
-    moe_weights<kDownWaves>(s, M, E, topk, norm, logits, ids, tile == 0 && split == 0, ids_out, weights_out);
 
     f32x4 acc[1][1] = {{f32x4{0, 0, 0, 0}}};
     for (int i = begin; i < end; ++i) {
@@ -665,7 +728,8 @@ __global__ __launch_bounds__(64 * kDownWaves, 4) void k_moe_down(
 template <class T, int GPU, bool ZP>
 __global__ __launch_bounds__(64 * kManyN * kManyG, 4) void k_moe_down_many(
     const uint16_t* __restrict__ h, int M, int F, int N, const uint8_t* __restrict__ wd, int E, int topk, int norm,
-    const double* __restrict__ logits, const int32_t* __restrict__ ids, uint32_t* __restrict__ arrived,
+    const double* __restrict__ logits, const int32_t* __restrict__ ids, const double* __restrict__ top,
+    uint32_t* __restrict__ arrived,
     float* __restrict__ parts, uint16_t* __restrict__ y, int32_t* __restrict__ ids_out,
     float* __restrict__ weights_out) {
     constexpr int kWaves = kManyN * kManyG, kThreads = 64 * kWaves, MT = 2, kStage = kManyG * MT * 4096;
@@ -675,7 +739,8 @@ __global__ __launch_bounds__(64 * kManyN * kManyG, 4) void k_moe_down_many(
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int group = wave / kManyN, wn = wave % kManyN;
     for (int i = tid; i < kWaves * M * 16; i += kThreads) sums[i] = 0.0f;
-    const int passes = moe_passes<kWaves, 8 * MT>(s, *reinterpret_cast<ByExpert*>(rows_lds), M, E, topk, ids);
+    const int passes = moe_passes<kWaves, 8 * MT>(s, *reinterpret_cast<ByExpert*>(rows_lds), M, E, topk, norm, logits, ids,
+                                                  top, blockIdx.x == 0 && blockIdx.y == 0, ids_out, weights_out);
 
     const W4gLayout l = w4g_layout(128 / GPU, ZP, N, F);
     const int tile = blockIdx.x * kManyN + wn, mine = tile < l.tiles ? tile : l.tiles - 1;
@@ -709,7 +774,6 @@ __global__ __launch_bounds__(64 * kManyN * kManyG, 4) void k_moe_down_many(
         turn();
         load(0);
     }
-    moe_weights<kWaves>(s, M, E, topk, norm, logits, ids, blockIdx.x == 0 && split == 0, ids_out, weights_out);
 
     f32x4 acc[MT][1];
 #pragma unroll
@@ -762,6 +826,7 @@ hipError_t moe_t(const MoeArgs& a, const MoeWs& l, int M, const uint16_t* x, uin
     double* logits = reinterpret_cast<double*>(ws + l.logits);
     int32_t* ids_ws = reinterpret_cast<int32_t*>(ws + l.ids);
     uint16_t* h = reinterpret_cast<uint16_t*>(ws + l.h);
+    double* top = reinterpret_cast<double*>(ws + l.top);
     static std::atomic<uint64_t> done{0};
     static_assert(kDownWaves == kManyN * kManyG, "either kernel's waves");
     const auto down = M <= kFewTokens ? k_moe_down<T, GPU, ZP> : k_moe_down_many<T, GPU, ZP>;
@@ -783,12 +848,12 @@ hipError_t moe_t(const MoeArgs& a, const MoeWs& l, int M, const uint16_t* x, uin
     const int per = kUpWaves / ks;
     if (M > kFewTokens)
         k_moe_gate_up_many<T, GPU, ZP><<<dim3((tiles + kManyWaves - 1) / kManyWaves, rows), 64 * kManyWaves, 0, st>>>(
-            x, M, a.K, a.F, a.wg, a.wu, a.E, a.topk, by_pair, logits, ids_ws, h);
+            x, M, a.K, a.F, a.wg, a.wu, a.E, a.topk, by_pair, logits, ids_ws, top, h);
     else
         k_moe_gate_up<T, GPU, ZP><<<dim3((tiles + per - 1) / per, rows), 64 * kUpWaves, 0, st>>>(
-        x, M, a.K, a.F, a.wg, a.wu, a.E, a.topk, by_pair, ks, logits, ids_ws, h);
+        x, M, a.K, a.F, a.wg, a.wu, a.E, a.topk, by_pair, ks, logits, ids_ws, top, h);
     down<<<dim3(grid.columns, grid.splits), 64 * kDownWaves, kDownWaves * M * 64, st>>>(
-        h, M, a.F, a.K, a.wd, a.E, a.topk, a.norm, logits, ids_ws, arrived, parts, y, ids, weights);
+        h, M, a.F, a.K, a.wd, a.E, a.topk, a.norm, logits, ids_ws, top, arrived, parts, y, ids, weights);
     return hipGetLastError();
 }
 
