@@ -122,58 +122,45 @@ __device__ __forceinline__ u64 order_key(double v) {
 constexpr int kUpWaves = 8;
 
 struct Choice {
+    int16_t above[8][kMoeMaxExperts];        // by wave and expert: the logits above its own in the wave's share
     int16_t rank_of[kChunk], list[kChunk];   // of the block's expert: rank by token (-1: not chosen), tokens
-    int chosen;
+    int found, chosen;
 };
-// The largest of the wave's values, by DPP steps (row shifts by 1, 2, 4, 8,
-// then the rows' last lanes broadcast) that end in lane 63.
-__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
-#define CR_MAX_STEP(ctrl, rows)                                                                                        \
-    {                                                                                                                  \
-        const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, ctrl, rows, 0xF, false);              \
-        v = o > v ? o : v;                                                                                             \
-    }
-    CR_MAX_STEP(0x111, 0xF)
-    CR_MAX_STEP(0x112, 0xF)
-    CR_MAX_STEP(0x114, 0xF)
-    CR_MAX_STEP(0x118, 0xF)
-    CR_MAX_STEP(0x142, 0xA)
-    CR_MAX_STEP(0x143, 0xC)
-#undef CR_MAX_STEP
-    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
-}
-// The expert of rank `want` in a row of logits: `want` + 1 times the largest
-// key, equal ones by index, taken out.  Every wave does it for itself: 0.1 us
-// a rank, with no LDS and no barrier, where counting for every expert the
-// logits above it (E^2 comparisons through LDS) took 3 us of 128 experts.
-template <int EACH>   // E <= 64 EACH
-__device__ __forceinline__ int moe_of_rank(const double* __restrict__ row, int E, int want) {
-    const int lane = threadIdx.x & 63;
+// The expert of rank `want` in a row of up to 64 EACH logits: each wave counts, for
+// every expert, which of its share of the row lie above it; the share comes
+// by uniform loads, so that a comparison takes a scalar operand and LDS only
+// the counts.  (The largest taken out `want` + 1 times by wave-wide maxima
+// costs 0.5 us a rank; counting by reads of LDS 3 us at 128 experts.)
+template <int WAVES, int EACH>
+__device__ __forceinline__ int moe_of_rank(Choice& c, const double* __restrict__ row, int E, int want) {
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int share = (E + WAVES - 1) / WAVES, j0 = wave * share, j1 = j0 + share < E ? j0 + share : E;
     u64 key[EACH];
+    int n[EACH];
 #pragma unroll
     for (int i = 0; i < EACH; ++i) {
         const int e = i * 64 + lane;
-        const double v = row[e < E ? e : E - 1];
-        key[i] = e < E ? order_key(v) : 0;   // 0 is below every value's key (-inf's is 0x000F..F)
+        key[i] = order_key(row[e < E ? e : E - 1]);
+        n[i] = 0;
     }
-    int at = 0;
-    for (int r = 0; r <= want; ++r) {
-        u64 best = key[0];
-        int mine = lane;
+#pragma unroll 2
+    for (int j = j0; j < j1; ++j) {
+        const u64 k = order_key(row[j]);
 #pragma unroll
-        for (int i = 1; i < EACH; ++i)
-            if (key[i] > best) {   // equal: the earlier one
-                best = key[i];
-                mine = i * 64 + lane;
-            }
-        const uint32_t hi = wave_max((uint32_t)(best >> 32));
-        const uint32_t lo = wave_max((uint32_t)(best >> 32) == hi ? (uint32_t)best : 0u);
-        const bool is = best == (((u64)hi << 32) | lo);
-        at = (int)~wave_max(is ? ~(uint32_t)mine : 0u);
-#pragma unroll
-        for (int i = 0; i < EACH; ++i) key[i] = at == i * 64 + lane ? 0 : key[i];
+        for (int i = 0; i < EACH; ++i) n[i] += k > key[i] || (k == key[i] && j < i * 64 + lane);
     }
-    return at;
+#pragma unroll
+    for (int i = 0; i < EACH; ++i)
+        if (i * 64 + lane < E) c.above[wave][i * 64 + lane] = (int16_t)n[i];
+    __syncthreads();
+    for (int e = tid; e < E; e += 64 * WAVES) {
+        int all = 0;
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) all += c.above[w][e];
+        if (all == want) c.found = e;   // ranks are a permutation: one thread
+    }
+    __syncthreads();
+    return __builtin_amdgcn_readfirstlane(c.found);
 }
 
 // The block's expert and its tokens (c.list, c.rank_of); returns their number,
@@ -190,8 +177,9 @@ __device__ __forceinline__ int moe_choice(Choice& c, int M, int E, int topk, int
         first = blockIdx.y / topk;
         const int want = blockIdx.y - first * topk;
         const double* row = logits + (size_t)first * E;
-        e = E <= 128 ? moe_of_rank<2>(row, E, want) : E <= 256 ? moe_of_rank<4>(row, E, want)
-                                                               : moe_of_rank<kMoeMaxExperts / 64>(row, E, want);
+        e = E <= 128 ? moe_of_rank<WAVES, 2>(c, row, E, want)
+                     : E <= 256 ? moe_of_rank<WAVES, 4>(c, row, E, want)
+                                : moe_of_rank<WAVES, kMoeMaxExperts / 64>(c, row, E, want);
         if (M == 1) {
             if (tid == 0) {
                 c.rank_of[0] = (int16_t)want;
@@ -206,8 +194,8 @@ __device__ __forceinline__ int moe_choice(Choice& c, int M, int E, int topk, int
         }
     }
     // the rank of e in every row: the logits above its own, counted by a wave,
-    // two rows and 256 logits under way at a time
-    constexpr int kRows = 2, kCols = 4;
+    // four rows and 128 logits under way at a time
+    constexpr int kRows = 4, kCols = 2;
     for (int m0 = wave; m0 < M; m0 += WAVES * kRows) {
         u64 mine[kRows];
         int n[kRows];
@@ -269,7 +257,7 @@ template <class T, int GPU, bool ZP>
 __global__ __launch_bounds__(64 * kUpWaves, 4) void k_moe_gate_up(const uint16_t* __restrict__ x, int M, int K, int F,
                                                                const uint8_t* __restrict__ wg,
                                                                const uint8_t* __restrict__ wu, int E, int topk,
-                                                               int by_pair, int ks,
+                                                               int by_pair, int ks_log2,
                                                                const double* __restrict__ logits,
                                                                int32_t* __restrict__ ids, double* __restrict__ top,
                                                                uint16_t* __restrict__ h) {
@@ -286,7 +274,8 @@ __global__ __launch_bounds__(64 * kUpWaves, 4) void k_moe_gate_up(const uint16_t
     wg += (size_t)e * l.total;
     wu += (size_t)e * l.total;
     const v4i xb = w4g_rows(x, M, K);
-    const int part_k = wave % ks, tile = blockIdx.x * (kUpWaves / ks) + wave / ks;
+    const int ks = 1 << ks_log2, part_k = wave & (ks - 1);
+    const int tile = blockIdx.x * (kUpWaves >> ks_log2) + (wave >> ks_log2);
     const bool work = tile < l.tiles;
     const char* my_rows = rows_lds[wave];
     const uint32_t my_lds = lds_address(my_rows);
@@ -298,11 +287,11 @@ __global__ __launch_bounds__(64 * kUpWaves, 4) void k_moe_gate_up(const uint16_t
             const int m = 4 * j + (lane >> 4);
             row[j] = (uint32_t)c.list[p0 + (m < n ? m : n - 1)] * (2u * K);
         }
-        f32x4 acc[1][2] = {{f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}}};
-        W4gUnit<GPU> next[2];
+        f32x4 acc[2][1][1] = {{{f32x4{0, 0, 0, 0}}}, {{f32x4{0, 0, 0, 0}}}};   // gate, up
+        W4gUnit<GPU> next[2][1];
         auto load = [&](int u) {
-            next[0] = w4g_load<GPU, ZP>(wg, l, (size_t)tile * l.units + u, lane);
-            next[1] = w4g_load<GPU, ZP>(wu, l, (size_t)tile * l.units + u, lane);
+            next[0][0] = w4g_load<GPU, ZP>(wg, l, (size_t)tile * l.units + u, lane);
+            next[1][0] = w4g_load<GPU, ZP>(wu, l, (size_t)tile * l.units + u, lane);
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 if (j < fills) w4g_x_to_lds(xb, row[j] + w4g_chunk(4 * j, u, K, lane), my_lds + j * 1024);
@@ -311,14 +300,19 @@ __global__ __launch_bounds__(64 * kUpWaves, 4) void k_moe_gate_up(const uint16_t
             load(part_k);
             for (int u = part_k; u < l.units; u += ks) {
                 w4g_wait();
-                const W4gUnit<GPU> w[2] = {next[0], next[1]};
+                const W4gUnit<GPU> w[2][1] = {{next[0][0]}, {next[1][0]}};
                 u32x4 a[GPU][1][4 / GPU];
 #pragma unroll
                 for (int d = 0; d < 4; ++d) a[d / (4 / GPU)][0][d % (4 / GPU)] = w4g_operand_rows(my_rows, d, lane);
                 w4g_wait_lds();
                 if (u + ks < l.units) load(u + ks);
+                // one weight's products after the other's: fewer registers
 #pragma unroll
-                for (int g = 0; g < GPU; ++g) w4g_mac<T, GPU, ZP, 1, 2>(g, w, a[g], acc);
+                for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                    for (int g = 0; g < GPU; ++g) w4g_mac<T, GPU, ZP, 1, 1>(g, w[i], a[g], acc[i]);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
             }
         }
         auto store = [&](int m, int n, float g, float u) {
@@ -330,16 +324,17 @@ __global__ __launch_bounds__(64 * kUpWaves, 4) void k_moe_gate_up(const uint16_t
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int m = (lane >> 4) * 4 + i;
-                    if (p0 + m < n_tok) store(m, tile * 16 + (lane & 15), acc[0][0][i], acc[0][1][i]);
+                    if (p0 + m < n_tok) store(m, tile * 16 + (lane & 15), acc[0][0][0][i], acc[1][0][0][i]);
                 }
             }
             continue;
         }
-        part[wave][0][lane] = acc[0][0];
-        part[wave][1][lane] = acc[0][1];
+        part[wave][0][lane] = acc[0][0][0];
+        part[wave][1][lane] = acc[1][0][0];
         __syncthreads();
-        for (int i = tid; i < 256 * (kUpWaves / ks); i += kThreads) {
-            const int m = (i >> 4) & 15, n = i & 15, w0 = (i >> 8) * ks, t = blockIdx.x * (kUpWaves / ks) + (i >> 8);
+        for (int i = tid; i < 256 * (kUpWaves >> ks_log2); i += kThreads) {
+            const int m = (i >> 4) & 15, n = i & 15, w0 = (i >> 8) << ks_log2;
+            const int t = blockIdx.x * (kUpWaves >> ks_log2) + (i >> 8);
             if (p0 + m >= n_tok || t >= l.tiles) continue;
             float g = 0.0f, u = 0.0f;
             for (int wv = w0; wv < w0 + ks; ++wv) {
@@ -843,15 +838,15 @@ hipError_t moe_t(const MoeArgs& a, const MoeWs& l, int M, const uint16_t* x, uin
     // a wave per tile where the chosen experts' tiles fill the chip's 4096
     // wave slots half, else as many waves on a tile's K as bring them there
     const int tiles = a.F / 16;
-    int ks = 1;
-    while (ks < kUpWaves && (long)rows * tiles * ks < 2048) ks *= 2;
-    const int per = kUpWaves / ks;
+    int ks_log2 = 0;
+    while ((1 << ks_log2) < kUpWaves && ((long)rows * tiles << ks_log2) < 2048) ++ks_log2;
+    const int per = kUpWaves >> ks_log2;
     if (M > kFewTokens)
         k_moe_gate_up_many<T, GPU, ZP><<<dim3((tiles + kManyWaves - 1) / kManyWaves, rows), 64 * kManyWaves, 0, st>>>(
             x, M, a.K, a.F, a.wg, a.wu, a.E, a.topk, by_pair, logits, ids_ws, top, h);
     else
         k_moe_gate_up<T, GPU, ZP><<<dim3((tiles + per - 1) / per, rows), 64 * kUpWaves, 0, st>>>(
-        x, M, a.K, a.F, a.wg, a.wu, a.E, a.topk, by_pair, ks, logits, ids_ws, top, h);
+        x, M, a.K, a.F, a.wg, a.wu, a.E, a.topk, by_pair, ks_log2, logits, ids_ws, top, h);
     down<<<dim3(grid.columns, grid.splits), 64 * kDownWaves, kDownWaves * M * 64, st>>>(
         h, M, a.F, a.K, a.wd, a.E, a.topk, a.norm, logits, ids_ws, top, arrived, parts, y, ids, weights);
     return hipGetLastError();
