@@ -7,8 +7,23 @@ namespace {
 // ---------------------------------------------------------------------------
 // Encoder.  Groups never cross a row (g divides K), so the weight is one
 // flat run of groups; g / 8 neighbouring lanes hold a group, 8 values each.
-// Bound by HBM: 2 B in, 0.5 B of codes and 2/g (3/g) B of scales out per value.
+// Bound by HBM: 2 B in, 0.5 B of codes and 2/g (3/g) B of scales out per value,
+// once the divisions are cheap: an IEEE division for each value took 66 us
+// for 100 M values in groups of 32 with zero points, this 53 to 57.
+//
+// rint(fl(v / s)) without the division: r = v fl(1/s) is within 2 steps of
+// v / s, and r + (v - r s) fl(1/s), the residue exact in an fma, is v / s
+// wherever that is a float32 (so ties stay ties) and within a step of it
+// otherwise.  That cannot pass a tie: v and s have at most 11 bits and a tie
+// k + 1/2 at most 5, so v and s (k + 1/2), where they differ, do so by more
+// than 2^-18 of themselves.  Scales whose reciprocal leaves float32's normal
+// range take the division.
 // ---------------------------------------------------------------------------
+__device__ __forceinline__ float quotient(float v, float s, float inv) {
+    const float r = v * inv;
+    return __builtin_fmaf(__builtin_fmaf(-r, s, v), inv, r);
+}
+
 template <class T, int G, bool ZP>
 __global__ __launch_bounds__(256) void k_w4g_encode(const uint16_t* __restrict__ w, size_t chunks,
                                                     uint32_t* __restrict__ codes, uint16_t* __restrict__ scales,
@@ -29,21 +44,40 @@ __global__ __launch_bounds__(256) void k_w4g_encode(const uint16_t* __restrict__
         lo = fminf(lo, v[i]);
         hi = fmaxf(hi, v[i]);
     }
-#pragma unroll
-    for (int m = 1; m < G / 8; m *= 2) {
-        lo = fminf(lo, __shfl_xor(lo, m));
-        hi = fmaxf(hi, __shfl_xor(hi, m));
+    lo = fminf(lo, lane_xor<1>(lo));
+    hi = fmaxf(hi, lane_xor<1>(hi));
+    lo = fminf(lo, lane_xor<2>(lo));
+    hi = fmaxf(hi, lane_xor<2>(hi));
+    if constexpr (G >= 64) {
+        lo = fminf(lo, lane_xor<4>(lo));
+        hi = fmaxf(hi, lane_xor<4>(hi));
+    }
+    if constexpr (G >= 128) {
+        lo = fminf(lo, lane_xor<8>(lo));
+        hi = fmaxf(hi, lane_xor<8>(hi));
     }
     const uint16_t s16 = T::from_f32(ZP ? (hi - lo) / 15.0f : fmaxf(hi, -lo) / 7.0f);
     const float s = T::to_f32(s16);
-    const float z = ZP && s > 0.0f ? fminf(fmaxf(rintf(-lo / s), 0.0f), 15.0f) : 0.0f;
+    float z = 0.0f, q[8];
+    if (s > 0x1p-100f && s < 0x1p100f) {
+        const float inv = 1.0f / s;
+        if constexpr (ZP) z = fminf(fmaxf(rintf(quotient(-lo, s, inv)), 0.0f), 15.0f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[i] = rintf(quotient(v[i], s, inv));
+    } else if (s > 0.0f) {
+        if constexpr (ZP) z = fminf(fmaxf(rintf(-lo / s), 0.0f), 15.0f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[i] = rintf(v[i] / s);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[i] = 0.0f;
+    }
     uint32_t out = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        float q;
-        if constexpr (ZP) q = s > 0.0f ? fminf(fmaxf(rintf(v[i] / s) + z, 0.0f), 15.0f) : 0.0f;
-        else q = s > 0.0f ? fminf(fmaxf(rintf(v[i] / s), -8.0f), 7.0f) + 8.0f : 8.0f;
-        out |= (uint32_t)q << (4 * i);
+        if constexpr (ZP) q[i] = fminf(fmaxf(q[i] + z, 0.0f), 15.0f);
+        else q[i] = fminf(fmaxf(q[i], -8.0f), 7.0f) + 8.0f;
+        out |= (uint32_t)q[i] << (4 * i);
     }
     if (!in) return;
     codes[c] = out;
