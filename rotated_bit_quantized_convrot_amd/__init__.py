@@ -537,10 +537,23 @@ _stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", _stream_of)
 def _call_on(device, fn, *args):
     """fn(*args, stream) with ``device`` current and on its current stream,
     whichever device is current outside."""
-    if device.index == torch.cuda.current_device():
-        return _check(fn(*args, _stream_of(device.index)))
-    with torch.cuda.device(device):
-        return _check(fn(*args, _stream_of(device.index)))
+    index = device.index
+    if index == torch.cuda.current_device():
+        status = fn(*args, _stream_of(index))
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, _stream_of(index))
+    if status:
+        _check(status)
+
+
+def _here(t: torch.Tensor, name: str, dtype, device):
+    """t is a contiguous tensor of this type on this device (one check of the
+    usual case: a call's host time is part of a token's)."""
+    if t.dtype is dtype and t.device == device and t.is_contiguous():
+        return
+    _dev(t, name, dtype)
+    raise ValueError(f"{name} is on {t.device}, expected {device}")
 
 
 @functools.lru_cache(maxsize=4096)
@@ -602,11 +615,11 @@ def pack_weight_w4g(codes: torch.Tensor, scales: torch.Tensor, zeros: Optional[t
     return out if codes.dim() == 3 else out[0]
 
 
-def _check_w4g(packed, name: str, count: int, N: int, K: int, group: int, zeros: bool):
+def _check_w4g(packed, name: str, device, count: int, N: int, K: int, group: int, zeros: bool):
     """Refuse packed weights smaller than their layout (the kernels would
     read past their end); sizes the library rejects give 0 bytes here and are
     left to its own error."""
-    _dev(packed, name, torch.uint8)
+    _here(packed, name, torch.uint8, device)
     need = count * w4g_packed_bytes(group, zeros, N, K)
     if packed.numel() < need:
         raise ValueError(f"{name} has {packed.numel()} bytes, {count} x N={N} K={K} group={group} needs {need}")
@@ -621,20 +634,20 @@ def linear_w4g(x, packed, N, group, zeros=False, bias=None, out=None):
     if x.dim() != 2:
         raise ValueError("x must be [M, K]")
     M, K = x.shape
-    _check_w4g(packed, "packed", 1, N, K, group, zeros)
+    device = x.device
+    _check_w4g(packed, "packed", device, 1, N, K, group, zeros)
     if bias is not None:
-        _dev(bias, "bias", x.dtype)
+        _here(bias, "bias", x.dtype, device)
         if bias.numel() != N:
             raise ValueError("bias must have N elements")
     if out is None:
-        out = x.new_empty((M, max(N, 0)))
+        out = x.new_empty((M, N if N > 0 else 0))
     else:
-        _dev(out, "out", x.dtype)
-        if tuple(out.shape) != (M, N):
+        _here(out, "out", x.dtype, device)
+        if out.shape != (M, N):
             raise ValueError("out must be [M, N]")
-    _same_device(x, packed=packed, bias=bias, out=out)
-    _call_on(x.device, lib().cr_linear_w4g, code, _ptr(x), M, K, _ptr(packed), group, int(zeros), N, _ptr(bias),
-             _ptr(out))
+    _call_on(device, lib().cr_linear_w4g, code, x.data_ptr(), M, K, packed.data_ptr(), group, bool(zeros), N,
+             None if bias is None else bias.data_ptr(), out.data_ptr())
     return out
 
 
@@ -656,31 +669,34 @@ def moe_w4g(x, router, gate, up, down, F, group, topk, zeros=False, norm=True, o
     index) and their weights (float32 [M, topk])."""
     code = _dtype16(x, "x")
     _dev(x, "x")
-    _dev(router, "router", x.dtype)
+    device = x.device
+    _here(router, "router", x.dtype, device)
     if x.dim() != 2 or router.dim() != 2 or router.shape[1] != x.shape[1]:
         raise ValueError("x must be [M, K] and router [E, K]")
     M, K = x.shape
     E = router.shape[0]
-    for t, name, n, k in ((gate, "gate", F, K), (up, "up", F, K), (down, "down", K, F)):
-        _check_w4g(t, name, E, n, k, group, zeros)
+    _check_w4g(gate, "gate", device, E, F, K, group, zeros)
+    _check_w4g(up, "up", device, E, F, K, group, zeros)
+    _check_w4g(down, "down", device, E, K, F, group, zeros)
     if out is None:
         out = torch.empty_like(x)
     else:
-        _dev(out, "out", x.dtype)
+        _here(out, "out", x.dtype, device)
         if out.shape != x.shape:
             raise ValueError("out must be [M, K]")
     ids = weights = None
     if routing:
-        ids = torch.empty((M, max(topk, 0)), dtype=torch.int32, device=x.device)
-        weights = torch.empty((M, max(topk, 0)), dtype=torch.float32, device=x.device)
+        shape = (M, topk if topk > 0 else 0)
+        ids = torch.empty(shape, dtype=torch.int32, device=device)
+        weights = torch.empty(shape, dtype=torch.float32, device=device)
     if workspace is None:
-        workspace = _empty_u8(max(moe_w4g_workspace_bytes(M, K, F, E, topk, group), 256), x.device)
+        need = moe_w4g_workspace_bytes(M, K, F, E, topk, group)
+        workspace = torch.empty(need if need > 256 else 256, dtype=torch.uint8, device=device)
     else:
-        _dev(workspace, "workspace", torch.uint8)
-    _same_device(x, router=router, gate=gate, up=up, down=down, out=out, workspace=workspace)
-    _call_on(x.device, lib().cr_moe_w4g, code, _ptr(x), M, K, _ptr(router), E, topk, int(norm), _ptr(gate), _ptr(up),
-             _ptr(down), F, group, int(zeros), _ptr(out), _ptr(ids), _ptr(weights), _ptr(workspace),
-             workspace.numel())
+        _here(workspace, "workspace", torch.uint8, device)
+    _call_on(device, lib().cr_moe_w4g, code, x.data_ptr(), M, K, router.data_ptr(), E, topk, bool(norm),
+             gate.data_ptr(), up.data_ptr(), down.data_ptr(), F, group, bool(zeros), out.data_ptr(), _ptr(ids),
+             _ptr(weights), workspace.data_ptr(), workspace.numel())
     return (out, ids, weights) if routing else out
 
 
