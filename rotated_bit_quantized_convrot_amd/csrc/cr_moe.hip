@@ -343,8 +343,7 @@ __global__ __launch_bounds__(64 * kUpWaves, 4) void k_moe_gate_up(const uint16_t
 // ---------------------------------------------------------------------------
 // Gate and up, more tokens: the same, but the block's waves own a tile each
 // and go through K together, so that the rows of x are brought once for all
-// of them, UI units at a time; up to 32 tokens at once, in one 16-row operand
-// or two.
+// of them; up to 32 tokens at once, in one 16-row operand or two.
 // ---------------------------------------------------------------------------
 constexpr int kManyWaves = 4;
 template <class T, int GPU, bool ZP>
@@ -353,7 +352,7 @@ __global__ __launch_bounds__(64 * kManyWaves, 4) void k_moe_gate_up_many(
     const uint8_t* __restrict__ wu, int E, int topk, int by_pair, const double* __restrict__ logits,
     int32_t* __restrict__ ids, double* __restrict__ top, uint16_t* __restrict__ h) {
     __shared__ Choice c;
-    constexpr int UI = 1, kStage = UI * 8192;
+    constexpr int kStage = 8192;
     __shared__ __attribute__((aligned(16))) char rows_lds[2 * kStage];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     int e;
@@ -376,47 +375,33 @@ __global__ __launch_bounds__(64 * kManyWaves, 4) void k_moe_gate_up_many(
             const int m = 16 * mt + r0 + (lane >> 4);
             row[mt] = (uint32_t)c.list[p0 + (m < n ? m : n - 1)] * (2u * K);
         }
-        W4gUnit<GPU> next[UI][2];
-        auto load = [&](int u0, int stage) {
+        W4gUnit<GPU> next[2];
+        auto load = [&](int u, int stage) {
 #pragma unroll
-            for (int i = 0; i < UI; ++i) {
-                const int u = u0 + i < l.units ? u0 + i : l.units - 1;
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
-                    if (16 * mt + r0 < n)
-                        w4g_x_to_lds(xb, row[mt] + w4g_chunk(r0, u, K, lane), lds0 + stage * kStage + i * 8192 + mt * 4096 + r0 * 256);
-                next[i][0] = w4g_load<GPU, ZP>(wg, l, (size_t)mine * l.units + u, lane);
-                next[i][1] = w4g_load<GPU, ZP>(wu, l, (size_t)mine * l.units + u, lane);
-            }
+            for (int mt = 0; mt < MT; ++mt)
+                if (16 * mt + r0 < n)
+                    w4g_x_to_lds(xb, row[mt] + w4g_chunk(r0, u, K, lane), lds0 + stage * kStage + mt * 4096 + r0 * 256);
+            next[0] = w4g_load<GPU, ZP>(wg, l, (size_t)mine * l.units + u, lane);
+            next[1] = w4g_load<GPU, ZP>(wu, l, (size_t)mine * l.units + u, lane);
         };
         f32x4 acc[MT][2];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) acc[mt][0] = acc[mt][1] = f32x4{0, 0, 0, 0};
         load(0, 0);
-        for (int u0 = 0, stage = 0; u0 < l.units; u0 += UI, stage ^= 1) {
+        for (int u = 0, stage = 0; u < l.units; ++u, stage ^= 1) {
             w4g_wait();
-            w4g_barrier();   // the units' rows are there, the other stage has been read
-            W4gUnit<GPU> w[UI][2];
+            w4g_barrier();   // the unit's rows are there, the other stage has been read
+            const W4gUnit<GPU> w[2] = {next[0], next[1]};
+            if (u + 1 < l.units) load(u + 1, stage ^ 1);
 #pragma unroll
-            for (int i = 0; i < UI; ++i) {
-                w[i][0] = next[i][0];
-                w[i][1] = next[i][1];
-            }
-            if (u0 + UI < l.units) load(u0 + UI, stage ^ 1);
+            for (int g = 0; g < GPU; ++g) {
+                u32x4 a[MT][4 / GPU];
 #pragma unroll
-            for (int i = 0; i < UI; ++i) {
-                if (u0 + i >= l.units) break;
+                for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-                for (int g = 0; g < GPU; ++g) {
-                    u32x4 a[MT][4 / GPU];
-#pragma unroll
-                    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                        for (int s = 0; s < 4 / GPU; ++s)
-                            a[mt][s] = w4g_operand_rows(rows_lds + stage * kStage + i * 8192 + mt * 4096,
-                                                        g * (4 / GPU) + s, lane);
-                    w4g_mac<T, GPU, ZP, MT, 2>(g, w[i], a, acc);
-                }
+                    for (int s = 0; s < 4 / GPU; ++s)
+                        a[mt][s] = w4g_operand_rows(rows_lds + stage * kStage + mt * 4096, g * (4 / GPU) + s, lane);
+                w4g_mac<T, GPU, ZP, MT, 2>(g, w, a, acc);
             }
         }
         w4g_barrier();   // before the next tokens' rows come into the first stage

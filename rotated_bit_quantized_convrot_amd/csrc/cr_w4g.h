@@ -242,7 +242,9 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
 // Every load of this wave has arrived / has been read from LDS.
 __device__ __forceinline__ void w4g_wait() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 __device__ __forceinline__ void w4g_wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
-__device__ __forceinline__ void w4g_barrier() { asm volatile("s_barrier" ::: "memory"); }
+// After it every wave of the block has read what it asked LDS for: loads that
+// go there may follow.
+__device__ __forceinline__ void w4g_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
 // Operand rows through LDS: rows of 256 bytes (the 128 k of a unit), 16-byte
 // chunk c of row r at slot c ^ (r % 16), so that the 16 rows of an operand

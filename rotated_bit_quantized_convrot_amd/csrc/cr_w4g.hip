@@ -210,6 +210,7 @@ __global__ __launch_bounds__(64 * WM * WN * KG) void k_w4g_linear(const uint16_t
         w4g_wait();
         // this unit's x is there, and the other stage has been read by all
         if constexpr (WM * WN > 1) w4g_barrier();
+        else w4g_wait_lds();
         W4gUnit<GPU> next[NT];
         if (it + 1 < iters) {
             weights(u + KG, next);
