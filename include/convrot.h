@@ -357,8 +357,8 @@ cr_status cr_pack_weight_w4g(const void* codes, const void* scales, const void* 
                              int group, void* w_packed, hipStream_t stream);
 
 /* y[m,n] = T(sum_k x[m,k] W[n,k] + bias[n]); x [M,K], y [M,N], bias [N] or
- * NULL; group and zeros as the weight was packed.  No workspace.  M = 0 is a
- * no-op. */
+ * NULL; group and zeros as the weight was packed.  No workspace.  y must not
+ * overlap x (CR_ERR_SHAPE).  M = 0 is a no-op. */
 cr_status cr_linear_w4g(int dtype, const void* x, int M, int K, const void* w_packed, int group, int zeros, int N,
                         const void* bias, void* y, hipStream_t stream);
 
@@ -369,14 +369,18 @@ cr_status cr_linear_w4g(int dtype, const void* x, int M, int K, const void* w_pa
  *   counts as larger than any number);
  *   p[e] = exp(l[e] - max l), c[r] = p[e_r] / sum of p over the chosen
  *   (norm nonzero) or over all experts;
- *   h[r] = T(c[r] * silu(Wg_e x) * (Wu_e x)), Wg, Wu [F,K]  (e = e_r)
- *   y = T(sum_r Wd_e h[r]), Wd [K,F].
- * h is held in the 16-bit type: it is the operand of the down product, and
- * rounding it costs what rounding y does.
+ *   h[r] = silu(Wg_e x) * (Wu_e x), Wg, Wu [F,K]  (e = e_r)
+ *   y = T(sum_r c[r] * Wd_e h[r]), Wd [K,F].
+ * The down product takes h as the sum of two bf16 values, within 2^-18 of it:
+ * one 16-bit value would cost what rounding y does.
  *   wg/wu/wd_packed  E packed weights each (cr_pack_weight_w4g, count = E)
  *   y [M,K] (out); ids [M,topk] int32 and weights [M,topk] float: the chosen
  *   experts and c (out, each may be NULL)
- *   ws / ws_bytes: at least cr_moe_w4g_workspace_bytes(M,K,F,E,topk,group).
+ *   ws / ws_bytes: at least cr_moe_w4g_workspace_bytes(M,K,F,E,topk,group);
+ *   calls that can run at the same time need a workspace each.  Nothing is
+ *   kept in it from one call to the next.
+ * y may be x, but not overlap it otherwise (CR_ERR_SHAPE).  Every sum has a
+ * fixed order: the same call gives the same bits.
  * K and F must be multiples of group, at most CR_MOE_MAX_DIM.  1 <= E <= CR_MOE_MAX_EXPERTS,
  * 1 <= topk <= min(E, CR_MOE_MAX_TOPK) (CR_ERR_SHAPE). */
 #define CR_MOE_MAX_EXPERTS 1024

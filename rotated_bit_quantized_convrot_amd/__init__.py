@@ -628,7 +628,7 @@ def _check_w4g(packed, name: str, device, count: int, N: int, K: int, group: int
 def linear_w4g(x, packed, N, group, zeros=False, bias=None, out=None):
     """y = x W^T (+ bias) with a weight from :func:`pack_weight_w4g`: x bf16 or
     fp16 [M, K] of the scales' type, y of the same type; ``group`` and
-    ``zeros`` as the weight was packed."""
+    ``zeros`` as the weight was packed; ``out`` must not overlap x."""
     code = _dtype16(x, "x")
     _dev(x, "x")
     if x.dim() != 2:
@@ -666,7 +666,8 @@ def moe_w4g(x, router, gate, up, down, F, group, topk, zeros=False, norm=True, o
     ``norm``: the chosen experts' weights sum to one, otherwise they are the
     softmax over all experts.  Returns y [M, K], with ``routing`` also the
     chosen experts (int32 [M, topk], by descending logit, equal ones by
-    index) and their weights (float32 [M, topk])."""
+    index) and their weights (float32 [M, topk]).  ``out`` may be x; calls
+    that can run at the same time need a ``workspace`` each."""
     code = _dtype16(x, "x")
     _dev(x, "x")
     device = x.device
@@ -803,6 +804,10 @@ def pack_linear(w: torch.Tensor, bias: Optional[torch.Tensor] = None, int8: bool
     weight-only instead, 4-bit with a scale per group of that many k (and
     zero points with ``zeros``); K must be a multiple of it."""
     N, K = w.shape
+    if w4g and (int8 or regular or group != 256):
+        raise ValueError("w4g is a format of its own: no int8, group or regular with it")
+    if zeros and not w4g:
+        raise ValueError("zeros needs w4g")
     if w4g:
         p = pack_weight_w4g(*encode_w4g(w, w4g, zeros))
         return PackedWeight(W4G, N, K, p, None, bias, w4g, zeros, w.dtype)

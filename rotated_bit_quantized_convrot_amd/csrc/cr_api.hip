@@ -358,6 +358,12 @@ cr_status check_w4g_shape(int N, int K, int group) {
     return CR_OK;
 }
 
+// [a, a + na) and [b, b + nb) share bytes.
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+    const uintptr_t p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
+    return p < q + nb && q < p + na;
+}
+
 // Weights one call takes: what a launch's grid covers (2^31 threads of 8).
 constexpr size_t kW4gMaxWeights = (size_t)1 << 34;
 
@@ -798,6 +804,7 @@ cr_status cr_linear_w4g(int dtype, const void* x, int M, int K, const void* w_pa
     if (M == 0) return ok();
     if (!x || !y) return fail(CR_ERR_NULL, "x or y is NULL");
     if (!aligned16(x) || !aligned16(y)) return fail(CR_ERR_ALIGN, "x or y not 16-byte aligned");
+    if (overlap(x, (size_t)M * K * 2, y, (size_t)M * N * 2)) return fail(CR_ERR_SHAPE, "y overlaps x");
     if ((s = check_device()) != CR_OK) return s;
     return launch_err(cr::launch_w4g_linear(dtype == CR_FP16, static_cast<const uint16_t*>(x), M, K,
                                             static_cast<const uint8_t*>(w_packed), group, zeros != 0, N,
@@ -824,6 +831,8 @@ cr_status cr_moe_w4g(int dtype, const void* x, int M, int K, const void* router,
     if (!x || !y || !ws) return fail(CR_ERR_NULL, "x, y or workspace is NULL");
     if (!aligned16(x) || !aligned16(y) || !aligned16(ws) || !aligned16(ids) || !aligned16(weights))
         return fail(CR_ERR_ALIGN, "x, y, ids, weights or workspace not 16-byte aligned");
+    const size_t bytes = (size_t)M * K * 2;
+    if (x != y && overlap(x, bytes, y, bytes)) return fail(CR_ERR_SHAPE, "y overlaps x without being x");
     const size_t need = cr_moe_w4g_workspace_bytes(M, K, F, E, topk, group);
     if (ws_bytes < need) return fail(CR_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", ws_bytes, need);
     if ((s = check_device()) != CR_OK) return s;

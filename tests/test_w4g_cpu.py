@@ -73,6 +73,33 @@ def test_linear_refusals(L):
     assert lin(0, None, 0, 256, P, 128, 0, 64, None, None, None) == OK
 
 
+def test_outputs_over_their_inputs_are_refused(L):
+    def at(a):
+        return ctypes.c_void_p(a)
+    # x is 4 x 256 and y 4 x 64 elements of 2 bytes
+    for y in (4096, 4096 + 2032, 4096 - 496):
+        assert L.cr_linear_w4g(0, at(4096), 4, 256, P, 128, 0, 64, None, at(y), None) == SHAPE
+        assert b"overlaps" in L.cr_last_error()
+    # a mixture of experts may write its rows over x, but over no others
+    need = L.cr_moe_w4g_workspace_bytes(4, 256, 128, 8, 2, 128)
+    for y in (4096 + 512, 4096 - 2032):
+        assert L.cr_moe_w4g(0, at(4096), 4, 256, P, 8, 2, 1, P, P, P, 128, 128, 0, at(y), None, None, P, need,
+                            None) == SHAPE
+    # next to each other they may lie: the next check's turn
+    for y in (4096 + 2048, 4096, 4096 - 2048):
+        assert L.cr_moe_w4g(0, at(4096), 4, 256, P, 8, 2, 1, P, P, P, 128, 128, 0, at(y), None, None, P, need - 1,
+                            None) == WORKSPACE
+
+
+def test_pack_linear_refuses_mixed_formats(host):
+    w = torch.zeros((64, 256), dtype=torch.bfloat16)
+    for k in (dict(int8=True), dict(regular=True), dict(group=64)):
+        with pytest.raises(ValueError, match="of its own"):
+            crp.pack_linear(w, w4g=64, **k)
+    with pytest.raises(ValueError, match="zeros needs"):
+        crp.pack_linear(w, zeros=True)
+
+
 def test_moe_refusals(L):
     need = L.cr_moe_w4g_workspace_bytes(4, 256, 128, 8, 2, 128)
     good = dict(dtype=0, x=P, M=4, K=256, router=P, E=8, topk=2, norm=1, wg=P, wu=P, wd=P, F=128, group=128, zeros=0,
