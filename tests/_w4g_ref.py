@@ -101,7 +101,9 @@ def moe(x, router, gate, up, down, topk, norm):
         steps += 2 * (Wd.shape[1] // group)
         err[m] += dh @ np.abs(Wd).T + F32 * (group + 8 + 2 * (Wd.shape[1] // group)) * ((np.abs(h) + dh) @ Bd.T)
     err += F32 * 2 * topk * np.abs(y)
-    return y, ids, c, c * c_rel, err + hs * (np.abs(y) + err) + tiny
+    # below 2^-126 float32 values lie 2^-149 apart: exp within 3 of those, over a sum of at least 1
+    # (it contains exp(0)), and the quotient within half a one
+    return y, ids, c, c * c_rel + 3.5 * 2.0 ** -149, err + hs * (np.abs(y) + err) + tiny
 
 
 def encode(w, group, zeros):

@@ -84,6 +84,17 @@ def test_all_tokens_on_one_expert():
     compare(got, R.moe(x, r, g, u, d, 1, False), torch.bfloat16)
 
 
+@pytest.mark.parametrize("E", [64, 200])
+def test_most_tokens_on_one_of_many_experts(E):
+    """Few tokens per expert on average, and one that has three tiles of them."""
+    x, r, g, u, d = layer(40, 128, 96, E, 32, torch.bfloat16, True, seed=E)
+    r[E - 3] = torch.sign(x.float().mean(0) + 1e-3).to(r.dtype)
+    x = (x.float().abs() * torch.sign(r[E - 3].float())).to(x.dtype)
+    got = run(x, r, g, u, d, 2, True, routing=True)
+    assert (got[1][:, 0] == E - 3).all()
+    compare(got, R.moe(x, r, g, u, d, 2, True), torch.bfloat16)
+
+
 def test_ties_go_to_the_lowest_index():
     x, r, g, u, d = layer(5, 128, 64, 70, 64, torch.bfloat16, False)
     r[:] = r[0]                              # every logit of a row equal
@@ -144,6 +155,32 @@ def test_moe_zero_rows_and_convenience():
     st = [tuple(t.cpu() for t in crp.encode_w4g(v.cuda(), 64, True)) for v in w]
     compare(crp.moe(x.cuda(), r.cuda(), pe, 2, routing=True), R.moe(x, r, *st, 2, True), torch.float16)
     assert torch.equal(crp.moe(x.cuda(), r.cuda(), pe, 2), crp.moe(x.cuda(), r.cuda(), pe, 2, routing=True)[0])
+
+
+@pytest.mark.parametrize("M", [3, 64, 100])
+def test_moe_in_place_and_on_another_stream(M):
+    """y in x's place; and the same layers on two streams at once, a workspace each."""
+    x, r, *w = layer(M, 512, 256, 16, 64, torch.bfloat16, False, seed=M)
+    packed = [crp.pack_weight_w4g(*dev(v)) for v in w]
+    xs = [x.cuda(), x.flip(0).cuda()]
+    r = r.cuda()
+    want = [crp.moe_w4g(t, r, *packed, 256, 64, 4, routing=True) for t in xs]
+    y = xs[0].clone()
+    crp.moe_w4g(y, r, *packed, 256, 64, 4, out=y)
+    assert torch.equal(y, want[0][0])
+    need = crp.moe_w4g_workspace_bytes(M, 512, 256, 16, 4, 64)
+    ws = [torch.empty(need, dtype=torch.uint8, device="cuda") for _ in xs]
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(8):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got[i].append(crp.moe_w4g(xs[i], r, *packed, 256, 64, 4, workspace=ws[i], routing=True))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for g in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(g, want[i]))
 
 
 @pytest.mark.parametrize("M", [1, 12, 64])
