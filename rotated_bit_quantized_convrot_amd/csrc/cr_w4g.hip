@@ -277,16 +277,22 @@ hipError_t tile(const LinearArgs& a, hipStream_t st) {
 }
 
 // Tile choice.  Fewer, wider blocks read x less often and share its operand
-// reads; narrow ones put more CUs to work.  The wide tile is taken where its
-// blocks fill half the chip (256 CUs).  Measured, us, bf16, groups of 128,
+// reads; narrow ones put more CUs to work.  Measured, us, bf16, groups of 128,
 // K x N = 2560 x 9728 / 9728 x 2560 / 2560 x 2560 (weights cold):
 //   M = 8     one tile, 4 K groups 6.6 / 14.0 / 4.3, 10 groups 7.2 / 8.1 / 3.6,
 //             16 groups 9.5 / 7.3 / 3.8
-//   M = 32    wide 10.2 / 19.1 / 5.9, narrow 13.0 / 12.9 / 4.5
-//   M = 48    wide 12.3 / 35.5 / 10.3, narrow 16.8 / 16.5 / 5.6
-//   M = 76    wide 15.1 / 42.1 / 12.7, narrow 24.7 / 24.2 / 8.4
-//   M = 1220  128 x 128 86.7 / 95.1, 80 x 64 112.7 / 120.9; M = 300 at
-//             2560 x 2560 (60 blocks of 128 x 128) 26.9 and 13.2
+//   M = 32    32 columns 8.7 / 19.1 / 5.9, 16 columns 13.0 / 12.9 / 4.5
+//   M = 48    64 columns 9.4, with two tiles a wave and half the waves
+//             11.4 / 35.5 / 10.3, 16 columns 16.8 / 16.5 / 5.6
+// Up to 48 rows the wide tile is taken where its blocks fill half the chip
+// (256 CUs).  Above that the time is that of the rounds of 256 blocks (one
+// fits a CU) times a block's, which go as 2 : 3 : 7 : 8 for 80 x 16, 80 x 64,
+// 112 x 128 and 128 x 128 (M = 76 at 2560 x 9728: 24.7 / 12.4 for the first
+// two); us, in that order, K x N x M:
+//   2560 x 9728 x 100    33 / 20 / 26 / 27        2560 x 2560 x 200  15 / 12 / 26 / 28
+//   2560 x 9728 x 300    66 / 33 / 28 / 30        4096 x 4096 x 300  39 / 17 / 37 / 39
+//   9728 x 2560 x 1220  183 / 99 / 85 / 91        4096 x 4096 x 1000 128 / 66 / 80 / 48
+//   2560 x 9728 x 1220  235 / 106 / 104 / 89
 template <class T, int GPU, bool ZP>
 hipError_t linear_t(const LinearArgs& a, hipStream_t st) {
     constexpr long kHalf = 128;
@@ -302,18 +308,15 @@ hipError_t linear_t(const LinearArgs& a, hipStream_t st) {
         return tile<T, GPU, ZP, 2, 1, 1, 1, 8>(a, st);
     }
     if (a.M <= 48) {
-        if ((tiles + 3) / 4 >= kHalf) return tile<T, GPU, ZP, 3, 2, 1, 2, 4>(a, st);
+        if ((tiles + 3) / 4 >= kHalf) return tile<T, GPU, ZP, 3, 1, 1, 4, 4>(a, st);
         return tile<T, GPU, ZP, 3, 1, 1, 1, 6>(a, st);
     }
-    if (a.M > 80) {
-        // 128 columns by 128 or 112 rows, whichever leaves less in rounds of
-        // 256 blocks (one fits a CU) times a block's work: 112 rows take
-        // M = 1220 at N = 2560 in one round of 220 blocks, 93 -> 85 us
-        const long columns = (a.N + 127) / 128, b8 = (a.M + 127) / 128 * columns, b7 = (a.M + 111) / 112 * columns;
-        if (b7 >= kHalf && (b7 + 255) / 256 * 7 < (b8 + 255) / 256 * 8) return tile<T, GPU, ZP, 7, 2, 1, 4, 2>(a, st);
-        if (b8 >= kHalf) return tile<T, GPU, ZP, 8, 2, 1, 4, 2>(a, st);
-    }
-    if ((a.M + 79) / 80 * ((tiles + 3) / 4) >= kHalf) return tile<T, GPU, ZP, 5, 2, 1, 2, 4>(a, st);
+    // the least time: rounds of 256 blocks (one fits a CU) times a block's
+    auto rounds = [&](long m, long n) { return ((a.M + m - 1) / m * ((a.N + n - 1) / n) + 255) / 256; };
+    const long c16 = 2 * rounds(80, 16), c64 = 3 * rounds(80, 64), c7 = 7 * rounds(112, 128), c8 = 8 * rounds(128, 128);
+    if (c8 < c7 && c8 < c64 && c8 < c16) return tile<T, GPU, ZP, 8, 2, 1, 4, 2>(a, st);
+    if (c7 < c64 && c7 < c16) return tile<T, GPU, ZP, 7, 2, 1, 4, 2>(a, st);
+    if (c64 < c16) return tile<T, GPU, ZP, 5, 1, 1, 4, 4>(a, st);
     return tile<T, GPU, ZP, 5, 1, 1, 1, 4>(a, st);
 }
 

@@ -115,6 +115,15 @@ def test_linear_row_counts(M):
     check_linear(M, 272, 512, 64, torch.bfloat16, M % 2 == 1, M % 3 == 0, seed=M)
 
 
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("M,N", [(20, 4105), (40, 8200), (130, 4101), (300, 9731), (1000, 4090)])
+def test_linear_wide_tiles(dtype, group, zeros, M, N):
+    """Every tile that takes many columns, in all its types, with a last one that is not full."""
+    check_linear(M, N, 3 * 128 if group == 128 else 3 * 128 + group, group, DT[dtype], zeros, bias=zeros, seed=N)
+
+
 @pytest.mark.parametrize("M,N,K,group,dtype", [(1, 2560, 2560, 128, "bf16"), (1, 9728, 2560, 64, "fp16"),
                                                (76, 2560, 2560, 128, "fp16"), (1220, 512, 2560, 128, "bf16"),
                                                (200, 4000, 1056, 32, "fp16"), (700, 1100, 1280, 64, "bf16")])
