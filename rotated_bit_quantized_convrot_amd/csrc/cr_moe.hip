@@ -64,8 +64,9 @@ MoeWs moe_ws(int M, int K, int F, int E, int topk) {
 // ---------------------------------------------------------------------------
 // Router logits in float64: which expert is chosen hangs on the order of
 // values that can be close, and the sums then do not depend on their order.
-// A wave per expert and token (the router's row comes from the caches again for each token: 4
-// tokens a wave took 9.7 us at 16 tokens, 128 experts, K = 2048, this 4.7).
+// A wave per expert and token (the router's row comes from the caches again
+// for each token: 4 tokens a wave took 9.7 us at 16 tokens, 128 experts,
+// K = 2048, this 4.7).
 // ---------------------------------------------------------------------------
 template <class T>
 __global__ __launch_bounds__(256) void k_moe_logits(const uint16_t* __restrict__ x, int K,
@@ -111,6 +112,9 @@ __device__ __forceinline__ u64 order_key(double v) {
 // a tile of 16 rows of the expert's gate and up weights and take the units of
 // K in turn, each loading one unit ahead of its products; tokens go 16 at a
 // time.  With ks = 1 nothing is waited for but a wave's own loads.
+// Bound by the weights' bytes, after some 3 us in which a block finds its
+// expert: us, F x K = 768 x 2048, 8 of 128 experts: 9.4 for a token (13 MB),
+// 37 for 16 (134 MB: 3.6 TB/s).
 // ---------------------------------------------------------------------------
 constexpr int kUpWaves = 8;
 
@@ -343,7 +347,8 @@ __global__ __launch_bounds__(64 * kUpWaves, 4) void k_moe_gate_up(const uint16_t
 // ---------------------------------------------------------------------------
 // Gate and up, more tokens: the same, but the block's waves own a tile each
 // and go through K together, so that the rows of x are brought once for all
-// of them; up to 32 tokens at once, in one 16-row operand or two.
+// of them; up to 32 tokens at once, in one 16-row operand or two.  52 us for
+// 64 tokens, 2 of 8 experts of 5632 x 4096 (196 MB: 3.8 TB/s).
 // ---------------------------------------------------------------------------
 constexpr int kManyWaves = 4;
 template <class T, int GPU, bool ZP>
@@ -431,7 +436,14 @@ __global__ __launch_bounds__(64 * kManyWaves, 4) void k_moe_gate_up_many(
 // blocks on the same columns, by the one that arrives last: the order of
 // every sum is fixed.  The blocks' sums go through device-scope stores and
 // loads, waited for before the arrival is counted; no fence of the caches is
-// needed.
+// needed.  us: 7 for one token and 8 of 128 experts of 2048 x 768 (7 MB), 23
+// for 16 tokens (67 MB: 2.9 TB/s), 68 for 64 tokens and 2 of 8 experts of
+// 4096 x 5632: there a wave takes 4 KB of h for each KB of weights, and those
+// rows' way through the L2 (16 TB/s) bounds it, not the 98 MB of weights.  Rows
+// loaded to registers instead took 108 us (64-byte pieces, where LDS takes
+// whole rows), in passes of 16 tokens as well; two tiles a wave 79 (their
+// sums leave room for one block a CU), and at most 32 tokens 39 for 44 us,
+// but 15.4 for 14 where the blocks then are few.
 // ---------------------------------------------------------------------------
 struct Passes {
     static constexpr int kPairs = kChunk * kMoeMaxTopk;

@@ -9,7 +9,8 @@ namespace {
 // flat run of groups; g / 8 neighbouring lanes hold a group, 8 values each.
 // Bound by HBM: 2 B in, 0.5 B of codes and 2/g (3/g) B of scales out per value,
 // once the divisions are cheap: an IEEE division for each value took 66 us
-// for 100 M values in groups of 32 with zero points, this 53 to 57.
+// for 100 M values in groups of 32 with zero points, this 51 to 57 (261 MB:
+// 4.6 to 5.1 TB/s).
 //
 // rint(fl(v / s)) without the division: r = v fl(1/s) is within 2 steps of
 // v / s, and r + (v - r s) fl(1/s), the residue exact in an fma, is v / s
