@@ -612,9 +612,14 @@ __device__ __forceinline__ void moe_finish(Passes& s, int M, int N, uint32_t* ar
     for (int i = tid; i < M * 16; i += kThreads) {
         const int m = i >> 4;
         const size_t n = (size_t)blockIdx.x * 16 + (i & 15);
-        float v = 0.0f;
-        for (int j = 0; j < splits; ++j)
-            v += __hip_atomic_load(&parts[((size_t)j * M + m) * N + n], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        // all under way at once: each comes from beyond the L2
+        float part[kMaxSplits], v = 0.0f;
+#pragma unroll
+        for (int j = 0; j < kMaxSplits; ++j)
+            part[j] = __hip_atomic_load(&parts[((size_t)(j < splits ? j : 0) * M + m) * N + n], __ATOMIC_RELAXED,
+                                        __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+        for (int j = 0; j < kMaxSplits; ++j) v += j < splits ? part[j] : 0.0f;
         y[(size_t)m * N + n] = T::from_f32(v);
     }
 }
