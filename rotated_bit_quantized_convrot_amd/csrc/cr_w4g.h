@@ -239,8 +239,16 @@ __device__ __forceinline__ void w4g_x_to_lds(v4i x, uint32_t off, uint32_t lds) 
 __device__ __forceinline__ uint32_t lds_address(const void* p) {
     return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char*)p;
 }
-// Every load of this wave has arrived / has been read from LDS.
-__device__ __forceinline__ void w4g_wait() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+// Every load of this wave has arrived / has been read from LDS.  The builtin,
+// not assembly: the compiler then knows that the loads it counts itself are
+// there.  Otherwise it waits for them at their first use, by a count that
+// leaves out the loads to LDS issued meanwhile, so that it would wait for the
+// next unit's as well.
+__device__ __forceinline__ void w4g_wait() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0)
+    asm volatile("" ::: "memory");
+}
 __device__ __forceinline__ void w4g_wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 // After it every wave of the block has read what it asked LDS for: loads that
 // go there may follow.
