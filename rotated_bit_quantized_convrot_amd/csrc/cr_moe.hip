@@ -30,15 +30,34 @@ namespace {
 
 constexpr int kChunk = kMoeChunk;   // tokens per pass
 
-// The down product's blocks on the same 16 columns: enough to fill the chip's
-// CUs twice, each wave with at least two (expert, unit) items.
-constexpr int kDownWaves = 8, kMaxSplits = 8;
-int down_splits(int M, int F, int N, int E, int topk) {
+// The down product's grid: blocks by columns, and on the same columns enough
+// to fill the chip's CUs twice, each wave (or group of waves) with at least
+// two (expert, unit) items.  Blocks of four tiles that share the rows of h pay
+// where an expert has some tokens and the wider blocks still fill the CUs
+// twice; us, apart / shared: 64 tokens on 8 experts, 4096 x 5632: 67 / 50,
+// 4096 x 1792: 25.5 / 24.4, 32 tokens, 4096 x 5632: 43 / 35; with half as many
+// blocks as that: 16 experts, 2048 x 1024: 18.8 / 20.8, 32 experts 26 / 30.
+constexpr int kDownWaves = 8, kMaxSplits = 8, kWideTiles = 4, kWideGroups = kDownWaves / kWideTiles;
+// gate / up and down: an expert has some tokens, so that sharing their rows
+// among tiles pays.  Gate / up, us, apart / shared: 64 tokens, 8 experts (16
+// each) 99 / 53, 32 experts (12) 35 / 25, 60 experts (4.3) 45 / 52, 128 experts
+// (4) 53 / 65; 8 experts, 32 tokens (8) 51 / 43, 20 tokens (5) 47 / 42.
+bool share_rows(int M, int E, int topk) { return M > 16 && (long)M * topk >= 5L * E; }
+struct DownGrid {
+    bool wide;
+    int columns, splits;
+};
+DownGrid down_grid(int M, int F, int N, int E, int topk) {
     const long pairs = (long)M * topk, items = (pairs < E ? pairs : E) * ((F + 127) / 128);
-    const long most = items / (2 * kDownWaves);
-    long s = 512 / ((N + 15) / 16);
+    DownGrid g;
+    const int wide = (N / 16 + kWideTiles - 1) / kWideTiles;
+    g.wide = share_rows(M, E, topk) && wide * kMaxSplits >= 512;
+    g.columns = g.wide ? wide : N / 16;
+    const long most = items / (2 * (g.wide ? kWideGroups : kDownWaves));
+    long s = 512 / g.columns;
     s = s < most ? s : most;
-    return s < 1 ? 1 : (s > kMaxSplits ? kMaxSplits : (int)s);
+    g.splits = s < 1 ? 1 : (s > kMaxSplits ? kMaxSplits : (int)s);
+    return g;
 }
 
 // Workspace of one pass (byte offsets, 256-byte regions).
@@ -49,7 +68,7 @@ inline size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 MoeWs moe_ws(int M, int K, int F, int E, int topk) {
     const size_t m = M < kChunk ? M : kChunk, pairs = m * topk;
     // neither the splits nor the tokens of a last, smaller pass are more
-    const size_t splits = m ? down_splits((int)m, F, K, E, topk) : 1, parts = splits > 1 ? splits * m : 0;
+    const size_t splits = m ? down_grid((int)m, F, K, E, topk).splits : 1, parts = splits > 1 ? splits * m : 0;
     MoeWs l;
     l.logits = 0;                                        // double [m][E]
     l.ids = l.logits + up256(m * E * 8);                 // int32 [m][topk]
@@ -429,21 +448,19 @@ __global__ __launch_bounds__(64 * kManyWaves, 4) void k_moe_gate_up_many(
 
 // ---------------------------------------------------------------------------
 // Down and combination.  The pairs are sorted by expert and cut into passes of
-// up to 8 tokens (operand row 2 t holds token t's h, row 2 t + 1 what is
+// up to 8 tokens, or 16 in two operands (operand row 2 t holds token t's h, row 2 t + 1 what is
 // left of it); the items (pass, unit of F) are shared out in contiguous runs.
 // At the end of a pass a wave adds c times its sums into its own rows of LDS;
 // the waves' rows are added in their order, and so are those of the gridDim.y
 // blocks on the same columns, by the one that arrives last: the order of
 // every sum is fixed.  The blocks' sums go through device-scope stores and
 // loads, waited for before the arrival is counted; no fence of the caches is
-// needed.  us: 7 for one token and 8 of 128 experts of 2048 x 768 (7 MB), 23
-// for 16 tokens (67 MB: 2.9 TB/s), 68 for 64 tokens and 2 of 8 experts of
-// 4096 x 5632: there a wave takes 4 KB of h for each KB of weights, and those
-// rows' way through the L2 (16 TB/s) bounds it, not the 98 MB of weights.  Rows
-// loaded to registers instead took 108 us (64-byte pieces, where LDS takes
-// whole rows), in passes of 16 tokens as well; two tiles a wave 79 (their
-// sums leave room for one block a CU), and at most 32 tokens 39 for 44 us,
-// but 15.4 for 14 where the blocks then are few.
+// needed.  us: 7 for one token and 8 of 128 experts of 2048 x 768 (7 MB), 21
+// for 16 tokens (67 MB: 3.2 TB/s).  With some tokens an expert a wave takes
+// 4 KB of h for each KB of weights, and those rows' way through the L2 bounds
+// it, not the weights (64 tokens, 2 of 8 experts of 4096 x 5632: 67 us for
+// 98 MB, 16 TB/s of rows): the wide form below takes 50.  Rows loaded to
+// registers instead took 108 us (64-byte pieces, where LDS takes whole rows).
 // ---------------------------------------------------------------------------
 struct Passes {
     static constexpr int kPairs = kChunk * kMoeMaxTopk;
@@ -464,12 +481,12 @@ struct ByExpert {
 // Fills the passes and the pairs' weights (the softmax's numerators over the
 // tokens' denominators); returns the number of passes.  One block writes the
 // choice out.  The choice is read once, everything else happens in LDS.
-template <int WAVES>
+template <int WAVES, int TOK>
 __device__ __forceinline__ int moe_passes(Passes& s, ByExpert& by, int M, int E, int topk, int norm,
                                           const double* __restrict__ logits, const int32_t* __restrict__ ids,
                                           const double* __restrict__ top, bool write, int32_t* __restrict__ ids_out,
                                           float* __restrict__ weights_out) {
-    constexpr int kThreads = 64 * WAVES, kEach = (kMoeMaxExperts + kThreads - 1) / kThreads, TOK = 8;
+    constexpr int kThreads = 64 * WAVES, kEach = (kMoeMaxExperts + kThreads - 1) / kThreads;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int pairs = M * topk;
     for (int p = tid; p < pairs; p += kThreads) {
@@ -572,34 +589,39 @@ __device__ __forceinline__ int moe_passes(Passes& s, ByExpert& by, int M, int E,
 }
 
 // A pass's sums times c into the wave's rows [M][16].
-__device__ __forceinline__ void moe_scatter(const Passes& s, int pass, int topk, f32x4& acc, float* sums) {
+template <int MT>
+__device__ __forceinline__ void moe_scatter(const Passes& s, int pass, int topk, f32x4 (&acc)[MT][1], float* sums) {
     const int lane = threadIdx.x & 63, n = s.n[pass], at = s.at[pass];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const int t = (lane >> 4) * 2 + j;
-        if (t < n) {
-            const int p = s.pair_of[at + t];
-            float& to = sums[p / topk * 16 + (lane & 15)];
-            to = __builtin_fmaf(s.c[p], acc[2 * j] + acc[2 * j + 1], to);
+    for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int t = mt * 8 + (lane >> 4) * 2 + j;
+            if (t < n) {
+                const int p = s.pair_of[at + t];
+                float& to = sums[p / topk * 16 + (lane & 15)];
+                to = __builtin_fmaf(s.c[p], acc[mt][0][2 * j] + acc[mt][0][2 * j + 1], to);
+            }
         }
+        acc[mt][0] = f32x4{0, 0, 0, 0};
     }
-    acc = f32x4{0, 0, 0, 0};
 }
 
-// Columns 16 blockIdx.x.. of y: this block's sums value(m, column) and, where
+// Columns C blockIdx.x.. of y: this block's sums value(m, column) and, where
 // more blocks share the columns, theirs.
-template <class T, int WAVES, class V>
+template <class T, int WAVES, int C, class V>
 __device__ __forceinline__ void moe_finish(Passes& s, int M, int N, uint32_t* arrived, float* parts, uint16_t* y,
                                            V value) {
     constexpr int kThreads = 64 * WAVES;
     const int tid = threadIdx.x, splits = gridDim.y;
-    for (int i = tid; i < M * 16; i += kThreads) {
-        const int m = i >> 4;
-        const size_t n = (size_t)blockIdx.x * 16 + (i & 15);
+    for (int i = tid; i < M * C; i += kThreads) {
+        const int m = i / C;
+        const size_t n = (size_t)blockIdx.x * C + i % C;
+        if (n >= (size_t)N) continue;
         if (splits == 1)
-            y[(size_t)m * N + n] = T::from_f32(value(m, i & 15));
+            y[(size_t)m * N + n] = T::from_f32(value(m, i % C));
         else
-            __hip_atomic_store(&parts[((size_t)blockIdx.y * M + m) * N + n], value(m, i & 15), __ATOMIC_RELAXED,
+            __hip_atomic_store(&parts[((size_t)blockIdx.y * M + m) * N + n], value(m, i % C), __ATOMIC_RELAXED,
                                __HIP_MEMORY_SCOPE_AGENT);
     }
     if (splits == 1) return;
@@ -609,9 +631,10 @@ __device__ __forceinline__ void moe_finish(Passes& s, int M, int N, uint32_t* ar
         s.before = __hip_atomic_fetch_add(&arrived[blockIdx.x], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     __syncthreads();
     if (s.before + 1 != (uint32_t)splits) return;
-    for (int i = tid; i < M * 16; i += kThreads) {
-        const int m = i >> 4;
-        const size_t n = (size_t)blockIdx.x * 16 + (i & 15);
+    for (int i = tid; i < M * C; i += kThreads) {
+        const int m = i / C;
+        const size_t n = (size_t)blockIdx.x * C + i % C;
+        if (n >= (size_t)N) continue;
         // all under way at once: each comes from beyond the L2
         float part[kMaxSplits], v = 0.0f;
 #pragma unroll
@@ -640,7 +663,7 @@ __global__ __launch_bounds__(64 * kDownWaves, 4) void k_moe_down(
     static_assert(sizeof(ByExpert) <= sizeof(rows_lds), "the rows' place holds it");
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     for (int i = tid; i < kDownWaves * M * 16; i += kThreads) sums[i] = 0.0f;
-    const int passes = moe_passes<kDownWaves>(s, *reinterpret_cast<ByExpert*>(rows_lds), M, E, topk, norm, logits, ids,
+    const int passes = moe_passes<kDownWaves, 8>(s, *reinterpret_cast<ByExpert*>(rows_lds), M, E, topk, norm, logits, ids,
                                               top, blockIdx.x == 0 && blockIdx.y == 0, ids_out, weights_out);
 
     const W4gLayout l = w4g_layout(128 / GPU, ZP, N, F);
@@ -695,13 +718,113 @@ __global__ __launch_bounds__(64 * kDownWaves, 4) void k_moe_down(
         }
 #pragma unroll
         for (int g = 0; g < GPU; ++g) w4g_mac<DownT<T>, GPU, ZP, 1, 1>(g, w, a[g], acc);
-        if (i + 1 == end || pass != done) moe_scatter(s, done, topk, acc[0][0], sums + wave * M * 16);
+        if (i + 1 == end || pass != done) moe_scatter<1>(s, done, topk, acc, sums + wave * M * 16);
     }
     __syncthreads();
-    moe_finish<T, kDownWaves>(s, M, N, arrived, parts, y, [&](int m, int n) {
+    moe_finish<T, kDownWaves, 16>(s, M, N, arrived, parts, y, [&](int m, int n) {
         float v = 0.0f;
 #pragma unroll
         for (int wv = 0; wv < kDownWaves; ++wv) v += sums[(wv * M + m) * 16 + n];
+        return v;
+    });
+}
+
+// The same with kWideTiles tiles of 16 columns a block, whose waves go through
+// the same items together, so that the rows of h are brought once for all of
+// them; kWideGroups such groups of waves a block, each with its share of the
+// items; passes of up to 16 tokens.
+template <class T, int GPU, bool ZP>
+__global__ __launch_bounds__(64 * kDownWaves, 4) void k_moe_down_wide(
+    const uint16_t* __restrict__ h, int M, int F, int N, const uint8_t* __restrict__ wd, int E, int topk, int norm,
+    const double* __restrict__ logits, const int32_t* __restrict__ ids, const double* __restrict__ top,
+    uint32_t* __restrict__ arrived,
+    float* __restrict__ parts, uint16_t* __restrict__ y, int32_t* __restrict__ ids_out,
+    float* __restrict__ weights_out) {
+    constexpr int kThreads = 64 * kDownWaves, MT = 2, kStage = kWideGroups * MT * 4096;
+    extern __shared__ __attribute__((aligned(16))) float sums[];   // [waves][M][16]
+    __shared__ Passes s;
+    __shared__ __attribute__((aligned(16))) char rows_lds[2 * kStage];
+    static_assert(sizeof(ByExpert) <= sizeof(rows_lds), "the rows' place holds it");
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int group = wave / kWideTiles, wn = wave % kWideTiles;
+    for (int i = tid; i < kDownWaves * M * 16; i += kThreads) sums[i] = 0.0f;
+    const int passes = moe_passes<kDownWaves, 8 * MT>(s, *reinterpret_cast<ByExpert*>(rows_lds), M, E, topk, norm,
+                                                      logits, ids, top, blockIdx.x == 0 && blockIdx.y == 0, ids_out,
+                                                      weights_out);
+
+    const W4gLayout l = w4g_layout(128 / GPU, ZP, N, F);
+    const int tile = blockIdx.x * kWideTiles + wn, mine = tile < l.tiles ? tile : l.tiles - 1;
+    const int split = blockIdx.y, splits = gridDim.y;
+    const v4i hb = w4g_rows(h, 2 * M * topk, F);
+    const int items = passes * l.units, run = (items + kWideGroups * splits - 1) / (kWideGroups * splits);
+    const int begin = (split * kWideGroups + group) * run, end = begin + run < items ? begin + run : items;
+    const uint32_t lds0 = lds_address(rows_lds) + group * MT * 4096;
+    int pass = begin / l.units, u = begin % l.units, n = 0;
+    const uint8_t* we = wd;
+    uint32_t row[MT];   // of this wave's instructions: rows 4 wn.. of both operands
+    W4gUnit<GPU> next[1];
+    auto turn = [&]() {
+        n = __builtin_amdgcn_readfirstlane(s.n[pass]);
+        const int at = s.at[pass];
+        we = wd + (size_t)__builtin_amdgcn_readfirstlane(s.expert[pass]) * l.total;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            const int r = 16 * mt + 4 * wn + (lane >> 4), t = (r >> 1) < n ? r >> 1 : n - 1;
+            row[mt] = (uint32_t)(2 * s.pair_of[at + t] + (r & 1)) * (2u * F);
+        }
+    };
+    auto load = [&](int stage) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+            if (8 * mt + 2 * wn < n)
+                w4g_x_to_lds(hb, row[mt] + w4g_chunk(4 * wn, u, F, lane), lds0 + stage * kStage + mt * 4096 + wn * 1024);
+        next[0] = w4g_load<GPU, ZP>(we, l, (size_t)mine * l.units + u, lane);
+    };
+    if (begin < end) {
+        turn();
+        load(0);
+    }
+
+    f32x4 acc[MT][1];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) acc[mt][0] = f32x4{0, 0, 0, 0};
+    for (int i = begin; i < begin + run; ++i) {   // as many turns for every wave: they meet in each
+        w4g_wait();
+        w4g_barrier();   // the item's rows are there, the other stage has been read
+        if (i >= end) continue;
+        const int stage = (i - begin) & 1;
+        const W4gUnit<GPU> w[1] = {next[0]};
+        const int done = pass, rows = n;
+        if (++u == l.units) {
+            u = 0;
+            ++pass;
+        }
+        if (i + 1 < end) {
+            if (pass != done) turn();
+            load(stage ^ 1);
+        }
+        const char* at = rows_lds + group * MT * 4096 + stage * kStage;
+        auto use = [&](auto mt_count) {
+            constexpr int C = decltype(mt_count)::value;
+#pragma unroll
+            for (int g = 0; g < GPU; ++g) {
+                u32x4 a[C][4 / GPU];
+#pragma unroll
+                for (int mt = 0; mt < C; ++mt)
+#pragma unroll
+                    for (int d = 0; d < 4 / GPU; ++d) a[mt][d] = w4g_operand_rows(at + mt * 4096, g * (4 / GPU) + d, lane);
+                w4g_mac<DownT<T>, GPU, ZP, C, 1>(g, w, a, reinterpret_cast<f32x4(&)[C][1]>(acc));
+            }
+        };
+        if (rows <= 8) use(std::integral_constant<int, 1>{});
+        else use(std::integral_constant<int, 2>{});
+        if (i + 1 == end || pass != done) moe_scatter<MT>(s, done, topk, acc, sums + wave * M * 16);
+    }
+    __syncthreads();
+    moe_finish<T, kDownWaves, 16 * kWideTiles>(s, M, N, arrived, parts, y, [&](int m, int c) {
+        float v = 0.0f;
+#pragma unroll
+        for (int g = 0; g < kWideGroups; ++g) v += sums[((g * kWideTiles + (c >> 4)) * M + m) * 16 + (c & 15)];
         return v;
     });
 }
@@ -714,15 +837,16 @@ hipError_t moe_t(const MoeArgs& a, const MoeWs& l, int M, const uint16_t* x, uin
     int32_t* ids_ws = reinterpret_cast<int32_t*>(ws + l.ids);
     uint16_t* h = reinterpret_cast<uint16_t*>(ws + l.h);
     double* top = reinterpret_cast<double*>(ws + l.top);
-    static std::atomic<uint64_t> done{0};
-    const auto down = k_moe_down<T, GPU, ZP>;
-    const hipError_t err = opt_in_lds(reinterpret_cast<const void*>(down), kDownWaves * kChunk * 64, done);
+    const DownGrid grid = down_grid(M, a.F, a.K, a.E, a.topk);
+    static std::atomic<uint64_t> done[2];
+    const auto down = grid.wide ? k_moe_down_wide<T, GPU, ZP> : k_moe_down<T, GPU, ZP>;
+    const hipError_t err =
+        opt_in_lds(reinterpret_cast<const void*>(down), kDownWaves * kChunk * 64, done[grid.wide]);
     if (err != hipSuccess) return err;
     uint32_t* arrived = reinterpret_cast<uint32_t*>(ws + l.arrived);
     float* parts = reinterpret_cast<float*>(ws + l.parts);
-    const int splits = down_splits(M, a.F, a.K, a.E, a.topk), out_tiles = a.K / 16;
     k_moe_logits<T><<<dim3((a.E + 3) / 4, M), 256, 0, st>>>(x, a.K, a.router, a.E, logits, arrived,
-                                                            splits > 1 ? out_tiles : 0);
+                                                            grid.splits > 1 ? grid.columns : 0);
     const int pairs = M * a.topk, by_pair = pairs < a.E, rows = by_pair ? pairs : a.E;
     // a wave per tile where the chosen experts' tiles fill the chip's 4096
     // wave slots half, else as many waves on a tile's K as bring them there
@@ -730,17 +854,15 @@ hipError_t moe_t(const MoeArgs& a, const MoeWs& l, int M, const uint16_t* x, uin
     int ks_log2 = 0;
     while ((1 << ks_log2) < kUpWaves && ((long)rows * tiles << ks_log2) < 2048) ++ks_log2;
     const int per = kUpWaves >> ks_log2;
-    // gate / up tiles that share the rows of x pay where an expert has more
-    // than about 5 tokens; us, apart / together: 64 tokens, 8 experts (16 each)
-    // 100 / 53, 32 experts (12) 35 / 25, 60 experts (4.3) 46 / 52, 128 experts
-    // (4) 53 / 65; 32 tokens, 8 experts (8) 51 / 46
-    if (M > 16 && pairs > 5 * a.E)
+    // its blocks of kManyWaves tiles take K whole: every CU has to have one (us,
+    // apart / shared: 256 blocks 20.5 / 19.6, 224 blocks 28 / 31)
+    if (share_rows(M, a.E, a.topk) && (long)rows * ((tiles + kManyWaves - 1) / kManyWaves) >= 256)
         k_moe_gate_up_many<T, GPU, ZP><<<dim3((tiles + kManyWaves - 1) / kManyWaves, rows), 64 * kManyWaves, 0, st>>>(
             x, M, a.K, a.F, a.wg, a.wu, a.E, a.topk, by_pair, logits, ids_ws, top, h);
     else
         k_moe_gate_up<T, GPU, ZP><<<dim3((tiles + per - 1) / per, rows), 64 * kUpWaves, 0, st>>>(
             x, M, a.K, a.F, a.wg, a.wu, a.E, a.topk, by_pair, ks_log2, logits, ids_ws, top, h);
-    down<<<dim3(out_tiles, splits), 64 * kDownWaves, kDownWaves * M * 64, st>>>(
+    down<<<dim3(grid.columns, grid.splits), 64 * kDownWaves, kDownWaves * M * 64, st>>>(
         h, M, a.F, a.K, a.wd, a.E, a.topk, a.norm, logits, ids_ws, top, arrived, parts, y, ids, weights);
     return hipGetLastError();
 }

@@ -73,6 +73,27 @@ def test_moe_widths(K, F):
     compare(run(*args, 2, True, routing=True), R.moe(*args, 2, True), torch.bfloat16)
 
 
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("M,E,F,topk", [(17, 8, 2176, 3), (100, 8, 2176, 2), (64, 5, 3328, 3)])
+def test_moe_wide_experts(dtype, group, zeros, M, E, F, topk):
+    """Many hidden columns and some tokens an expert (up to more than two operands of them): gate and up
+    with shared rows, the last block not full in groups of 32."""
+    args = layer(M, 128 + group, F - 32 * (group == 32), E, group, DT[dtype], zeros, seed=M)
+    compare(run(*args, topk, zeros, routing=True), R.moe(*args, topk, zeros), DT[dtype])
+
+
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("M,E", [(17, 6), (40, 6), (64, 2), (131, 3)])
+def test_moe_wide_outputs(dtype, group, zeros, M, E):
+    """Many columns and some tokens an expert: the down product's wide blocks, the last one not full."""
+    args = layer(M, 4096 + group, 256 + group, E, group, DT[dtype], zeros, seed=M)
+    compare(run(*args, 2, zeros, routing=True), R.moe(*args, 2, zeros), DT[dtype])
+
+
 def test_all_tokens_on_one_expert():
     """One expert takes every token (more than one tile of them), the others none."""
     x, r, g, u, d = layer(64, 128, 128, 10, 64, torch.bfloat16, False)
