@@ -848,11 +848,17 @@ hipError_t moe_t(const MoeArgs& a, const MoeWs& l, int M, const uint16_t* x, uin
     k_moe_logits<T><<<dim3((a.E + 3) / 4, M), 256, 0, st>>>(x, a.K, a.router, a.E, logits, arrived,
                                                             grid.splits > 1 ? grid.columns : 0);
     const int pairs = M * a.topk, by_pair = pairs < a.E, rows = by_pair ? pairs : a.E;
-    // a wave per tile where the chosen experts' tiles fill the chip's 4096
-    // wave slots half, else as many waves on a tile's K as bring them there
-    const int tiles = a.F / 16;
+    // waves that share a tile's K: as many as give the chip's 1024 SIMDs one
+    // each, and further up to its 4096 wave slots while each keeps 8 units; us,
+    // by waves a tile (units of a wave): 8 x 48 tiles 4 (4) 9.9, 8 (2) 10.5;
+    // 16 x 48 tiles 2 (8) 13.3, 4 (4) 13.8, 8 (2) 17.3; 20 x 88 tiles 1 (11)
+    // 15.4, 4 (2.8) 20; 8 x 352 tiles 1 (32) 48, 2 (16) 42.7
+    const int tiles = a.F / 16, units = (a.K + 127) / 128;
     int ks_log2 = 0;
-    while ((1 << ks_log2) < kUpWaves && ((long)rows * tiles << ks_log2) < 2048) ++ks_log2;
+    for (; (1 << ks_log2) < kUpWaves; ++ks_log2) {
+        const long waves = (long)rows * tiles << ks_log2;
+        if (waves >= 1024 && (waves >= 4096 || units >> (ks_log2 + 1) < 8)) break;
+    }
     const int per = kUpWaves >> ks_log2;
     // its blocks of kManyWaves tiles take K whole: every CU has to have one (us,
     // apart / shared: 256 blocks 20.5 / 19.6, 224 blocks 28 / 31)
