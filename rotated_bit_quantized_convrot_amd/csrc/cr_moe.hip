@@ -132,7 +132,7 @@ __device__ __forceinline__ u64 order_key(double v) {
 // K in turn, each loading one unit ahead of its products; tokens go 16 at a
 // time.  With ks = 1 nothing is waited for but a wave's own loads.
 // Bound by the weights' bytes, after some 3 us in which a block finds its
-// expert: us, F x K = 768 x 2048, 8 of 128 experts: 9.4 for a token (13 MB),
+// expert: us, F x K = 768 x 2048, 8 of 128 experts: 9 for a token (13 MB),
 // 37 for 16 (134 MB: 3.6 TB/s).
 // ---------------------------------------------------------------------------
 constexpr int kUpWaves = 8;

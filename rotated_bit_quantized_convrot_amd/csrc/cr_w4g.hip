@@ -288,12 +288,12 @@ hipError_t tile(const LinearArgs& a, hipStream_t st) {
 // Up to 48 rows the wide tile is taken where its blocks fill half the chip
 // (256 CUs).  Above that the time is that of the rounds of 256 blocks (one
 // fits a CU) times a block's, which go as 2 : 3 : 7 : 8 for 80 x 16, 80 x 64,
-// 112 x 128 and 128 x 128 (M = 76 at 2560 x 9728: 24.7 / 12.4 for the first
+// 112 x 128 and 128 x 128 (M = 76 at 2560 x 9728: 20.4 / 12.0 for the first
 // two); us, in that order, K x N x M:
-//   2560 x 9728 x 100    33 / 20 / 26 / 27        2560 x 2560 x 200  15 / 12 / 26 / 28
-//   2560 x 9728 x 300    66 / 33 / 28 / 30        4096 x 4096 x 300  39 / 17 / 37 / 39
-//   9728 x 2560 x 1220  183 / 99 / 85 / 91        4096 x 4096 x 1000 128 / 66 / 80 / 48
-//   2560 x 9728 x 1220  235 / 106 / 104 / 89
+//   2560 x 9728 x 100    33 / 20 / 23 / 24       2560 x 2560 x 200   15 / 12 / 23 / 25
+//   2560 x 9728 x 300    64 / 32 / 26 / 28       4096 x 4096 x 300   38 / 17 / 33 / 35
+//   9728 x 2560 x 1220  179 / 97 / 75 / 81       4096 x 4096 x 1000 125 / 64 / 73 / 45
+//   2560 x 9728 x 1220  230 / 103 / 93 / 80
 template <class T, int GPU, bool ZP>
 hipError_t linear_t(const LinearArgs& a, hipStream_t st) {
     constexpr long kHalf = 128;
