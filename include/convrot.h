@@ -371,8 +371,7 @@ cr_status cr_linear_w4g(int dtype, const void* x, int M, int K, const void* w_pa
  *   (norm nonzero) or over all experts;
  *   h[r] = silu(Wg_e x) * (Wu_e x), Wg, Wu [F,K]  (e = e_r)
  *   y = T(sum_r c[r] * Wd_e h[r]), Wd [K,F].
- * The down product takes h as the sum of two bf16 values, within 2^-18 of it:
- * one 16-bit value would cost what rounding y does.
+ * The down product takes h as it is in float32.
  *   wg/wu/wd_packed  E packed weights each (cr_pack_weight_w4g, count = E)
  *   y [M,K] (out); ids [M,topk] int32 and weights [M,topk] float: the chosen
  *   experts and c (out, each may be NULL)

@@ -12,12 +12,11 @@
 // there is no launch for the choice: whether expert e is chosen by token m is
 // a count of the logits above l[m,e], which every block of the gate / up
 // kernel makes for itself; the down kernel reads the chosen ids.
-// h goes to the down product as two bf16 values (the rounded one and what is
-// left of it, 16 bits of significand together, in bf16's range for either T),
-// in neighbouring rows of one 16-row operand: eight tokens' h cost no more
-// MFMAs than one 16-bit rounding of it would, and y's rounding stays the only
-// one that counts.
-// Both products bring 16 operand rows a wave to its own piece of LDS, by as
+// h goes to the down product as it is in float32, as the sum of three bf16
+// values of 8 bits each (in bf16's range for either T): y's rounding is the
+// only one to fewer bits.  The three are operands of MFMAs into the same
+// sums, so they cost rows and MFMAs, and no accumulators.
+// Both products bring a wave's operand rows to its own piece of LDS, by as
 // many 4-row instructions as it has rows (an expert of a few tokens has 1 to
 // 3, so most of a 16-row load by registers would be for nothing), and
 // take them to registers before the next unit's are brought to the same place.
@@ -29,20 +28,31 @@ namespace cr {
 namespace {
 
 constexpr int kChunk = kMoeChunk;   // tokens per pass
+constexpr int kParts = 3;           // bf16 values whose sum is h
 
 // The down product's grid: blocks by columns, and on the same columns enough
 // to fill the chip's CUs twice, each wave (or group of waves) with at least
-// two (expert, unit) items.  Blocks of four tiles that share the rows of h pay
-// where an expert has some tokens and the wider blocks still fill the CUs
-// twice; us, apart / shared: 64 tokens on 8 experts, 4096 x 5632: 67 / 50,
-// 4096 x 1792: 25.5 / 24.4, 32 tokens, 4096 x 5632: 43 / 35; with half as many
-// blocks as that: 16 experts, 2048 x 1024: 18.8 / 20.8, 32 experts 26 / 30.
+// two (expert, unit) items.
 constexpr int kDownWaves = 8, kMaxSplits = 8, kWideTiles = 4, kWideGroups = kDownWaves / kWideTiles;
-// gate / up and down: an expert has some tokens, so that sharing their rows
-// among tiles pays.  Gate / up, us, apart / shared: 64 tokens, 8 experts (16
-// each) 99 / 53, 32 experts (12) 35 / 25, 60 experts (4.3) 45 / 52, 128 experts
-// (4) 53 / 65; 8 experts, 32 tokens (8) 51 / 43, 20 tokens (5) 47 / 42.
+constexpr int kDownTok = 5, kWideTok = 16;   // tokens of a pass, apart and in wide blocks
+// Gate / up: an expert has some tokens, so that sharing their rows among tiles
+// pays; us, apart / shared: 64 tokens, 8 experts (16 each) 99 / 53, 32 experts
+// (12) 35 / 25, 60 experts (4.3) 45 / 52, 128 experts (4) 53 / 65; 8 experts, 32
+// tokens (8) 51 / 43, 20 tokens (5) 47 / 42.  With up to 16 tokens there is little
+// in it: 16 on 8 of 8 experts 51 / 46 and 17.9 / 18.8, 12 on 4 of 8 21 / 23.
 bool share_rows(int M, int E, int topk) { return M > 16 && (long)M * topk >= 5L * E; }
+// Down: blocks of four tiles that share the rows of h pay where an expert's
+// tokens are more than a pass of a block apart takes, the more of them the
+// fewer blocks the columns can give (K / 64 times kMaxSplits: 512 at K = 4096);
+// us, apart / wide, by tokens an expert:
+//   K = 4096   6: 76 / 70   8: 54 / 38   16: 90 / 56.5 (64 tokens, 2 of 8, F = 5632), 34 / 27 (F = 1792)
+//   K = 2880   6: 26 / 24   8: 31 / 25.5, 105 / 72 (32 experts)   16: 46 / 34
+//   K = 2048   8: 17 / 18, 26 / 30, 41 / 41   12: 42 / 38   16: 50 / 46, 23.5 / 22.6, 27 / 18
+//   K = 1536  32: 26.3 / 25.9   K = 1024   8: 9.4 / 11   16: 23 / 31
+bool wide_down(int M, int wide_columns, int E, int topk) {
+    const long pairs = (long)M * topk, blocks = (long)wide_columns * kMaxSplits;
+    return pairs >= 12L * E ? blocks >= 256 : pairs >= 5L * E && blocks >= 352;
+}
 struct DownGrid {
     bool wide;
     int columns, splits;
@@ -51,7 +61,7 @@ DownGrid down_grid(int M, int F, int N, int E, int topk) {
     const long pairs = (long)M * topk, items = (pairs < E ? pairs : E) * ((F + 127) / 128);
     DownGrid g;
     const int wide = (N / 16 + kWideTiles - 1) / kWideTiles;
-    g.wide = share_rows(M, E, topk) && wide * kMaxSplits >= 512;
+    g.wide = wide_down(M, wide, E, topk);
     g.columns = g.wide ? wide : N / 16;
     const long most = items / (2 * (g.wide ? kWideGroups : kDownWaves));
     long s = 512 / g.columns;
@@ -73,8 +83,8 @@ MoeWs moe_ws(int M, int K, int F, int E, int topk) {
     l.logits = 0;                                        // double [m][E]
     l.ids = l.logits + up256(m * E * 8);                 // int32 [m][topk]
     l.top = l.ids + up256(pairs * 4);                    // double [m][topk]: the chosen logits
-    l.h = l.top + up256(pairs * 8);                      // bf16 [m topk][2][F]
-    l.arrived = l.h + up256(pairs * F * 4);              // uint32 [K / 16]
+    l.h = l.top + up256(pairs * 8);                      // bf16 [m topk][kParts][F]
+    l.arrived = l.h + up256(pairs * F * 2 * kParts);     // uint32 [K / 16]
     l.parts = l.arrived + up256((size_t)(K / 16) * 4);   // float [splits][m][K]
     l.total = l.parts + up256(parts * K * 4);
     return l;
@@ -260,13 +270,18 @@ __device__ __forceinline__ int moe_choice(Choice& c, int M, int E, int topk, int
     return __builtin_amdgcn_readfirstlane(c.chosen);
 }
 
-// silu(g) u as two bf16 values, into element n of both rows of pair p's h.
+// silu(g) u into element n of pair p's h: the upper 8 bits of its significand,
+// the next 8 and the last 8, each a bf16 value; the differences are exact
+// (down to bf16's smallest number).  An infinity has no rest.
 __device__ __forceinline__ void moe_store_h(uint16_t* h, int p, int F, int n, float g, float u) {
-    const float v = g / (1.0f + expf(-g)) * u;
-    uint16_t* to = h + (size_t)p * 2 * F + n;
-    const uint16_t hi = Bf16::from_f32(v);
-    to[0] = hi;
-    to[F] = Bf16::from_f32(v - Bf16::to_f32(hi));
+    float v = g / (1.0f + expf(-g)) * u;
+    uint16_t* to = h + (size_t)p * kParts * F + n;
+#pragma unroll
+    for (int i = 0; i < kParts; ++i) {
+        const uint32_t top = __float_as_uint(v) & 0xFFFF0000u;
+        to[(size_t)i * F] = (uint16_t)(top >> 16);
+        v = (top & 0x7F800000u) == 0x7F800000u ? 0.0f : v - __uint_as_float(top);
+    }
 }
 
 template <class T, int GPU, bool ZP>
@@ -448,19 +463,24 @@ __global__ __launch_bounds__(64 * kManyWaves, 4) void k_moe_gate_up_many(
 
 // ---------------------------------------------------------------------------
 // Down and combination.  The pairs are sorted by expert and cut into passes of
-// up to 8 tokens, or 16 in two operands (operand row 2 t holds token t's h, row 2 t + 1 what is
-// left of it); the items (pass, unit of F) are shared out in contiguous runs.
+// up to kDownTok tokens, whose rows of h lie in LDS with a token's three parts
+// next to each other; the items (pass, unit of F) are shared out in contiguous
+// runs.
 // At the end of a pass a wave adds c times its sums into its own rows of LDS;
 // the waves' rows are added in their order, and so are those of the gridDim.y
 // blocks on the same columns, by the one that arrives last: the order of
 // every sum is fixed.  The blocks' sums go through device-scope stores and
 // loads, waited for before the arrival is counted; no fence of the caches is
-// needed.  us: 7 for one token and 8 of 128 experts of 2048 x 768 (7 MB), 21
-// for 16 tokens (67 MB: 3.2 TB/s).  With some tokens an expert a wave takes
+// needed.  us: 7.6 for one token and 8 of 128 experts of 2048 x 768 (7 MB), 22
+// for 16 tokens (67 MB: 3.1 TB/s).  With some tokens an expert a wave takes
 // 4 KB of h for each KB of weights, and those rows' way through the L2 bounds
-// it, not the weights (64 tokens, 2 of 8 experts of 4096 x 5632: 67 us for
-// 98 MB, 16 TB/s of rows): the wide form below takes 50.  Rows loaded to
-// registers instead took 108 us (64-byte pieces, where LDS takes whole rows).
+// it, not the weights: 64 tokens, 2 of 8 experts of 4096 x 5632 take 90 us for
+// 98 MB, the wide form below 56.5.  (With h rounded to two bf16 values, 16 bits,
+// the three sizes took 7, 21 and 49, and one output in 400 of the last was
+// rounded otherwise than a float32 h's, against one in 900.)
+// An operand holds a token's parts in three of its 16 rows, five tokens in
+// all: an operand a part took 25 us where this takes 22, three times the reads
+// of LDS.
 // ---------------------------------------------------------------------------
 struct Passes {
     static constexpr int kPairs = kChunk * kMoeMaxTopk;
@@ -588,23 +608,12 @@ __device__ __forceinline__ int moe_passes(Passes& s, ByExpert& by, int M, int E,
     return __builtin_amdgcn_readfirstlane(passes);
 }
 
-// A pass's sums times c into the wave's rows [M][16].
-template <int MT>
-__device__ __forceinline__ void moe_scatter(const Passes& s, int pass, int topk, f32x4 (&acc)[MT][1], float* sums) {
-    const int lane = threadIdx.x & 63, n = s.n[pass], at = s.at[pass];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int t = mt * 8 + (lane >> 4) * 2 + j;
-            if (t < n) {
-                const int p = s.pair_of[at + t];
-                float& to = sums[p / topk * 16 + (lane & 15)];
-                to = __builtin_fmaf(s.c[p], acc[mt][0][2 * j] + acc[mt][0][2 * j + 1], to);
-            }
-        }
-        acc[mt][0] = f32x4{0, 0, 0, 0};
-    }
+// c times token t's sum v of a pass into the wave's rows [M][16].
+__device__ __forceinline__ void moe_add(const Passes& s, int n, int at, int t, int topk, float v, float* sums) {
+    if (t >= n) return;
+    const int p = s.pair_of[at + t];
+    float& to = sums[p / topk * 16 + (threadIdx.x & 15)];
+    to = __builtin_fmaf(s.c[p], v, to);
 }
 
 // Columns C blockIdx.x.. of y: this block's sums value(m, column) and, where
@@ -659,39 +668,45 @@ __global__ __launch_bounds__(64 * kDownWaves, 4) void k_moe_down(
     constexpr int kThreads = 64 * kDownWaves;
     extern __shared__ __attribute__((aligned(16))) float sums[];   // [waves][M][16]
     __shared__ Passes s;
-    __shared__ __attribute__((aligned(16))) char rows_lds[kDownWaves][4096];
+    constexpr int kFills = 4;
+    static_assert(kParts * kDownTok == 4 * kFills - 1, "one operand, a row left over");
+    __shared__ __attribute__((aligned(16))) char rows_lds[kDownWaves][kFills * 1024];
     static_assert(sizeof(ByExpert) <= sizeof(rows_lds), "the rows' place holds it");
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     for (int i = tid; i < kDownWaves * M * 16; i += kThreads) sums[i] = 0.0f;
-    const int passes = moe_passes<kDownWaves, 8>(s, *reinterpret_cast<ByExpert*>(rows_lds), M, E, topk, norm, logits, ids,
-                                              top, blockIdx.x == 0 && blockIdx.y == 0, ids_out, weights_out);
+    const int passes = moe_passes<kDownWaves, kDownTok>(s, *reinterpret_cast<ByExpert*>(rows_lds), M, E, topk, norm,
+                                                        logits, ids, top, blockIdx.x == 0 && blockIdx.y == 0, ids_out,
+                                                        weights_out);
 
     const W4gLayout l = w4g_layout(128 / GPU, ZP, N, F);
     const int tile = blockIdx.x, split = blockIdx.y, splits = gridDim.y;
-    const v4i hb = w4g_rows(h, 2 * M * topk, F);
+    const v4i hb = w4g_rows(h, kParts * M * topk, F);
     const int items = passes * l.units, run = (items + kDownWaves * splits - 1) / (kDownWaves * splits);
     const int begin = (split * kDownWaves + wave) * run, end = begin + run < items ? begin + run : items;
     const char* my_rows = rows_lds[wave];
     const uint32_t my_lds = lds_address(my_rows);
+    // operand rows 4 t..4 t + 2 are the parts of token t < 4, so that their sums
+    // lie in one lane, rows 3, 7 and 11 those of token 4
+    const int quad = (lane >> 2) & 3, my_row = (lane & 3) < 3 ? 3 * quad + (lane & 3) : 12 + quad;
     // the next item to load: its pass, its unit, and what changes with the pass
     int pass = begin / l.units, u = begin % l.units, fills = 0;
     const uint8_t* we = wd;
-    uint32_t row[4];
+    uint32_t row[kFills];
     W4gUnit<GPU> next[1];
     auto turn = [&]() {
         const int n = __builtin_amdgcn_readfirstlane(s.n[pass]), at = s.at[pass];
         we = wd + (size_t)__builtin_amdgcn_readfirstlane(s.expert[pass]) * l.total;
-        fills = (n + 1) >> 1;
+        fills = (kParts * n + 3) >> 2;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int r = 4 * j + (lane >> 4), t = (r >> 1) < n ? r >> 1 : n - 1;
-            row[j] = (uint32_t)(2 * s.pair_of[at + t] + (r & 1)) * (2u * F);
+        for (int j = 0; j < kFills; ++j) {
+            const int r = 4 * j + (lane >> 4), t = r / kParts < n ? r / kParts : n - 1;
+            row[j] = (uint32_t)(kParts * s.pair_of[at + t] + r % kParts) * (2u * F);
         }
     };
     auto load = [&]() {
         next[0] = w4g_load<GPU, ZP>(we, l, (size_t)tile * l.units + u, lane);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < kFills; ++j)
             if (j < fills) w4g_x_to_lds(hb, row[j] + w4g_chunk(4 * j, u, F, lane), my_lds + j * 1024);
     };
     if (begin < end) {
@@ -705,7 +720,7 @@ __global__ __launch_bounds__(64 * kDownWaves, 4) void k_moe_down(
         const W4gUnit<GPU> w[1] = {next[0]};
         u32x4 a[GPU][1][4 / GPU];
 #pragma unroll
-        for (int d = 0; d < 4; ++d) a[d / (4 / GPU)][0][d % (4 / GPU)] = w4g_operand_rows(my_rows, d, lane);
+        for (int d = 0; d < 4; ++d) a[d / (4 / GPU)][0][d % (4 / GPU)] = w4g_operand_row(my_rows, my_row, d, lane);
         w4g_wait_lds();
         const int done = pass;
         if (++u == l.units) {
@@ -718,7 +733,14 @@ __global__ __launch_bounds__(64 * kDownWaves, 4) void k_moe_down(
         }
 #pragma unroll
         for (int g = 0; g < GPU; ++g) w4g_mac<DownT<T>, GPU, ZP, 1, 1>(g, w, a[g], acc);
-        if (i + 1 == end || pass != done) moe_scatter<1>(s, done, topk, acc, sums + wave * M * 16);
+        if (i + 1 == end || pass != done) {
+            f32x4& v = acc[0][0];
+            const int n = s.n[done], at = s.at[done];
+            const float last = v[3] + __shfl_down(v[3], 16) + __shfl_down(v[3], 32);
+            moe_add(s, n, at, lane >> 4, topk, v[0] + v[1] + v[2], sums + wave * M * 16);
+            if (lane < 16) moe_add(s, n, at, 4, topk, last, sums + wave * M * 16);
+            v = f32x4{0, 0, 0, 0};
+        }
     }
     __syncthreads();
     moe_finish<T, kDownWaves, 16>(s, M, N, arrived, parts, y, [&](int m, int n) {
@@ -732,7 +754,10 @@ __global__ __launch_bounds__(64 * kDownWaves, 4) void k_moe_down(
 // The same with kWideTiles tiles of 16 columns a block, whose waves go through
 // the same items together, so that the rows of h are brought once for all of
 // them; kWideGroups such groups of waves a block, each with its share of the
-// items; passes of up to 16 tokens.
+// items; passes of up to kWideTok tokens, an operand of 16 rows for each part.
+// The rows are taken to registers before the next item's are brought to the
+// same place, which leaves room for two blocks on a CU: with two places and
+// one block 73 us where this takes 56.5.
 template <class T, int GPU, bool ZP>
 __global__ __launch_bounds__(64 * kDownWaves, 4) void k_moe_down_wide(
     const uint16_t* __restrict__ h, int M, int F, int N, const uint8_t* __restrict__ wd, int E, int topk, int norm,
@@ -740,85 +765,87 @@ __global__ __launch_bounds__(64 * kDownWaves, 4) void k_moe_down_wide(
     uint32_t* __restrict__ arrived,
     float* __restrict__ parts, uint16_t* __restrict__ y, int32_t* __restrict__ ids_out,
     float* __restrict__ weights_out) {
-    constexpr int kThreads = 64 * kDownWaves, MT = 2, kStage = kWideGroups * MT * 4096;
+    constexpr int kThreads = 64 * kDownWaves, kFills = kParts * kWideTok / 4, kRows = kFills * 1024,
+                  kMine = kFills / kWideTiles;
+    static_assert(kWideTok == 16 && kFills % kWideTiles == 0, "an operand a part, the waves share the fills evenly");
     extern __shared__ __attribute__((aligned(16))) float sums[];   // [waves][M][16]
     __shared__ Passes s;
-    __shared__ __attribute__((aligned(16))) char rows_lds[2 * kStage];
+    __shared__ __attribute__((aligned(16))) char rows_lds[kWideGroups * kRows];
     static_assert(sizeof(ByExpert) <= sizeof(rows_lds), "the rows' place holds it");
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int group = wave / kWideTiles, wn = wave % kWideTiles;
     for (int i = tid; i < kDownWaves * M * 16; i += kThreads) sums[i] = 0.0f;
-    const int passes = moe_passes<kDownWaves, 8 * MT>(s, *reinterpret_cast<ByExpert*>(rows_lds), M, E, topk, norm,
-                                                      logits, ids, top, blockIdx.x == 0 && blockIdx.y == 0, ids_out,
-                                                      weights_out);
+    const int passes = moe_passes<kDownWaves, kWideTok>(s, *reinterpret_cast<ByExpert*>(rows_lds), M, E, topk, norm,
+                                                        logits, ids, top, blockIdx.x == 0 && blockIdx.y == 0, ids_out,
+                                                        weights_out);
 
     const W4gLayout l = w4g_layout(128 / GPU, ZP, N, F);
     const int tile = blockIdx.x * kWideTiles + wn, mine = tile < l.tiles ? tile : l.tiles - 1;
     const int split = blockIdx.y, splits = gridDim.y;
-    const v4i hb = w4g_rows(h, 2 * M * topk, F);
+    const v4i hb = w4g_rows(h, kParts * M * topk, F);
     const int items = passes * l.units, run = (items + kWideGroups * splits - 1) / (kWideGroups * splits);
     const int begin = (split * kWideGroups + group) * run, end = begin + run < items ? begin + run : items;
-    const uint32_t lds0 = lds_address(rows_lds) + group * MT * 4096;
+    const char* my_rows = rows_lds + group * kRows;
+    const uint32_t my_lds = lds_address(my_rows);
     int pass = begin / l.units, u = begin % l.units, n = 0;
     const uint8_t* we = wd;
-    uint32_t row[MT];   // of this wave's instructions: rows 4 wn.. of both operands
+    uint32_t row[kMine];   // of this wave's instructions wn, wn + kWideTiles..
     W4gUnit<GPU> next[1];
     auto turn = [&]() {
         n = __builtin_amdgcn_readfirstlane(s.n[pass]);
         const int at = s.at[pass];
         we = wd + (size_t)__builtin_amdgcn_readfirstlane(s.expert[pass]) * l.total;
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-            const int r = 16 * mt + 4 * wn + (lane >> 4), t = (r >> 1) < n ? r >> 1 : n - 1;
-            row[mt] = (uint32_t)(2 * s.pair_of[at + t] + (r & 1)) * (2u * F);
+        for (int i = 0; i < kMine; ++i) {
+            const int r = 4 * (i * kWideTiles + wn) + (lane >> 4), p = r / kWideTok, t = r % kWideTok;
+            row[i] = (uint32_t)(kParts * s.pair_of[at + (t < n ? t : n - 1)] + p) * (2u * F);
         }
     };
-    auto load = [&](int stage) {
+    auto load = [&]() {
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-            if (8 * mt + 2 * wn < n)
-                w4g_x_to_lds(hb, row[mt] + w4g_chunk(4 * wn, u, F, lane), lds0 + stage * kStage + mt * 4096 + wn * 1024);
+        for (int i = 0; i < kMine; ++i) {
+            const int j = i * kWideTiles + wn;
+            if (4 * j % kWideTok < n) w4g_x_to_lds(hb, row[i] + w4g_chunk(4 * j, u, F, lane), my_lds + j * 1024);
+        }
         next[0] = w4g_load<GPU, ZP>(we, l, (size_t)mine * l.units + u, lane);
     };
     if (begin < end) {
         turn();
-        load(0);
+        load();
     }
 
-    f32x4 acc[MT][1];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) acc[mt][0] = f32x4{0, 0, 0, 0};
+    f32x4 acc[1][1] = {{f32x4{0, 0, 0, 0}}};
     for (int i = begin; i < begin + run; ++i) {   // as many turns for every wave: they meet in each
         w4g_wait();
-        w4g_barrier();   // the item's rows are there, the other stage has been read
-        if (i >= end) continue;
-        const int stage = (i - begin) & 1;
+        w4g_barrier();   // the item's rows are there
         const W4gUnit<GPU> w[1] = {next[0]};
-        const int done = pass, rows = n;
+        u32x4 a[GPU][1][kParts * (4 / GPU)];
+#pragma unroll
+        for (int p = 0; p < kParts; ++p)
+#pragma unroll
+            for (int d = 0; d < 4; ++d)
+                a[d / (4 / GPU)][0][p * (4 / GPU) + d % (4 / GPU)] = w4g_operand_rows(my_rows + p * 4096, d, lane);
+        w4g_barrier();   // and have been read
+        if (i >= end) continue;
+        const int done = pass;
         if (++u == l.units) {
             u = 0;
             ++pass;
         }
         if (i + 1 < end) {
             if (pass != done) turn();
-            load(stage ^ 1);
+            load();
         }
-        const char* at = rows_lds + group * MT * 4096 + stage * kStage;
-        auto use = [&](auto mt_count) {
-            constexpr int C = decltype(mt_count)::value;
 #pragma unroll
-            for (int g = 0; g < GPU; ++g) {
-                u32x4 a[C][4 / GPU];
+        for (int g = 0; g < GPU; ++g) w4g_mac<DownT<T>, GPU, ZP, 1, 1, kParts>(g, w, a[g], acc);
+        if (i + 1 == end || pass != done) {
+            f32x4& v = acc[0][0];
+            const int n_done = s.n[done], at = s.at[done];
 #pragma unroll
-                for (int mt = 0; mt < C; ++mt)
-#pragma unroll
-                    for (int d = 0; d < 4 / GPU; ++d) a[mt][d] = w4g_operand_rows(at + mt * 4096, g * (4 / GPU) + d, lane);
-                w4g_mac<DownT<T>, GPU, ZP, C, 1>(g, w, a, reinterpret_cast<f32x4(&)[C][1]>(acc));
-            }
-        };
-        if (rows <= 8) use(std::integral_constant<int, 1>{});
-        else use(std::integral_constant<int, 2>{});
-        if (i + 1 == end || pass != done) moe_scatter<MT>(s, done, topk, acc, sums + wave * M * 16);
+            for (int t = 0; t < 4; ++t)
+                moe_add(s, n_done, at, (lane >> 4) * 4 + t, topk, v[t], sums + wave * M * 16);
+            v = f32x4{0, 0, 0, 0};
+        }
     }
     __syncthreads();
     moe_finish<T, kDownWaves, 16 * kWideTiles>(s, M, N, arrived, parts, y, [&](int m, int c) {

@@ -162,9 +162,10 @@ __device__ __forceinline__ uint32_t w4g_zero(const W4gUnit<GPU>& w, int g, int l
 // (zero where there is no such k; rows do not mix, so what a row that does
 // not exist holds is no matter); acc in the MFMA's C layout: column
 // n = lane % 16, rows m = 4 (lane / 16) + i.  The group's sum is held in
-// float32 and scaled there.
-template <class T, int GPU, bool ZP, int MT, int NT>
-__device__ __forceinline__ void w4g_mac(int g, const W4gUnit<GPU> (&w)[NT], const u32x4 (&a)[MT][4 / GPU],
+// float32 and scaled there.  P: x is the sum of P values in T, part p of step
+// s in a[mt][p SPG + s]; their products meet in one sum.
+template <class T, int GPU, bool ZP, int MT, int NT, int P = 1>
+__device__ __forceinline__ void w4g_mac(int g, const W4gUnit<GPU> (&w)[NT], const u32x4 (&a)[MT][P * (4 / GPU)],
                                         f32x4 (&acc)[MT][NT]) {
     constexpr int SPG = 4 / GPU;   // MFMA steps per group
     const int lane = threadIdx.x & 63;
@@ -187,12 +188,12 @@ __device__ __forceinline__ void w4g_mac(int g, const W4gUnit<GPU> (&w)[NT], cons
         for (int mt = 0; mt < MT; ++mt) {
             f32x4 xs = {0, 0, 0, 0};
 #pragma unroll
-            for (int s = 0; s < SPG; ++s) xs = T::mfma(a[mt][s], minus, xs);
+            for (int s = 0; s < P * SPG; ++s) xs = T::mfma(a[mt][s], minus, xs);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 f32x4 t = {0, 0, 0, 0};
 #pragma unroll
-                for (int s = 0; s < SPG; ++s) t = T::mfma(a[mt][s], b[nt][s], t);
+                for (int s = 0; s < P * SPG; ++s) t = T::mfma(a[mt][s], b[nt][s % SPG], t);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     acc[mt][nt][i] = __builtin_fmaf(s16[nt], __builtin_fmaf(xs[i], z[nt], t[i]), acc[mt][nt][i]);
@@ -209,7 +210,9 @@ __device__ __forceinline__ void w4g_mac(int g, const W4gUnit<GPU> (&w)[NT], cons
             for (int s = 0; s < SPG; ++s) {
                 b[nt][s] = T::operand(w[nt].codes[g * SPG + s], 0xBC00BC00u + z * 0x00400040u);
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt) t[mt] = T::mfma(a[mt][s], b[nt][s], t[mt]);
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int p = 0; p < P; ++p) t[mt] = T::mfma(a[mt][p * SPG + s], b[nt][s], t[mt]);
             }
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
@@ -264,9 +267,12 @@ __device__ __forceinline__ uint32_t w4g_chunk(int r0, int u, int K, int lane) {
     const uint32_t b = u * 256u + (((uint32_t)lane & 15u) ^ (row & 15u)) * 16u;
     return b < 2u * K ? b : 2u * K - 16u;
 }
-// Step d's operand of the 16 rows at `rows`.
+// Step d's operand of this lane's row r of those at `rows`; of the first 16.
+__device__ __forceinline__ u32x4 w4g_operand_row(const char* rows, int r, int d, int lane) {
+    return *reinterpret_cast<const u32x4*>(rows + r * 256 + (((d * 4 + (lane >> 4)) ^ (r & 15)) * 16));
+}
 __device__ __forceinline__ u32x4 w4g_operand_rows(const char* rows, int d, int lane) {
-    return *reinterpret_cast<const u32x4*>(rows + (lane & 15) * 256 + (((d * 4 + (lane >> 4)) ^ (lane & 15)) * 16));
+    return w4g_operand_row(rows, lane & 15, d, lane);
 }
 
 }  // namespace cr
