@@ -270,11 +270,13 @@ __device__ __forceinline__ int moe_choice(Choice& c, int M, int E, int topk, int
     return __builtin_amdgcn_readfirstlane(c.chosen);
 }
 
-// silu(g) u into element n of pair p's h: the upper 8 bits of its significand,
-// the next 8 and the last 8, each a bf16 value; the differences are exact
-// (down to bf16's smallest number).  An infinity has no rest.
+// silu(16 g) 16 u, of the products' accumulators g and u, into element n of
+// pair p's h: the upper 8 bits of its significand, the next 8 and the last 8,
+// each a bf16 value; the differences are exact (down to bf16's smallest
+// number).  An infinity has no rest.
 __device__ __forceinline__ void moe_store_h(uint16_t* h, int p, int F, int n, float g, float u) {
-    float v = g / (1.0f + expf(-g)) * u;
+    g *= 16.0f;
+    float v = g / (1.0f + expf(-g)) * (16.0f * u);
     uint16_t* to = h + (size_t)p * kParts * F + n;
 #pragma unroll
     for (int i = 0; i < kParts; ++i) {
@@ -616,8 +618,8 @@ __device__ __forceinline__ void moe_add(const Passes& s, int n, int at, int t, i
     to = __builtin_fmaf(s.c[p], v, to);
 }
 
-// Columns C blockIdx.x.. of y: this block's sums value(m, column) and, where
-// more blocks share the columns, theirs.
+// Columns C blockIdx.x.. of y: 16 times this block's sums value(m, column) and,
+// where more blocks share the columns, theirs.
 template <class T, int WAVES, int C, class V>
 __device__ __forceinline__ void moe_finish(Passes& s, int M, int N, uint32_t* arrived, float* parts, uint16_t* y,
                                            V value) {
@@ -628,7 +630,7 @@ __device__ __forceinline__ void moe_finish(Passes& s, int M, int N, uint32_t* ar
         const size_t n = (size_t)blockIdx.x * C + i % C;
         if (n >= (size_t)N) continue;
         if (splits == 1)
-            y[(size_t)m * N + n] = T::from_f32(value(m, i % C));
+            y[(size_t)m * N + n] = T::from_f32(16.0f * value(m, i % C));
         else
             __hip_atomic_store(&parts[((size_t)blockIdx.y * M + m) * N + n], value(m, i % C), __ATOMIC_RELAXED,
                                __HIP_MEMORY_SCOPE_AGENT);
@@ -652,7 +654,7 @@ __device__ __forceinline__ void moe_finish(Passes& s, int M, int N, uint32_t* ar
                                         __HIP_MEMORY_SCOPE_AGENT);
 #pragma unroll
         for (int j = 0; j < kMaxSplits; ++j) v += j < splits ? part[j] : 0.0f;
-        y[(size_t)m * N + n] = T::from_f32(v);
+        y[(size_t)m * N + n] = T::from_f32(16.0f * v);
     }
 }
 

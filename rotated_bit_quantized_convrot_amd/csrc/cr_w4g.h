@@ -27,8 +27,9 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 
 // The 16-bit types: the MFMA, conversions, and an MFMA operand of 8 codes.
-// The operand holds (q - z) / 16, exact in both types; the factor 16 goes
-// into the group's scale.
+// The operand holds (q - z) / 16, exact in both types; the accumulators hold
+// a sixteenth of the sums, and the factor 16 is left to who takes them (in the
+// scales it would make infinities of those from 2^124 up).
 //   fp16  (1 + q / 16) is the code put into the top mantissa bits of 1.0, and
 //         one packed add takes 1 + z / 16 off.
 //   bf16  has no packed add; v_cvt_off_f32_i4 turns a two's-complement nibble
@@ -145,11 +146,11 @@ __device__ __forceinline__ W4gUnit<GPU> w4g_load(const uint8_t* w, const W4gLayo
     }
     return r;
 }
-// 16 times the scale, and the zero point, of group g.
+// The scale and the zero point of group g.
 template <class T, int GPU>
-__device__ __forceinline__ float w4g_scale16(const W4gUnit<GPU>& w, int g, int lane) {
+__device__ __forceinline__ float w4g_scale(const W4gUnit<GPU>& w, int g, int lane) {
     const uint32_t v = GPU == 1 ? w.scale[0] >> (16 * (lane & 1)) : w.scale[g / 2] >> (16 * (g % 2));
-    return 16.0f * T::to_f32(v & 0xFFFFu);
+    return T::to_f32(v & 0xFFFFu);
 }
 template <int GPU>
 __device__ __forceinline__ uint32_t w4g_zero(const W4gUnit<GPU>& w, int g, int lane) {
@@ -157,7 +158,7 @@ __device__ __forceinline__ uint32_t w4g_zero(const W4gUnit<GPU>& w, int g, int l
     return (w.zero >> (row + 4 * g)) & 15u;
 }
 
-// acc[mt][nt] += x W^T over group g of a unit.  a[mt][s]: x rows
+// acc[mt][nt] += x W^T / 16 over group g of a unit.  a[mt][s]: x rows
 // 16 mt + lane % 16 at k = 32 (g SPG + s) + 8 (lane / 16) + 0..7 of the unit
 // (zero where there is no such k; rows do not mix, so what a row that does
 // not exist holds is no matter); acc in the MFMA's C layout: column
@@ -170,9 +171,9 @@ __device__ __forceinline__ void w4g_mac(int g, const W4gUnit<GPU> (&w)[NT], cons
     constexpr int SPG = 4 / GPU;   // MFMA steps per group
     const int lane = threadIdx.x & 63;
     u32x4 b[NT][SPG];
-    float s16[NT];
+    float scale[NT];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) s16[nt] = w4g_scale16<T, GPU>(w[nt], g, lane);
+    for (int nt = 0; nt < NT; ++nt) scale[nt] = w4g_scale<T, GPU>(w[nt], g, lane);
     if constexpr (ZP && !T::kZeroInOperand) {
         // -sum x of the group comes from one more MFMA, against -1, in the lanes that need it; the
         // operands are made first, so that one row tile's sums are alive at a time
@@ -196,7 +197,7 @@ __device__ __forceinline__ void w4g_mac(int g, const W4gUnit<GPU> (&w)[NT], cons
                 for (int s = 0; s < P * SPG; ++s) t = T::mfma(a[mt][s], b[nt][s % SPG], t);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    acc[mt][nt][i] = __builtin_fmaf(s16[nt], __builtin_fmaf(xs[i], z[nt], t[i]), acc[mt][nt][i]);
+                    acc[mt][nt][i] = __builtin_fmaf(scale[nt], __builtin_fmaf(xs[i], z[nt], t[i]), acc[mt][nt][i]);
             }
         }
     } else {
@@ -217,7 +218,7 @@ __device__ __forceinline__ void w4g_mac(int g, const W4gUnit<GPU> (&w)[NT], cons
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) acc[mt][nt][i] = __builtin_fmaf(s16[nt], t[mt][i], acc[mt][nt][i]);
+                for (int i = 0; i < 4; ++i) acc[mt][nt][i] = __builtin_fmaf(scale[nt], t[mt][i], acc[mt][nt][i]);
         }
     }
 }

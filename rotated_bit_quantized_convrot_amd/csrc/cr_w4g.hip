@@ -251,6 +251,7 @@ __global__ __launch_bounds__(64 * WM * WN * KG) void k_w4g_linear(const uint16_t
 #pragma unroll
         for (int g = 0; g < KG; ++g)
             v += part[((g * (WN * NT) + (n >> 4)) * (WM * MT) + (m >> 4)) * 64 + ((m & 15) >> 2) * 16 + (n & 15)][m & 3];
+        v *= 16.0f;
         if (bias != nullptr) v += T::to_f32(bias[gn]);
         y[(size_t)(m0 + m) * N + gn] = T::from_f32(v);
     }
