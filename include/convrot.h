@@ -326,8 +326,10 @@ cr_status cr_mlp_w4a4(const void* x_bf16, int M, int K, const void* wg_packed, c
  * activations, scales, bias and outputs of a call: CR_BF16 or CR_FP16
  * (CR_ERR_KIND otherwise).  Products are exact and sums are held in float32,
  * group by group, each multiplied by its scale there; the only rounding to
- * 16 bits is the output's.  An x row with an infinity or a NaN gives
- * infinities and NaN in its own row of y and touches no other. */
+ * 16 bits is the output's.  Where that leaves an infinity or a NaN the value
+ * is formed again in float64 from the definition, so that y is infinite or NaN
+ * only where the definition is, or passes the range of float32 or of the type.
+ * An infinity or a NaN in a row of x touches no other row of y. */
 #define CR_BF16 0
 #define CR_FP16 1
 

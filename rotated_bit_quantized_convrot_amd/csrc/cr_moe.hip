@@ -270,13 +270,11 @@ __device__ __forceinline__ int moe_choice(Choice& c, int M, int E, int topk, int
     return __builtin_amdgcn_readfirstlane(c.chosen);
 }
 
-// silu(16 g) 16 u, of the products' accumulators g and u, into element n of
-// pair p's h: the upper 8 bits of its significand, the next 8 and the last 8,
+// silu(g) u into element n of pair p's h: the upper 8 bits of its significand, the next 8 and the last 8,
 // each a bf16 value; the differences are exact (down to bf16's smallest
 // number).  An infinity has no rest.
 __device__ __forceinline__ void moe_store_h(uint16_t* h, int p, int F, int n, float g, float u) {
-    g *= 16.0f;
-    float v = g / (1.0f + expf(-g)) * (16.0f * u);
+    float v = g / (1.0f + expf(-g)) * u;
     uint16_t* to = h + (size_t)p * kParts * F + n;
 #pragma unroll
     for (int i = 0; i < kParts; ++i) {
@@ -284,6 +282,22 @@ __device__ __forceinline__ void moe_store_h(uint16_t* h, int p, int F, int n, fl
         to[(size_t)i * F] = (uint16_t)(top >> 16);
         v = (top & 0x7F800000u) == 0x7F800000u ? 0.0f : v - __uint_as_float(top);
     }
+}
+
+// Element f of pair p's h from the products' definition: for accumulators
+// that are not finite.  Kept out of the loops that store the others: inlined
+// there once for each of their elements, it took 81 us where this takes 73 (64
+// tokens, 2 of 8 experts of 5632 x 4096 with zero points; 69 with neither).
+template <class T, int GPU, bool ZP>
+__device__ __forceinline__ void moe_hidden_defined(const uint16_t* x, int K, int F, const uint8_t* wg, const uint8_t* wu,
+                                                   const W4gLayout& l, uint16_t* h, int p, int f) {
+    float v[2] = {0.0f, 0.0f};
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i) {
+        v[0] = v[1];
+        v[1] = w4g_defined_row<T, GPU, ZP>(x, K, i ? wu : wg, l, f);
+    }
+    moe_store_h(h, p, F, f, v[0], v[1]);
 }
 
 template <class T, int GPU, bool ZP>
@@ -312,6 +326,8 @@ __global__ __launch_bounds__(64 * kUpWaves, 4) void k_moe_gate_up(const uint16_t
     const bool work = tile < l.tiles;
     const char* my_rows = rows_lds[wave];
     const uint32_t my_lds = lds_address(my_rows);
+    uint32_t again = 0;   // this thread's elements to be formed from the definition: four for each 16 tokens
+    static_assert(256 * (kUpWaves / 2) <= 4 * kThreads && kChunk <= 128, "its bits");
     for (int p0 = 0; p0 < n_tok; p0 += 16) {
         const int n = n_tok - p0 < 16 ? n_tok - p0 : 16, fills = (n + 3) >> 2;
         uint32_t row[4];
@@ -350,14 +366,16 @@ __global__ __launch_bounds__(64 * kUpWaves, 4) void k_moe_gate_up(const uint16_t
         }
         auto store = [&](int m, int n, float g, float u) {
             const int t = c.list[p0 + m];
-            moe_store_h(h, t * topk + c.rank_of[t], F, n, g, u);
+            moe_store_h(h, t * topk + c.rank_of[t], F, n, 16.0f * g, 16.0f * u);
+            return w4g_finite(16.0f * g) && w4g_finite(16.0f * u);
         };
         if (ks == 1) {
             if (work) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int m = (lane >> 4) * 4 + i;
-                    if (p0 + m < n_tok) store(m, tile * 16 + (lane & 15), acc[0][0][0][i], acc[1][0][0][i]);
+                    if (p0 + m < n_tok && !store(m, tile * 16 + (lane & 15), acc[0][0][0][i], acc[1][0][0][i]))
+                        again |= 1u << (p0 / 4 + i);
                 }
             }
             continue;
@@ -374,9 +392,16 @@ __global__ __launch_bounds__(64 * kUpWaves, 4) void k_moe_gate_up(const uint16_t
                 g += part[wv][0][(m >> 2) * 16 + n][m & 3];
                 u += part[wv][1][(m >> 2) * 16 + n][m & 3];
             }
-            store(m, t * 16 + n, g, u);
+            if (!store(m, t * 16 + n, g, u)) again |= 1u << (p0 / 4 + i / kThreads);
         }
         __syncthreads();
+    }
+    for (; again; again &= again - 1) {
+        const int b = __builtin_ctz(again), i = tid + kThreads * (b & 3);
+        const int m = b / 4 * 16 + (ks == 1 ? (lane >> 4) * 4 + (b & 3) : (i >> 4) & 15);
+        const int f = ks == 1 ? tile * 16 + (lane & 15) : (blockIdx.x * (kUpWaves >> ks_log2) + (i >> 8)) * 16 + (i & 15);
+        const int t = c.list[m];
+        moe_hidden_defined<T, GPU, ZP>(x + (size_t)t * K, K, F, wg, wu, l, h, t * topk + c.rank_of[t], f);
     }
 }
 
@@ -406,6 +431,7 @@ __global__ __launch_bounds__(64 * kManyWaves, 4) void k_moe_gate_up_many(
     const v4i xb = w4g_rows(x, M, K);
     const int tile = blockIdx.x * kManyWaves + wave, mine = tile < l.tiles ? tile : l.tiles - 1;
     const uint32_t lds0 = lds_address(rows_lds);
+    uint32_t again = 0;   // this lane's elements to be formed from the definition: four for each 16 tokens
     auto run = [&](auto mt_count, int p0) {
         constexpr int MT = decltype(mt_count)::value;
         // wave w brings rows 4 w..4 w + 3, and 16 more than that
@@ -454,12 +480,19 @@ __global__ __launch_bounds__(64 * kManyWaves, 4) void k_moe_gate_up_many(
                 const int m = mt * 16 + (lane >> 4) * 4 + i;
                 if (m >= n) continue;
                 const int t = c.list[p0 + m];
-                moe_store_h(h, t * topk + c.rank_of[t], F, tile * 16 + (lane & 15), acc[mt][0][i], acc[mt][1][i]);
+                const float g = 16.0f * acc[mt][0][i], v = 16.0f * acc[mt][1][i];
+                moe_store_h(h, t * topk + c.rank_of[t], F, tile * 16 + (lane & 15), g, v);
+                if (!w4g_finite(g) || !w4g_finite(v)) again |= 1u << (p0 / 4 + mt * 4 + i);
             }
     };
     for (int p0 = 0; p0 < n_tok; p0 += 32) {
         if (n_tok - p0 <= 16) run(std::integral_constant<int, 1>{}, p0);
         else run(std::integral_constant<int, 2>{}, p0);
+    }
+    for (; again; again &= again - 1) {
+        const int b = __builtin_ctz(again), t = c.list[b / 4 * 16 + (lane >> 4) * 4 + (b & 3)];
+        moe_hidden_defined<T, GPU, ZP>(x + (size_t)t * K, K, F, wg, wu, l, h, t * topk + c.rank_of[t],
+                                       tile * 16 + (lane & 15));
     }
 }
 
@@ -618,21 +651,48 @@ __device__ __forceinline__ void moe_add(const Passes& s, int n, int at, int t, i
     to = __builtin_fmaf(s.c[p], v, to);
 }
 
+// y[m,n] by the definition, for what is not finite otherwise.
+template <class T, int GPU, bool ZP>
+__device__ __forceinline__ float moe_defined(const Passes& s, const uint16_t* h, int F, const uint8_t* wd,
+                                             const W4gLayout& l, const int32_t* ids, int topk, int m, int n) {
+    double y = 0.0;
+    for (int p = m * topk; p < (m + 1) * topk && y == y; ++p) {
+        const double c = s.c[p];
+        if (c == c)   // a NaN of the softmax needs no sum
+            y += c * w4g_defined<T, GPU, ZP>(wd + (size_t)ids[p] * l.total, l, n, F, [&](int k, float (&v)[8]) {
+                const uint16_t* hp = h + (size_t)p * kParts * F + k;
+                w4g_values<Bf16>(hp, v);
+#pragma unroll
+                for (int i = 1; i < kParts; ++i) {
+                    float part[8];
+                    w4g_values<Bf16>(hp + (size_t)i * F, part);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[j] += part[j];
+                }
+            });
+        else
+            y = c;
+    }
+    return (float)y;
+}
+
 // Columns C blockIdx.x.. of y: 16 times this block's sums value(m, column) and,
-// where more blocks share the columns, theirs.
-template <class T, int WAVES, int C, class V>
+// where more blocks share the columns, theirs; defined(m, n) where that is not
+// finite.
+template <class T, int WAVES, int C, class V, class D>
 __device__ __forceinline__ void moe_finish(Passes& s, int M, int N, uint32_t* arrived, float* parts, uint16_t* y,
-                                           V value) {
+                                           V value, D defined) {
     constexpr int kThreads = 64 * WAVES;
     const int tid = threadIdx.x, splits = gridDim.y;
     for (int i = tid; i < M * C; i += kThreads) {
         const int m = i / C;
         const size_t n = (size_t)blockIdx.x * C + i % C;
         if (n >= (size_t)N) continue;
+        const float v = value(m, i % C);
         if (splits == 1)
-            y[(size_t)m * N + n] = T::from_f32(16.0f * value(m, i % C));
+            y[(size_t)m * N + n] = T::from_f32(w4g_finite(16.0f * v) ? 16.0f * v : defined(m, (int)n));
         else
-            __hip_atomic_store(&parts[((size_t)blockIdx.y * M + m) * N + n], value(m, i % C), __ATOMIC_RELAXED,
+            __hip_atomic_store(&parts[((size_t)blockIdx.y * M + m) * N + n], v, __ATOMIC_RELAXED,
                                __HIP_MEMORY_SCOPE_AGENT);
     }
     if (splits == 1) return;
@@ -654,7 +714,7 @@ __device__ __forceinline__ void moe_finish(Passes& s, int M, int N, uint32_t* ar
                                         __HIP_MEMORY_SCOPE_AGENT);
 #pragma unroll
         for (int j = 0; j < kMaxSplits; ++j) v += j < splits ? part[j] : 0.0f;
-        y[(size_t)m * N + n] = T::from_f32(16.0f * v);
+        y[(size_t)m * N + n] = T::from_f32(w4g_finite(16.0f * v) ? 16.0f * v : defined(m, (int)n));
     }
 }
 
@@ -750,7 +810,7 @@ __global__ __launch_bounds__(64 * kDownWaves, 4) void k_moe_down(
 #pragma unroll
         for (int wv = 0; wv < kDownWaves; ++wv) v += sums[(wv * M + m) * 16 + n];
         return v;
-    });
+    }, [&](int m, int n) { return moe_defined<T, GPU, ZP>(s, h, F, wd, l, ids, topk, m, n); });
 }
 
 // The same with kWideTiles tiles of 16 columns a block, whose waves go through
@@ -855,7 +915,7 @@ __global__ __launch_bounds__(64 * kDownWaves, 4) void k_moe_down_wide(
 #pragma unroll
         for (int g = 0; g < kWideGroups; ++g) v += sums[((g * kWideTiles + (c >> 4)) * M + m) * 16 + (c & 15)];
         return v;
-    });
+    }, [&](int m, int n) { return moe_defined<T, GPU, ZP>(s, h, F, wd, l, ids, topk, m, n); });
 }
 
 template <class T, int GPU, bool ZP>

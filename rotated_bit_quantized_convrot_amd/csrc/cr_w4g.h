@@ -223,6 +223,52 @@ __device__ __forceinline__ void w4g_mac(int g, const W4gUnit<GPU> (&w)[NT], cons
     }
 }
 
+// 8 values of T.
+template <class T>
+__device__ __forceinline__ void w4g_values(const uint16_t* p, float (&v)[8]) {
+    const u32x4 raw = *reinterpret_cast<const u32x4*>(p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = T::to_f32(raw[i] & 0xFFFFu);
+        v[2 * i + 1] = T::to_f32(raw[i] >> 16);
+    }
+}
+
+// sum_k x[k] W[n,k] by the definition, in float64; x8(k, v) gives x[k..k + 7].
+// For the sums that w4g_mac leaves infinite or NaN, and only for those: a
+// group's own sum, taken before its scale, can overflow where the result does
+// not; an infinity times (q - 8) / 16 and times (8 - z) / 16 can cancel; and
+// the chunks past K meet the row's last values with a scale of 0.  Ends at the
+// first NaN.
+template <class T, int GPU, bool ZP, class X>
+__device__ __forceinline__ double w4g_defined(const uint8_t* w, const W4gLayout& l, int n, int K, X x8) {
+    const int row = n & 15;
+    double sum = 0.0;
+    for (int k = 0; k < K && sum == sum; k += 8) {
+        const size_t tu = (size_t)(n >> 4) * l.units + (k >> 7);
+        const int g = (k & 127) / (128 / GPU);
+        const uint32_t c =
+            *reinterpret_cast<const uint32_t*>(w + tu * 1024 + (row + 2 * (k & 24)) * 16 + ((k >> 5) & 3) * 4) ^ 0x88888888u;
+        const double s = T::to_f32(*reinterpret_cast<const uint16_t*>(w + l.scales + ((tu * 16 + row) * GPU + g) * 2));
+        int z = 8;
+        if constexpr (ZP) z = (w[l.zeros + (tu * 16 + row) * w4g_zero_bytes(GPU) + (g >> 1)] >> (4 * (g & 1))) & 15;
+        float v[8];
+        x8(k, v);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            sum = fma((double)v[2 * j], s * ((int)(c >> (4 * j) & 15u) - z), sum);
+            sum = fma((double)v[2 * j + 1], s * ((int)(c >> (16 + 4 * j) & 15u) - z), sum);
+        }
+    }
+    return sum;
+}
+__device__ __forceinline__ bool w4g_finite(float v) { return fabsf(v) < __builtin_inff(); }
+// The same with x a row of T.
+template <class T, int GPU, bool ZP>
+__device__ __forceinline__ float w4g_defined_row(const uint16_t* x, int K, const uint8_t* w, const W4gLayout& l, int n) {
+    return (float)w4g_defined<T, GPU, ZP>(w, l, n, K, [&](int k, float (&v)[8]) { w4g_values<T>(x + k, v); });
+}
+
 // Rows of x behind a buffer descriptor.  One tile's rows, or one pass's: the
 // offsets stay in 32 bits whatever the matrix.
 __device__ __forceinline__ v4i w4g_rows(const uint16_t* x, int rows, int K) {

@@ -252,6 +252,7 @@ __global__ __launch_bounds__(64 * WM * WN * KG) void k_w4g_linear(const uint16_t
         for (int g = 0; g < KG; ++g)
             v += part[((g * (WN * NT) + (n >> 4)) * (WM * MT) + (m >> 4)) * 64 + ((m & 15) >> 2) * 16 + (n & 15)][m & 3];
         v *= 16.0f;
+        if (!w4g_finite(v)) v = w4g_defined_row<T, GPU, ZP>(x + (size_t)(m0 + m) * K, K, w, l, (int)gn);
         if (bias != nullptr) v += T::to_f32(bias[gn]);
         y[(size_t)(m0 + m) * N + gn] = T::from_f32(v);
     }
