@@ -341,7 +341,8 @@ size_t cr_w4g_packed_bytes(int group, int zeros, int N, int K);
  * group by group (float32, IEEE divisions, rint half to even):
  *   zeros NULL  s = T(absmax / 7), q = clamp(rint(w / s), -8, 7) + 8
  *               (8 where s = 0);
- *   otherwise   lo = min(0, min w), hi = max(0, max w), s = T((hi - lo) / 15),
+ *   otherwise   lo = min(0, min w), hi = max(0, max w), s = T((hi - lo) / 15)
+ *               (finite also where hi - lo passes float32),
  *               z = clamp(rint(-lo / s), 0, 15),
  *               q = clamp(rint(w / s) + z, 0, 15) (both 0 where s = 0).
  *   codes  [N,K/2] uint8, two to a byte, low nibble = even k   (out)

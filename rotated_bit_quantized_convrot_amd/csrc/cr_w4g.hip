@@ -57,7 +57,14 @@ __global__ __launch_bounds__(256) void k_w4g_encode(const uint16_t* __restrict__
         lo = fminf(lo, lane_xor<8>(lo));
         hi = fmaxf(hi, lane_xor<8>(hi));
     }
-    const uint16_t s16 = T::from_f32(ZP ? (hi - lo) / 15.0f : fmaxf(hi, -lo) / 7.0f);
+    float step = fmaxf(hi, -lo) / 7.0f;
+    if constexpr (ZP) {
+        // bf16 values can lie further apart than float32 reaches: then in halves
+        const bool far = hi - lo == __builtin_inff();
+        step = (far ? 0.5f * hi - 0.5f * lo : hi - lo) / 15.0f;
+        step = far ? 2.0f * step : step;
+    }
+    const uint16_t s16 = T::from_f32(step);
     const float s = T::to_f32(s16);
     float z = 0.0f, q[8];
     if (s > 0x1p-100f && s < 0x1p100f) {

@@ -129,3 +129,25 @@ def test_moe_of_the_largest_values(zeros, M, K, F, E, topk, which):
         ref, rids, _, _, tol = R.moe(x, r, gate, up, down, topk, True)
     assert np.array_equal(ids.cpu().numpy(), rids) and np.isfinite(ref).all()
     assert (np.abs(y.cpu().double().numpy() - ref) <= tol).all()
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("zeros", [False, True])
+def test_encode_the_largest_weights(group, zeros):
+    """Weights up to bf16's largest number in either sign: the codes of the same weights 2^-10 times as large,
+    scales 2^10 times theirs; and the linear on them."""
+    rng = np.random.default_rng(group)
+    w = torch.from_numpy(rng.uniform(-1, 1, size=(33, 256)) * 2.0 ** 127).to(BF16)
+    w[:, ::group] = torch.finfo(BF16).max
+    w[1:, 5::group] = torch.finfo(BF16).min
+    c, s, z = crp.encode_w4g(w.cuda(), group, zeros)
+    c1, s1, z1 = crp.encode_w4g((w.float() * 2.0 ** -10).to(BF16).cuda(), group, zeros)
+    for a, b in zip((c1, s1, z1), R.encode((w.float() * 2.0 ** -10).to(BF16), group, zeros)):
+        assert (a is None) == (b is None) and (a is None or torch.equal(a.cpu(), b))
+    assert torch.isfinite(s.float()).all()
+    assert torch.equal(c, c1) and torch.equal(s.float(), s1.float() * 2.0 ** 10)
+    assert z is None or torch.equal(z, z1)
+    x = (activations(3, 256, BF16, 1).float() * 2.0 ** -20).to(BF16)
+    ref, tol = R.linear(x, tuple(None if t is None else t.cpu() for t in (c, s, z)))
+    y = crp.linear_w4g(x.cuda(), crp.pack_weight_w4g(c, s, z), 33, group, zeros=zeros)
+    assert (np.abs(y.cpu().double().numpy() - ref) <= tol).all()
