@@ -616,13 +616,17 @@ def pack_weight_w4g(codes: torch.Tensor, scales: torch.Tensor, zeros: Optional[t
 
 
 def _check_w4g(packed, name: str, device, count: int, N: int, K: int, group: int, zeros: bool):
-    """Refuse packed weights smaller than their layout (the kernels would
-    read past their end); sizes the library rejects give 0 bytes here and are
-    left to its own error."""
+    """Refuse packed weights of another size than their layout's: smaller ones
+    would be read past their end, and those packed with another group, with or
+    without zero points, or for another number of weights give wrong numbers
+    (weights of up to some 15 tiles of 16 x 128 can have the same size for
+    either; their caller has to know).  Sizes the library rejects give 0 bytes
+    here and are left to its own error."""
     _here(packed, name, torch.uint8, device)
     need = count * w4g_packed_bytes(group, zeros, N, K)
-    if packed.numel() < need:
-        raise ValueError(f"{name} has {packed.numel()} bytes, {count} x N={N} K={K} group={group} needs {need}")
+    if need and packed.numel() != need:
+        raise ValueError(f"{name} has {packed.numel()} bytes, {count} x N={N} K={K} group={group} zeros={bool(zeros)} "
+                         f"needs {need}")
 
 
 def linear_w4g(x, packed, N, group, zeros=False, bias=None, out=None):
