@@ -148,9 +148,12 @@ __device__ __forceinline__ u64 order_key(double v) {
 constexpr int kUpWaves = 8;
 
 struct Choice {
-    int16_t above[8][kMoeMaxExperts];        // by wave and expert: the logits above its own in the wave's share
     int16_t rank_of[kChunk], list[kChunk];   // of the block's expert: rank by token (-1: not chosen), tokens
-    int found, chosen;
+    int chosen;
+};
+struct ByRank {
+    int16_t above[kUpWaves][kMoeMaxExperts];   // by wave and expert: the logits above its own in the wave's share
+    int found;
 };
 // The expert of rank `want` in a row of up to 64 EACH logits: each wave counts, for
 // every expert, which of its share of the row lie above it; the share comes
@@ -158,7 +161,7 @@ struct Choice {
 // the counts.  (The largest taken out `want` + 1 times by wave-wide maxima
 // costs 0.5 us a rank; counting by reads of LDS 3 us at 128 experts.)
 template <int WAVES, int EACH>
-__device__ __forceinline__ int moe_of_rank(Choice& c, const double* __restrict__ row, int E, int want) {
+__device__ __forceinline__ int moe_of_rank(ByRank& c, const double* __restrict__ row, int E, int want) {
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int share = (E + WAVES - 1) / WAVES, j0 = wave * share, j1 = j0 + share < E ? j0 + share : E;
     u64 key[EACH];
@@ -189,36 +192,14 @@ __device__ __forceinline__ int moe_of_rank(Choice& c, const double* __restrict__
     return __builtin_amdgcn_readfirstlane(c.found);
 }
 
-// The block's expert and its tokens (c.list, c.rank_of); returns their number,
-// 0 where the block has nothing to do, the expert in e.  Blocks of the first
-// tile write the choice down: ids and logits by (token, rank).
+// The tokens of expert e (c.list, c.rank_of); returns their number, 0 where one
+// before token `first` chose it too.  Blocks of the first tile write the choice
+// down: ids and logits by (token, rank).
 template <int WAVES>
-__device__ __forceinline__ int moe_choice(Choice& c, int M, int E, int topk, int by_pair,
+__device__ __forceinline__ int moe_tokens(Choice& c, int M, int E, int topk, int e, int first,
                                           const double* __restrict__ logits, int32_t* __restrict__ ids,
-                                          double* __restrict__ top, int& e) {
+                                          double* __restrict__ top) {
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    int first = 0;
-    e = blockIdx.y;
-    if (by_pair) {
-        first = blockIdx.y / topk;
-        const int want = blockIdx.y - first * topk;
-        const double* row = logits + (size_t)first * E;
-        e = E <= 128 ? moe_of_rank<WAVES, 2>(c, row, E, want)
-                     : E <= 256 ? moe_of_rank<WAVES, 4>(c, row, E, want)
-                                : moe_of_rank<WAVES, kMoeMaxExperts / 64>(c, row, E, want);
-        if (M == 1) {
-            if (tid == 0) {
-                c.rank_of[0] = (int16_t)want;
-                c.list[0] = 0;
-                if (blockIdx.x == 0) {
-                    ids[want] = e;
-                    top[want] = logits[e];
-                }
-            }
-            __syncthreads();
-            return 1;
-        }
-    }
     // the rank of e in every row: the logits above its own, counted by a wave,
     // four rows and 128 logits under way at a time
     constexpr int kRows = 4, kCols = 2;
@@ -270,6 +251,30 @@ __device__ __forceinline__ int moe_choice(Choice& c, int M, int E, int topk, int
     return __builtin_amdgcn_readfirstlane(c.chosen);
 }
 
+// The same where blockIdx.y is a (token, rank) pair: the expert comes out in e,
+// and a block that has nothing to do gets 0.
+template <int WAVES>
+__device__ __forceinline__ int moe_choice_by_pair(Choice& c, ByRank& by, int M, int E, int topk,
+                                                  const double* __restrict__ logits, int32_t* __restrict__ ids,
+                                                  double* __restrict__ top, int& e) {
+    const int first = blockIdx.y / topk, want = blockIdx.y - first * topk;
+    const double* row = logits + (size_t)first * E;
+    e = E <= 128 ? moe_of_rank<WAVES, 2>(by, row, E, want)
+                 : E <= 256 ? moe_of_rank<WAVES, 4>(by, row, E, want)
+                            : moe_of_rank<WAVES, kMoeMaxExperts / 64>(by, row, E, want);
+    if (M > 1) return moe_tokens<WAVES>(c, M, E, topk, e, first, logits, ids, top);
+    if (threadIdx.x == 0) {
+        c.rank_of[0] = (int16_t)want;
+        c.list[0] = 0;
+        if (blockIdx.x == 0) {
+            ids[want] = e;
+            top[want] = logits[e];
+        }
+    }
+    __syncthreads();
+    return 1;
+}
+
 // silu(g) u into element n of pair p's h: the upper 8 bits of its significand, the next 8 and the last 8,
 // each a bf16 value; the differences are exact (down to bf16's smallest
 // number).  An infinity has no rest.
@@ -285,9 +290,9 @@ __device__ __forceinline__ void moe_store_h(uint16_t* h, int p, int F, int n, fl
 }
 
 // Element f of pair p's h from the products' definition: for accumulators
-// that are not finite.  Kept out of the loops that store the others: inlined
-// there once for each of their elements, it took 81 us where this takes 73 (64
-// tokens, 2 of 8 experts of 5632 x 4096 with zero points; 69 with neither).
+// that are not finite.  Kept out of the loops that store the others, where a
+// copy for each of their elements cost 8 us of 73 (64 tokens, 2 of 8 experts of
+// 5632 x 4096 with zero points).
 template <class T, int GPU, bool ZP>
 __device__ __forceinline__ void moe_hidden_defined(const uint16_t* x, int K, int F, const uint8_t* wg, const uint8_t* wu,
                                                    const W4gLayout& l, uint16_t* h, int p, int f) {
@@ -309,12 +314,14 @@ __global__ __launch_bounds__(64 * kUpWaves, 4) void k_moe_gate_up(const uint16_t
                                                                int32_t* __restrict__ ids, double* __restrict__ top,
                                                                uint16_t* __restrict__ h) {
     __shared__ Choice c;
+    __shared__ ByRank by_rank;
     __shared__ __attribute__((aligned(16))) char rows_lds[kUpWaves][4096];
     __shared__ f32x4 part[kUpWaves][2][64];
     constexpr int kThreads = 64 * kUpWaves;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    int e;
-    const int n_tok = moe_choice<kUpWaves>(c, M, E, topk, by_pair, logits, ids, top, e);
+    int e = blockIdx.y;
+    const int n_tok = by_pair ? moe_choice_by_pair<kUpWaves>(c, by_rank, M, E, topk, logits, ids, top, e)
+                              : moe_tokens<kUpWaves>(c, M, E, topk, e, 0, logits, ids, top);
     if (n_tok == 0) return;
 
     const W4gLayout l = w4g_layout(128 / GPU, ZP, F, K);
@@ -415,14 +422,14 @@ constexpr int kManyWaves = 4;
 template <class T, int GPU, bool ZP>
 __global__ __launch_bounds__(64 * kManyWaves, 4) void k_moe_gate_up_many(
     const uint16_t* __restrict__ x, int M, int K, int F, const uint8_t* __restrict__ wg,
-    const uint8_t* __restrict__ wu, int E, int topk, int by_pair, const double* __restrict__ logits,
-    int32_t* __restrict__ ids, double* __restrict__ top, uint16_t* __restrict__ h) {
+    const uint8_t* __restrict__ wu, int E, int topk, const double* __restrict__ logits, int32_t* __restrict__ ids,
+    double* __restrict__ top, uint16_t* __restrict__ h) {
     __shared__ Choice c;
     constexpr int kStage = 8192;
     __shared__ __attribute__((aligned(16))) char rows_lds[2 * kStage];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    int e;
-    const int n_tok = moe_choice<kManyWaves>(c, M, E, topk, by_pair, logits, ids, top, e);
+    const int e = blockIdx.y;   // no fewer pairs than experts here: share_rows
+    const int n_tok = moe_tokens<kManyWaves>(c, M, E, topk, e, 0, logits, ids, top);
     if (n_tok == 0) return;
 
     const W4gLayout l = w4g_layout(128 / GPU, ZP, F, K);
@@ -535,8 +542,9 @@ struct ByExpert {
 
 // Fills the passes and the pairs' weights (the softmax's numerators over the
 // tokens' denominators); returns the number of passes.  One block writes the
-// choice out.  The choice is read once, everything else happens in LDS.
-template <int WAVES, int TOK>
+// choice out.  The choice is read once, everything else happens in LDS.  ONE:
+// the call can be of a single token.
+template <int WAVES, int TOK, bool ONE>
 __device__ __forceinline__ int moe_passes(Passes& s, ByExpert& by, int M, int E, int topk, int norm,
                                           const double* __restrict__ logits, const int32_t* __restrict__ ids,
                                           const double* __restrict__ top, bool write, int32_t* __restrict__ ids_out,
@@ -548,7 +556,8 @@ __device__ __forceinline__ int moe_passes(Passes& s, ByExpert& by, int M, int E,
         by.expert[p] = (int16_t)ids[p];
         by.top[p] = top[p];
     }
-    if (M > 1)
+    const bool more = !ONE || M > 1;
+    if (more)
         for (int e = tid; e < E; e += kThreads) by.tokens[e] = 0;
     if (!norm) {
         for (int m = wave; m < M; m += WAVES) {
@@ -566,7 +575,7 @@ __device__ __forceinline__ int moe_passes(Passes& s, ByExpert& by, int M, int E,
     for (int p = tid; p < pairs; p += kThreads) {
         const int m = p / topk;
         s.c[p] = expf((float)(by.top[p] - by.top[m * topk]));
-        if (M > 1) {
+        if (more) {
             atomicOr(&by.tokens[by.expert[p]], 1ull << m);
         } else {
             s.pair_of[p] = s.at[p] = (int16_t)p;
@@ -581,7 +590,7 @@ __device__ __forceinline__ int moe_passes(Passes& s, ByExpert& by, int M, int E,
         s.total[tid] = v;
     }
     int passes = topk;
-    if (M > 1) {
+    if (more) {
         // a thread's kEach experts: their pairs and passes, and those before them
         int n[kEach], a = 0, b = 0;
 #pragma unroll
@@ -637,7 +646,7 @@ __device__ __forceinline__ int moe_passes(Passes& s, ByExpert& by, int M, int E,
             if (ids_out) ids_out[p] = e;
             if (weights_out) weights_out[p] = c;
         }
-        if (M > 1) s.pair_of[by.pairs_at[e] + __popcll(by.tokens[e] & ((1ull << m) - 1))] = (int16_t)p;
+        if (more) s.pair_of[by.pairs_at[e] + __popcll(by.tokens[e] & ((1ull << m) - 1))] = (int16_t)p;
     }
     __syncthreads();
     return __builtin_amdgcn_readfirstlane(passes);
@@ -736,7 +745,7 @@ __global__ __launch_bounds__(64 * kDownWaves, 4) void k_moe_down(
     static_assert(sizeof(ByExpert) <= sizeof(rows_lds), "the rows' place holds it");
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     for (int i = tid; i < kDownWaves * M * 16; i += kThreads) sums[i] = 0.0f;
-    const int passes = moe_passes<kDownWaves, kDownTok>(s, *reinterpret_cast<ByExpert*>(rows_lds), M, E, topk, norm,
+    const int passes = moe_passes<kDownWaves, kDownTok, true>(s, *reinterpret_cast<ByExpert*>(rows_lds), M, E, topk, norm,
                                                         logits, ids, top, blockIdx.x == 0 && blockIdx.y == 0, ids_out,
                                                         weights_out);
 
@@ -837,7 +846,7 @@ __global__ __launch_bounds__(64 * kDownWaves, 4) void k_moe_down_wide(
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int group = wave / kWideTiles, wn = wave % kWideTiles;
     for (int i = tid; i < kDownWaves * M * 16; i += kThreads) sums[i] = 0.0f;
-    const int passes = moe_passes<kDownWaves, kWideTok>(s, *reinterpret_cast<ByExpert*>(rows_lds), M, E, topk, norm,
+    const int passes = moe_passes<kDownWaves, kWideTok, false>(s, *reinterpret_cast<ByExpert*>(rows_lds), M, E, topk, norm,
                                                         logits, ids, top, blockIdx.x == 0 && blockIdx.y == 0, ids_out,
                                                         weights_out);
 
@@ -953,7 +962,7 @@ hipError_t moe_t(const MoeArgs& a, const MoeWs& l, int M, const uint16_t* x, uin
     // apart / shared: 256 blocks 20.5 / 19.6, 224 blocks 28 / 31)
     if (share_rows(M, a.E, a.topk) && (long)rows * ((tiles + kManyWaves - 1) / kManyWaves) >= 256)
         k_moe_gate_up_many<T, GPU, ZP><<<dim3((tiles + kManyWaves - 1) / kManyWaves, rows), 64 * kManyWaves, 0, st>>>(
-            x, M, a.K, a.F, a.wg, a.wu, a.E, a.topk, by_pair, logits, ids_ws, top, h);
+            x, M, a.K, a.F, a.wg, a.wu, a.E, a.topk, logits, ids_ws, top, h);
     else
         k_moe_gate_up<T, GPU, ZP><<<dim3((tiles + per - 1) / per, rows), 64 * kUpWaves, 0, st>>>(
             x, M, a.K, a.F, a.wg, a.wu, a.E, a.topk, by_pair, ks_log2, logits, ids_ws, top, h);
