@@ -14,8 +14,8 @@
 // kernel makes for itself; the down kernel reads the chosen ids.
 // h goes to the down product as it is in float32, as the sum of three bf16
 // values of 8 bits each (in bf16's range for either T): y's rounding is the
-// only one to fewer bits.  The three are operands of MFMAs into the same
-// sums, so they cost rows and MFMAs, and no accumulators.
+// only one to fewer bits.  The three are rows of one MFMA operand, or operands
+// of MFMAs into the same sums.
 // Both products bring a wave's operand rows to its own piece of LDS, by as
 // many 4-row instructions as it has rows (an expert of a few tokens has 1 to
 // 3, so most of a 16-row load by registers would be for nothing), and
@@ -36,9 +36,9 @@ constexpr int kParts = 3;           // bf16 values whose sum is h
 constexpr int kDownWaves = 8, kMaxSplits = 8, kWideTiles = 4, kWideGroups = kDownWaves / kWideTiles;
 constexpr int kDownTok = 5, kWideTok = 16;   // tokens of a pass, apart and in wide blocks
 // Gate / up: an expert has some tokens, so that sharing their rows among tiles
-// pays; us, apart / shared: 64 tokens, 8 experts (16 each) 99 / 53, 32 experts
-// (12) 35 / 25, 60 experts (4.3) 45 / 52, 128 experts (4) 53 / 65; 8 experts, 32
-// tokens (8) 51 / 43, 20 tokens (5) 47 / 42.  With up to 16 tokens there is little
+// pays; us, apart / shared: 64 tokens, 8 experts (16 each) 85 / 54, 32 experts
+// (12) 27 / 27, 60 experts (4.3) 45 / 52, 128 experts (4) 53 / 65; 8 experts, 32
+// tokens (8) 45 / 43, 20 tokens (5) 45 / 42.  With up to 16 tokens there is little
 // in it: 16 on 8 of 8 experts 51 / 46 and 17.9 / 18.8, 12 on 4 of 8 21 / 23.
 bool share_rows(int M, int E, int topk) { return M > 16 && (long)M * topk >= 5L * E; }
 // Down: blocks of four tiles that share the rows of h pay where an expert's
@@ -143,7 +143,7 @@ __device__ __forceinline__ u64 order_key(double v) {
 // time.  With ks = 1 nothing is waited for but a wave's own loads.
 // Bound by the weights' bytes, after some 3 us in which a block finds its
 // expert: us, F x K = 768 x 2048, 8 of 128 experts: 9 for a token (13 MB),
-// 37 for 16 (134 MB: 3.6 TB/s).
+// 38 for 16 (134 MB: 3.5 TB/s).
 // ---------------------------------------------------------------------------
 constexpr int kUpWaves = 8;
 
@@ -513,13 +513,13 @@ __global__ __launch_bounds__(64 * kManyWaves, 4) void k_moe_gate_up_many(
 // blocks on the same columns, by the one that arrives last: the order of
 // every sum is fixed.  The blocks' sums go through device-scope stores and
 // loads, waited for before the arrival is counted; no fence of the caches is
-// needed.  us: 7.6 for one token and 8 of 128 experts of 2048 x 768 (7 MB), 22
+// needed.  us: 7.2 for one token and 8 of 128 experts of 2048 x 768 (7 MB), 22
 // for 16 tokens (67 MB: 3.1 TB/s).  With some tokens an expert a wave takes
 // 4 KB of h for each KB of weights, and those rows' way through the L2 bounds
 // it, not the weights: 64 tokens, 2 of 8 experts of 4096 x 5632 take 90 us for
 // 98 MB, the wide form below 56.5.  (With h rounded to two bf16 values, 16 bits,
 // the three sizes took 7, 21 and 49, and one output in 400 of the last was
-// rounded otherwise than a float32 h's, against one in 900.)
+// rounded otherwise than by the plain float32 form; now one in 900 is.)
 // An operand holds a token's parts in three of its 16 rows, five tokens in
 // all: an operand a part took 25 us where this takes 22, three times the reads
 // of LDS.

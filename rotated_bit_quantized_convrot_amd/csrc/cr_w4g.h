@@ -239,7 +239,9 @@ __device__ __forceinline__ void w4g_values(const uint16_t* p, float (&v)[8]) {
 // group's own sum, taken before its scale, can overflow where the result does
 // not; an infinity times (q - 8) / 16 and times (8 - z) / 16 can cancel; and
 // the chunks past K meet the row's last values with a scale of 0.  Ends at the
-// first NaN.
+// first NaN.  1220 rows of K = 9728 against N = 2560, ms a call: 0.08 where all
+// are finite, 0.09 where all hold NaN, 0.45 with an infinity in one row, 12.5
+// with one in each.
 template <class T, int GPU, bool ZP, class X>
 __device__ __forceinline__ double w4g_defined(const uint8_t* w, const W4gLayout& l, int n, int K, X x8) {
     const int row = n & 15;

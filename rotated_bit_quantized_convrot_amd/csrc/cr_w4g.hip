@@ -289,20 +289,20 @@ hipError_t tile(const LinearArgs& a, hipStream_t st) {
 // Tile choice.  Fewer, wider blocks read x less often and share its operand
 // reads; narrow ones put more CUs to work.  Measured, us, bf16, groups of 128,
 // K x N = 2560 x 9728 / 9728 x 2560 / 2560 x 2560 (weights cold):
-//   M = 8     one tile, 4 K groups 6.6 / 14.0 / 4.3, 10 groups 7.2 / 8.1 / 3.6,
-//             16 groups 9.5 / 7.3 / 3.8
-//   M = 32    32 columns 8.7 / 19.1 / 5.9, 16 columns 13.0 / 12.9 / 4.5
-//   M = 48    64 columns 9.4, with two tiles a wave and half the waves
-//             11.4 / 35.5 / 10.3, 16 columns 16.8 / 16.5 / 5.6
+//   M = 8     one tile, 4 K groups 6.4 / 11.3 / 4.2, 10 groups 6.7 / 7.6 / 3.9,
+//             16 groups 9.0 / 7.0 / 4.1
+//   M = 32    32 columns 9.4 / 16.2 / 6.0, 16 columns 11.8 / 10.1 / 4.6
+//   M = 48    64 columns 9.9 / 22.5 / 8.6, with two tiles a wave and half the
+//             waves 10.9 / 25.4 / 9.4, 16 columns 15.1 / 13.3 / 5.6
 // Up to 48 rows the wide tile is taken where its blocks fill half the chip
 // (256 CUs).  Above that the time is that of the rounds of 256 blocks (one
 // fits a CU) times a block's, which go as 2 : 3 : 7 : 8 for 80 x 16, 80 x 64,
-// 112 x 128 and 128 x 128 (M = 76 at 2560 x 9728: 20.4 / 12.0 for the first
+// 112 x 128 and 128 x 128 (M = 76 at 2560 x 9728: 21.0 / 12.1 for the first
 // two); us, in that order, K x N x M:
-//   2560 x 9728 x 100    33 / 20 / 23 / 24       2560 x 2560 x 200   15 / 12 / 23 / 25
-//   2560 x 9728 x 300    64 / 32 / 26 / 28       4096 x 4096 x 300   38 / 17 / 33 / 35
-//   9728 x 2560 x 1220  179 / 97 / 75 / 81       4096 x 4096 x 1000 125 / 64 / 73 / 45
-//   2560 x 9728 x 1220  230 / 103 / 93 / 80
+//   2560 x 9728 x 100    33 / 20 / 24 / 25       2560 x 2560 x 200   15 / 12 / 23 / 25
+//   2560 x 9728 x 300    66 / 32 / 27 / 28       4096 x 4096 x 300   39 / 18 / 33 / 36
+//   9728 x 2560 x 1220  190 / 98 / 77 / 82       4096 x 4096 x 1000 121 / 61 / 68 / 41
+//   2560 x 9728 x 1220  239 / 105 / 97 / 82
 template <class T, int GPU, bool ZP>
 hipError_t linear_t(const LinearArgs& a, hipStream_t st) {
     constexpr long kHalf = 128;
