@@ -394,6 +394,92 @@ cr_status cr_moe_w4g(int dtype, const void* x, int M, int K, const void* router,
                      const void* wg_packed, const void* wu_packed, const void* wd_packed, int F, int group, int zeros,
                      void* y, int32_t* ids, float* weights, void* ws, size_t ws_bytes, hipStream_t stream);
 
+/* ---- attention ----------------------------------------------------------
+ * Tensors of tokens and heads: `dtype` (CR_BF16 or CR_FP16) values, the head's
+ * D = 64, 128 or 256 side by side, token t's head h at t * row + h * head
+ * values from the pointer (strides: not negative, multiples of 8, so that a
+ * projection's fused output can be taken apart without a copy).  Outputs are
+ * contiguous [T,Hq,D] and must not overlap an input (CR_ERR_SHAPE).  Query
+ * head h reads key / value head h / (Hq / Hkv) (Hq a multiple of Hkv, 1 <= Hq
+ * <= CR_MAX_HEADS).
+ * T rows hold B sequences (0 <= B <= CR_MAX_SEQS), sequence b rows cu[b] up to
+ * cu[b+1] of int32 cu [B+1] on the device, which must not decrease; an empty
+ * sequence has none.  Rows before cu[0] and from cu[B] on are not read, and
+ * their outputs are left as they were.
+ * Scores are scale * q . k, held in float32 with the softmax's sums. */
+#define CR_MAX_HEADS 1024
+#define CR_MAX_SEQS 65536
+
+/* Attention of whole prompts: row i of a sequence over its rows up to i
+ * (causal nonzero) or over all of them.  The softmax's weights go to the
+ * product with v in the 16-bit type.  Infinities and NaN in rows that a row
+ * does not see do not reach it; among those that it sees they give what the
+ * definition gives. */
+cr_status cr_attn_prompt(int dtype, const void* q, int64_t q_row, int64_t q_head, const void* k, int64_t k_row,
+                         int64_t k_head, const void* v, int64_t v_row, int64_t v_head, int T, int Hq, int Hkv, int D,
+                         const int32_t* cu, int B, int causal, float scale, void* y, hipStream_t stream);
+
+/* A paged cache of keys and values held in 4 bits: `pages` pages of `page`
+ * tokens (16, 32, .. 1024) for `heads` key / value heads of `dim` (64, 128 or
+ * 256).  A token's head x (float32, exact from its 16 bits) is kept as
+ *   x' = H x / sqrt(dim) with `rotate` (Sylvester Hadamard matrix: butterflies
+ *   of strides 1, 2, .. dim / 2, (a, b) -> (a + b, a - b), then times
+ *   float32(1 / sqrt(dim))), x without;
+ *   for each `group` (32, 64 or 128, at most dim) consecutive d
+ *     lo = min(0, min x'), hi = max(0, max x'),
+ *     s = hi / 15 - lo / 15, to the nearest float32 whose low four bits are 0,
+ *     z = clamp(rint(-lo / s), 0, 15), c = clamp(rint(x' / s) + z, 0, 15)
+ *     (both 0 where s = 0)
+ * and stands for x' = s (c - z).  A group that holds an infinity or a NaN
+ * stands for NaN.
+ *   codes   [pages][K, V][heads][page * dim / 2] bytes, 16-byte aligned
+ *     K     token r of a page at r * dim / 2; its dword i * dim / 32 + s holds
+ *           d = 32 s + 8 i + 0..7: d + 2 j in bits 4 j, d + 2 j + 1 in bits
+ *           16 + 4 j
+ *     V     16 tokens at (r / 16) * 8 dim; byte (16 e + m) * 16 + r % 16 holds
+ *           d = 32 e + m in its low four bits, d = 32 e + 16 + m in the others
+ *   scales  [pages][K, V][heads][page][dim / group] words: the bits of s, the
+ *           low four z; 16-byte aligned
+ * Both belong to the caller and need no initialisation: only rows that were
+ * written are read. */
+typedef struct {
+    void* codes;
+    void* scales;
+    int pages, page, heads, dim, group, rotate;
+} cr_kv4;
+
+/* Bytes of a cache's codes and scales (0 on bad values). */
+size_t cr_kv4_codes_bytes(const cr_kv4* cache);
+size_t cr_kv4_scales_bytes(const cr_kv4* cache);
+
+/* Where a call's tokens are in the cache: lens [B] int32 is the number of
+ * sequence b's tokens in it, the call's own rows (its last ones) among them;
+ * its token p is in page table[b * width + p / page] (int32 [B,width]), row
+ * p % page.  The arrays are on the device and cannot be checked by the host;
+ * the kernels stay inside the buffers whatever they hold: a table entry that
+ * is no page holds no tokens, lens counts at most width * page, and rows for
+ * which lens has no place come before the first token. */
+
+/* Writes the rows of k and v (T, heads, dim) to their places in the cache.
+ * Rows without a place are left out.  Two rows of one call must not share a
+ * place. */
+cr_status cr_kv4_append(int dtype, const void* k, int64_t k_row, int64_t k_head, const void* v, int64_t v_row,
+                        int64_t v_head, int T, const cr_kv4* cache, const int32_t* table, int width,
+                        const int32_t* lens, const int32_t* cu, int B, hipStream_t stream);
+
+/* Attention of a call's rows (q, already in the cache: cr_kv4_append comes
+ * first) over the cache: row i of a sequence's n sees its tokens up to
+ * lens[b] - n + i.  A row that sees none gives zeros.  With the cache's
+ * rotation q is rotated and the output turned back.
+ *   ws / ws_bytes: at least cr_attn_kv4_workspace_bytes(...); calls that can
+ *   run at the same time need a workspace each.  Nothing is kept in it.
+ * Every sum has a fixed order: the same call gives the same bits. */
+size_t cr_attn_kv4_workspace_bytes(int T, int Hq, const cr_kv4* cache, int width, int B);
+
+cr_status cr_attn_kv4(int dtype, const void* q, int64_t q_row, int64_t q_head, int T, int Hq, const cr_kv4* cache,
+                      const int32_t* table, int width, const int32_t* lens, const int32_t* cu, int B, float scale,
+                      void* y, void* ws, size_t ws_bytes, hipStream_t stream);
+
 /* ---- status ----------------------------------------------------------- */
 const char* cr_status_str(cr_status s);
 const char* cr_last_error(void);   /* thread-local detail of the last failure */
@@ -474,6 +560,17 @@ cr_status cr_dbg_big_plan(int bn, int splits);
  * setting one); results do not depend on it.  Process-wide, read at each
  * call. */
 cr_status cr_dbg_small_plan(int splits);
+
+/* Where the kernels find a row of the 4-bit cache, by the functions that they
+ * use, on the host (every pointer is a host pointer; the cache's own are not
+ * read): row `row` of a call's T belongs to sequence place[0] (-1: none) and
+ * is its token place[1] (negative: before the first); that token is in page
+ * place[2] (-1: none), its K codes place[3] bytes and V's first byte place[4]
+ * bytes into the codes for `head`, its scales place[5] and place[6] words into
+ * the scales (-1 each without a page); place[7] is the sequence's number of
+ * tokens. */
+cr_status cr_dbg_kv4_place(const cr_kv4* cache, const int32_t* table, int width, const int32_t* lens,
+                           const int32_t* cu, int B, int T, int row, int head, int64_t* place);
 
 /* The int32 accumulators [M,N] of the linear of `kind` (same kernels as the
  * linear, epilogue replaced by a plain int32 store). */

@@ -17,6 +17,9 @@ Formats (model cards cited by title and section):
   * W4G - weight-only: 16-bit activations (bf16 or fp16), 4-bit weights with
     a scale, and optionally a zero point, per group of 32, 64 or 128 along K;
     linears and a mixture-of-experts layer.
+  * KV4 - a paged cache of attention keys and values, rotated per head and
+    held in 4 bits with a scale and a zero point per group of 32, 64 or 128;
+    attention over it, and over whole prompts in 16 bits.
 """
 from __future__ import annotations
 
@@ -43,6 +46,8 @@ __all__ = [
     "dbg_fused_config", "dbg_fused_timeouts", "dbg_big_plan", "dbg_small_plan",
     "W4G", "w4g_packed_bytes", "encode_w4g", "pack_weight_w4g", "linear_w4g",
     "moe_w4g_workspace_bytes", "moe_w4g", "PackedExperts", "pack_experts", "moe",
+    "attn_prompt", "KV4Cache", "kv4_cache", "kv4_append", "attn_kv4_workspace_bytes", "attn_kv4",
+    "dbg_kv4_place",
 ]
 
 W4A4, INT8TW, W4A8, INT8ROT, W4A4_G64, W4A4_G16, W4A4_RH = 0, 1, 2, 3, 4, 5, 6
@@ -73,6 +78,8 @@ EXPORTS = [
     "cr_dbg_fused_config", "cr_dbg_fused_timeouts", "cr_dbg_big_plan", "cr_dbg_small_plan",
     "cr_w4g_packed_bytes", "cr_encode_w4g", "cr_pack_weight_w4g", "cr_linear_w4g",
     "cr_moe_w4g_workspace_bytes", "cr_moe_w4g",
+    "cr_attn_prompt", "cr_kv4_codes_bytes", "cr_kv4_scales_bytes", "cr_kv4_append", "cr_attn_kv4_workspace_bytes",
+    "cr_attn_kv4", "cr_dbg_kv4_place",
 ]
 
 
@@ -94,6 +101,7 @@ def lib() -> ctypes.CDLL:
                            "`python -m rotated_bit_quantized_convrot_amd.build_lib`")
     L = ctypes.CDLL(_LIB_PATH)
     vp, i, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+    i64, f32 = ctypes.c_int64, ctypes.c_float
     sig = {
         "cr_packed_bytes": (sz, [i, i, i]),
         "cr_workspace_bytes": (sz, [i, i, i, i]),
@@ -134,6 +142,13 @@ def lib() -> ctypes.CDLL:
         "cr_linear_w4g": (i, [i, vp, i, i, vp, i, i, i, vp, vp, vp]),
         "cr_moe_w4g_workspace_bytes": (sz, [i, i, i, i, i, i]),
         "cr_moe_w4g": (i, [i, vp, i, i, vp, i, i, i, vp, vp, vp, i, i, i, vp, vp, vp, vp, sz, vp]),
+        "cr_attn_prompt": (i, [i, vp, i64, i64, vp, i64, i64, vp, i64, i64, i, i, i, i, vp, i, i, f32, vp, vp]),
+        "cr_kv4_codes_bytes": (sz, [vp]),
+        "cr_kv4_scales_bytes": (sz, [vp]),
+        "cr_kv4_append": (i, [i, vp, i64, i64, vp, i64, i64, i, vp, vp, i, vp, vp, i, vp]),
+        "cr_attn_kv4_workspace_bytes": (sz, [i, i, vp, i, i]),
+        "cr_attn_kv4": (i, [i, vp, i64, i64, i, i, vp, vp, i, vp, vp, i, f32, vp, vp, sz, vp]),
+        "cr_dbg_kv4_place": (i, [vp, vp, i, vp, vp, i, i, i, i, vp]),
         "cr_probe_mfma_i8": (i, [i, i, vp, vp, vp]),
         "cr_probe_read": (i, [vp, sz, vp, vp]),
         "cr_probe_copy": (i, [vp, vp, sz, vp]),
@@ -706,6 +721,182 @@ def moe_w4g(x, router, gate, up, down, F, group, topk, zeros=False, norm=True, o
 
 
 # ---------------------------------------------------------------------------
+# Attention over whole prompts, and over a cache held in 4 bits
+# ---------------------------------------------------------------------------
+
+def _heads(t: torch.Tensor, name: str, dtype, device):
+    """t is [T, heads, dim] of this type on this device, a head's values side
+    by side: (pointer, stride of a token, stride of a head)."""
+    if t.dtype is not dtype or t.device != device or not t.is_cuda:
+        raise ValueError(f"{name} must be {dtype} on {device}, got {t.dtype} on {t.device}")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [T, heads, dim]")
+    (n, heads, dim), (row, head, one) = t.shape, t.stride()
+    if one != 1 and dim != 1:
+        raise ValueError(f"{name}: the values of a head must lie side by side")
+    return t.data_ptr(), row if n > 1 else 0, head if heads > 1 else 0
+
+
+def _int32(t: torch.Tensor, name: str, device, shape):
+    _here(t, name, torch.int32, device)
+    if t.shape != shape:
+        raise ValueError(f"{name} must be int32 {list(shape)}, got {list(t.shape)}")
+
+
+def _sequences(cu: torch.Tensor, device) -> int:
+    _here(cu, "cu_seqlens", torch.int32, device)
+    if cu.dim() != 1 or cu.numel() < 1:
+        raise ValueError("cu_seqlens must be int32 [B + 1]")
+    return cu.numel() - 1
+
+
+def _attn_out(out, q):
+    if out is None:
+        return torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    _here(out, "out", q.dtype, q.device)
+    if out.shape != q.shape:
+        raise ValueError("out must have the shape of q")
+    return out
+
+
+def attn_prompt(q, k, v, cu_seqlens, causal=True, scale=None, out=None):
+    """Attention of whole prompts: q [T, heads, dim], k and v [T, kv heads,
+    dim] bf16 or fp16 (views into a fused projection's output do: only a
+    head's values have to lie side by side), dim 64, 128 or 256; sequence b is
+    the rows from ``cu_seqlens[b]`` up to ``cu_seqlens[b + 1]`` (int32 [B + 1]
+    on the device).  Each row attends to its own sequence, up to itself if
+    ``causal``; ``scale`` multiplies the scores (default: 1 / sqrt(dim)).
+    Returns y [T, heads, dim]; rows outside the sequences are not written."""
+    code = _dtype16(q, "q")
+    device = q.device
+    qp, qr, qh = _heads(q, "q", q.dtype, device)
+    kp, kr, kh = _heads(k, "k", q.dtype, device)
+    vp, vr, vh = _heads(v, "v", q.dtype, device)
+    T, Hq, D = q.shape
+    if k.shape != v.shape or k.shape[0] != T or k.shape[2] != D:
+        raise ValueError("k and v must be [T, kv heads, dim] of q's T and dim")
+    B = _sequences(cu_seqlens, device)
+    out = _attn_out(out, q)
+    _call_on(device, lib().cr_attn_prompt, code, qp, qr, qh, kp, kr, kh, vp, vr, vh, T, Hq, k.shape[1], D,
+             cu_seqlens.data_ptr(), B, bool(causal), D ** -0.5 if scale is None else scale, out.data_ptr())
+    return out
+
+
+class _Kv4(ctypes.Structure):
+    """cr_kv4 of include/convrot.h."""
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)] + [
+        (n, ctypes.c_int) for n in ("pages", "page", "heads", "dim", "group", "rotate")]
+
+
+@dataclasses.dataclass(frozen=True, eq=False)
+class KV4Cache:
+    """A paged cache of keys and values held in 4 bits (layout: cr_kv4 in
+    include/convrot.h): codes uint8 [pages, 2, heads, page * dim / 2], scales
+    int32 [pages, 2, heads, page * dim / group]."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+    page: int
+    heads: int
+    dim: int
+    group: int
+    rotate: bool
+
+    def __post_init__(self):
+        pages = self.codes.shape[0]
+        c = _Kv4(self.codes.data_ptr(), self.scales.data_ptr(), pages, self.page, self.heads, self.dim, self.group,
+                 self.rotate)
+        nc, ns = lib().cr_kv4_codes_bytes(ctypes.byref(c)), lib().cr_kv4_scales_bytes(ctypes.byref(c))
+        if nc == 0:
+            raise ConvRotError(2, lib().cr_last_error().decode())
+        _dev(self.codes, "codes", torch.uint8)
+        _here(self.scales, "scales", torch.int32, self.codes.device)
+        if self.codes.numel() != nc or 4 * self.scales.numel() != ns:
+            raise ValueError(f"codes and scales must have {nc} and {ns} bytes")
+        object.__setattr__(self, "_c", c)
+        object.__setattr__(self, "_at", ctypes.addressof(c))
+
+
+def kv4_cache(pages: int, page: int, heads: int, dim: int, group: int = 64, rotate: bool = True,
+              device="cuda") -> KV4Cache:
+    """A cache of ``pages`` pages of ``page`` tokens (16, 32, .. 1024) for
+    ``heads`` key / value heads of ``dim``, with a scale and a zero point for
+    each ``group`` along a head, of heads rotated (Hadamard) or not."""
+    c = _Kv4(None, None, pages, page, heads, dim, group, rotate)
+    if lib().cr_kv4_codes_bytes(ctypes.byref(c)) == 0:
+        raise ConvRotError(3 if "group" in lib().cr_last_error().decode() else 2, lib().cr_last_error().decode())
+    return KV4Cache(torch.zeros((pages, 2, heads, page * dim // 2), dtype=torch.uint8, device=device),
+                    torch.zeros((pages, 2, heads, page * dim // group), dtype=torch.int32, device=device),
+                    page, heads, dim, group, bool(rotate))
+
+
+def _kv4_call(cache: KV4Cache, table, lens, cu_seqlens, device):
+    if cache.codes.device != device:
+        raise ValueError(f"the cache is on {cache.codes.device}, expected {device}")
+    B = _sequences(cu_seqlens, device)
+    _int32(lens, "lens", device, (B,))
+    if table.dim() != 2:
+        raise ValueError("table must be int32 [B, pages of a sequence]")
+    width = table.shape[1]
+    _int32(table, "table", device, (B, width))
+    return B, width
+
+
+def kv4_append(k, v, cache: KV4Cache, table, lens, cu_seqlens) -> None:
+    """Writes new tokens' k and v [T, heads, dim] into the cache.  Sequence b's
+    rows (``cu_seqlens`` as for :func:`attn_prompt`) are its last ones of
+    ``lens[b]``, the tokens that it has in the cache after the call; token p is
+    in page ``table[b, p // page]``, row ``p % page``.  Rows without a place (a
+    table entry that is no page) are left out."""
+    code = _dtype16(k, "k")
+    device = k.device
+    kp, kr, kh = _heads(k, "k", k.dtype, device)
+    vp, vr, vh = _heads(v, "v", k.dtype, device)
+    if k.shape != v.shape or k.shape[1:] != (cache.heads, cache.dim):
+        raise ValueError(f"k and v must be [T, {cache.heads}, {cache.dim}]")
+    B, width = _kv4_call(cache, table, lens, cu_seqlens, device)
+    _call_on(device, lib().cr_kv4_append, code, kp, kr, kh, vp, vr, vh, k.shape[0], cache._at, table.data_ptr(), width,
+             lens.data_ptr(), cu_seqlens.data_ptr(), B)
+
+
+@functools.lru_cache(maxsize=4096)
+def _attn_kv4_workspace(T, Hq, page, heads, dim, group, width, B) -> int:
+    c = _Kv4(None, None, 1, page, heads, dim, group, 0)
+    return int(lib().cr_attn_kv4_workspace_bytes(T, Hq, ctypes.byref(c), width, B))
+
+
+def attn_kv4_workspace_bytes(T: int, heads: int, cache: KV4Cache, width: int, B: int) -> int:
+    """Bytes of workspace :func:`attn_kv4` needs for T rows of ``heads`` query
+    heads in B sequences whose table is ``width`` pages wide."""
+    return _attn_kv4_workspace(T, heads, cache.page, cache.heads, cache.dim, cache.group, width, B)
+
+
+def attn_kv4(q, cache: KV4Cache, table, lens, cu_seqlens, scale=None, out=None, workspace=None):
+    """Attention of q [T, query heads, dim] over the cache, causal: sequence
+    b's rows are its last ones of ``lens[b]`` (written before by
+    :func:`kv4_append`, with the same table, lens and cu_seqlens), and row i of
+    n attends to its tokens up to ``lens[b] - n + i``; a row that sees none
+    gives zeros.  One row a sequence is decoding.  Calls that can run at the
+    same time need a ``workspace`` each."""
+    code = _dtype16(q, "q")
+    device = q.device
+    qp, qr, qh = _heads(q, "q", q.dtype, device)
+    T, Hq, D = q.shape
+    if D != cache.dim:
+        raise ValueError(f"q must be [T, heads, {cache.dim}]")
+    B, width = _kv4_call(cache, table, lens, cu_seqlens, device)
+    out = _attn_out(out, q)
+    if workspace is None:
+        need = _attn_kv4_workspace(T, Hq, cache.page, cache.heads, D, cache.group, width, B)
+        workspace = torch.empty(need if need > 256 else 256, dtype=torch.uint8, device=device)
+    else:
+        _here(workspace, "workspace", torch.uint8, device)
+    _call_on(device, lib().cr_attn_kv4, code, qp, qr, qh, T, Hq, cache._at, table.data_ptr(), width, lens.data_ptr(),
+             cu_seqlens.data_ptr(), B, D ** -0.5 if scale is None else scale, out.data_ptr(), workspace.data_ptr(),
+             workspace.numel())
+    return out
+
+
+# ---------------------------------------------------------------------------
 # Two-phase form: quantise x once, run GEMMs against one or more weights
 # ---------------------------------------------------------------------------
 
@@ -776,6 +967,22 @@ def dbg_linear_acc(kind: int, x: torch.Tensor, packed: torch.Tensor, N: int, wor
     _check(lib().cr_dbg_linear_acc(kind, _ptr(x), M, K, _ptr(packed), N, _ptr(acc),
                                    _ptr(workspace), workspace.numel(), _stream()))
     return acc
+
+
+def dbg_kv4_place(pages, page, heads, dim, group, table, lens, cu_seqlens, T, row, head=0) -> dict:
+    """Where the kernels find a row of the 4-bit cache, by their own functions
+    on the host: ``table``, ``lens`` and ``cu_seqlens`` int32 on the CPU."""
+    c = _Kv4(None, None, pages, page, heads, dim, group, 0)
+    for t, n in ((table, "table"), (lens, "lens"), (cu_seqlens, "cu_seqlens")):
+        if t.is_cuda or t.dtype != torch.int32 or not t.is_contiguous():
+            raise ValueError(f"{n} must be a contiguous int32 tensor on the CPU")
+    if table.dim() != 2 or lens.numel() != table.shape[0] or cu_seqlens.numel() != table.shape[0] + 1:
+        raise ValueError("table must be [B, width], lens [B] and cu_seqlens [B + 1]")
+    out = (ctypes.c_int64 * 8)()
+    _check(lib().cr_dbg_kv4_place(ctypes.byref(c), table.data_ptr(), table.shape[1], lens.data_ptr(),
+                                  cu_seqlens.data_ptr(), table.shape[0], T, row, head, out))
+    names = ("sequence", "token", "page", "k_codes", "v_codes", "k_scales", "v_scales", "tokens")
+    return dict(zip(names, out))
 
 
 # ---------------------------------------------------------------------------

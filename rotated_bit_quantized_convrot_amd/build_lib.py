@@ -20,7 +20,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libconvrot.so")
 SOURCES = ["cr_api.hip", "cr_quant.hip", "cr_gemm.hip", "cr_gemm_small.hip", "cr_probe.hip", "cr_encode.hip",
-           "cr_w4g.hip", "cr_moe.hip"]
+           "cr_w4g.hip", "cr_moe.hip", "cr_attn.hip", "cr_kv4.hip"]
 ARCH = "gfx950"
 
 

@@ -47,6 +47,7 @@ cr_status check_device() {
     return CR_OK;
 }
 
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 size_t a256(size_t v) { return (v + 255) / 256 * 256; }
@@ -380,6 +381,76 @@ cr_status check_moe_shape(int M, int K, int F, int E, int topk, int group) {
     return CR_OK;
 }
 static_assert(cr::kMoeMaxExperts == CR_MOE_MAX_EXPERTS && cr::kMoeMaxTopk == CR_MOE_MAX_TOPK, "header and library agree");
+
+// ---- attention --------------------------------------------------------------
+struct Heads {
+    const char* name;
+    const void* p;
+    int64_t row, head;
+    int count;
+};
+// Past the last value of T rows of n heads, in values from the first.
+int64_t span(const Heads& x, int T, int D) { return (T - 1) * x.row + (x.count - 1) * x.head + D; }
+
+cr_status check_heads(const Heads& x, int T, int D) {
+    if (!x.p) return fail(CR_ERR_NULL, "%s is NULL", x.name);
+    if (!aligned16(x.p)) return fail(CR_ERR_ALIGN, "%s not 16-byte aligned", x.name);
+    if (x.row < 0 || x.head < 0 || x.row % 8 || x.head % 8)
+        return fail(CR_ERR_ALIGN, "%s: strides %lld, %lld must be multiples of 8 and not negative", x.name,
+                    (long long)x.row, (long long)x.head);
+    // the kernels' offsets inside a tile of rows are 32-bit
+    if (x.row > CR_MAX_DIM * 8 || x.head > ((int64_t)1 << 40))
+        return fail(CR_ERR_SHAPE, "%s: stride beyond the limit", x.name);
+    return CR_OK;
+}
+cr_status check_apart(const Heads& x, int T, int D, const void* y, size_t y_bytes) {
+    if (overlap(x.p, (size_t)span(x, T, D) * 2, y, y_bytes)) return fail(CR_ERR_SHAPE, "y overlaps %s", x.name);
+    return CR_OK;
+}
+cr_status check_attn(int dtype, int T, int Hq, int Hkv, int D, int B, float scale) {
+    cr_status s;
+    if ((s = check_dtype(dtype)) != CR_OK) return s;
+    if (T < 0 || T > CR_MAX_DIM) return fail(CR_ERR_SHAPE, "bad T=%d", T);
+    if (B < 0 || B > CR_MAX_SEQS) return fail(CR_ERR_SHAPE, "bad B=%d", B);
+    if (D != 64 && D != 128 && D != 256) return fail(CR_ERR_SHAPE, "head of %d (need 64, 128 or 256)", D);
+    if (Hq < 1 || Hq > CR_MAX_HEADS || Hkv < 1 || Hq % Hkv)
+        return fail(CR_ERR_SHAPE, "%d heads on %d (need a multiple, up to %d)", Hq, Hkv, CR_MAX_HEADS);
+    if (!(scale - scale == 0.0f)) return fail(CR_ERR_SHAPE, "scale is not finite");
+    return CR_OK;
+}
+cr_status check_kv4(const cr_kv4* c) {
+    if (!c) return fail(CR_ERR_NULL, "cache is NULL");
+    if (c->page < 16 || c->page > 1024 || (c->page & (c->page - 1)))
+        return fail(CR_ERR_SHAPE, "page of %d tokens (need 16, 32, .. 1024)", c->page);
+    if (c->pages < 1 || c->pages > (1 << 26)) return fail(CR_ERR_SHAPE, "bad pages=%d", c->pages);
+    if (c->heads < 1 || c->heads > CR_MAX_HEADS) return fail(CR_ERR_SHAPE, "bad heads=%d", c->heads);
+    if (c->dim != 64 && c->dim != 128 && c->dim != 256)
+        return fail(CR_ERR_SHAPE, "head of %d (need 64, 128 or 256)", c->dim);
+    if ((c->group != 32 && c->group != 64 && c->group != 128) || c->group > c->dim)
+        return fail(CR_ERR_GROUP, "scale group %d of a head of %d (need 32, 64 or 128)", c->group, c->dim);
+    return CR_OK;
+}
+cr_status check_kv4_call(const cr_kv4* c, const int32_t* table, int width, const int32_t* lens, const int32_t* cu) {
+    if (!c->codes || !c->scales) return fail(CR_ERR_NULL, "the cache's codes or scales are NULL");
+    if (!aligned16(c->codes) || !aligned16(c->scales))
+        return fail(CR_ERR_ALIGN, "the cache's codes or scales not 16-byte aligned");
+    if (!table || !lens || !cu) return fail(CR_ERR_NULL, "table, lens or cu is NULL");
+    if (!aligned4(table) || !aligned4(lens) || !aligned4(cu))
+        return fail(CR_ERR_ALIGN, "table, lens or cu not 4-byte aligned");
+    return CR_OK;
+}
+cr_status check_width(int width) {
+    if (width < 1 || width > CR_MAX_DIM) return fail(CR_ERR_SHAPE, "bad table width=%d", width);
+    return CR_OK;
+}
+cr::Kv4 kv4_of(const cr_kv4* c, const int32_t* table, int width, const int32_t* lens, const int32_t* cu, int B, int T) {
+    cr::Kv4 k{};
+    k.codes = static_cast<uint8_t*>(c->codes); k.scales = static_cast<uint32_t*>(c->scales);
+    k.pages = c->pages; k.page_log2 = __builtin_ctz(c->page); k.heads = c->heads; k.dim = c->dim; k.group = c->group;
+    k.rotate = c->rotate != 0;
+    k.table = table; k.lens = lens; k.cu = cu; k.width = width; k.B = B; k.T = T;
+    return k;
+}
 
 }  // namespace
 
@@ -844,6 +915,123 @@ cr_status cr_moe_w4g(int dtype, const void* x, int M, int K, const void* router,
     a.M = M; a.K = K; a.F = F; a.E = E; a.topk = topk; a.group = group;
     a.y = static_cast<uint16_t*>(y); a.ids = ids; a.weights = weights; a.ws = ws;
     return launch_err(cr::launch_moe(a, stream), "mixture-of-experts layer");
+}
+
+cr_status cr_attn_prompt(int dtype, const void* q, int64_t q_row, int64_t q_head, const void* k, int64_t k_row,
+                         int64_t k_head, const void* v, int64_t v_row, int64_t v_head, int T, int Hq, int Hkv, int D,
+                         const int32_t* cu, int B, int causal, float scale, void* y, hipStream_t stream) {
+    cr_status s;
+    if ((s = check_attn(dtype, T, Hq, Hkv, D, B, scale)) != CR_OK) return s;
+    if (T == 0 || B == 0) return ok();
+    const Heads in[3] = {{"q", q, q_row, q_head, Hq}, {"k", k, k_row, k_head, Hkv}, {"v", v, v_row, v_head, Hkv}};
+    for (const Heads& x : in)
+        if ((s = check_heads(x, T, D)) != CR_OK) return s;
+    if (!cu || !y) return fail(CR_ERR_NULL, "cu or y is NULL");
+    if (!aligned4(cu)) return fail(CR_ERR_ALIGN, "cu not 4-byte aligned");
+    if (!aligned16(y)) return fail(CR_ERR_ALIGN, "y not 16-byte aligned");
+    for (const Heads& x : in)
+        if ((s = check_apart(x, T, D, y, (size_t)T * Hq * D * 2)) != CR_OK) return s;
+    if ((s = check_device()) != CR_OK) return s;
+    cr::AttnArgs a{};
+    a.fp16 = dtype == CR_FP16; a.causal = causal != 0;
+    a.q = static_cast<const uint16_t*>(q); a.k = static_cast<const uint16_t*>(k); a.v = static_cast<const uint16_t*>(v);
+    a.q_row = q_row; a.q_head = q_head; a.k_row = k_row; a.k_head = k_head; a.v_row = v_row; a.v_head = v_head;
+    a.T = T; a.Hq = Hq; a.Hkv = Hkv; a.D = D; a.cu = cu; a.B = B; a.scale = scale;
+    a.y = static_cast<uint16_t*>(y);
+    return launch_err(cr::launch_attn_prompt(a, stream), "attention over prompts");
+}
+
+size_t cr_kv4_codes_bytes(const cr_kv4* c) {
+    if (check_kv4(c) != CR_OK) return 0;
+    return (size_t)c->pages * 2 * c->heads * c->page * (c->dim / 2);
+}
+
+size_t cr_kv4_scales_bytes(const cr_kv4* c) {
+    if (check_kv4(c) != CR_OK) return 0;
+    return (size_t)c->pages * 2 * c->heads * c->page * (c->dim / c->group) * 4;
+}
+
+cr_status cr_kv4_append(int dtype, const void* k, int64_t k_row, int64_t k_head, const void* v, int64_t v_row,
+                        int64_t v_head, int T, const cr_kv4* cache, const int32_t* table, int width,
+                        const int32_t* lens, const int32_t* cu, int B, hipStream_t stream) {
+    cr_status s;
+    if ((s = check_kv4(cache)) != CR_OK) return s;
+    if ((s = check_attn(dtype, T, cache->heads, cache->heads, cache->dim, B, 1.0f)) != CR_OK) return s;
+    if ((s = check_width(width)) != CR_OK) return s;
+    if (T == 0 || B == 0) return ok();
+    const Heads in[2] = {{"k", k, k_row, k_head, cache->heads}, {"v", v, v_row, v_head, cache->heads}};
+    for (const Heads& x : in)
+        if ((s = check_heads(x, T, cache->dim)) != CR_OK) return s;
+    if ((s = check_kv4_call(cache, table, width, lens, cu)) != CR_OK) return s;
+    if ((s = check_device()) != CR_OK) return s;
+    return launch_err(cr::launch_kv4_append(dtype == CR_FP16, static_cast<const uint16_t*>(k), k_row, k_head,
+                                            static_cast<const uint16_t*>(v), v_row, v_head,
+                                            kv4_of(cache, table, width, lens, cu, B, T), stream),
+                      "writing the 4-bit cache");
+}
+
+size_t cr_attn_kv4_workspace_bytes(int T, int Hq, const cr_kv4* cache, int width, int B) {
+    if (check_kv4(cache) != CR_OK) return 0;
+    if (check_attn(CR_BF16, T, Hq, cache->heads, cache->dim, B, 1.0f) != CR_OK || check_width(width) != CR_OK) return 0;
+    const size_t n = cr::attn_kv4_workspace(T, Hq, cache->heads, cache->dim, cache->page, width, B);
+    return n < 256 ? 256 : n;
+}
+
+cr_status cr_attn_kv4(int dtype, const void* q, int64_t q_row, int64_t q_head, int T, int Hq, const cr_kv4* cache,
+                      const int32_t* table, int width, const int32_t* lens, const int32_t* cu, int B, float scale,
+                      void* y, void* ws, size_t ws_bytes, hipStream_t stream) {
+    cr_status s;
+    if ((s = check_kv4(cache)) != CR_OK) return s;
+    if ((s = check_attn(dtype, T, Hq, cache->heads, cache->dim, B, scale)) != CR_OK) return s;
+    if ((s = check_width(width)) != CR_OK) return s;
+    if (T == 0 || B == 0) return ok();
+    const Heads x{"q", q, q_row, q_head, Hq};
+    if ((s = check_heads(x, T, cache->dim)) != CR_OK) return s;
+    if ((s = check_kv4_call(cache, table, width, lens, cu)) != CR_OK) return s;
+    if (!y || !ws) return fail(CR_ERR_NULL, "y or workspace is NULL");
+    if (!aligned16(y) || !aligned16(ws)) return fail(CR_ERR_ALIGN, "y or workspace not 16-byte aligned");
+    if ((s = check_apart(x, T, cache->dim, y, (size_t)T * Hq * cache->dim * 2)) != CR_OK) return s;
+    const size_t need = cr_attn_kv4_workspace_bytes(T, Hq, cache, width, B);
+    if (ws_bytes < need) return fail(CR_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", ws_bytes, need);
+    if ((s = check_device()) != CR_OK) return s;
+    cr::AttnArgs a{};
+    a.fp16 = dtype == CR_FP16;
+    a.q = static_cast<const uint16_t*>(q); a.q_row = q_row; a.q_head = q_head;
+    a.T = T; a.Hq = Hq; a.Hkv = cache->heads; a.D = cache->dim; a.scale = scale;
+    a.y = static_cast<uint16_t*>(y);
+    return launch_err(cr::launch_attn_kv4(a, kv4_of(cache, table, width, lens, cu, B, T), ws, stream),
+                      "attention over the 4-bit cache");
+}
+
+cr_status cr_dbg_kv4_place(const cr_kv4* cache, const int32_t* table, int width, const int32_t* lens,
+                           const int32_t* cu, int B, int T, int row, int head, int64_t* place) {
+    cr_status s;
+    if ((s = check_kv4(cache)) != CR_OK) return s;
+    if ((s = check_attn(CR_BF16, T, cache->heads, cache->heads, cache->dim, B, 1.0f)) != CR_OK) return s;
+    if ((s = check_width(width)) != CR_OK) return s;
+    if (row < 0 || row >= T || head < 0 || head >= cache->heads) return fail(CR_ERR_SHAPE, "bad row=%d head=%d", row, head);
+    if (!table || !lens || !cu || !place) return fail(CR_ERR_NULL, "NULL argument");
+    const cr::Kv4 c = kv4_of(cache, table, width, lens, cu, B, T);
+    for (int i = 0; i < 8; ++i) place[i] = -1;
+    for (int b = 0; b < B; ++b) {
+        const cr::Kv4Seq q = cr::kv4_seq(c, b);
+        if (row < q.first || row >= q.first + q.rows) continue;
+        const int pos = q.tokens - q.rows + (row - q.first);
+        place[0] = b;
+        place[1] = pos;
+        place[7] = q.tokens;
+        const int page = pos < 0 ? -1 : cr::kv4_page(c, b, pos);
+        if (page < 0) break;
+        const int r = pos & (cache->page - 1);
+        place[2] = page;
+        for (int which = 0; which < 2; ++which) {
+            place[3 + which] = (int64_t)cr::kv4_codes_at(c, page, which, head) +
+                               (which ? cr::kv4_v_byte(c.dim, r, 0) : cr::kv4_k_byte(c.dim, r, 0));
+            place[5 + which] = (int64_t)cr::kv4_scales_at(c, page, which, head) + r * (c.dim / c.group);
+        }
+        break;
+    }
+    return ok();
 }
 
 }  // extern "C"

@@ -6,6 +6,8 @@
 
 #include <atomic>
 
+#include "cr_kv4.h"
+
 namespace cr {
 
 // W4A4 rotation selector for the group-256 regular Hadamard (J - 2I)^(x4) / 16,
@@ -135,6 +137,27 @@ struct MoeArgs {
 };
 size_t moe_workspace(int M, int K, int F, int E, int topk);
 hipError_t launch_moe(const MoeArgs& a, hipStream_t st);
+
+// Attention over whole prompts (cr_attn.hip).  Strides are in values; rows of
+// the packed tensors are tokens.
+struct AttnArgs {
+    bool fp16, causal;
+    const uint16_t *q, *k, *v;                           // [T, Hq, D], [T, Hkv, D]
+    int64_t q_row, q_head, k_row, k_head, v_row, v_head;
+    int T, Hq, Hkv, D;
+    const int32_t* cu;                                   // [B + 1] first rows of the sequences
+    int B;
+    float scale;
+    uint16_t* y;                                         // [T, Hq, D], contiguous
+};
+hipError_t launch_attn_prompt(const AttnArgs& a, hipStream_t st);
+
+// The 4-bit cache (cr_kv4.hip): its writer, and attention over it (of `a`: the
+// types, q, Hq, scale and y).
+hipError_t launch_kv4_append(bool fp16, const uint16_t* k, int64_t k_row, int64_t k_head, const uint16_t* v,
+                             int64_t v_row, int64_t v_head, const Kv4& c, hipStream_t st);
+size_t attn_kv4_workspace(int T, int Hq, int heads, int dim, int page, int width, int B);
+hipError_t launch_attn_kv4(const AttnArgs& a, const Kv4& c, void* ws, hipStream_t st);
 
 struct GemmArgs {
     int kind;              // WKind
