@@ -4,17 +4,36 @@
 //   y[i, h] = T(sum_j p[i, j] v[j, h / G] / sum_j p[i, j]),
 //   p[i, j] = exp(scale q[i, h] . k[j, h / G]),
 // j over the tokens of i's sequence, up to i if causal.
+#include <type_traits>
+
 #include "cr_w4g.h"
 
 namespace cr {
 namespace {
 
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+
+__device__ __forceinline__ f32x16 mfma32(Bf16, u32x4 a, u32x4 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16 mfma32(Fp16, u32x4 a, u32x4 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+}
+__device__ __forceinline__ uint32_t pack2(Bf16, float a, float b) { return pack_bf16x2(a, b); }
+__device__ __forceinline__ uint32_t pack2(Fp16, float a, float b) {
+    f32x2_t f;
+    f.x = a; f.y = b;
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f, f16x2));
+}
+
 // One row by the definition, in float64, by one wave: lane l takes
 // d = l D / 64 and on.  Two passes over the keys: the largest score, then the
 // sums, so that infinities and NaN come out as they do in the definition.
 template <class T, int D>
-__device__ void attn_row_defined(const uint16_t* q, const uint16_t* k, int64_t k_row, const uint16_t* v, int64_t v_row,
-                                 int keys, float scale, uint16_t* y) {
+__device__ __noinline__ void attn_row_defined(const uint16_t* q, const uint16_t* k, int64_t k_row, const uint16_t* v,
+                                              int64_t v_row, int keys, float scale, uint16_t* y) {
     constexpr int N = D / 64;
     const int lane = threadIdx.x & 63, d = lane * N;
     double top = -__builtin_inf(), sum = 0.0, o[N] = {};
@@ -38,44 +57,271 @@ __device__ void attn_row_defined(const uint16_t* q, const uint16_t* k, int64_t k
         }
     }
 #pragma unroll
-    for (int i = 0; i < N; ++i) y[d + i] = keys > 0 ? T::from_f32((float)(o[i] / sum)) : 0;
+    for (int i = 0; i < N; ++i) y[d + i] = T::from_f32((float)(o[i] / sum));
 }
 
-// The sequence that row t is in, or -1.
-__device__ int sequence_of(const int32_t* cu, int B, int T, int t) {
-    for (int b = 0; b < B; ++b) {
-        const int first = min(max(cu[b], 0), T), last = min(max(cu[b + 1], first), T);
-        if (t >= first && t < last) return b;
+// The sequence and the tile of BM rows in it that tile `t` from the end is:
+// sequences' tiles counted one after the other.  Every wave counts for itself.
+struct Tile {
+    int first, len, row;   // the sequence's first row and its length; the tile's first row in it
+};
+template <int BM>
+__device__ __forceinline__ bool find_tile(const int32_t* cu, int B, int T, int t, Tile* out) {
+    const int lane = threadIdx.x & 63;
+    int total = 0;
+    for (int b0 = 0; b0 < B; b0 += 64) {
+        const int b = min(b0 + lane, B - 1);
+        const int first = min(max(cu[b], 0), T), len = min(max(cu[b + 1], first), T) - first;
+        int n = b0 + lane < B ? (len + BM - 1) / BM : 0;
+#pragma unroll
+        for (int m = 1; m < 64; m <<= 1) n += __shfl_xor(n, m);
+        total += n;
     }
-    return -1;
+    int left = total - 1 - t;   // tiles before this one
+    if (left < 0) return false;
+    for (int b0 = 0; b0 < B; b0 += 64) {
+        const int b = min(b0 + lane, B - 1);
+        const int first = min(max(cu[b], 0), T), len = min(max(cu[b + 1], first), T) - first;
+        const int n = b0 + lane < B ? (len + BM - 1) / BM : 0;
+        int upto = n;
+#pragma unroll
+        for (int m = 1; m < 64; m <<= 1) {
+            const int p = __shfl_up(upto, m);
+            if (lane >= m) upto += p;
+        }
+        const uint64_t after = __ballot(upto > left);
+        if (after) {
+            const int l = __builtin_ctzll(after);
+            out->first = __builtin_amdgcn_readfirstlane(__shfl(first, l));
+            out->len = __builtin_amdgcn_readfirstlane(__shfl(len, l));
+            out->row = __builtin_amdgcn_readfirstlane((left - __shfl(upto - n, l)) * BM);
+            return true;
+        }
+        left -= __shfl(upto, 63);
+    }
+    return false;
 }
 
-template <class T, int D>
-__global__ void k_attn_prompt(AttnArgs a) {
-    const int t = blockIdx.x, h = blockIdx.y;
-    const int b = sequence_of(a.cu, a.B, a.T, t);
-    if (b < 0) return;
-    const int first = min(max(a.cu[b], 0), a.T), last = min(max(a.cu[b + 1], first), a.T);
+// Rows of K or V in LDS: 16-byte chunk c of row r at chunk c ^ swizzle(r).
+// K is read 16 rows at one chunk, V 8 rows at two pairs of chunks (below): either
+// way all banks are hit alike.
+template <int D, bool V>
+__device__ __forceinline__ int swizzle(int r) {
+    constexpr int rows = D >= 128 ? 1 : 128 / D;   // rows in 256 bytes
+    return V ? ((r / rows) & (rows > 1 ? 3 : 7)) * 2 : (r / rows) & (rows > 1 ? 7 : 15);
+}
+
+// One block: BM = 32 NW rows of one head, a wave 32 of them, over tiles of BN
+// keys that all waves share in LDS, the next tile's on their way meanwhile.
+//   S^T = K Q^T   MFMA 32x32x16: a lane holds 16 keys' scores of one row
+//   O^T = V^T P^T the same lane's weights are the second operand as they lie:
+//                 step s takes its scores 8 s + 0..7, keys 16 s + 8 (i / 4) + 4 (lane / 32) + i % 4;
+//                 V's operand comes transposed from LDS, 4 keys a read
+template <class T, int D, int NW, int BN>
+__global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_prompt(AttnArgs a) {
+    constexpr int BM = 32 * NW, KS = D / 16, DT = D / 32, MT = BN / 32, PS = BN / 16;
+    constexpr int kTile = BN * D * 2, kLoads = kTile / 1024 / NW;   // bytes of a K or V tile; 1 KiB loads of a wave
+    constexpr float kMove = 8.0f;   // the maximum follows when weights would pass 2^8
+    // fp16 weights: 2^6 at the maximum, so that fewer fall below its normal range
+    constexpr float kBias = std::is_same_v<T, Fp16> ? 6.0f : 0.0f;
+    extern __shared__ __align__(1024) char lds[];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    Tile t;
+    if (!find_tile<BM>(a.cu, a.B, a.T, blockIdx.y + blockIdx.z * gridDim.y, &t)) return;
+    // blocks go to the 8 XCDs in turn: heads of one key head to the same one
+    int h = blockIdx.x;
+    if ((a.Hq & 7) == 0) h = (h & 7) * (a.Hq >> 3) + (h >> 3);
     const int g = h / (a.Hq / a.Hkv);
-    attn_row_defined<T, D>(a.q + t * a.q_row + h * a.q_head, a.k + first * a.k_row + g * a.k_head, a.k_row,
-                           a.v + first * a.v_row + g * a.v_head, a.v_row, a.causal ? t - first + 1 : last - first,
-                           a.scale, a.y + ((int64_t)t * a.Hq + h) * D);
+    const uint16_t* q = a.q + t.first * a.q_row + h * a.q_head;
+    const uint16_t* k = a.k + t.first * a.k_row + g * a.k_head;
+    const uint16_t* v = a.v + t.first * a.v_row + g * a.v_head;
+    const int row0 = t.row + wave * 32, row = row0 + (lane & 31);
+    const int keys = a.causal ? min(t.len, t.row + BM) : t.len;
+    const int tiles = (keys + BN - 1) / BN;
+    const int mine = row0 >= t.len ? 0 : a.causal ? min(row0 + 32, t.len) : t.len;   // keys this wave's rows see
+
+    // the wave's part of a tile's loads: load i fills 1 KiB of K or V, lane by lane
+    uint32_t k_off[kLoads], v_off[kLoads];
+    auto offsets = [&](int rows) {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int at = (wave * kLoads + i) * 64 + lane, r = at / (D / 8), c = at % (D / 8), rr = min(r, rows - 1);
+            k_off[i] = (uint32_t)rr * (uint32_t)a.k_row * 2 + (c ^ swizzle<D, false>(r)) * 16;
+            v_off[i] = (uint32_t)rr * (uint32_t)a.v_row * 2 + (c ^ swizzle<D, true>(r)) * 16;
+        }
+    };
+    auto rows_at = [&](const uint16_t* p, int64_t stride, int j) {
+        const uint64_t at = (uint64_t)(uintptr_t)(p + (int64_t)j * stride);
+        v4i r;
+        r.x = __builtin_amdgcn_readfirstlane((int)(uint32_t)at);
+        r.y = __builtin_amdgcn_readfirstlane((int)((uint32_t)(at >> 32) & 0xFFFFu));
+        r.z = -1;   // every offset lies inside (rows past the last bring the last)
+        r.w = 0x00020000;
+        return r;
+    };
+    const uint32_t lds0 = lds_address(lds);
+    auto load = [&](int tile, int buffer) {
+        const int j = tile * BN;
+        if (keys - j < BN) offsets(t.len - j < BN ? t.len - j : BN);
+        const v4i kr = rows_at(k, a.k_row, j), vr = rows_at(v, a.v_row, j);
+        const uint32_t to = __builtin_amdgcn_readfirstlane(lds0 + buffer * 2 * kTile + wave * kLoads * 1024);
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) w4g_x_to_lds(kr, k_off[i], to + i * 1024);
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) w4g_x_to_lds(vr, v_off[i], to + kTile + i * 1024);
+    };
+    offsets(min(t.len, BN));
+    load(0, 0);
+
+    u32x4 qv[KS];
+    {
+        const uint16_t* p = q + (int64_t)min(row, t.len - 1) * a.q_row + 8 * (lane >> 5);
+#pragma unroll
+        for (int s = 0; s < KS; ++s) qv[s] = *reinterpret_cast<const u32x4*>(p + 16 * s);
+    }
+    f32x16 o[DT] = {};
+    // a scale of 0 would make NaN of the scores that are masked; all weights are 1 with this one too
+    const float c = a.scale == 0.0f ? 1e-30f : a.scale * 1.4426950408889634f;
+    float top = -__builtin_inff(), sum = 0.0f;   // of the scores times c; this lane's keys
+
+    for (int j = 0; j < tiles; ++j) {
+        w4g_wait();
+        w4g_barrier();
+        if (j + 1 < tiles) load(j + 1, (j + 1) & 1);
+        if (j * BN >= mine) continue;
+        const char* kt = lds + (j & 1) * 2 * kTile;
+        const char* vt = kt + kTile;
+        f32x16 s[MT];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            s[mt] = f32x16{};
+            const int r = 32 * mt + (lane & 31);
+            const char* p = kt + r * (2 * D);
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks)
+                s[mt] = mfma32(T(), *reinterpret_cast<const u32x4*>(p + ((2 * ks + (lane >> 5)) ^ swizzle<D, false>(r)) * 16),
+                               qv[ks], s[mt]);
+        }
+        // this lane's score i of part mt: key j BN + 32 mt + 8 (i / 4) + 4 (lane / 32) + i % 4
+        if (j * BN + BN > (a.causal ? min(row0 + 1, t.len) : t.len)) {
+            const int last = (a.causal ? min(row, t.len - 1) : t.len - 1) - j * BN - 4 * (lane >> 5);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (32 * mt + 8 * (i / 4) + i % 4 > last) s[mt][i] = c < 0.0f ? __builtin_inff() : -__builtin_inff();
+        }
+        float m = s[0][0] * c;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) m = fmaxf(m, s[mt][i] * c);
+        if (__any(m > top + kMove)) {
+            m = fmaxf(m, __shfl_xor(m, 32));
+            const float up = fmaxf(top, m), f = top == up ? 1.0f : __builtin_amdgcn_exp2f(top - up);
+            top = up;
+            sum *= f;
+#pragma unroll
+            for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[dt][i] *= f;
+        }
+        u32x4 p[PS];
+        const float off = kBias - top;
+#pragma unroll
+        for (int ps = 0; ps < PS; ++ps) {
+            float e[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[ps / 2][8 * (ps % 2) + i], c, off));
+                sum += e[i];
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) p[ps][i] = pack2(T(), e[2 * i], e[2 * i + 1]);
+        }
+        // V^T: the 16 lanes of a group take 4 keys x 16 d, lane i the keys' d = i
+        const int vr = 4 * (lane >> 5) + ((lane & 15) >> 2), vc = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+#pragma unroll
+        for (int ps = 0; ps < PS; ++ps) {
+#pragma unroll
+            for (int dt = 0; dt < DT; ++dt) {
+                u32x4 b;
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const int r = 16 * ps + 8 * x + vr;
+                    const char* at = vt + r * (2 * D) + ((4 * dt + vc) ^ swizzle<D, true>(r)) * 16 + (lane & 1) * 8;
+                    const s16x4 w = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                        (lds_s16x4*)(__attribute__((address_space(3))) char*)at);
+                    const uint2 u = __builtin_bit_cast(uint2, w);
+                    b[2 * x] = u.x;
+                    b[2 * x + 1] = u.y;
+                }
+                o[dt] = mfma32(T(), b, p[ps], o[dt]);
+            }
+        }
+    }
+
+    if (row0 >= t.len) return;
+    sum += __shfl_xor(sum, 32);
+    const float inv = 1.0f / sum;
+    bool bad = false;
+    float y[DT][16];
+#pragma unroll
+    for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            y[dt][i] = o[dt][i] * inv;
+            bad |= !w4g_finite(y[dt][i]);
+        }
+    const uint64_t wrong = __ballot(bad);
+    const uint32_t again = (uint32_t)(wrong | wrong >> 32);   // rows that are infinite or NaN somewhere
+    uint16_t* out = a.y + ((int64_t)(t.first + row) * a.Hq + h) * D + 4 * (lane >> 5);
+    if (row < t.len && !(again >> (lane & 31) & 1)) {
+#pragma unroll
+        for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) {
+                uint2 w;
+                w.x = pack2(T(), y[dt][i], y[dt][i + 1]);
+                w.y = pack2(T(), y[dt][i + 2], y[dt][i + 3]);
+                *reinterpret_cast<uint2*>(out + 32 * dt + 2 * i) = w;
+            }
+    }
+    // A weight of 0 times an infinity that the row does not see, a score that
+    // passes float32: the definition decides.
+    for (uint32_t r = __builtin_amdgcn_readfirstlane(again); r != 0; r &= r - 1) {
+        const int i = row0 + __builtin_ctz(r);
+        if (i >= t.len) break;
+        attn_row_defined<T, D>(q + i * a.q_row, k, a.k_row, v, a.v_row, a.causal ? i + 1 : t.len, a.scale,
+                               a.y + ((int64_t)(t.first + i) * a.Hq + h) * D);
+    }
 }
 
+template <class T, int D, int NW, int BN>
+hipError_t launch(const AttnArgs& a, hipStream_t st) {
+    constexpr int BM = 32 * NW, lds = 4 * BN * D * 2;
+    static std::atomic<uint64_t> done{0};
+    if (lds > 65536) {
+        const hipError_t e = opt_in_lds(reinterpret_cast<const void*>(&k_attn_prompt<T, D, NW, BN>), lds, done);
+        if (e != hipSuccess) return e;
+    }
+    // tiles that B sequences of T rows can have
+    const int64_t tiles = a.B == 1 ? (a.T + BM - 1) / BM : ((int64_t)a.T + (int64_t)a.B * (BM - 1)) / BM;
+    const int y = (int)(tiles < 32768 ? tiles : 32768);
+    k_attn_prompt<T, D, NW, BN><<<dim3(a.Hq, y, (unsigned)((tiles + y - 1) / y)), 64 * NW, lds, st>>>(a);
+    return hipGetLastError();
+}
 template <class T>
-void launch(const AttnArgs& a, hipStream_t st) {
-    const dim3 grid(a.T, a.Hq);
-    if (a.D == 64) k_attn_prompt<T, 64><<<grid, 64, 0, st>>>(a);
-    if (a.D == 128) k_attn_prompt<T, 128><<<grid, 64, 0, st>>>(a);
-    if (a.D == 256) k_attn_prompt<T, 256><<<grid, 64, 0, st>>>(a);
+hipError_t launch_by_dim(const AttnArgs& a, hipStream_t st) {
+    if (a.D == 64) return launch<T, 64, 4, 64>(a, st);
+    if (a.D == 128) return launch<T, 128, 4, 64>(a, st);
+    return launch<T, 256, 4, 32>(a, st);
 }
 
 }  // namespace
 
 hipError_t launch_attn_prompt(const AttnArgs& a, hipStream_t st) {
-    if (a.fp16) launch<Fp16>(a, st);
-    else launch<Bf16>(a, st);
-    return hipGetLastError();
+    return a.fp16 ? launch_by_dim<Fp16>(a, st) : launch_by_dim<Bf16>(a, st);
 }
 
 }  // namespace cr
