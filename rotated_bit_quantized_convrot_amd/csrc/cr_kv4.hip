@@ -7,6 +7,8 @@
 //   lo = min(0, min x'), hi = max(0, max x'), s = hi / 15 - lo / 15 to the
 //   nearest float32 whose low four bits are 0, z = clamp(rint(-lo / s), 0, 15),
 //   c = clamp(rint(x' / s) + z, 0, 15); both 0 where s = 0.
+#include <type_traits>
+
 #include "cr_w4g.h"
 #include "cr_kv4.h"
 
@@ -104,66 +106,519 @@ __global__ void k_kv4_append(AppendArgs a) {
         a.c.scales[kv4_scales_at(a.c, page, which, h) + row * (D / a.c.group) + d / a.c.group] = sb | (uint32_t)z;
 }
 
-// x'[d], a value of the cache.
+// ---------------------------------------------------------------------------
+// Attention over the cache
+// ---------------------------------------------------------------------------
+//
+// Of a sequence's n query rows and a key head, the n G rows (row i, head of
+// the group) go in tiles of 16, one to a column of MFMA 16x16x32; the tokens
+// in spans over blocks, and a span's steps of 64 tokens over the block's waves.
+//   S^T = K q^T      a lane holds 16 tokens' scores of one row: of step
+//                    tokens 16 (lane / 16) + 0..15
+//   O^T = V^T P^T    the weights are the second operand as they lie; V is laid
+//                    out so that a lane's 16 bytes are these tokens of two d
+// The operands hold 1 + c / 16, the code put into the mantissa of 1.0 (two
+// instructions a pair); what that adds, (1 + z / 16) sum q and
+// (1 + z / 16) sum p, is known and taken off in float32.
+// q (rotated: float32) and the weights times V's scales go in as two bf16
+// values of 8 bits each, in bf16's range whatever T.
+constexpr int kWaves = 4, kStep = 64;
+constexpr int kMinSpan = kWaves * kStep;
+
 template <int D>
-__device__ __forceinline__ double kv4_value(const Kv4& c, int page, int which, int h, int row, int d) {
-    const uint8_t* codes = c.codes + kv4_codes_at(c, page, which, h);
-    const uint32_t w = c.scales[kv4_scales_at(c, page, which, h) + row * (D / c.group) + d / c.group];
-    int q;
-    if (which == 0) {
-        const uint32_t dw = *reinterpret_cast<const uint32_t*>(
-            codes + kv4_k_byte(D, row, (d / 8 % 4) * (D / 32) + d / 32));
-        q = dw >> (4 * (d % 8 / 2) + 16 * (d % 2)) & 15;
-    } else {
-        q = codes[kv4_v_byte(D, row, 16 * (d / 32) + d % 16)] >> (d % 32 >= 16 ? 4 : 0) & 15;
+constexpr int max_tiles() { return D == 64 ? 4 : D == 128 ? 2 : 1; }
+
+// One block's work: tile group `tile` of sequence b (rows 16 RT tile ..),
+// tokens span * chunk .. of it; its slot among all blocks of a head.
+struct Kv4Work {
+    int b, first, rows, tokens, tile, chunk, chunks, span, slot;
+};
+// The work of block `index` of `slots` (by_tile: of tile group `index`, its
+// chunk 0).  The span is the shortest, from kMinSpan on, with which all spans
+// of all tile groups have a slot; slots = 0: one span takes everything.  Every
+// wave counts for itself, 64 sequences at a time.
+template <int RT>
+__device__ __forceinline__ bool kv4_work(const Kv4& c, int G, int slots, bool by_tile, int index, Kv4Work* w) {
+    const int lane = threadIdx.x & 63;
+    int span = 0x40000000;
+    if (slots > 0) {
+        int groups = 0;
+        long long total = 0;
+        for (int b0 = 0; b0 < c.B; b0 += 64) {
+            const Kv4Seq s = kv4_seq(c, min(b0 + lane, c.B - 1));
+            int n = b0 + lane < c.B ? (int)(((long long)s.rows * G + 16 * RT - 1) / (16 * RT)) : 0;
+            long long t = (long long)n * s.tokens;
+#pragma unroll
+            for (int m = 1; m < 64; m <<= 1) {
+                n += __shfl_xor(n, m);
+                t += __shfl_xor(t, m);
+            }
+            groups += n;
+            total += t;
+        }
+        if (groups >= slots) groups = slots - 1;   // not so: the grid has two slots a group
+        const long long left = slots - groups, e = (total + left - 1) / left;
+        span = (int)((e < kMinSpan ? kMinSpan : e + kMinSpan - 1) / kMinSpan) * kMinSpan;
     }
-    return (double)__uint_as_float(w & ~15u) * (q - (int)(w & 15u));
+    int at = 0, slot = 0;
+    for (int b0 = 0; b0 < c.B; b0 += 64) {
+        const Kv4Seq s = kv4_seq(c, min(b0 + lane, c.B - 1));
+        const int n = b0 + lane < c.B ? (int)(((long long)s.rows * G + 16 * RT - 1) / (16 * RT)) : 0;
+        const int chunks = s.tokens > span ? (s.tokens + span - 1) / span : 1;
+        int tiles = n, all = n * chunks;
+#pragma unroll
+        for (int m = 1; m < 64; m <<= 1) {
+            const int t = __shfl_up(tiles, m), x = __shfl_up(all, m);
+            if (lane >= m) { tiles += t; all += x; }
+        }
+        const uint64_t after = __ballot((by_tile ? at + tiles : slot + all) > index);
+        if (after) {
+            const int l = __builtin_ctzll(after);
+            auto of = [&](int v) { return __builtin_amdgcn_readfirstlane(__shfl(v, l)); };
+            w->b = b0 + l;
+            w->first = of(s.first);
+            w->rows = of(s.rows);
+            w->tokens = of(s.tokens);
+            w->chunks = of(chunks);
+            w->span = span;
+            const int before = __builtin_amdgcn_readfirstlane(slot) + of(all - n * chunks);
+            if (by_tile) {
+                w->tile = index - __builtin_amdgcn_readfirstlane(at) - of(tiles - n);
+                w->chunk = 0;
+            } else {
+                w->tile = (index - before) / w->chunks;
+                w->chunk = (index - before) % w->chunks;
+            }
+            w->slot = before + w->tile * w->chunks + w->chunk;
+            return true;
+        }
+        at += __shfl(tiles, 63);
+        slot += __shfl(all, 63);
+    }
+    return false;
 }
 
-// One wave a row and head.
+// Partial results of a slot: sums [16 RT][D], then the maxima and the sums of
+// weights [16 RT] each.
+template <int D, int RT>
+constexpr size_t part_words() { return 16 * RT * (D + 2); }
+
+// Four operand pairs of a dword of codes: 1 + c / 16 in bf16.
+__device__ __forceinline__ u32x4 kv4_operand(uint32_t w) {
+    u32x4 b;
+    b[0] = (w << 3 & 0x00780078u) | 0x3F803F80u;
+    b[1] = (w >> 1 & 0x00780078u) | 0x3F803F80u;
+    b[2] = (w >> 5 & 0x00780078u) | 0x3F803F80u;
+    b[3] = (w >> 9 & 0x00780078u) | 0x3F803F80u;
+    return b;
+}
+// 16 tokens of V (4 dwords, a byte a token): operand of tokens 8 u + 0..7 in
+// the order 0 2, 1 3, 4 6, 5 7, of the bytes' low or high nibbles.
+template <bool HIGH>
+__device__ __forceinline__ u32x4 kv4_v_operand(uint32_t a, uint32_t b) {
+    constexpr uint32_t m = 0x00780078u, one = 0x3F803F80u;
+    u32x4 r;
+    r[0] = ((HIGH ? a >> 1 : a << 3) & m) | one;
+    r[1] = ((HIGH ? a >> 9 : a >> 5) & m) | one;
+    r[2] = ((HIGH ? b >> 1 : b << 3) & m) | one;
+    r[3] = ((HIGH ? b >> 9 : b >> 5) & m) | one;
+    return r;
+}
+// x as hi + lo of 8 bits each (to 2^-17 of x).
+__device__ __forceinline__ void split2(float a, float b, uint32_t* hi, uint32_t* lo) {
+    *hi = pack_bf16x2(a, b);
+    *lo = pack_bf16x2(a - __uint_as_float(*hi << 16), b - __uint_as_float(*hi & 0xFFFF0000u));
+}
+
+// Floats of a row in LDS, so that 16 rows' 16 bytes hit all banks; of the block.
+template <int D>
+constexpr int lds_row() { return D + 4; }
+template <int D>
+constexpr int lds_words() { return kWaves * 16 * lds_row<D>(); }
+
+template <int N>
+struct Words {
+    uint32_t w[N];
+};
+
+// y = sums over the sum of weights, turned back; 0 for a row that saw nothing.
 template <class T, int D>
-__global__ void k_attn_kv4(Kv4 c, AttnArgs a) {
-    constexpr int N = D / 64;
-    const int t = blockIdx.x, h = blockIdx.y, lane = threadIdx.x, d = lane * N, g = h / (a.Hq / c.heads);
-    int b = 0;
-    Kv4Seq s = {};
-    for (; b < c.B; ++b) {
-        s = kv4_seq(c, b);
-        if (t >= s.first && t < s.first + s.rows) break;
+__device__ __forceinline__ void kv4_finish(float (&x)[D / 64], float total, int rotate, uint16_t* y) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) x[i] = total == 0.0f ? 0.0f : x[i] / total;
+    if (rotate) rotate_head<D>(x);
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) y[lane * (D / 64) + i] = T::from_f32(x[i]);
+}
+
+// LO: q needs its second part (rotated, or fp16's 11 bits).
+template <class T, int D, int NG, int RT, bool LO>
+__global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void k_attn_kv4(Kv4 c, AttnArgs a, int slots, float* parts) {
+    constexpr int KS = D / 32, SPG = KS / NG, DT = D / 16, DPG = DT / NG;
+    constexpr float kMove = 8.0f;   // the maximum follows when weights would pass 2^8
+    constexpr int kRow = lds_row<D>();
+    // the waves' words of a step ([K, V][group][token]); then their sums of a tile
+    extern __shared__ __align__(16) uint32_t lds[];
+    static_assert(kWaves * 2 * kStep * NG <= lds_words<D>(), "words fit where the sums go");
+    float* lds_o = reinterpret_cast<float*>(lds);
+    __shared__ float lds_top[kWaves][16], lds_sum[kWaves][16];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, quad = lane >> 4;
+    const int g = blockIdx.x, G = a.Hq / c.heads;
+    Kv4Work w;
+    if (!kv4_work<RT>(c, G, slots, false, blockIdx.y + blockIdx.z * gridDim.y, &w)) return;
+    const int begin = w.chunk * w.span, end = min(begin + w.span, w.tokens);
+
+    // rows of the tiles: what they see, and q
+    int seen[RT];
+    u32x4 qh[RT][KS], ql[RT][LO ? KS : 1];
+    float qs[RT][NG];
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+        // a column past the last row repeats it
+        const long long r = min((long long)(w.tile * RT + t) * 16 + col, (long long)w.rows * G - 1);
+        const int i = (int)(r / G), h = g * G + (int)(r % G);
+        seen[t] = w.tokens - w.rows + i + 1;
+        const uint16_t* p = a.q + (w.first + i) * a.q_row + h * a.q_head + 8 * quad;
+        float x[KS][8];
+#pragma unroll
+        for (int s = 0; s < KS; ++s) w4g_values<T>(p + 32 * s, x[s]);
+        if (LO && c.rotate) {
+            // d = 32 s + 8 quad + j: strides 1, 2, 4 among j, 8, 16 among quads, 32 .. among s
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+#pragma unroll
+                for (int m = 1; m < 8; m <<= 1)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if ((j & m) == 0) {
+                            const float u = x[s][j], v = x[s][j + m];
+                            x[s][j] = u + v;
+                            x[s][j + m] = u - v;
+                        }
+#pragma unroll
+                for (int m = 16; m < 64; m <<= 1)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float v = __shfl_xor(x[s][j], m);
+                        x[s][j] = (lane & m) ? v - x[s][j] : x[s][j] + v;
+                    }
+            }
+#pragma unroll
+            for (int m = 1; m < KS; m <<= 1)
+#pragma unroll
+                for (int s = 0; s < KS; ++s)
+                    if ((s & m) == 0)
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const float u = x[s][j], v = x[s + m][j];
+                            x[s][j] = u + v;
+                            x[s + m][j] = u - v;
+                        }
+#pragma unroll
+            for (int s = 0; s < KS; ++s)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[s][j] *= kv4_norm<D>();
+        }
+        // the sums of what the operands hold, group by group
+#pragma unroll
+        for (int n = 0; n < NG; ++n) qs[t][n] = 0.0f;
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint32_t hi, lo;
+                split2(x[s][2 * j], x[s][2 * j + 1], &hi, &lo);
+                qh[t][s][j] = hi;
+                float v = bf16_lo(hi) + bf16_hi(hi);
+                if constexpr (LO) {
+                    ql[t][s][j] = lo;
+                    v += bf16_lo(lo) + bf16_hi(lo);
+                }
+                qs[t][s / SPG] += v;
+            }
+#pragma unroll
+        for (int n = 0; n < NG; ++n) {
+            qs[t][n] += __shfl_xor(qs[t][n], 16);
+            qs[t][n] += __shfl_xor(qs[t][n], 32);
+        }
     }
-    if (b == c.B) return;
-    const int pos = s.tokens - s.rows + (t - s.first);
-    float q[N];
+
+    f32x4 o[RT][DT] = {}, zp[RT][NG] = {};   // zp: sums of weights times 1 + z / 16
+    float top[RT], sum[RT];
 #pragma unroll
-    for (int i = 0; i < N; ++i) q[i] = T::to_f32(a.q[t * a.q_row + h * a.q_head + d + i]);
-    if (c.rotate) rotate_head<D>(q);
-    double top = -__builtin_inf(), sum = 0.0, acc[N] = {};
-    for (int pass = 0; pass < 2; ++pass)
-        for (int j = 0; j <= pos; ++j) {
-            const int page = kv4_page(c, b, j), row = j & ((1 << c.page_log2) - 1);
-            if (page < 0) continue;
-            double v = 0.0;
+    for (int t = 0; t < RT; ++t) {
+        top[t] = -__builtin_inff();
+        sum[t] = 0.0f;
+    }
+    // masked scores become -infinity times cs; a scale of 0 would make NaN of them, and 1e-30 gives equal weights too
+    const float cs = 16.0f * (a.scale == 0.0f ? 1e-30f : a.scale * 1.4426950408889634f);
+    const float none = cs < 0.0f ? __builtin_inff() : -__builtin_inff();
+
+    // page of the 16 tokens from `pos` on, -1 past the end
+    auto page_at = [&](int pos) { return pos < end ? kv4_page(c, w.b, pos) : -1; };
+    const int S1 = (1 << c.page_log2) - 1;
+    const size_t code_page = ((size_t)2 * c.heads << c.page_log2) * (D / 2);
+    const size_t word_page = ((size_t)2 * c.heads << c.page_log2) * NG;
+    const uint8_t* codes_k = c.codes + kv4_codes_at(c, 0, 0, g);
+    const uint8_t* codes_v = c.codes + kv4_codes_at(c, 0, 1, g);
+    const uint32_t* words_k = c.scales + kv4_scales_at(c, 0, 0, g);
+    const uint32_t* words_v = c.scales + kv4_scales_at(c, 0, 1, g);
+
+    u32x4 vc[DT / 2];
+    uint32_t kc[4][KS];
+    Words<NG> kw, vw;
+    // K rows: MFMA row m of tile (u, j) is token 16 (m / 4) + 8 u + 4 j + m % 4, so that a lane's four results are
+    // tokens 16 quad + 8 u + 4 j + 0..3
+    auto load_k = [&](int pos, int page_k, int page_w) {
+        const int row = ((pos + 16 * (col >> 2)) & S1) + (col & 3);
+        const uint8_t* p = codes_k + (size_t)(page_k < 0 ? 0 : page_k) * code_page + kv4_k_byte(D, row, quad * KS);
 #pragma unroll
-            for (int i = 0; i < N; ++i) v = fma((double)q[i], kv4_value<D>(c, page, 0, g, row, d + i), v);
+        for (int x = 0; x < 4; ++x) {
+            const Words<KS> v = *reinterpret_cast<const Words<KS>*>(__builtin_assume_aligned(p + x * 4 * (D / 2), KS >= 4 ? 16 : 8));
 #pragma unroll
-            for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m);
-            v *= a.scale;
-            if (pass == 0) {
-                top = v > top || v != v ? v : top;
-                if (top != top) break;
-            } else {
-                const double p = exp(v - top);
-                sum += p;
+            for (int s = 0; s < KS; ++s) kc[x][s] = v.w[s];
+        }
+        kw = *reinterpret_cast<const Words<NG>*>(__builtin_assume_aligned(
+            words_k + (size_t)(page_w < 0 ? 0 : page_w) * word_page + ((pos + lane) & S1) * NG, NG >= 4 ? 16 : 4 * NG));
+    };
+    auto load_v = [&](int pos, int page) {
+        const size_t p = (size_t)(page < 0 ? 0 : page);
+        const uint8_t* q = codes_v + p * code_page + kv4_v_byte(D, (pos + 16 * quad) & S1, col);
 #pragma unroll
-                for (int i = 0; i < N; ++i) acc[i] = fma(p, kv4_value<D>(c, page, 1, g, row, d + i), acc[i]);
+        for (int e = 0; e < DT / 2; ++e) vc[e] = *reinterpret_cast<const u32x4*>(q + 256 * e);
+        vw = *reinterpret_cast<const Words<NG>*>(__builtin_assume_aligned(
+            words_v + p * word_page + ((pos + lane) & S1) * NG, NG >= 4 ? 16 : 4 * NG));
+    };
+    constexpr int kStride = kWaves * kStep;
+    int pos = begin + wave * kStep;
+    int page_k = page_at(pos + 16 * (col >> 2)), page_v = page_at(pos + 16 * quad);
+    int next_k = page_at(pos + kStride + 16 * (col >> 2)), next_v = page_at(pos + kStride + 16 * quad);
+    if (pos < end) {
+        load_k(pos, page_k, page_v);
+        load_v(pos, page_v);
+    }
+    uint32_t* wk = lds + wave * 2 * kStep * NG;
+    uint32_t* wv = wk + kStep * NG;
+    for (; pos < end; pos += kStride) {
+        // words through LDS: a token's own lane has them, its 16 lanes need them; of tokens that are not there, zeros
+        {
+            const bool there = pos + lane < end && page_v >= 0;
+#pragma unroll
+            for (int n = 0; n < NG; ++n) {
+                wk[n * kStep + lane] = there ? kw.w[n] : 0;
+                wv[n * kStep + lane] = there ? vw.w[n] : 0;
+            }
+            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+            __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+        }
+        float s[RT][16];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+#pragma unroll
+            for (int t = 0; t < RT; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s[t][4 * x + i] = 0.0f;
+#pragma unroll
+            for (int n = 0; n < NG; ++n) {
+                const u32x4 word = *reinterpret_cast<const u32x4*>(wk + n * kStep + 16 * quad + 4 * x);
+                f32x4 acc[RT] = {};
+#pragma unroll
+                for (int k = n * SPG; k < (n + 1) * SPG; ++k) {
+                    const u32x4 op = kv4_operand(kc[x][k]);
+#pragma unroll
+                    for (int t = 0; t < RT; ++t) {
+                        acc[t] = Bf16::mfma(op, qh[t][k], acc[t]);
+                        if constexpr (LO) acc[t] = Bf16::mfma(op, ql[t][k], acc[t]);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float sc = __uint_as_float(word[i] & ~15u), z = __uint_as_float((word[i] & 15u) << 19 | 0x3F800000u);
+#pragma unroll
+                    for (int t = 0; t < RT; ++t)
+                        s[t][4 * x + i] = __builtin_fmaf(sc, __builtin_fmaf(-z, qs[t][n], acc[t][i]), s[t][4 * x + i]);
+                }
             }
         }
-    float o[N];
+        // the next step's K while this one's weights and V are at work
+        const int page_w = page_v;
+        page_k = next_k;
+        const int ahead = pos + kStride, ahead2 = pos + 2 * kStride, page_n = next_v;
+        load_k(ahead, page_k, page_n);
+        next_k = page_at(ahead2 + 16 * (col >> 2));
+        next_v = page_at(ahead2 + 16 * quad);
+
+        int lim[RT];
+        bool cut = false;
 #pragma unroll
-    for (int i = 0; i < N; ++i) o[i] = sum > 0.0 || sum != sum ? (float)(acc[i] / sum) : 0.0f;
-    if (c.rotate) rotate_head<D>(o);
+        for (int t = 0; t < RT; ++t) {
+            lim[t] = page_w < 0 ? 0 : min(seen[t], end) - pos - 16 * quad;
+            cut |= lim[t] < 16;
+        }
+        const bool masked = __any(cut);
+        if (masked) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) a.y[((int64_t)t * a.Hq + h) * D + d + i] = T::from_f32(o[i]);
+            for (int t = 0; t < RT; ++t)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (i >= lim[t]) s[t][i] = none;
+        }
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+            float m = s[t][0] * cs;
+#pragma unroll
+            for (int i = 1; i < 16; ++i) m = fmaxf(m, s[t][i] * cs);
+            if (__any(m > top[t] + kMove)) {
+                m = fmaxf(m, __shfl_xor(m, 16));
+                m = fmaxf(m, __shfl_xor(m, 32));
+                const float up = fmaxf(top[t], m), f = top[t] == up ? 1.0f : __builtin_amdgcn_exp2f(top[t] - up);
+                top[t] = up;
+                sum[t] *= f;
+#pragma unroll
+                for (int d = 0; d < DT; ++d) o[t][d] *= f;
+#pragma unroll
+                for (int n = 0; n < NG; ++n) zp[t][n] *= f;
+            }
+            const float off = top[t] == -__builtin_inff() ? 0.0f : -top[t];   // a row that has seen nothing yet
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                s[t][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][i], cs, off));
+                sum[t] += s[t][i];
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < NG; ++n) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                // weights times scales, in V's order of tokens, and the operand 1 + z / 16
+                const u32x4 word[2] = {*reinterpret_cast<const u32x4*>(wv + n * kStep + 16 * quad + 8 * u),
+                                       *reinterpret_cast<const u32x4*>(wv + n * kStep + 16 * quad + 8 * u + 4)};
+                u32x4 hi[RT], lo[RT], zo;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int t0 = 4 * (j / 2) + j % 2, t1 = t0 + 2;
+                    const uint32_t w0 = word[j / 2][j % 2], w1 = word[j / 2][j % 2 + 2];
+                    const float s0 = __uint_as_float(w0 & ~15u), s1 = __uint_as_float(w1 & ~15u);
+                    zo[j] = ((w0 & 15u) | (w1 & 15u) << 16) << 3 | 0x3F803F80u;
+#pragma unroll
+                    for (int t = 0; t < RT; ++t) {
+                        float x0 = s[t][8 * u + t0] * s0, x1 = s[t][8 * u + t1] * s1;
+                        if (masked) {
+                            x0 = 8 * u + t0 < lim[t] ? x0 : 0.0f;
+                            x1 = 8 * u + t1 < lim[t] ? x1 : 0.0f;
+                        }
+                        uint32_t h, l;
+                        split2(x0, x1, &h, &l);
+                        hi[t][j] = h;
+                        lo[t][j] = l;
+                    }
+                }
+#pragma unroll
+                for (int t = 0; t < RT; ++t) {
+                    zp[t][n] = Bf16::mfma(zo, hi[t], zp[t][n]);
+                    zp[t][n] = Bf16::mfma(zo, lo[t], zp[t][n]);
+                }
+#pragma unroll
+                for (int d = n * DPG; d < (n + 1) * DPG; ++d) {
+                    const u32x4 op = d % 2 ? kv4_v_operand<true>(vc[d / 2][2 * u], vc[d / 2][2 * u + 1])
+                                           : kv4_v_operand<false>(vc[d / 2][2 * u], vc[d / 2][2 * u + 1]);
+#pragma unroll
+                    for (int t = 0; t < RT; ++t) {
+                        o[t][d] = Bf16::mfma(op, hi[t], o[t][d]);
+                        o[t][d] = Bf16::mfma(op, lo[t], o[t][d]);
+                    }
+                }
+            }
+        }
+        load_v(ahead, page_n);
+        page_v = page_n;
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+    }
+
+    // the waves' results joined: rows of the tile, wave by wave
+    const bool whole = w.chunks == 1;
+    float* part = parts + ((size_t)g * slots + w.slot) * part_words<D, RT>();
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+        sum[t] += __shfl_xor(sum[t], 16);
+        sum[t] += __shfl_xor(sum[t], 32);
+        __syncthreads();   // the words, or the last tile's rows, were read
+        if (quad == 0) {
+            lds_top[wave][col] = top[t];
+            lds_sum[wave][col] = sum[t];
+        }
+#pragma unroll
+        for (int d = 0; d < DT; ++d) {
+            f32x4 v;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = 16.0f * (o[t][d][i] - zp[t][d / DPG][i]);
+            *reinterpret_cast<f32x4*>(lds_o + (wave * 16 + col) * kRow + 16 * d + 4 * quad) = v;
+        }
+        __syncthreads();
+        const long long r0 = (long long)(w.tile * RT + t) * 16;
+        const int n = (int)min(16ll, (long long)w.rows * G - r0);
+        for (int r = wave; r < n; r += kWaves) {
+            float m = lds_top[0][r], total = 0.0f, x[D / 64] = {};
+#pragma unroll
+            for (int k = 1; k < kWaves; ++k) m = fmaxf(m, lds_top[k][r]);
+#pragma unroll
+            for (int k = 0; k < kWaves; ++k) {
+                // a wave that has seen nothing has sums of 0, or NaN
+                const float f = lds_top[k][r] == m || lds_top[k][r] == -__builtin_inff()
+                                    ? 1.0f : __builtin_amdgcn_exp2f(lds_top[k][r] - m);
+                total = __builtin_fmaf(f, lds_sum[k][r], total);
+#pragma unroll
+                for (int i = 0; i < D / 64; ++i)
+                    x[i] = __builtin_fmaf(f, lds_o[(k * 16 + r) * kRow + lane * (D / 64) + i], x[i]);
+            }
+            if (whole) {
+                const int i0 = (int)((r0 + r) / G), h = g * G + (int)((r0 + r) % G);
+                kv4_finish<T, D>(x, total, c.rotate, a.y + ((int64_t)(w.first + i0) * a.Hq + h) * D);
+            } else {
+                float* p = part + (16 * t + r) * D + lane * (D / 64);
+#pragma unroll
+                for (int i = 0; i < D / 64; ++i) p[i] = x[i];
+                if (lane == 0) {
+                    part[16 * RT * D + 16 * t + r] = m;
+                    part[16 * RT * (D + 1) + 16 * t + r] = total;
+                }
+            }
+        }
+    }
+}
+
+// The slots of a tile group's spans joined, a wave a row.
+template <class T, int D, int RT>
+__global__ __launch_bounds__(256) void k_attn_kv4_join(Kv4 c, AttnArgs a, int slots, const float* parts) {
+    constexpr int N = D / 64, R = 16 * RT;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int g = blockIdx.x, G = a.Hq / c.heads;
+    Kv4Work w;
+    if (!kv4_work<RT>(c, G, slots, true, blockIdx.y + blockIdx.z * gridDim.y, &w) || w.chunks == 1) return;
+    const long long r0 = (long long)w.tile * R;
+    const int n = (int)min((long long)R, (long long)w.rows * G - r0);
+    const float* part = parts + ((size_t)g * slots + w.slot) * part_words<D, RT>();
+    for (int r = wave; r < n; r += 4) {
+        float m = -__builtin_inff();
+        for (int k = lane; k < w.chunks; k += 64) m = fmaxf(m, part[k * part_words<D, RT>() + R * D + r]);
+#pragma unroll
+        for (int x = 1; x < 64; x <<= 1) m = fmaxf(m, __shfl_xor(m, x));
+        float total = 0.0f, x[N] = {};
+#pragma unroll 8
+        for (int k = 0; k < w.chunks; ++k) {
+            const float* p = part + k * part_words<D, RT>();
+            const float top = p[R * D + r];
+            const float f = top == m || top == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(top - m);
+            total = __builtin_fmaf(f, p[R * (D + 1) + r], total);
+#pragma unroll
+            for (int i = 0; i < N; ++i) x[i] = __builtin_fmaf(f, p[r * D + lane * N + i], x[i]);
+        }
+        const int i0 = (int)((r0 + r) / G), h = g * G + (int)((r0 + r) % G);
+        kv4_finish<T, D>(x, total, c.rotate, a.y + ((int64_t)(w.first + i0) * a.Hq + h) * D);
+    }
 }
 
 template <class F>
@@ -186,15 +641,84 @@ hipError_t launch_kv4_append(bool fp16, const uint16_t* k, int64_t k_row, int64_
     return hipGetLastError();
 }
 
-size_t attn_kv4_workspace(int, int, int, int, int, int, int) { return 0; }
+namespace {
 
-hipError_t launch_attn_kv4(const AttnArgs& a, const Kv4& c, void*, hipStream_t st) {
-    const dim3 grid(c.T, a.Hq);
-    by_dim(c.dim, [&](auto d) {
-        if (a.fp16) k_attn_kv4<Fp16, d><<<grid, 64, 0, st>>>(c, a);
-        else k_attn_kv4<Bf16, d><<<grid, 64, 0, st>>>(c, a);
-    });
+// Rows a block takes, in tiles of 16, the tile groups that there can be, and
+// the blocks a head gets: spans for all CUs twice, two a tile group at least
+// (so that every group's last, shorter span has one), none where no sequence
+// is worth a second span.
+struct Grid {
+    int tiles, groups, slots;
+};
+Grid attn_kv4_grid(int T, int G, int heads, int dim, int page, int width, int B) {
+    Grid g;
+    const int most = dim == 64 ? 4 : dim == 128 ? 2 : 1;
+    const int64_t rows = ((int64_t)T * G + B - 1) / B;   // of a sequence, on average
+    g.tiles = rows <= 16 || most == 1 ? 1 : rows <= 32 || most == 2 ? 2 : 4;
+    g.groups = (int)(((int64_t)T * G + (int64_t)(B < T ? B : T) * (16 * g.tiles - 1)) / (16 * g.tiles));
+    g.slots = 0;
+    if ((int64_t)width * page > 2 * kMinSpan) {
+        const int64_t fill = 512 / heads;
+        g.slots = (int)(2 * (int64_t)g.groups > fill ? 2 * (int64_t)g.groups : fill);
+    }
+    return g;
+}
+size_t part_bytes(int dim, int tiles) { return (size_t)16 * tiles * (dim + 2) * 4; }
+
+template <class T, int D, int NG, int RT>
+hipError_t run_attn_kv4(const AttnArgs& a, const Kv4& c, const Grid& g, float* ws, hipStream_t st) {
+    const auto grid = [&](int n) {
+        const int y = n < 32768 ? n : 32768;
+        return dim3(c.heads, y, (n + y - 1) / y);
+    };
+    const int n = g.slots ? g.slots : g.groups;
+    constexpr int lds = 4 * lds_words<D>();
+    hipError_t e = hipSuccess;
+    const auto go = [&](auto kernel, std::atomic<uint64_t>& done) {
+        if (lds > 65536 && (e = opt_in_lds(reinterpret_cast<const void*>(kernel), lds, done)) != hipSuccess) return;
+        kernel<<<grid(n), 64 * kWaves, lds, st>>>(c, a, g.slots, ws);
+        e = hipGetLastError();
+    };
+    static std::atomic<uint64_t> done[2];
+    if (c.rotate || a.fp16) go(k_attn_kv4<T, D, NG, RT, true>, done[0]);
+    else go(k_attn_kv4<T, D, NG, RT, false>, done[1]);
+    if (e != hipSuccess || g.slots == 0) return e;
+    k_attn_kv4_join<T, D, RT><<<grid(g.groups), 256, 0, st>>>(c, a, g.slots, ws);
     return hipGetLastError();
+}
+
+}  // namespace
+
+size_t attn_kv4_workspace(int T, int Hq, int heads, int dim, int page, int width, int B) {
+    if (T == 0 || B == 0) return 0;
+    const Grid g = attn_kv4_grid(T, Hq / heads, heads, dim, page, width, B);
+    return (size_t)g.slots * heads * part_bytes(dim, g.tiles);
+}
+
+hipError_t launch_attn_kv4(const AttnArgs& a, const Kv4& c, void* ws, hipStream_t st) {
+    const Grid g = attn_kv4_grid(c.T, a.Hq / c.heads, c.heads, c.dim, 1 << c.page_log2, c.width, c.B);
+    hipError_t e = hipErrorInvalidValue;
+    by_dim(c.dim, [&](auto d) {
+        auto groups = [&](auto ng) {
+            auto tiles = [&](auto rt) {
+                if constexpr (rt <= max_tiles<d>()) {
+                    if (g.tiles != rt) return;
+                    e = a.fp16 ? run_attn_kv4<Fp16, d, ng, rt>(a, c, g, (float*)ws, st)
+                               : run_attn_kv4<Bf16, d, ng, rt>(a, c, g, (float*)ws, st);
+                }
+            };
+            if (c.dim / c.group != ng) return;
+            tiles(std::integral_constant<int, 1>());
+            tiles(std::integral_constant<int, 2>());
+            tiles(std::integral_constant<int, 4>());
+        };
+        constexpr int D = d;
+        if constexpr (D <= 128) groups(std::integral_constant<int, 1>());
+        groups(std::integral_constant<int, 2>());
+        if constexpr (D >= 128) groups(std::integral_constant<int, 4>());
+        if constexpr (D == 256) groups(std::integral_constant<int, 8>());
+    });
+    return e;
 }
 
 }  // namespace cr
