@@ -28,6 +28,14 @@ __device__ __forceinline__ uint32_t pack2(Fp16, float a, float b) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(f, f16x2));
 }
 
+// sum + the two values of p
+__device__ __forceinline__ float add2(Bf16, uint32_t p, float sum) {
+    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2_t, p), __builtin_bit_cast(bf16x2_t, 0x3F803F80u), sum, false);
+}
+__device__ __forceinline__ float add2(Fp16, uint32_t p, float sum) {
+    return __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2, p), __builtin_bit_cast(f16x2, 0x3C003C00u), sum, false);
+}
+
 // One row by the definition, in float64, by one wave: lane l takes
 // d = l D / 64 and on.  Two passes over the keys: the largest score, then the
 // sums, so that infinities and NaN come out as they do in the definition.
@@ -103,29 +111,31 @@ __device__ __forceinline__ bool find_tile(const int32_t* cu, int B, int T, int t
 }
 
 // Rows of K or V in LDS: 16-byte chunk c of row r at chunk c ^ swizzle(r).
-// K is read 16 rows at one chunk, V 8 rows at two pairs of chunks (below): either
+// K is read 16 rows at one chunk, V 4 rows at four chunks (64 bytes): either
 // way all banks are hit alike.
 template <int D, bool V>
 __device__ __forceinline__ int swizzle(int r) {
     constexpr int rows = D >= 128 ? 1 : 128 / D;   // rows in 256 bytes
-    return V ? ((r / rows) & (rows > 1 ? 3 : 7)) * 2 : (r / rows) & (rows > 1 ? 7 : 15);
+    return V ? ((r / rows) & (rows > 1 ? 1 : 3)) * 4 : (r / rows) & (rows > 1 ? 7 : 15);
 }
 
 // One block: BM = 32 NW rows of one head, a wave 32 of them, over tiles of BN
-// keys that all waves share in LDS, the next tile's on their way meanwhile.
+// keys that NW waves share in LDS, the next tile's on their way meanwhile.
+// KG = 2: twice the waves, the second half on the odd tiles, its sums joined to
+// the first half's at the end.
 //   S^T = K Q^T   MFMA 32x32x16: a lane holds 16 keys' scores of one row
 //   O^T = V^T P^T the same lane's weights are the second operand as they lie:
 //                 step s takes its scores 8 s + 0..7, keys 16 s + 8 (i / 4) + 4 (lane / 32) + i % 4;
 //                 V's operand comes transposed from LDS, 4 keys a read
-template <class T, int D, int NW, int BN>
-__global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_prompt(AttnArgs a) {
+template <class T, int D, int NW, int BN, int KG>
+__global__ __launch_bounds__(64 * NW * KG, D == 256 ? 1 : 2) void k_attn_prompt(AttnArgs a) {
     constexpr int BM = 32 * NW, KS = D / 16, DT = D / 32, MT = BN / 32, PS = BN / 16;
     constexpr int kTile = BN * D * 2, kLoads = kTile / 1024 / NW;   // bytes of a K or V tile; 1 KiB loads of a wave
     constexpr float kMove = 8.0f;   // the maximum follows when weights would pass 2^8
     // fp16 weights: 2^6 at the maximum, so that fewer fall below its normal range
     constexpr float kBias = std::is_same_v<T, Fp16> ? 6.0f : 0.0f;
     extern __shared__ __align__(1024) char lds[];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = (threadIdx.x >> 6) % NW, kg = (threadIdx.x >> 6) / NW;
     Tile t;
     if (!find_tile<BM>(a.cu, a.B, a.T, blockIdx.y + blockIdx.z * gridDim.y, &t)) return;
     // blocks go to the 8 XCDs in turn: heads of one key head to the same one
@@ -159,7 +169,8 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_prompt(AttnA
         r.w = 0x00020000;
         return r;
     };
-    const uint32_t lds0 = lds_address(lds);
+    char* mem = lds + kg * 4 * kTile;   // of this half of the waves: two buffers of K and V
+    const uint32_t lds0 = lds_address(mem);
     auto load = [&](int tile, int buffer) {
         const int j = tile * BN;
         if (keys - j < BN) offsets(t.len - j < BN ? t.len - j : BN);
@@ -171,37 +182,41 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_prompt(AttnA
         for (int i = 0; i < kLoads; ++i) w4g_x_to_lds(vr, v_off[i], to + kTile + i * 1024);
     };
     offsets(min(t.len, BN));
-    load(0, 0);
+    if (kg < tiles) load(kg, 0);
 
     u32x4 qv[KS];
     {
         const uint16_t* p = q + (int64_t)min(row, t.len - 1) * a.q_row + 8 * (lane >> 5);
 #pragma unroll
-        for (int s = 0; s < KS; ++s) qv[s] = *reinterpret_cast<const u32x4*>(p + 16 * s);
+        for (int s = 0; s < KS; ++s) {
+            qv[s] = *reinterpret_cast<const u32x4*>(p + 16 * s);
+            if (a.scale < 0.0f) qv[s] ^= 0x80008000u;   // the sign goes to q
+        }
     }
     f32x16 o[DT] = {};
     // a scale of 0 would make NaN of the scores that are masked; all weights are 1 with this one too
-    const float c = a.scale == 0.0f ? 1e-30f : a.scale * 1.4426950408889634f;
+    const float c = a.scale == 0.0f ? 1e-30f : fabsf(a.scale) * 1.4426950408889634f;
     float top = -__builtin_inff(), sum = 0.0f;   // of the scores times c; this lane's keys
 
-    for (int j = 0; j < tiles; ++j) {
+    for (int turn = 0; turn * KG < tiles; ++turn) {
+        const int j = turn * KG + kg;
         w4g_wait();
         w4g_barrier();
-        if (j + 1 < tiles) load(j + 1, (j + 1) & 1);
+        if (j + KG < tiles) load(j + KG, (turn + 1) & 1);
         if (j * BN >= mine) continue;
-        const char* kt = lds + (j & 1) * 2 * kTile;
+        const char* kt = mem + (turn & 1) * 2 * kTile;
         const char* vt = kt + kTile;
         f32x16 s[MT];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-            s[mt] = f32x16{};
-            const int r = 32 * mt + (lane & 31);
-            const char* p = kt + r * (2 * D);
+        for (int mt = 0; mt < MT; ++mt) s[mt] = f32x16{};
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks)
-                s[mt] = mfma32(T(), *reinterpret_cast<const u32x4*>(p + ((2 * ks + (lane >> 5)) ^ swizzle<D, false>(r)) * 16),
+        for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                const int r = 32 * mt + (lane & 31);
+                s[mt] = mfma32(T(), *reinterpret_cast<const u32x4*>(kt + r * (2 * D) + ((2 * ks + (lane >> 5)) ^ swizzle<D, false>(r)) * 16),
                                qv[ks], s[mt]);
-        }
+            }
         // this lane's score i of part mt: key j BN + 32 mt + 8 (i / 4) + 4 (lane / 32) + i % 4
         if (j * BN + BN > (a.causal ? min(row0 + 1, t.len) : t.len)) {
             const int last = (a.causal ? min(row, t.len - 1) : t.len - 1) - j * BN - 4 * (lane >> 5);
@@ -209,13 +224,14 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_prompt(AttnA
             for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
-                    if (32 * mt + 8 * (i / 4) + i % 4 > last) s[mt][i] = c < 0.0f ? __builtin_inff() : -__builtin_inff();
+                    if (32 * mt + 8 * (i / 4) + i % 4 > last) s[mt][i] = -__builtin_inff();
         }
-        float m = s[0][0] * c;
+        float m = s[0][0];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) m = fmaxf(m, s[mt][i] * c);
+            for (int i = 0; i < 16; ++i) m = fmaxf(m, s[mt][i]);
+        m *= c;
         if (__any(m > top + kMove)) {
             m = fmaxf(m, __shfl_xor(m, 32));
             const float up = fmaxf(top, m), f = top == up ? 1.0f : __builtin_amdgcn_exp2f(top - up);
@@ -232,12 +248,12 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_prompt(AttnA
         for (int ps = 0; ps < PS; ++ps) {
             float e[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[ps / 2][8 * (ps % 2) + i], c, off));
-                sum += e[i];
-            }
+            for (int i = 0; i < 8; ++i) e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[ps / 2][8 * (ps % 2) + i], c, off));
 #pragma unroll
-            for (int i = 0; i < 4; ++i) p[ps][i] = pack2(T(), e[2 * i], e[2 * i + 1]);
+            for (int i = 0; i < 4; ++i) {
+                p[ps][i] = pack2(T(), e[2 * i], e[2 * i + 1]);
+                sum = add2(T(), p[ps][i], sum);
+            }
         }
         // V^T: the 16 lanes of a group take 4 keys x 16 d, lane i the keys' d = i
         const int vr = 4 * (lane >> 5) + ((lane & 15) >> 2), vc = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
@@ -261,8 +277,34 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_prompt(AttnA
         }
     }
 
-    if (row0 >= t.len) return;
     sum += __shfl_xor(sum, 32);
+    if constexpr (KG == 2) {
+        // sums as they lie in the registers: lane by lane, 16 bytes each
+        f32x4* to = reinterpret_cast<f32x4*>(lds) + wave * (DT * 4 * 64) + lane;
+        float* stat = reinterpret_cast<float*>(lds + NW * DT * 4096) + wave * 128 + lane;
+        __syncthreads();   // the last tiles were read
+        if (kg == 1) {
+#pragma unroll
+            for (int i = 0; i < DT * 4; ++i)
+                to[i * 64] = f32x4{o[i / 4][i % 4 * 4], o[i / 4][i % 4 * 4 + 1], o[i / 4][i % 4 * 4 + 2], o[i / 4][i % 4 * 4 + 3]};
+            stat[0] = top;
+            stat[64] = sum;
+        }
+        __syncthreads();
+        if (kg == 1) return;
+        const float other = stat[0], up = fmaxf(top, other);
+        // a half that has seen no key has sums of 0, or NaN
+        const float f0 = top == up || top == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(top - up);
+        const float f1 = other == up || other == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(other - up);
+        sum = sum * f0 + stat[64] * f1;
+#pragma unroll
+        for (int i = 0; i < DT * 4; ++i) {
+            const f32x4 v = to[i * 64];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) o[i / 4][i % 4 * 4 + x] = o[i / 4][i % 4 * 4 + x] * f0 + v[x] * f1;
+        }
+    }
+    if (row0 >= t.len) return;
     const float inv = 1.0f / sum;
     bool bad = false;
     float y[DT][16];
@@ -297,25 +339,31 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attn_prompt(AttnA
     }
 }
 
-template <class T, int D, int NW, int BN>
+template <class T, int D, int NW, int BN, int KG>
 hipError_t launch(const AttnArgs& a, hipStream_t st) {
-    constexpr int BM = 32 * NW, lds = 4 * BN * D * 2;
+    constexpr int BM = 32 * NW, lds = KG * 4 * BN * D * 2;
+    static_assert(KG == 1 || NW * (D / 32 * 4096 + 512) <= lds, "the second half's sums fit");
     static std::atomic<uint64_t> done{0};
     if (lds > 65536) {
-        const hipError_t e = opt_in_lds(reinterpret_cast<const void*>(&k_attn_prompt<T, D, NW, BN>), lds, done);
+        const hipError_t e = opt_in_lds(reinterpret_cast<const void*>(&k_attn_prompt<T, D, NW, BN, KG>), lds, done);
         if (e != hipSuccess) return e;
     }
     // tiles that B sequences of T rows can have
     const int64_t tiles = a.B == 1 ? (a.T + BM - 1) / BM : ((int64_t)a.T + (int64_t)a.B * (BM - 1)) / BM;
     const int y = (int)(tiles < 32768 ? tiles : 32768);
-    k_attn_prompt<T, D, NW, BN><<<dim3(a.Hq, y, (unsigned)((tiles + y - 1) / y)), 64 * NW, lds, st>>>(a);
+    k_attn_prompt<T, D, NW, BN, KG><<<dim3(a.Hq, y, (unsigned)((tiles + y - 1) / y)), 64 * NW * KG, lds, st>>>(a);
     return hipGetLastError();
 }
+#ifndef V64
+#define V64 4, 64, 2
+#define V128 4, 64, 2
+#define V256 2, 32, 2
+#endif
 template <class T>
 hipError_t launch_by_dim(const AttnArgs& a, hipStream_t st) {
-    if (a.D == 64) return launch<T, 64, 4, 64>(a, st);
-    if (a.D == 128) return launch<T, 128, 4, 64>(a, st);
-    return launch<T, 256, 4, 32>(a, st);
+    if (a.D == 64) return launch<T, 64, V64>(a, st);
+    if (a.D == 128) return launch<T, 128, V128>(a, st);
+    return launch<T, 256, V256>(a, st);
 }
 
 }  // namespace
