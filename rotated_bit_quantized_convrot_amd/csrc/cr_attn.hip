@@ -36,36 +36,53 @@ __device__ __forceinline__ float add2(Fp16, uint32_t p, float sum) {
     return __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2, p), __builtin_bit_cast(f16x2, 0x3C003C00u), sum, false);
 }
 
-// One row by the definition, in float64, by one wave: lane l takes
-// d = l D / 64 and on.  Two passes over the keys: the largest score, then the
-// sums, so that infinities and NaN come out as they do in the definition.
+// One row by one wave, without matrix cores: only what the row sees is touched.
+// A lane takes a key of 64, then d = l D / 64 and on.  Ends when every value
+// is NaN.
 template <class T, int D>
-__device__ __noinline__ void attn_row_defined(const uint16_t* q, const uint16_t* k, int64_t k_row, const uint16_t* v,
-                                              int64_t v_row, int keys, float scale, uint16_t* y) {
+__device__ __forceinline__ void attn_row(const uint16_t* q, const uint16_t* k, int64_t k_row, const uint16_t* v, int64_t v_row,
+                              int keys, float scale, uint16_t* y) {
     constexpr int N = D / 64;
-    const int lane = threadIdx.x & 63, d = lane * N;
-    double top = -__builtin_inf(), sum = 0.0, o[N] = {};
-    for (int pass = 0; pass < 2; ++pass) {
-        for (int j = 0; j < keys; ++j) {
-            double s = 0.0;
+    const int lane = threadIdx.x & 63;
+    float top = -__builtin_inff(), sum = 0.0f, o[N] = {};
+    for (int j0 = 0; j0 < keys; j0 += 64) {
+        const int n = min(64, keys - j0);
+        const uint16_t* kr = k + (int64_t)(j0 + min(lane, n - 1)) * k_row;
+        float s = 0.0f;
+        for (int d = 0; d < D; d += 8) {
+            float x[8], w[8];
+            w4g_values<T>(q + d, x);
+            w4g_values<T>(kr + d, w);
 #pragma unroll
-            for (int i = 0; i < N; ++i) s = fma((double)T::to_f32(q[d + i]), (double)T::to_f32(k[j * k_row + d + i]), s);
+            for (int i = 0; i < 8; ++i) s = __builtin_fmaf(x[i], w[i], s);
+        }
+        s = lane < n ? s * scale : -__builtin_inff();
+        float m = s;
 #pragma unroll
-            for (int m = 1; m < 64; m <<= 1) s += __shfl_xor(s, m);
-            s *= scale;
-            if (pass == 0) {
-                top = s > top || s != s ? s : top;
-                if (top != top) break;
-            } else {
-                const double p = exp(s - top);
-                sum += p;
+        for (int x = 1; x < 64; x <<= 1) m = fmaxf(m, __shfl_xor(m, x));
+        const float up = fmaxf(top, m), f = top == up ? 1.0f : expf(top - up);
+        const float p = lane < n ? expf(s - up) : 0.0f;
+        float all = p;
 #pragma unroll
-                for (int i = 0; i < N; ++i) o[i] = fma(p, (double)T::to_f32(v[j * v_row + d + i]), o[i]);
-            }
+        for (int x = 1; x < 64; x <<= 1) all += __shfl_xor(all, x);
+        sum = sum * f + all;
+        top = up;
+        bool open = false;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            o[i] *= f;
+            open |= o[i] == o[i];
+        }
+        if (!__any(open)) break;
+        for (int j = 0; j < n; ++j) {
+            const float w = __shfl(p, j);
+            const uint16_t* vr = v + (int64_t)(j0 + j) * v_row + lane * N;
+#pragma unroll
+            for (int i = 0; i < N; ++i) o[i] = __builtin_fmaf(w, T::to_f32(vr[i]), o[i]);
         }
     }
 #pragma unroll
-    for (int i = 0; i < N; ++i) y[d + i] = T::from_f32((float)(o[i] / sum));
+    for (int i = 0; i < N; ++i) y[lane * N + i] = T::from_f32(o[i] / sum);
 }
 
 // The sequence and the tile of BM rows in it that tile `t` from the end is:
@@ -329,12 +346,12 @@ __global__ __launch_bounds__(64 * NW * KG, D == 256 ? 1 : 2) void k_attn_prompt(
                 *reinterpret_cast<uint2*>(out + 32 * dt + 2 * i) = w;
             }
     }
-    // A weight of 0 times an infinity that the row does not see, a score that
-    // passes float32: the definition decides.
+    // A weight of 0 times an infinity or a NaN of a key that the row does not see
+    // made some of these: once more, without that key.
     for (uint32_t r = __builtin_amdgcn_readfirstlane(again); r != 0; r &= r - 1) {
         const int i = row0 + __builtin_ctz(r);
         if (i >= t.len) break;
-        attn_row_defined<T, D>(q + i * a.q_row, k, a.k_row, v, a.v_row, a.causal ? i + 1 : t.len, a.scale,
+        attn_row<T, D>(q + i * a.q_row, k, a.k_row, v, a.v_row, a.causal ? i + 1 : t.len, a.scale,
                                a.y + ((int64_t)(t.first + i) * a.Hq + h) * D);
     }
 }
@@ -354,16 +371,26 @@ hipError_t launch(const AttnArgs& a, hipStream_t st) {
     k_attn_prompt<T, D, NW, BN, KG><<<dim3(a.Hq, y, (unsigned)((tiles + y - 1) / y)), 64 * NW * KG, lds, st>>>(a);
     return hipGetLastError();
 }
-#ifndef V64
-#define V64 4, 64, 2
-#define V128 4, 64, 2
-#define V256 2, 32, 2
-#endif
+// Blocks of 128 rows fill the 256 CUs twice, or the keys are split over two
+// halves of a block's waves, or its rows are 64 as well (D = 256, one wave a
+// SIMD: 64 rows and two halves, or 128).  Few blocks: what a block takes is
+// what the call takes.  Many: 64 rows load each key twice as often.  us, 128
+// rows / 128 rows in halves / 64 rows in halves, causal, one sequence:
+//   D = 128, 32 heads: 300 tokens (96 blocks) 11.8 / 12.6 / 10.6,
+//     600 (160) 18.6 / 17.1 / 16.9, 1220 (320) 31 / 27 / 39, 2500 (640) 67 / 78 / 107
+//   D = 64, 16 heads: 1220 tokens (160 blocks) 22.7 / 17.8 / 15.4
+//   D = 256, 16 heads: 300 tokens (48 blocks) 21.6 / - / 17.9, 8 heads: 16384 (1024) 1455 / - / 1780
+template <class T, int D>
+hipError_t launch_by_size(const AttnArgs& a, hipStream_t st) {
+    const int64_t blocks = ((int64_t)a.T / 128 + (a.B + 1) / 2) * a.Hq;   // half a tile lost a sequence
+    if constexpr (D == 256) return blocks <= 448 ? launch<T, D, 2, 32, 2>(a, st) : launch<T, D, 4, 32, 1>(a, st);
+    else if (blocks <= 192) return launch<T, D, 2, 64, 2>(a, st);
+    else if (blocks <= 448) return launch<T, D, 4, 64, 2>(a, st);
+    else return launch<T, D, 4, 64, 1>(a, st);
+}
 template <class T>
 hipError_t launch_by_dim(const AttnArgs& a, hipStream_t st) {
-    if (a.D == 64) return launch<T, 64, V64>(a, st);
-    if (a.D == 128) return launch<T, 128, V128>(a, st);
-    return launch<T, 256, V256>(a, st);
+    return a.D == 64 ? launch_by_size<T, 64>(a, st) : a.D == 128 ? launch_by_size<T, 128>(a, st) : launch_by_size<T, 256>(a, st);
 }
 
 }  // namespace

@@ -51,6 +51,17 @@ def test_lengths(n, causal):
     check(*make([n], 2, 1, 128, torch.bfloat16, seed=n), [n], causal, torch.bfloat16)
 
 
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("lens,Hq,Hkv", [([700], 40, 5), ([130, 700, 1, 257, 64], 48, 4), ([500, 333, 129], 16, 16),
+                                         ([65], 300, 100)])
+def test_many_blocks(dtype, D, causal, lens, Hq, Hkv):
+    """Enough rows and heads for every way that the rows and keys are split
+    over blocks and waves."""
+    check(*make(lens, Hq, Hkv, D, DT[dtype], seed=Hq), lens, causal, DT[dtype])
+
+
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("causal", [True, False])
 def test_many_short_sequences(D, causal):
@@ -127,24 +138,27 @@ def special(D, Hq=4, Hkv=2, n=300, dtype=torch.bfloat16):
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
 @pytest.mark.parametrize("where", ["k", "v"])
-def test_a_bad_token_reaches_only_rows_that_see_it(D, bad, where):
+@pytest.mark.parametrize("heads", [2, 130, 200])   # of each half: the ways of test_many_blocks
+def test_a_bad_token_reaches_only_rows_that_see_it(D, bad, where, heads):
     q, k, v = special(D)
+    q = q.repeat_interleave(heads // 2, 1)
     clean = crp.attn_prompt(q, k, v, torch.tensor([0, 150, 300], dtype=torch.int32).cuda())
     (k if where == "k" else v)[77, 1, 5] = bad
     y = crp.attn_prompt(q, k, v, torch.tensor([0, 150, 300], dtype=torch.int32).cuda())
     # heads 0, 1 and rows before it, and the other sequence, as they were (to the weights' rounding)
     near = lambda a, b: (a.float() - b.float()).abs().max() <= 4 * torch.finfo(torch.bfloat16).eps
-    assert near(y[:, :2], clean[:, :2]) and near(y[:77], clean[:77]) and near(y[150:], clean[150:])
-    seen = y[77:150, 2:].float()
+    H = heads
+    assert near(y[:, :H], clean[:, :H]) and near(y[:77], clean[:77]) and near(y[150:], clean[150:])
+    seen = y[77:150, H:].float()
     if where == "v":
         others = [d for d in range(D) if d != 5]
-        assert near(y[77:150, 2:][..., others], clean[77:150, 2:][..., others])
+        assert near(y[77:150, H:][..., others], clean[77:150, H:][..., others])
         assert (seen[..., 5] == bad).all() if bad == bad else seen[..., 5].isnan().all()
     elif bad != bad:
         assert seen.isnan().all()
     else:
         # a score of +-infinity: NaN, or a key with no weight
-        up = (q[77:150, 2:, 5].float() * bad) > 0
+        up = (q[77:150, H:, 5].float() * bad) > 0
         assert seen[up].isnan().all() and seen[~up].isfinite().all()
 
 
