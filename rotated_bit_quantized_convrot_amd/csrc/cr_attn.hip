@@ -152,7 +152,7 @@ __global__ __launch_bounds__(64 * NW * KG, D == 256 ? 1 : 2) void k_attn_prompt(
     // fp16 weights: 2^6 at the maximum, so that fewer fall below its normal range
     constexpr float kBias = std::is_same_v<T, Fp16> ? 6.0f : 0.0f;
     extern __shared__ __align__(1024) char lds[];
-    const int lane = threadIdx.x & 63, wave = (threadIdx.x >> 6) % NW, kg = (threadIdx.x >> 6) / NW;
+    const int lane = threadIdx.x & 63, wave = wave_of_block() % NW, kg = wave_of_block() / NW;
     Tile t;
     if (!find_tile<BM>(a.cu, a.B, a.T, blockIdx.y + blockIdx.z * gridDim.y, &t)) return;
     // blocks go to the 8 XCDs in turn: heads of one key head to the same one

@@ -122,17 +122,32 @@ __global__ void k_kv4_append(AppendArgs a) {
 // (1 + z / 16) sum p, is known and taken off in float32.
 // q (rotated: float32) and the weights times V's scales go in as two bf16
 // values of 8 bits each, in bf16's range whatever T.
-constexpr int kWaves = 4, kStep = 64;
-constexpr int kMinSpan = kWaves * kStep;
+constexpr int kStep = 64;
+constexpr int kMinSpan = 4 * kStep;
 
 template <int D>
-constexpr int max_tiles() { return D == 64 ? 4 : D == 128 ? 2 : 1; }
+constexpr int max_tiles() { return D == 64 ? 3 : D == 128 ? 2 : 1; }
 
 // One block's work: tile group `tile` of sequence b (rows 16 RT tile ..),
 // tokens span * chunk .. of it; its slot among all blocks of a head.
 struct Kv4Work {
     int b, first, rows, tokens, tile, chunk, chunks, span, slot;
 };
+// Sums over the lanes up to each, by DPP (row_shr 1, 2, 4, 8, row_bcast 15, 31).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int dpp_or_zero(int v) { return __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false); }
+template <class F>
+__device__ __forceinline__ int wave_scan(int v, F add) {
+    v = add(v, dpp_or_zero<0x111, 0xF>(v));
+    v = add(v, dpp_or_zero<0x112, 0xF>(v));
+    v = add(v, dpp_or_zero<0x114, 0xF>(v));
+    v = add(v, dpp_or_zero<0x118, 0xF>(v));
+    v = add(v, dpp_or_zero<0x142, 0xA>(v));
+    return add(v, dpp_or_zero<0x143, 0xC>(v));
+}
+__device__ __forceinline__ int add_ints(int a, int b) { return a + b; }
+__device__ __forceinline__ int add_floats(int a, int b) { return __float_as_int(__int_as_float(a) + __int_as_float(b)); }
+
 // The work of block `index` of `slots` (by_tile: of tile group `index`, its
 // chunk 0).  The span is the shortest, from kMinSpan on, with which all spans
 // of all tile groups have a slot; slots = 0: one span takes everything.  Every
@@ -140,50 +155,41 @@ struct Kv4Work {
 template <int RT>
 __device__ __forceinline__ bool kv4_work(const Kv4& c, int G, int slots, bool by_tile, int index, Kv4Work* w) {
     const int lane = threadIdx.x & 63;
+    auto groups_of = [&](const Kv4Seq& s) { return (int)(((long long)s.rows * G + 16 * RT - 1) / (16 * RT)); };
+    Kv4Seq first = kv4_seq(c, min(lane, c.B - 1));
     int span = 0x40000000;
     if (slots > 0) {
         int groups = 0;
-        long long total = 0;
+        float total = 0.0f;   // of tokens, group by group
         for (int b0 = 0; b0 < c.B; b0 += 64) {
-            const Kv4Seq s = kv4_seq(c, min(b0 + lane, c.B - 1));
-            int n = b0 + lane < c.B ? (int)(((long long)s.rows * G + 16 * RT - 1) / (16 * RT)) : 0;
-            long long t = (long long)n * s.tokens;
-#pragma unroll
-            for (int m = 1; m < 64; m <<= 1) {
-                n += __shfl_xor(n, m);
-                t += __shfl_xor(t, m);
-            }
-            groups += n;
-            total += t;
+            const Kv4Seq s = b0 == 0 ? first : kv4_seq(c, min(b0 + lane, c.B - 1));
+            const int n = b0 + lane < c.B ? groups_of(s) : 0;
+            groups += __builtin_amdgcn_readlane(wave_scan(n, add_ints), 63);
+            total += __int_as_float(__builtin_amdgcn_readlane(wave_scan(__float_as_int((float)n * (float)s.tokens), add_floats), 63));
         }
-        if (groups >= slots) groups = slots - 1;   // not so: the grid has two slots a group
-        const long long left = slots - groups, e = (total + left - 1) / left;
-        span = (int)((e < kMinSpan ? kMinSpan : e + kMinSpan - 1) / kMinSpan) * kMinSpan;
+        // the grid has two slots a group, so that some are left; a little more than the sum, which is rounded
+        const float left = (float)max(slots - groups, 1), e = total * 1.0001f / left;
+        span = e < (float)kMinSpan ? kMinSpan : ((int)fminf(e, 1073741824.0f) / kMinSpan + 1) * kMinSpan;
     }
     int at = 0, slot = 0;
     for (int b0 = 0; b0 < c.B; b0 += 64) {
-        const Kv4Seq s = kv4_seq(c, min(b0 + lane, c.B - 1));
-        const int n = b0 + lane < c.B ? (int)(((long long)s.rows * G + 16 * RT - 1) / (16 * RT)) : 0;
+        const Kv4Seq s = b0 == 0 ? first : kv4_seq(c, min(b0 + lane, c.B - 1));
+        const int n = b0 + lane < c.B ? groups_of(s) : 0;
         const int chunks = s.tokens > span ? (s.tokens + span - 1) / span : 1;
-        int tiles = n, all = n * chunks;
-#pragma unroll
-        for (int m = 1; m < 64; m <<= 1) {
-            const int t = __shfl_up(tiles, m), x = __shfl_up(all, m);
-            if (lane >= m) { tiles += t; all += x; }
-        }
+        const int tiles = wave_scan(n, add_ints), all = wave_scan(n * chunks, add_ints);
         const uint64_t after = __ballot((by_tile ? at + tiles : slot + all) > index);
         if (after) {
             const int l = __builtin_ctzll(after);
-            auto of = [&](int v) { return __builtin_amdgcn_readfirstlane(__shfl(v, l)); };
+            auto of = [&](int v) { return __builtin_amdgcn_readlane(v, l); };
             w->b = b0 + l;
             w->first = of(s.first);
             w->rows = of(s.rows);
             w->tokens = of(s.tokens);
             w->chunks = of(chunks);
             w->span = span;
-            const int before = __builtin_amdgcn_readfirstlane(slot) + of(all - n * chunks);
+            const int before = slot + of(all - n * chunks);
             if (by_tile) {
-                w->tile = index - __builtin_amdgcn_readfirstlane(at) - of(tiles - n);
+                w->tile = index - at - of(tiles - n);
                 w->chunk = 0;
             } else {
                 w->tile = (index - before) / w->chunks;
@@ -192,8 +198,8 @@ __device__ __forceinline__ bool kv4_work(const Kv4& c, int G, int slots, bool by
             w->slot = before + w->tile * w->chunks + w->chunk;
             return true;
         }
-        at += __shfl(tiles, 63);
-        slot += __shfl(all, 63);
+        at += __builtin_amdgcn_readlane(tiles, 63);
+        slot += __builtin_amdgcn_readlane(all, 63);
     }
     return false;
 }
@@ -204,25 +210,26 @@ template <int D, int RT>
 constexpr size_t part_words() { return 16 * RT * (D + 2); }
 
 // Four operand pairs of a dword of codes: 1 + c / 16 in bf16.
-__device__ __forceinline__ u32x4 kv4_operand(uint32_t w) {
-    u32x4 b;
-    b[0] = (w << 3 & 0x00780078u) | 0x3F803F80u;
-    b[1] = (w >> 1 & 0x00780078u) | 0x3F803F80u;
-    b[2] = (w >> 5 & 0x00780078u) | 0x3F803F80u;
-    b[3] = (w >> 9 & 0x00780078u) | 0x3F803F80u;
-    return b;
+// The constants come in registers: as literals they would cost an instruction
+// more a pair.
+struct Mantissa {
+    uint32_t mask = 0x00780078u, one = 0x3F803F80u;
+    __device__ __forceinline__ uint32_t operator()(uint32_t w) const { return (w & mask) | one; }
+};
+__device__ __forceinline__ Mantissa mantissa() {
+    Mantissa m;
+    asm("" : "+v"(m.mask), "+v"(m.one));
+    return m;
+}
+__device__ __forceinline__ u32x4 kv4_operand(Mantissa m, uint32_t w) {
+    return u32x4{m(w << 3), m(w >> 1), m(w >> 5), m(w >> 9)};
 }
 // 16 tokens of V (4 dwords, a byte a token): operand of tokens 8 u + 0..7 in
 // the order 0 2, 1 3, 4 6, 5 7, of the bytes' low or high nibbles.
 template <bool HIGH>
-__device__ __forceinline__ u32x4 kv4_v_operand(uint32_t a, uint32_t b) {
-    constexpr uint32_t m = 0x00780078u, one = 0x3F803F80u;
-    u32x4 r;
-    r[0] = ((HIGH ? a >> 1 : a << 3) & m) | one;
-    r[1] = ((HIGH ? a >> 9 : a >> 5) & m) | one;
-    r[2] = ((HIGH ? b >> 1 : b << 3) & m) | one;
-    r[3] = ((HIGH ? b >> 9 : b >> 5) & m) | one;
-    return r;
+__device__ __forceinline__ u32x4 kv4_v_operand(Mantissa m, uint32_t a, uint32_t b) {
+    if constexpr (HIGH) return u32x4{m(a >> 1), m(a >> 9), m(b >> 1), m(b >> 9)};
+    else return u32x4{m(a << 3), m(a >> 5), m(b << 3), m(b >> 5)};
 }
 // x as hi + lo of 8 bits each (to 2^-17 of x).
 __device__ __forceinline__ void split2(float a, float b, uint32_t* hi, uint32_t* lo) {
@@ -233,8 +240,15 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t* hi, uint32_t*
 // Floats of a row in LDS, so that 16 rows' 16 bytes hit all banks; of the block.
 template <int D>
 constexpr int lds_row() { return D + 4; }
-template <int D>
-constexpr int lds_words() { return kWaves * 16 * lds_row<D>(); }
+template <int D, int W>
+constexpr int lds_words() { return W * 16 * lds_row<D>(); }
+
+// A step's scales s and 1 + z / 16 (of V: the operand, in its order of tokens).
+template <int NG>
+struct Stage {
+    float ks[NG][kStep], kz[NG][kStep], vs[NG][kStep];
+    uint16_t vz[NG][kStep];
+};
 
 template <int N>
 struct Words {
@@ -252,27 +266,70 @@ __device__ __forceinline__ void kv4_finish(float (&x)[D / 64], float total, int 
     for (int i = 0; i < D / 64; ++i) y[lane * (D / 64) + i] = T::from_f32(x[i]);
 }
 
+// Nothing is moved across it: made ahead, operands and scales would take
+// registers that there are not.
+#define KEEP_ORDER() __builtin_amdgcn_sched_barrier(0)
+
 // LO: q needs its second part (rotated, or fp16's 11 bits).
-template <class T, int D, int NG, int RT, bool LO>
-__global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void k_attn_kv4(Kv4 c, AttnArgs a, int slots, float* parts) {
+template <class T, int D, int NG, int RT, bool LO, int W>
+__global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_attn_kv4(Kv4 c, AttnArgs a, int slots, float* parts) {
     constexpr int KS = D / 32, SPG = KS / NG, DT = D / 16, DPG = DT / NG;
     constexpr float kMove = 8.0f;   // the maximum follows when weights would pass 2^8
     constexpr int kRow = lds_row<D>();
-    // the waves' words of a step ([K, V][group][token]); then their sums of a tile
+    // the waves' scales of a step; then their sums of a tile
     extern __shared__ __align__(16) uint32_t lds[];
-    static_assert(kWaves * 2 * kStep * NG <= lds_words<D>(), "words fit where the sums go");
+    static_assert(W * sizeof(Stage<NG>) <= 4 * lds_words<D, W>(), "a step's scales fit where the sums go");
     float* lds_o = reinterpret_cast<float*>(lds);
-    __shared__ float lds_top[kWaves][16], lds_sum[kWaves][16];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, quad = lane >> 4;
+    __shared__ float lds_top[W][16], lds_sum[W][16];
+    const int lane = threadIdx.x & 63, wave = wave_of_block(), col = lane & 15, quad = lane >> 4;
     const int g = blockIdx.x, G = a.Hq / c.heads;
     Kv4Work w;
     if (!kv4_work<RT>(c, G, slots, false, blockIdx.y + blockIdx.z * gridDim.y, &w)) return;
     const int begin = w.chunk * w.span, end = min(begin + w.span, w.tokens);
 
+    // page of the 16 tokens from `pos` on, -1 past the end
+    auto page_at = [&](int pos) { return pos < end ? kv4_page(c, w.b, pos) : -1; };
+    const int S1 = (1 << c.page_log2) - 1;
+    const size_t code_page = ((size_t)2 * c.heads << c.page_log2) * (D / 2);
+    const size_t word_page = ((size_t)2 * c.heads << c.page_log2) * NG;
+    const uint8_t* codes_k = c.codes + kv4_codes_at(c, 0, 0, g);
+    const uint8_t* codes_v = c.codes + kv4_codes_at(c, 0, 1, g);
+    const uint32_t* words_k = c.scales + kv4_scales_at(c, 0, 0, g);
+    const uint32_t* words_v = c.scales + kv4_scales_at(c, 0, 1, g);
+
+    u32x4 vc[DT / 2];
+    uint32_t kc[4][KS];
+    Words<NG> kw, vw;
+    // K rows: MFMA row m of tile (u, j) is token 16 (m / 4) + 8 u + 4 j + m % 4, so that a lane's four results are
+    // tokens 16 quad + 8 u + 4 j + 0..3
+    auto load_k = [&](int pos, int page_k, int page_w) {
+        const int row = ((pos + 16 * (col >> 2)) & S1) + (col & 3);
+        const uint8_t* p = codes_k + (size_t)(page_k < 0 ? 0 : page_k) * code_page + kv4_k_byte(D, row, quad * KS);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const Words<KS> v = *reinterpret_cast<const Words<KS>*>(__builtin_assume_aligned(p + x * 4 * (D / 2), KS >= 4 ? 16 : 8));
+#pragma unroll
+            for (int s = 0; s < KS; ++s) kc[x][s] = v.w[s];
+        }
+        kw = *reinterpret_cast<const Words<NG>*>(__builtin_assume_aligned(
+            words_k + (size_t)(page_w < 0 ? 0 : page_w) * word_page + ((pos + lane) & S1) * NG, NG >= 4 ? 16 : 4 * NG));
+    };
+    auto load_v = [&](int pos, int page) {
+        const size_t p = (size_t)(page < 0 ? 0 : page);
+        const uint8_t* q = codes_v + p * code_page + kv4_v_byte(D, (pos + 16 * quad) & S1, col);
+#pragma unroll
+        for (int e = 0; e < DT / 2; ++e) vc[e] = *reinterpret_cast<const u32x4*>(q + 256 * e);
+        vw = *reinterpret_cast<const Words<NG>*>(__builtin_assume_aligned(
+            words_v + p * word_page + ((pos + lane) & S1) * NG, NG >= 4 ? 16 : 4 * NG));
+    };
+    const Mantissa man = mantissa();
+    constexpr int kStride = W * kStep;
+    int pos = begin + wave * kStep;
+    int page_k = page_at(pos + 16 * (col >> 2)), page_v = page_at(pos + 16 * quad);
+    int next_k = page_at(pos + kStride + 16 * (col >> 2)), next_v = page_at(pos + kStride + 16 * quad);
     // rows of the tiles: what they see, and q
     int seen[RT];
     u32x4 qh[RT][KS], ql[RT][LO ? KS : 1];
-    float qs[RT][NG];
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
         // a column past the last row repeats it
@@ -280,9 +337,28 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void k_attn_kv4(Kv4 
         const int i = (int)(r / G), h = g * G + (int)(r % G);
         seen[t] = w.tokens - w.rows + i + 1;
         const uint16_t* p = a.q + (w.first + i) * a.q_row + h * a.q_head + 8 * quad;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) qh[t][s] = *reinterpret_cast<const u32x4*>(p + 32 * s);
+    }
+    if (pos < end) {
+        load_k(pos, page_k, page_v);
+        load_v(pos, page_v);
+    }
+    float qs[RT][NG];
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
         float x[KS][8];
 #pragma unroll
-        for (int s = 0; s < KS; ++s) w4g_values<T>(p + 32 * s, x[s]);
+        for (int s = 0; s < KS; ++s) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                x[s][2 * j] = T::to_f32(qh[t][s][j] & 0xFFFFu);
+                x[s][2 * j + 1] = T::to_f32(qh[t][s][j] >> 16);
+            }
+            if (a.scale < 0.0f)   // its sign goes to q
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[s][j] = -x[s][j];
+        }
         if (LO && c.rotate) {
             // d = 32 s + 8 quad + j: strides 1, 2, 4 among j, 8, 16 among quads, 32 .. among s
 #pragma unroll
@@ -352,62 +428,22 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void k_attn_kv4(Kv4 
         sum[t] = 0.0f;
     }
     // masked scores become -infinity times cs; a scale of 0 would make NaN of them, and 1e-30 gives equal weights too
-    const float cs = 16.0f * (a.scale == 0.0f ? 1e-30f : a.scale * 1.4426950408889634f);
-    const float none = cs < 0.0f ? __builtin_inff() : -__builtin_inff();
+    const float cs = 16.0f * (a.scale == 0.0f ? 1e-30f : fabsf(a.scale) * 1.4426950408889634f);
 
-    // page of the 16 tokens from `pos` on, -1 past the end
-    auto page_at = [&](int pos) { return pos < end ? kv4_page(c, w.b, pos) : -1; };
-    const int S1 = (1 << c.page_log2) - 1;
-    const size_t code_page = ((size_t)2 * c.heads << c.page_log2) * (D / 2);
-    const size_t word_page = ((size_t)2 * c.heads << c.page_log2) * NG;
-    const uint8_t* codes_k = c.codes + kv4_codes_at(c, 0, 0, g);
-    const uint8_t* codes_v = c.codes + kv4_codes_at(c, 0, 1, g);
-    const uint32_t* words_k = c.scales + kv4_scales_at(c, 0, 0, g);
-    const uint32_t* words_v = c.scales + kv4_scales_at(c, 0, 1, g);
-
-    u32x4 vc[DT / 2];
-    uint32_t kc[4][KS];
-    Words<NG> kw, vw;
-    // K rows: MFMA row m of tile (u, j) is token 16 (m / 4) + 8 u + 4 j + m % 4, so that a lane's four results are
-    // tokens 16 quad + 8 u + 4 j + 0..3
-    auto load_k = [&](int pos, int page_k, int page_w) {
-        const int row = ((pos + 16 * (col >> 2)) & S1) + (col & 3);
-        const uint8_t* p = codes_k + (size_t)(page_k < 0 ? 0 : page_k) * code_page + kv4_k_byte(D, row, quad * KS);
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            const Words<KS> v = *reinterpret_cast<const Words<KS>*>(__builtin_assume_aligned(p + x * 4 * (D / 2), KS >= 4 ? 16 : 8));
-#pragma unroll
-            for (int s = 0; s < KS; ++s) kc[x][s] = v.w[s];
-        }
-        kw = *reinterpret_cast<const Words<NG>*>(__builtin_assume_aligned(
-            words_k + (size_t)(page_w < 0 ? 0 : page_w) * word_page + ((pos + lane) & S1) * NG, NG >= 4 ? 16 : 4 * NG));
-    };
-    auto load_v = [&](int pos, int page) {
-        const size_t p = (size_t)(page < 0 ? 0 : page);
-        const uint8_t* q = codes_v + p * code_page + kv4_v_byte(D, (pos + 16 * quad) & S1, col);
-#pragma unroll
-        for (int e = 0; e < DT / 2; ++e) vc[e] = *reinterpret_cast<const u32x4*>(q + 256 * e);
-        vw = *reinterpret_cast<const Words<NG>*>(__builtin_assume_aligned(
-            words_v + p * word_page + ((pos + lane) & S1) * NG, NG >= 4 ? 16 : 4 * NG));
-    };
-    constexpr int kStride = kWaves * kStep;
-    int pos = begin + wave * kStep;
-    int page_k = page_at(pos + 16 * (col >> 2)), page_v = page_at(pos + 16 * quad);
-    int next_k = page_at(pos + kStride + 16 * (col >> 2)), next_v = page_at(pos + kStride + 16 * quad);
-    if (pos < end) {
-        load_k(pos, page_k, page_v);
-        load_v(pos, page_v);
-    }
-    uint32_t* wk = lds + wave * 2 * kStep * NG;
-    uint32_t* wv = wk + kStep * NG;
+    Stage<NG>& stage = reinterpret_cast<Stage<NG>*>(lds)[wave];
     for (; pos < end; pos += kStride) {
-        // words through LDS: a token's own lane has them, its 16 lanes need them; of tokens that are not there, zeros
+        // scales and 1 + z / 16 through LDS: a token's own lane has them, its 16 lanes need them; of tokens that are
+        // not there, zeros
         {
             const bool there = pos + lane < end && page_v >= 0;
+            const int place = (lane & ~7) | (lane & 4) | (lane & 1) << 1 | (lane >> 1 & 1);   // 0 2, 1 3, 4 6, 5 7
 #pragma unroll
             for (int n = 0; n < NG; ++n) {
-                wk[n * kStep + lane] = there ? kw.w[n] : 0;
-                wv[n * kStep + lane] = there ? vw.w[n] : 0;
+                const uint32_t k = there ? kw.w[n] : 0, v = there ? vw.w[n] : 0;
+                stage.ks[n][lane] = __uint_as_float(k & ~15u);
+                stage.kz[n][lane] = __uint_as_float((k & 15u) << 19 | 0x3F800000u);
+                stage.vs[n][lane] = __uint_as_float(v & ~15u);
+                stage.vz[n][place] = (uint16_t)((v & 15u) << 3 | 0x3F80u);
             }
             __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
             __builtin_amdgcn_wave_barrier();
@@ -416,17 +452,15 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void k_attn_kv4(Kv4 
         float s[RT][16];
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-#pragma unroll
-            for (int t = 0; t < RT; ++t)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) s[t][4 * x + i] = 0.0f;
+            KEEP_ORDER();
 #pragma unroll
             for (int n = 0; n < NG; ++n) {
-                const u32x4 word = *reinterpret_cast<const u32x4*>(wk + n * kStep + 16 * quad + 4 * x);
+                const f32x4 sc = *reinterpret_cast<const f32x4*>(&stage.ks[n][16 * quad + 4 * x]);
+                const f32x4 z = *reinterpret_cast<const f32x4*>(&stage.kz[n][16 * quad + 4 * x]);
                 f32x4 acc[RT] = {};
 #pragma unroll
                 for (int k = n * SPG; k < (n + 1) * SPG; ++k) {
-                    const u32x4 op = kv4_operand(kc[x][k]);
+                    const u32x4 op = kv4_operand(man, kc[x][k]);
 #pragma unroll
                     for (int t = 0; t < RT; ++t) {
                         acc[t] = Bf16::mfma(op, qh[t][k], acc[t]);
@@ -434,12 +468,12 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void k_attn_kv4(Kv4 
                     }
                 }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float sc = __uint_as_float(word[i] & ~15u), z = __uint_as_float((word[i] & 15u) << 19 | 0x3F800000u);
+                for (int i = 0; i < 4; ++i)
 #pragma unroll
-                    for (int t = 0; t < RT; ++t)
-                        s[t][4 * x + i] = __builtin_fmaf(sc, __builtin_fmaf(-z, qs[t][n], acc[t][i]), s[t][4 * x + i]);
-                }
+                    for (int t = 0; t < RT; ++t) {
+                        const float d = __builtin_fmaf(-z[i], qs[t][n], acc[t][i]);
+                        s[t][4 * x + i] = n == 0 ? sc[i] * d : __builtin_fmaf(sc[i], d, s[t][4 * x + i]);
+                    }
             }
         }
         // the next step's K while this one's weights and V are at work
@@ -463,13 +497,14 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void k_attn_kv4(Kv4 
             for (int t = 0; t < RT; ++t)
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
-                    if (i >= lim[t]) s[t][i] = none;
+                    if (i >= lim[t]) s[t][i] = -__builtin_inff();
         }
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
-            float m = s[t][0] * cs;
+            float m = s[t][0];
 #pragma unroll
-            for (int i = 1; i < 16; ++i) m = fmaxf(m, s[t][i] * cs);
+            for (int i = 1; i < 16; ++i) m = fmaxf(m, s[t][i]);
+            m *= cs;
             if (__any(m > top[t] + kMove)) {
                 m = fmaxf(m, __shfl_xor(m, 16));
                 m = fmaxf(m, __shfl_xor(m, 32));
@@ -492,16 +527,16 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void k_attn_kv4(Kv4 
         for (int n = 0; n < NG; ++n) {
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
+                KEEP_ORDER();
                 // weights times scales, in V's order of tokens, and the operand 1 + z / 16
-                const u32x4 word[2] = {*reinterpret_cast<const u32x4*>(wv + n * kStep + 16 * quad + 8 * u),
-                                       *reinterpret_cast<const u32x4*>(wv + n * kStep + 16 * quad + 8 * u + 4)};
-                u32x4 hi[RT], lo[RT], zo;
+                const f32x4 sc[2] = {*reinterpret_cast<const f32x4*>(&stage.vs[n][16 * quad + 8 * u]),
+                                     *reinterpret_cast<const f32x4*>(&stage.vs[n][16 * quad + 8 * u + 4])};
+                const u32x4 zo = *reinterpret_cast<const u32x4*>(&stage.vz[n][16 * quad + 8 * u]);
+                u32x4 hi[RT], lo[RT];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int t0 = 4 * (j / 2) + j % 2, t1 = t0 + 2;
-                    const uint32_t w0 = word[j / 2][j % 2], w1 = word[j / 2][j % 2 + 2];
-                    const float s0 = __uint_as_float(w0 & ~15u), s1 = __uint_as_float(w1 & ~15u);
-                    zo[j] = ((w0 & 15u) | (w1 & 15u) << 16) << 3 | 0x3F803F80u;
+                    const float s0 = sc[j / 2][j % 2], s1 = sc[j / 2][j % 2 + 2];
 #pragma unroll
                     for (int t = 0; t < RT; ++t) {
                         float x0 = s[t][8 * u + t0] * s0, x1 = s[t][8 * u + t1] * s1;
@@ -522,8 +557,8 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void k_attn_kv4(Kv4 
                 }
 #pragma unroll
                 for (int d = n * DPG; d < (n + 1) * DPG; ++d) {
-                    const u32x4 op = d % 2 ? kv4_v_operand<true>(vc[d / 2][2 * u], vc[d / 2][2 * u + 1])
-                                           : kv4_v_operand<false>(vc[d / 2][2 * u], vc[d / 2][2 * u + 1]);
+                    const u32x4 op = d % 2 ? kv4_v_operand<true>(man, vc[d / 2][2 * u], vc[d / 2][2 * u + 1])
+                                           : kv4_v_operand<false>(man, vc[d / 2][2 * u], vc[d / 2][2 * u + 1]);
 #pragma unroll
                     for (int t = 0; t < RT; ++t) {
                         o[t][d] = Bf16::mfma(op, hi[t], o[t][d]);
@@ -560,12 +595,12 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void k_attn_kv4(Kv4 
         __syncthreads();
         const long long r0 = (long long)(w.tile * RT + t) * 16;
         const int n = (int)min(16ll, (long long)w.rows * G - r0);
-        for (int r = wave; r < n; r += kWaves) {
+        for (int r = wave; r < n; r += W) {
             float m = lds_top[0][r], total = 0.0f, x[D / 64] = {};
 #pragma unroll
-            for (int k = 1; k < kWaves; ++k) m = fmaxf(m, lds_top[k][r]);
+            for (int k = 1; k < W; ++k) m = fmaxf(m, lds_top[k][r]);
 #pragma unroll
-            for (int k = 0; k < kWaves; ++k) {
+            for (int k = 0; k < W; ++k) {
                 // a wave that has seen nothing has sums of 0, or NaN
                 const float f = lds_top[k][r] == m || lds_top[k][r] == -__builtin_inff()
                                     ? 1.0f : __builtin_amdgcn_exp2f(lds_top[k][r] - m);
@@ -590,34 +625,78 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void k_attn_kv4(Kv4 
     }
 }
 
-// The slots of a tile group's spans joined, a wave a row.
+// The slots of a tile group's spans joined: a block a row, its waves every
+// fourth span, 16 at a time, so that few loads wait for each other.
+constexpr int kJoinWaves = 4;
 template <class T, int D, int RT>
-__global__ __launch_bounds__(256) void k_attn_kv4_join(Kv4 c, AttnArgs a, int slots, const float* parts) {
-    constexpr int N = D / 64, R = 16 * RT;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int g = blockIdx.x, G = a.Hq / c.heads;
+__global__ __launch_bounds__(64 * kJoinWaves) void k_attn_kv4_join(Kv4 c, AttnArgs a, int slots, int row_blocks,
+                                                                   const float* parts) {
+    constexpr int N = D / 64, R = 16 * RT, W = kJoinWaves;
+    constexpr size_t P = part_words<D, RT>();
+    __shared__ float lds_x[W][D], lds_sum[W], lds_top[W];
+    const int lane = threadIdx.x & 63, wave = wave_of_block();
+    const int g = blockIdx.x / row_blocks, G = a.Hq / c.heads;
     Kv4Work w;
     if (!kv4_work<RT>(c, G, slots, true, blockIdx.y + blockIdx.z * gridDim.y, &w) || w.chunks == 1) return;
     const long long r0 = (long long)w.tile * R;
     const int n = (int)min((long long)R, (long long)w.rows * G - r0);
-    const float* part = parts + ((size_t)g * slots + w.slot) * part_words<D, RT>();
-    for (int r = wave; r < n; r += 4) {
-        float m = -__builtin_inff();
-        for (int k = lane; k < w.chunks; k += 64) m = fmaxf(m, part[k * part_words<D, RT>() + R * D + r]);
+    const float* part = parts + ((size_t)g * slots + w.slot) * P;
+    for (int r = blockIdx.x % row_blocks; r < n; r += row_blocks) {
+        float m = -__builtin_inff(), total = 0.0f, x[N] = {};
+        for (int k0 = wave; k0 < w.chunks; k0 += W * 16) {
+            // lane i: the maximum and the sum of span k0 + W i, i < 16
+            const int some = min(16, (w.chunks - k0 + W - 1) / W), k = k0 + W * min(lane, some - 1);
+            const float top = part[k * P + R * D + r], sum = part[k * P + R * (D + 1) + r];
+            float y[16][N];
 #pragma unroll
-        for (int x = 1; x < 64; x <<= 1) m = fmaxf(m, __shfl_xor(m, x));
-        float total = 0.0f, x[N] = {};
-#pragma unroll 8
-        for (int k = 0; k < w.chunks; ++k) {
-            const float* p = part + k * part_words<D, RT>();
-            const float top = p[R * D + r];
-            const float f = top == m || top == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(top - m);
-            total = __builtin_fmaf(f, p[R * (D + 1) + r], total);
+            for (int i = 0; i < 16; ++i)
 #pragma unroll
-            for (int i = 0; i < N; ++i) x[i] = __builtin_fmaf(f, p[r * D + lane * N + i], x[i]);
+                for (int d = 0; d < N; ++d) y[i][d] = part[(k0 + W * min(i, some - 1)) * P + r * D + lane * N + d];
+            float up = fmaxf(m, top);
+#pragma unroll
+            for (int i = 1; i < 16; i <<= 1) up = fmaxf(up, __shfl_xor(up, i));
+            up = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(up)));
+            // sums of a span that saw nothing are 0, or NaN
+            const float f = top == up || top == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(top - up);
+            const float f0 = m == up || m == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(m - up);
+            m = up;
+            total *= f0;
+#pragma unroll
+            for (int d = 0; d < N; ++d) x[d] *= f0;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                if (i >= some) continue;
+                const float fi = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(f), i));
+                total = __builtin_fmaf(fi, __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(sum), i)), total);
+#pragma unroll
+                for (int d = 0; d < N; ++d) x[d] = __builtin_fmaf(fi, y[i][d], x[d]);
+            }
         }
-        const int i0 = (int)((r0 + r) / G), h = g * G + (int)((r0 + r) % G);
-        kv4_finish<T, D>(x, total, c.rotate, a.y + ((int64_t)(w.first + i0) * a.Hq + h) * D);
+#pragma unroll
+        for (int d = 0; d < N; ++d) lds_x[wave][lane * N + d] = x[d];
+        if (lane == 0) {
+            lds_sum[wave] = total;
+            lds_top[wave] = m;
+        }
+        __syncthreads();
+        if (wave == 0) {
+            float up = m;
+#pragma unroll
+            for (int k = 1; k < W; ++k) up = fmaxf(up, lds_top[k]);
+            total = 0.0f;
+#pragma unroll
+            for (int d = 0; d < N; ++d) x[d] = 0.0f;
+#pragma unroll
+            for (int k = 0; k < W; ++k) {
+                const float f = lds_top[k] == up || lds_top[k] == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(lds_top[k] - up);
+                total = __builtin_fmaf(f, lds_sum[k], total);
+#pragma unroll
+                for (int d = 0; d < N; ++d) x[d] = __builtin_fmaf(f, lds_x[k][lane * N + d], x[d]);
+            }
+            const int i0 = (int)((r0 + r) / G), h = g * G + (int)((r0 + r) % G);
+            kv4_finish<T, D>(x, total, c.rotate, a.y + ((int64_t)(w.first + i0) * a.Hq + h) * D);
+        }
+        __syncthreads();
     }
 }
 
@@ -647,17 +726,20 @@ namespace {
 // the blocks a head gets: spans for all CUs twice, two a tile group at least
 // (so that every group's last, shorter span has one), none where no sequence
 // is worth a second span.
+// Tokens up to which one block takes a sequence, with twice the waves: two
+// turns of them.
+constexpr int kOneSpan = 1024;
 struct Grid {
     int tiles, groups, slots;
 };
 Grid attn_kv4_grid(int T, int G, int heads, int dim, int page, int width, int B) {
     Grid g;
-    const int most = dim == 64 ? 4 : dim == 128 ? 2 : 1;
+    const int most = dim == 64 ? max_tiles<64>() : dim == 128 ? max_tiles<128>() : max_tiles<256>();
     const int64_t rows = ((int64_t)T * G + B - 1) / B;   // of a sequence, on average
-    g.tiles = rows <= 16 || most == 1 ? 1 : rows <= 32 || most == 2 ? 2 : 4;
+    g.tiles = rows > 16 * most ? most : (int)(rows + 15) / 16;
     g.groups = (int)(((int64_t)T * G + (int64_t)(B < T ? B : T) * (16 * g.tiles - 1)) / (16 * g.tiles));
     g.slots = 0;
-    if ((int64_t)width * page > 2 * kMinSpan) {
+    if ((int64_t)width * page > kOneSpan) {
         const int64_t fill = 512 / heads;
         g.slots = (int)(2 * (int64_t)g.groups > fill ? 2 * (int64_t)g.groups : fill);
     }
@@ -665,25 +747,27 @@ Grid attn_kv4_grid(int T, int G, int heads, int dim, int page, int width, int B)
 }
 size_t part_bytes(int dim, int tiles) { return (size_t)16 * tiles * (dim + 2) * 4; }
 
-template <class T, int D, int NG, int RT>
+template <class T, int D, int NG, int RT, int W>
 hipError_t run_attn_kv4(const AttnArgs& a, const Kv4& c, const Grid& g, float* ws, hipStream_t st) {
-    const auto grid = [&](int n) {
+    const auto grid = [&](int n, int x) {
         const int y = n < 32768 ? n : 32768;
-        return dim3(c.heads, y, (n + y - 1) / y);
+        return dim3(x, y, (n + y - 1) / y);
     };
-    const int n = g.slots ? g.slots : g.groups;
-    constexpr int lds = 4 * lds_words<D>();
+    constexpr int lds = 4 * lds_words<D, W>();
     hipError_t e = hipSuccess;
     const auto go = [&](auto kernel, std::atomic<uint64_t>& done) {
         if (lds > 65536 && (e = opt_in_lds(reinterpret_cast<const void*>(kernel), lds, done)) != hipSuccess) return;
-        kernel<<<grid(n), 64 * kWaves, lds, st>>>(c, a, g.slots, ws);
+        kernel<<<grid(g.slots ? g.slots : g.groups, c.heads), 64 * W, lds, st>>>(c, a, g.slots, ws);
         e = hipGetLastError();
     };
     static std::atomic<uint64_t> done[2];
-    if (c.rotate || a.fp16) go(k_attn_kv4<T, D, NG, RT, true>, done[0]);
-    else go(k_attn_kv4<T, D, NG, RT, false>, done[1]);
+    if (c.rotate || a.fp16) go(k_attn_kv4<T, D, NG, RT, true, W>, done[0]);
+    else go(k_attn_kv4<T, D, NG, RT, false, W>, done[1]);
     if (e != hipSuccess || g.slots == 0) return e;
-    k_attn_kv4_join<T, D, RT><<<grid(g.groups), 256, 0, st>>>(c, a, g.slots, ws);
+    // as many blocks as a group has rows on average
+    const int64_t rows = ((int64_t)c.T * (a.Hq / c.heads) + g.groups - 1) / g.groups;
+    const int row_blocks = (int)(rows < 16 * RT ? rows : 16 * RT);
+    k_attn_kv4_join<T, D, RT><<<grid(g.groups, c.heads * row_blocks), 64 * kJoinWaves, 0, st>>>(c, a, g.slots, row_blocks, ws);
     return hipGetLastError();
 }
 
@@ -703,14 +787,21 @@ hipError_t launch_attn_kv4(const AttnArgs& a, const Kv4& c, void* ws, hipStream_
             auto tiles = [&](auto rt) {
                 if constexpr (rt <= max_tiles<d>()) {
                     if (g.tiles != rt) return;
-                    e = a.fp16 ? run_attn_kv4<Fp16, d, ng, rt>(a, c, g, (float*)ws, st)
-                               : run_attn_kv4<Bf16, d, ng, rt>(a, c, g, (float*)ws, st);
+                    const auto run = [&](auto waves) {
+                        e = a.fp16 ? run_attn_kv4<Fp16, d, ng, rt, waves>(a, c, g, (float*)ws, st)
+                                   : run_attn_kv4<Bf16, d, ng, rt, waves>(a, c, g, (float*)ws, st);
+                    };
+                    // (a head of 256 takes the registers of two waves)
+                    if constexpr (d < 256 && rt == 1) {
+                        if (g.slots == 0) return run(std::integral_constant<int, 8>());
+                    }
+                    run(std::integral_constant<int, 4>());
                 }
             };
             if (c.dim / c.group != ng) return;
             tiles(std::integral_constant<int, 1>());
             tiles(std::integral_constant<int, 2>());
-            tiles(std::integral_constant<int, 4>());
+            tiles(std::integral_constant<int, 3>());
         };
         constexpr int D = d;
         if constexpr (D <= 128) groups(std::integral_constant<int, 1>());

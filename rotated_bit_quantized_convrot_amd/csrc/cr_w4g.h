@@ -223,6 +223,10 @@ __device__ __forceinline__ void w4g_mac(int g, const W4gUnit<GPU> (&w)[NT], cons
     }
 }
 
+// This wave's number in its block, in a scalar register: what follows from it
+// (loop bounds, addresses) is then known to be the same in all lanes.
+__device__ __forceinline__ int wave_of_block() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
+
 // 8 values of T.
 template <class T>
 __device__ __forceinline__ void w4g_values(const uint16_t* p, float (&v)[8]) {
