@@ -266,10 +266,6 @@ __device__ __forceinline__ void kv4_finish(float (&x)[D / 64], float total, int 
     for (int i = 0; i < D / 64; ++i) y[lane * (D / 64) + i] = T::from_f32(x[i]);
 }
 
-// Nothing is moved across it: made ahead, operands and scales would take
-// registers that there are not.
-#define KEEP_ORDER() __builtin_amdgcn_sched_barrier(0)
-
 // LO: q needs its second part (rotated, or fp16's 11 bits).
 template <class T, int D, int NG, int RT, bool LO, int W>
 __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_attn_kv4(Kv4 c, AttnArgs a, int slots, float* parts) {
@@ -452,7 +448,14 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_attn_kv4(Kv4 c, At
         float s[RT][16];
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-            KEEP_ORDER();
+            // one tile's sums at a time: made side by side, all 16 would take registers that there are not
+            if (NG * RT > 1 && x > 0) {
+#pragma unroll
+                for (int t = 0; t < RT; ++t)
+                    asm volatile("" : "+v"(s[t][4 * x - 4]), "+v"(s[t][4 * x - 3]), "+v"(s[t][4 * x - 2]), "+v"(s[t][4 * x - 1]));
+#pragma unroll
+                for (int k = 0; k < KS; ++k) asm volatile("" : "+v"(kc[x][k]));
+            }
 #pragma unroll
             for (int n = 0; n < NG; ++n) {
                 const f32x4 sc = *reinterpret_cast<const f32x4*>(&stage.ks[n][16 * quad + 4 * x]);
@@ -527,7 +530,12 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_attn_kv4(Kv4 c, At
         for (int n = 0; n < NG; ++n) {
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                KEEP_ORDER();
+                if constexpr (NG * RT > 1) {   // as above
+#pragma unroll
+                    for (int t = 0; t < RT; ++t)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) asm volatile("" : "+v"(s[t][8 * u + i]));
+                }
                 // weights times scales, in V's order of tokens, and the operand 1 + z / 16
                 const f32x4 sc[2] = {*reinterpret_cast<const f32x4*>(&stage.vs[n][16 * quad + 8 * u]),
                                      *reinterpret_cast<const f32x4*>(&stage.vs[n][16 * quad + 8 * u + 4])};
@@ -549,6 +557,10 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_attn_kv4(Kv4 c, At
                         hi[t][j] = h;
                         lo[t][j] = l;
                     }
+                }
+                if constexpr (NG * RT > 1) {
+#pragma unroll
+                    for (int t = 0; t < RT; ++t) asm volatile("" : "+v"(hi[t]), "+v"(lo[t]));
                 }
 #pragma unroll
                 for (int t = 0; t < RT; ++t) {
