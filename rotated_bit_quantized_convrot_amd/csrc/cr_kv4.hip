@@ -271,7 +271,7 @@ template <class T, int D, int NG, int RT, bool LO, int W>
 __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_attn_kv4(Kv4 c, AttnArgs a, int slots, float* parts) {
     constexpr int KS = D / 32, SPG = KS / NG, DT = D / 16, DPG = DT / NG;
     constexpr float kMove = 8.0f;   // the maximum follows when weights would pass 2^8
-    constexpr int kRow = lds_row<D>();
+    constexpr int kRow = lds_row<D>(), DEPTH = RT == 1 && (D == 64 || (D == 128 && NG <= 2)) ? 2 : 1;
     // the waves' scales of a step; then their sums of a tile
     extern __shared__ __align__(16) uint32_t lds[];
     static_assert(W * sizeof(Stage<NG>) <= 4 * lds_words<D, W>(), "a step's scales fit where the sums go");
@@ -293,36 +293,43 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_attn_kv4(Kv4 c, At
     const uint32_t* words_k = c.scales + kv4_scales_at(c, 0, 0, g);
     const uint32_t* words_v = c.scales + kv4_scales_at(c, 0, 1, g);
 
-    u32x4 vc[DT / 2];
-    uint32_t kc[4][KS];
-    Words<NG> kw, vw;
+    // steps in flight, each in registers of its own
+    u32x4 vc[DEPTH][DT / 2];
+    uint32_t kc[DEPTH][4][KS];
+    Words<NG> kw[DEPTH], vw[DEPTH];
+    int pv[DEPTH];   // pages of tokens 16 quad + 0..15
     // K rows: MFMA row m of tile (u, j) is token 16 (m / 4) + 8 u + 4 j + m % 4, so that a lane's four results are
     // tokens 16 quad + 8 u + 4 j + 0..3
-    auto load_k = [&](int pos, int page_k, int page_w) {
+    auto load_k = [&](int at, int pos, int page_k, int page_w) {
         const int row = ((pos + 16 * (col >> 2)) & S1) + (col & 3);
         const uint8_t* p = codes_k + (size_t)(page_k < 0 ? 0 : page_k) * code_page + kv4_k_byte(D, row, quad * KS);
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
             const Words<KS> v = *reinterpret_cast<const Words<KS>*>(__builtin_assume_aligned(p + x * 4 * (D / 2), KS >= 4 ? 16 : 8));
 #pragma unroll
-            for (int s = 0; s < KS; ++s) kc[x][s] = v.w[s];
+            for (int s = 0; s < KS; ++s) kc[at][x][s] = v.w[s];
         }
-        kw = *reinterpret_cast<const Words<NG>*>(__builtin_assume_aligned(
+        kw[at] = *reinterpret_cast<const Words<NG>*>(__builtin_assume_aligned(
             words_k + (size_t)(page_w < 0 ? 0 : page_w) * word_page + ((pos + lane) & S1) * NG, NG >= 4 ? 16 : 4 * NG));
     };
-    auto load_v = [&](int pos, int page) {
+    auto load_v = [&](int at, int pos, int page) {
         const size_t p = (size_t)(page < 0 ? 0 : page);
         const uint8_t* q = codes_v + p * code_page + kv4_v_byte(D, (pos + 16 * quad) & S1, col);
 #pragma unroll
-        for (int e = 0; e < DT / 2; ++e) vc[e] = *reinterpret_cast<const u32x4*>(q + 256 * e);
-        vw = *reinterpret_cast<const Words<NG>*>(__builtin_assume_aligned(
+        for (int e = 0; e < DT / 2; ++e) vc[at][e] = *reinterpret_cast<const u32x4*>(q + 256 * e);
+        vw[at] = *reinterpret_cast<const Words<NG>*>(__builtin_assume_aligned(
             words_v + p * word_page + ((pos + lane) & S1) * NG, NG >= 4 ? 16 : 4 * NG));
     };
     const Mantissa man = mantissa();
     constexpr int kStride = W * kStep;
     int pos = begin + wave * kStep;
-    int page_k = page_at(pos + 16 * (col >> 2)), page_v = page_at(pos + 16 * quad);
-    int next_k = page_at(pos + kStride + 16 * (col >> 2)), next_v = page_at(pos + kStride + 16 * quad);
+    int pk[DEPTH];
+#pragma unroll
+    for (int i = 0; i < DEPTH; ++i) {
+        pk[i] = page_at(pos + i * kStride + 16 * (col >> 2));
+        pv[i] = page_at(pos + i * kStride + 16 * quad);
+    }
+    int next_k = page_at(pos + DEPTH * kStride + 16 * (col >> 2)), next_v = page_at(pos + DEPTH * kStride + 16 * quad);
     // rows of the tiles: what they see, and q
     int seen[RT];
     u32x4 qh[RT][KS], ql[RT][LO ? KS : 1];
@@ -336,10 +343,12 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_attn_kv4(Kv4 c, At
 #pragma unroll
         for (int s = 0; s < KS; ++s) qh[t][s] = *reinterpret_cast<const u32x4*>(p + 32 * s);
     }
-    if (pos < end) {
-        load_k(pos, page_k, page_v);
-        load_v(pos, page_v);
-    }
+#pragma unroll
+    for (int i = 0; i < DEPTH; ++i)
+        if (pos + i * kStride < end) {
+            load_k(i, pos + i * kStride, pk[i], pv[i]);
+            load_v(i, pos + i * kStride, pv[i]);
+        }
     float qs[RT][NG];
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
@@ -417,6 +426,7 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_attn_kv4(Kv4 c, At
     }
 
     f32x4 o[RT][DT] = {}, zp[RT][NG] = {};   // zp: sums of weights times 1 + z / 16
+    uint32_t poison[RT] = {};                // bit n: group n of V is NaN
     float top[RT], sum[RT];
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
@@ -427,18 +437,22 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_attn_kv4(Kv4 c, At
     const float cs = 16.0f * (a.scale == 0.0f ? 1e-30f : fabsf(a.scale) * 1.4426950408889634f);
 
     Stage<NG>& stage = reinterpret_cast<Stage<NG>*>(lds)[wave];
-    for (; pos < end; pos += kStride) {
+    auto step = [&](auto slot) {
+        constexpr int at = slot;
         // scales and 1 + z / 16 through LDS: a token's own lane has them, its 16 lanes need them; of tokens that are
         // not there, zeros
+        uint64_t nans[NG];   // tokens whose V is NaN
         {
-            const bool there = pos + lane < end && page_v >= 0;
+            const bool there = pos + lane < end && pv[at] >= 0;
             const int place = (lane & ~7) | (lane & 4) | (lane & 1) << 1 | (lane >> 1 & 1);   // 0 2, 1 3, 4 6, 5 7
 #pragma unroll
             for (int n = 0; n < NG; ++n) {
-                const uint32_t k = there ? kw.w[n] : 0, v = there ? vw.w[n] : 0;
+                const uint32_t k = there ? kw[at].w[n] : 0, v = there ? vw[at].w[n] : 0;
                 stage.ks[n][lane] = __uint_as_float(k & ~15u);
                 stage.kz[n][lane] = __uint_as_float((k & 15u) << 19 | 0x3F800000u);
-                stage.vs[n][lane] = __uint_as_float(v & ~15u);
+                const bool nan = (v & 0x7F800000u) == 0x7F800000u;
+                nans[n] = __ballot(nan);
+                stage.vs[n][lane] = nan ? 0.0f : __uint_as_float(v & ~15u);
                 stage.vz[n][place] = (uint16_t)((v & 15u) << 3 | 0x3F80u);
             }
             __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
@@ -454,7 +468,7 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_attn_kv4(Kv4 c, At
                 for (int t = 0; t < RT; ++t)
                     asm volatile("" : "+v"(s[t][4 * x - 4]), "+v"(s[t][4 * x - 3]), "+v"(s[t][4 * x - 2]), "+v"(s[t][4 * x - 1]));
 #pragma unroll
-                for (int k = 0; k < KS; ++k) asm volatile("" : "+v"(kc[x][k]));
+                for (int k = 0; k < KS; ++k) asm volatile("" : "+v"(kc[at][x][k]));
             }
 #pragma unroll
             for (int n = 0; n < NG; ++n) {
@@ -463,7 +477,7 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_attn_kv4(Kv4 c, At
                 f32x4 acc[RT] = {};
 #pragma unroll
                 for (int k = n * SPG; k < (n + 1) * SPG; ++k) {
-                    const u32x4 op = kv4_operand(man, kc[x][k]);
+                    const u32x4 op = kv4_operand(man, kc[at][x][k]);
 #pragma unroll
                     for (int t = 0; t < RT; ++t) {
                         acc[t] = Bf16::mfma(op, qh[t][k], acc[t]);
@@ -479,19 +493,18 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_attn_kv4(Kv4 c, At
                     }
             }
         }
-        // the next step's K while this one's weights and V are at work
-        const int page_w = page_v;
-        page_k = next_k;
-        const int ahead = pos + kStride, ahead2 = pos + 2 * kStride, page_n = next_v;
-        load_k(ahead, page_k, page_n);
-        next_k = page_at(ahead2 + 16 * (col >> 2));
-        next_v = page_at(ahead2 + 16 * quad);
+        // a later step's K while this one's weights and V are at work
+        const int page = pv[at], ahead = pos + DEPTH * kStride;
+        if (ahead < end) load_k(at, ahead, next_k, next_v);
+        pv[at] = next_v;
+        next_k = page_at(ahead + kStride + 16 * (col >> 2));
+        next_v = page_at(ahead + kStride + 16 * quad);
 
         int lim[RT];
         bool cut = false;
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
-            lim[t] = page_w < 0 ? 0 : min(seen[t], end) - pos - 16 * quad;
+            lim[t] = page < 0 ? 0 : min(seen[t], end) - pos - 16 * quad;
             cut |= lim[t] < 16;
         }
         const bool masked = __any(cut);
@@ -501,7 +514,18 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_attn_kv4(Kv4 c, At
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
                     if (i >= lim[t]) s[t][i] = -__builtin_inff();
+            asm volatile("");   // a branch, not 32 instructions of every step
         }
+        // rows that see a token whose V is NaN: their sums are made NaN at the end (0 times it would reach the others)
+#pragma unroll
+        for (int n = 0; n < NG; ++n)
+            if (nans[n] != 0) {
+#pragma unroll
+                for (int t = 0; t < RT; ++t) {
+                    const uint32_t visible = lim[t] >= 16 ? 0xFFFFu : lim[t] > 0 ? (1u << lim[t]) - 1 : 0u;
+                    if ((uint32_t)(nans[n] >> (16 * quad)) & visible) poison[t] |= 1u << n;
+                }
+            }
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
             float m = s[t][0];
@@ -547,11 +571,7 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_attn_kv4(Kv4 c, At
                     const float s0 = sc[j / 2][j % 2], s1 = sc[j / 2][j % 2 + 2];
 #pragma unroll
                     for (int t = 0; t < RT; ++t) {
-                        float x0 = s[t][8 * u + t0] * s0, x1 = s[t][8 * u + t1] * s1;
-                        if (masked) {
-                            x0 = 8 * u + t0 < lim[t] ? x0 : 0.0f;
-                            x1 = 8 * u + t1 < lim[t] ? x1 : 0.0f;
-                        }
+                        const float x0 = s[t][8 * u + t0] * s0, x1 = s[t][8 * u + t1] * s1;
                         uint32_t h, l;
                         split2(x0, x1, &h, &l);
                         hi[t][j] = h;
@@ -569,8 +589,8 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_attn_kv4(Kv4 c, At
                 }
 #pragma unroll
                 for (int d = n * DPG; d < (n + 1) * DPG; ++d) {
-                    const u32x4 op = d % 2 ? kv4_v_operand<true>(man, vc[d / 2][2 * u], vc[d / 2][2 * u + 1])
-                                           : kv4_v_operand<false>(man, vc[d / 2][2 * u], vc[d / 2][2 * u + 1]);
+                    const u32x4 op = d % 2 ? kv4_v_operand<true>(man, vc[at][d / 2][2 * u], vc[at][d / 2][2 * u + 1])
+                                           : kv4_v_operand<false>(man, vc[at][d / 2][2 * u], vc[at][d / 2][2 * u + 1]);
 #pragma unroll
                     for (int t = 0; t < RT; ++t) {
                         o[t][d] = Bf16::mfma(op, hi[t], o[t][d]);
@@ -579,10 +599,17 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_attn_kv4(Kv4 c, At
                 }
             }
         }
-        load_v(ahead, page_n);
-        page_v = page_n;
+        if (ahead < end) load_v(at, ahead, pv[at]);
+        pos += kStride;
         __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
         __builtin_amdgcn_wave_barrier();
+    };
+    while (pos < end) {
+        step(std::integral_constant<int, 0>());
+        if constexpr (DEPTH == 2) {
+            if (pos >= end) break;
+            step(std::integral_constant<int, 1>());
+        }
     }
 
     // the waves' results joined: rows of the tile, wave by wave
@@ -592,6 +619,8 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_attn_kv4(Kv4 c, At
     for (int t = 0; t < RT; ++t) {
         sum[t] += __shfl_xor(sum[t], 16);
         sum[t] += __shfl_xor(sum[t], 32);
+        poison[t] |= __shfl_xor(poison[t], 16);
+        poison[t] |= __shfl_xor(poison[t], 32);
         __syncthreads();   // the words, or the last tile's rows, were read
         if (quad == 0) {
             lds_top[wave][col] = top[t];
@@ -601,7 +630,8 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_attn_kv4(Kv4 c, At
         for (int d = 0; d < DT; ++d) {
             f32x4 v;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = 16.0f * (o[t][d][i] - zp[t][d / DPG][i]);
+            for (int i = 0; i < 4; ++i)
+                v[i] = poison[t] >> (d / DPG) & 1 ? __uint_as_float(kKv4Nan) : 16.0f * (o[t][d][i] - zp[t][d / DPG][i]);
             *reinterpret_cast<f32x4*>(lds_o + (wave * 16 + col) * kRow + 16 * d + 4 * quad) = v;
         }
         __syncthreads();
