@@ -18,6 +18,17 @@ namespace {
 template <int D>
 constexpr float kv4_norm() { return D == 64 ? 0.125f : D == 128 ? 0.08838834764831845f : 0.0625f; }
 
+template <int M, int N>
+__device__ __forceinline__ void rotate_lanes(float (&x)[N], int lane) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        float p;
+        if constexpr (M == 32) p = __shfl_xor(x[i], 32);
+        else p = lane_xor<M>(x[i]);
+        x[i] = (lane & M) ? p - x[i] : x[i] + p;
+    }
+}
+
 // Lane l holds d = l D / 64 and on.
 template <int D>
 __device__ __forceinline__ void rotate_head(float (&x)[D / 64]) {
@@ -32,13 +43,12 @@ __device__ __forceinline__ void rotate_head(float (&x)[D / 64]) {
                 x[i] = a + b;
                 x[i + h] = a - b;
             }
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1)
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const float p = __shfl_xor(x[i], m);
-            x[i] = (lane & m) ? p - x[i] : x[i] + p;
-        }
+    rotate_lanes<1>(x, lane);
+    rotate_lanes<2>(x, lane);
+    rotate_lanes<4>(x, lane);
+    rotate_lanes<8>(x, lane);
+    rotate_lanes<16>(x, lane);
+    rotate_lanes<32>(x, lane);
 #pragma unroll
     for (int i = 0; i < N; ++i) x[i] *= kv4_norm<D>();
 }
@@ -149,33 +159,40 @@ __device__ __forceinline__ int add_ints(int a, int b) { return a + b; }
 __device__ __forceinline__ int add_floats(int a, int b) { return __float_as_int(__int_as_float(a) + __int_as_float(b)); }
 
 // The work of block `index` of `slots` (by_tile: of tile group `index`, its
-// chunk 0).  The span is the shortest, from kMinSpan on, with which all spans
-// of all tile groups have a slot; slots = 0: one span takes everything.  Every
-// wave counts for itself, 64 sequences at a time.
+// chunk 0).  Every wave counts for itself, 64 sequences at a time.
+//   `fill` blocks of a head run at once.  A block's start and end cost as much
+// as some 500 tokens, so the spans are the shortest with which all blocks run
+// at once, up to twice fill's share; then at most fill / 2 blocks more than
+// tile groups are needed, which is what the grid has.  A sequence's spans are
+// equal.  slots = 0: one span takes everything.
 template <int RT>
-__device__ __forceinline__ bool kv4_work(const Kv4& c, int G, int slots, bool by_tile, int index, Kv4Work* w) {
+__device__ __forceinline__ bool kv4_work(const Kv4& c, int G, int slots, int fill, bool by_tile, int index, Kv4Work* w) {
     const int lane = threadIdx.x & 63;
-    auto groups_of = [&](const Kv4Seq& s) { return (int)(((long long)s.rows * G + 16 * RT - 1) / (16 * RT)); };
-    Kv4Seq first = kv4_seq(c, min(lane, c.B - 1));
+    auto groups_of = [&](const Kv4Seq& s) { return (s.rows * G + 16 * RT - 1) / (16 * RT); };   // rows * G <= 2^30
+    const Kv4Seq first = kv4_seq(c, min(lane, c.B - 1));
     int span = 0x40000000;
     if (slots > 0) {
-        int groups = 0;
         float total = 0.0f;   // of tokens, group by group
         for (int b0 = 0; b0 < c.B; b0 += 64) {
             const Kv4Seq s = b0 == 0 ? first : kv4_seq(c, min(b0 + lane, c.B - 1));
             const int n = b0 + lane < c.B ? groups_of(s) : 0;
-            groups += __builtin_amdgcn_readlane(wave_scan(n, add_ints), 63);
             total += __int_as_float(__builtin_amdgcn_readlane(wave_scan(__float_as_int((float)n * (float)s.tokens), add_floats), 63));
         }
-        // the grid has two slots a group, so that some are left; a little more than the sum, which is rounded
-        const float left = (float)max(slots - groups, 1), e = total * 1.0001f / left;
-        span = e < (float)kMinSpan ? kMinSpan : ((int)fminf(e, 1073741824.0f) / kMinSpan + 1) * kMinSpan;
+        const int n = lane < c.B ? groups_of(first) : 0;
+        for (int f = 8; f <= 16; f += f < 10 ? 1 : f < 12 ? 2 : 4) {   // 8, 9, 10, 12, 16 eighths
+            const float e = fminf(total * (float)f / (8.0f * (float)fill), 1073741824.0f);
+            // (the sum is rounded: a little more than it where that could cost a slot)
+            span = ((int)(f == 16 ? e * 1.0001f + 1.0f : e) + kMinSpan - 1) / kMinSpan * kMinSpan;
+            span = max(span, kMinSpan);
+            if (c.B > 64) continue;
+            if (__builtin_amdgcn_readlane(wave_scan(n * max((first.tokens + span - 1) / span, 1), add_ints), 63) <= fill) break;
+        }
     }
     int at = 0, slot = 0;
     for (int b0 = 0; b0 < c.B; b0 += 64) {
         const Kv4Seq s = b0 == 0 ? first : kv4_seq(c, min(b0 + lane, c.B - 1));
         const int n = b0 + lane < c.B ? groups_of(s) : 0;
-        const int chunks = s.tokens > span ? (s.tokens + span - 1) / span : 1;
+        const int chunks = max((s.tokens + span - 1) / span, 1);
         const int tiles = wave_scan(n, add_ints), all = wave_scan(n * chunks, add_ints);
         const uint64_t after = __ballot((by_tile ? at + tiles : slot + all) > index);
         if (after) {
@@ -186,7 +203,7 @@ __device__ __forceinline__ bool kv4_work(const Kv4& c, int G, int slots, bool by
             w->rows = of(s.rows);
             w->tokens = of(s.tokens);
             w->chunks = of(chunks);
-            w->span = span;
+            w->span = ((w->tokens + w->chunks - 1) / w->chunks + kMinSpan - 1) / kMinSpan * kMinSpan;
             const int before = slot + of(all - n * chunks);
             if (by_tile) {
                 w->tile = index - at - of(tiles - n);
@@ -268,7 +285,7 @@ __device__ __forceinline__ void kv4_finish(float (&x)[D / 64], float total, int 
 
 // LO: q needs its second part (rotated, or fp16's 11 bits).
 template <class T, int D, int NG, int RT, bool LO, int W>
-__global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_attn_kv4(Kv4 c, AttnArgs a, int slots, float* parts) {
+__global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_attn_kv4(Kv4 c, AttnArgs a, int slots, int fill, float* parts) {
     constexpr int KS = D / 32, SPG = KS / NG, DT = D / 16, DPG = DT / NG;
     constexpr float kMove = 8.0f;   // the maximum follows when weights would pass 2^8
     constexpr int kRow = lds_row<D>(), DEPTH = RT == 1 && (D == 64 || (D == 128 && NG <= 2)) ? 2 : 1;
@@ -280,7 +297,7 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_attn_kv4(Kv4 c, At
     const int lane = threadIdx.x & 63, wave = wave_of_block(), col = lane & 15, quad = lane >> 4;
     const int g = blockIdx.x, G = a.Hq / c.heads;
     Kv4Work w;
-    if (!kv4_work<RT>(c, G, slots, false, blockIdx.y + blockIdx.z * gridDim.y, &w)) return;
+    if (!kv4_work<RT>(c, G, slots, fill, false, blockIdx.y + blockIdx.z * gridDim.y, &w)) return;
     const int begin = w.chunk * w.span, end = min(begin + w.span, w.tokens);
 
     // page of the 16 tokens from `pos` on, -1 past the end
@@ -336,8 +353,7 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_attn_kv4(Kv4 c, At
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
         // a column past the last row repeats it
-        const long long r = min((long long)(w.tile * RT + t) * 16 + col, (long long)w.rows * G - 1);
-        const int i = (int)(r / G), h = g * G + (int)(r % G);
+        const int r = min((w.tile * RT + t) * 16 + col, w.rows * G - 1), i = r / G, h = g * G + r % G;
         seen[t] = w.tokens - w.rows + i + 1;
         const uint16_t* p = a.q + (w.first + i) * a.q_row + h * a.q_head + 8 * quad;
 #pragma unroll
@@ -349,57 +365,59 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_attn_kv4(Kv4 c, At
             load_k(i, pos + i * kStride, pk[i], pv[i]);
             load_v(i, pos + i * kStride, pv[i]);
         }
+    // The Hadamard matrix as an operand: (-1)^popcount(d & d'), row m of tile u for d' = 32 (u / 2) + 8 (m / 4) +
+    // 4 (u % 2) + m % 4, so that a lane's results are the d' = 32 s + 8 quad + 0..7 that it needs; here the bits of
+    // d = 8 quad + j and of d' below 32.
+    u32x4 hadamard[2];
+    if (LO && c.rotate) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint32_t v = 0x3F803F80u;
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+                    v ^= (uint32_t)((__popc((2 * j + x) & (4 * u + (col & 3))) ^ __popc(quad & (col >> 2))) & 1) << (15 + 16 * x);
+                hadamard[u][j] = v;
+            }
+    }
     float qs[RT][NG];
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
         float x[KS][8];
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
+            if (a.scale < 0.0f) qh[t][s] ^= 0x80008000u;   // its sign goes to q
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 x[s][2 * j] = T::to_f32(qh[t][s][j] & 0xFFFFu);
                 x[s][2 * j + 1] = T::to_f32(qh[t][s][j] >> 16);
             }
-            if (a.scale < 0.0f)   // its sign goes to q
-#pragma unroll
-                for (int j = 0; j < 8; ++j) x[s][j] = -x[s][j];
         }
         if (LO && c.rotate) {
-            // d = 32 s + 8 quad + j: strides 1, 2, 4 among j, 8, 16 among quads, 32 .. among s
-#pragma unroll
-            for (int s = 0; s < KS; ++s) {
-#pragma unroll
-                for (int m = 1; m < 8; m <<= 1)
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        if ((j & m) == 0) {
-                            const float u = x[s][j], v = x[s][j + m];
-                            x[s][j] = u + v;
-                            x[s][j + m] = u - v;
-                        }
-#pragma unroll
-                for (int m = 16; m < 64; m <<= 1)
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float v = __shfl_xor(x[s][j], m);
-                        x[s][j] = (lane & m) ? v - x[s][j] : x[s][j] + v;
-                    }
-            }
-#pragma unroll
-            for (int m = 1; m < KS; m <<= 1)
-#pragma unroll
-                for (int s = 0; s < KS; ++s)
-                    if ((s & m) == 0)
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const float u = x[s][j], v = x[s + m][j];
-                            x[s][j] = u + v;
-                            x[s + m][j] = u - v;
-                        }
+            u32x4 part[2][KS];
 #pragma unroll
             for (int s = 0; s < KS; ++s)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) x[s][j] *= kv4_norm<D>();
+                for (int j = 0; j < 4; ++j) {
+                    uint32_t hi, lo;
+                    split2(x[s][2 * j], x[s][2 * j + 1], &hi, &lo);
+                    part[0][s][j] = hi;
+                    part[1][s][j] = lo;
+                }
+#pragma unroll
+            for (int u = 0; u < DT; ++u) {
+                f32x4 acc = {0, 0, 0, 0};
+#pragma unroll
+                for (int s = 0; s < KS; ++s) {
+                    const u32x4 sign = __builtin_popcount(s & (u / 2)) & 1 ? hadamard[u % 2] ^ 0x80008000u : hadamard[u % 2];
+                    acc = Bf16::mfma(sign, part[0][s], acc);
+                    // (fp16's second parts are exact, bf16 has none)
+                    if constexpr (std::is_same_v<T, Fp16>) acc = Bf16::mfma(sign, part[1][s], acc);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[u / 2][4 * (u % 2) + j] = acc[j] * kv4_norm<D>();
+            }
         }
         // the sums of what the operands hold, group by group
 #pragma unroll
@@ -635,8 +653,7 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_attn_kv4(Kv4 c, At
             *reinterpret_cast<f32x4*>(lds_o + (wave * 16 + col) * kRow + 16 * d + 4 * quad) = v;
         }
         __syncthreads();
-        const long long r0 = (long long)(w.tile * RT + t) * 16;
-        const int n = (int)min(16ll, (long long)w.rows * G - r0);
+        const int r0 = (w.tile * RT + t) * 16, n = min(16, w.rows * G - r0);
         for (int r = wave; r < n; r += W) {
             float m = lds_top[0][r], total = 0.0f, x[D / 64] = {};
 #pragma unroll
@@ -652,7 +669,7 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_attn_kv4(Kv4 c, At
                     x[i] = __builtin_fmaf(f, lds_o[(k * 16 + r) * kRow + lane * (D / 64) + i], x[i]);
             }
             if (whole) {
-                const int i0 = (int)((r0 + r) / G), h = g * G + (int)((r0 + r) % G);
+                const int i0 = (r0 + r) / G, h = g * G + (r0 + r) % G;
                 kv4_finish<T, D>(x, total, c.rotate, a.y + ((int64_t)(w.first + i0) * a.Hq + h) * D);
             } else {
                 float* p = part + (16 * t + r) * D + lane * (D / 64);
@@ -671,7 +688,7 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_attn_kv4(Kv4 c, At
 // fourth span, 16 at a time, so that few loads wait for each other.
 constexpr int kJoinWaves = 4;
 template <class T, int D, int RT>
-__global__ __launch_bounds__(64 * kJoinWaves) void k_attn_kv4_join(Kv4 c, AttnArgs a, int slots, int row_blocks,
+__global__ __launch_bounds__(64 * kJoinWaves) void k_attn_kv4_join(Kv4 c, AttnArgs a, int slots, int fill, int row_blocks,
                                                                    const float* parts) {
     constexpr int N = D / 64, R = 16 * RT, W = kJoinWaves;
     constexpr size_t P = part_words<D, RT>();
@@ -679,9 +696,8 @@ __global__ __launch_bounds__(64 * kJoinWaves) void k_attn_kv4_join(Kv4 c, AttnAr
     const int lane = threadIdx.x & 63, wave = wave_of_block();
     const int g = blockIdx.x / row_blocks, G = a.Hq / c.heads;
     Kv4Work w;
-    if (!kv4_work<RT>(c, G, slots, true, blockIdx.y + blockIdx.z * gridDim.y, &w) || w.chunks == 1) return;
-    const long long r0 = (long long)w.tile * R;
-    const int n = (int)min((long long)R, (long long)w.rows * G - r0);
+    if (!kv4_work<RT>(c, G, slots, fill, true, blockIdx.y + blockIdx.z * gridDim.y, &w) || w.chunks == 1) return;
+    const int r0 = w.tile * R, n = min(R, w.rows * G - r0);
     const float* part = parts + ((size_t)g * slots + w.slot) * P;
     for (int r = blockIdx.x % row_blocks; r < n; r += row_blocks) {
         float m = -__builtin_inff(), total = 0.0f, x[N] = {};
@@ -735,7 +751,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void k_attn_kv4_join(Kv4 c, AttnAr
 #pragma unroll
                 for (int d = 0; d < N; ++d) x[d] = __builtin_fmaf(f, lds_x[k][lane * N + d], x[d]);
             }
-            const int i0 = (int)((r0 + r) / G), h = g * G + (int)((r0 + r) % G);
+            const int i0 = (r0 + r) / G, h = g * G + (r0 + r) % G;
             kv4_finish<T, D>(x, total, c.rotate, a.y + ((int64_t)(w.first + i0) * a.Hq + h) * D);
         }
         __syncthreads();
@@ -764,15 +780,15 @@ hipError_t launch_kv4_append(bool fp16, const uint16_t* k, int64_t k_row, int64_
 
 namespace {
 
-// Rows a block takes, in tiles of 16, the tile groups that there can be, and
-// the blocks a head gets: spans for all CUs twice, two a tile group at least
-// (so that every group's last, shorter span has one), none where no sequence
-// is worth a second span.
+// Rows a block takes, in tiles of 16; the tile groups that there can be; the
+// blocks of a head that the chip runs at once (two a CU, one where a wave takes
+// the registers of two) and those that the grid has; none where no sequence is
+// worth a second span.
 // Tokens up to which one block takes a sequence, with twice the waves: two
 // turns of them.
 constexpr int kOneSpan = 1024;
 struct Grid {
-    int tiles, groups, slots;
+    int tiles, groups, slots, fill;
 };
 Grid attn_kv4_grid(int T, int G, int heads, int dim, int page, int width, int B) {
     Grid g;
@@ -780,10 +796,11 @@ Grid attn_kv4_grid(int T, int G, int heads, int dim, int page, int width, int B)
     const int64_t rows = ((int64_t)T * G + B - 1) / B;   // of a sequence, on average
     g.tiles = rows > 16 * most ? most : (int)(rows + 15) / 16;
     g.groups = (int)(((int64_t)T * G + (int64_t)(B < T ? B : T) * (16 * g.tiles - 1)) / (16 * g.tiles));
-    g.slots = 0;
+    g.slots = g.fill = 0;
     if ((int64_t)width * page > kOneSpan) {
-        const int64_t fill = 512 / heads;
-        g.slots = (int)(2 * (int64_t)g.groups > fill ? 2 * (int64_t)g.groups : fill);
+        g.fill = (dim == 256 ? 256 : 512) / heads;
+        if (g.fill < 1) g.fill = 1;
+        g.slots = g.fill / 2 + g.groups + 1 > g.fill ? g.fill / 2 + g.groups + 1 : g.fill;
     }
     return g;
 }
@@ -799,7 +816,7 @@ hipError_t run_attn_kv4(const AttnArgs& a, const Kv4& c, const Grid& g, float* w
     hipError_t e = hipSuccess;
     const auto go = [&](auto kernel, std::atomic<uint64_t>& done) {
         if (lds > 65536 && (e = opt_in_lds(reinterpret_cast<const void*>(kernel), lds, done)) != hipSuccess) return;
-        kernel<<<grid(g.slots ? g.slots : g.groups, c.heads), 64 * W, lds, st>>>(c, a, g.slots, ws);
+        kernel<<<grid(g.slots ? g.slots : g.groups, c.heads), 64 * W, lds, st>>>(c, a, g.slots, g.fill, ws);
         e = hipGetLastError();
     };
     static std::atomic<uint64_t> done[2];
@@ -809,7 +826,7 @@ hipError_t run_attn_kv4(const AttnArgs& a, const Kv4& c, const Grid& g, float* w
     // as many blocks as a group has rows on average
     const int64_t rows = ((int64_t)c.T * (a.Hq / c.heads) + g.groups - 1) / g.groups;
     const int row_blocks = (int)(rows < 16 * RT ? rows : 16 * RT);
-    k_attn_kv4_join<T, D, RT><<<grid(g.groups, c.heads * row_blocks), 64 * kJoinWaves, 0, st>>>(c, a, g.slots, row_blocks, ws);
+    k_attn_kv4_join<T, D, RT><<<grid(g.groups, c.heads * row_blocks), 64 * kJoinWaves, 0, st>>>(c, a, g.slots, g.fill, row_blocks, ws);
     return hipGetLastError();
 }
 
