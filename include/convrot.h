@@ -472,7 +472,8 @@ cr_status cr_kv4_append(int dtype, const void* k, int64_t k_row, int64_t k_head,
  * lens[b] - n + i.  A row that sees none gives zeros.  With the cache's
  * rotation q is rotated and the output turned back.
  *   ws / ws_bytes: at least cr_attn_kv4_workspace_bytes(...); calls that can
- *   run at the same time need a workspace each.  Nothing is kept in it.
+ *   run at the same time need a workspace each.  Nothing is kept in it.  Where
+ *   the size is 256 (a table of up to 1024 tokens) none is used: ws may be NULL.
  * Every sum has a fixed order: the same call gives the same bits. */
 size_t cr_attn_kv4_workspace_bytes(int T, int Hq, const cr_kv4* cache, int width, int B);
 

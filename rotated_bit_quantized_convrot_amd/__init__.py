@@ -728,7 +728,7 @@ def _heads(t: torch.Tensor, name: str, dtype, device):
     """t is [T, heads, dim] of this type on this device, a head's values side
     by side: (pointer, stride of a token, stride of a head)."""
     if t.dtype is not dtype or t.device != device or not t.is_cuda:
-        raise ValueError(f"{name} must be {dtype} on {device}, got {t.dtype} on {t.device}")
+        raise ValueError(f"{name} must be {dtype} on {device}, a GPU, got {t.dtype} on {t.device}")
     if t.dim() != 3:
         raise ValueError(f"{name} must be [T, heads, dim]")
     (n, heads, dim), (row, head, one) = t.shape, t.stride()
@@ -752,7 +752,7 @@ def _sequences(cu: torch.Tensor, device) -> int:
 
 def _attn_out(out, q):
     if out is None:
-        return torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        return q.new_empty(q.shape)
     _here(out, "out", q.dtype, q.device)
     if out.shape != q.shape:
         raise ValueError("out must have the shape of q")
@@ -885,14 +885,17 @@ def attn_kv4(q, cache: KV4Cache, table, lens, cu_seqlens, scale=None, out=None, 
         raise ValueError(f"q must be [T, heads, {cache.dim}]")
     B, width = _kv4_call(cache, table, lens, cu_seqlens, device)
     out = _attn_out(out, q)
-    if workspace is None:
-        need = _attn_kv4_workspace(T, Hq, cache.page, cache.heads, D, cache.group, width, B)
-        workspace = torch.empty(need if need > 256 else 256, dtype=torch.uint8, device=device)
-    else:
+    ws, ws_bytes = None, 0
+    if workspace is not None:
         _here(workspace, "workspace", torch.uint8, device)
+    else:
+        need = _attn_kv4_workspace(T, Hq, cache.page, cache.heads, D, cache.group, width, B)
+        if need > 256:   # 256: short tables, none is used
+            workspace = q.new_empty(need, dtype=torch.uint8)
+    if workspace is not None:
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel()
     _call_on(device, lib().cr_attn_kv4, code, qp, qr, qh, T, Hq, cache._at, table.data_ptr(), width, lens.data_ptr(),
-             cu_seqlens.data_ptr(), B, D ** -0.5 if scale is None else scale, out.data_ptr(), workspace.data_ptr(),
-             workspace.numel())
+             cu_seqlens.data_ptr(), B, D ** -0.5 if scale is None else scale, out.data_ptr(), ws, ws_bytes)
     return out
 
 

@@ -988,10 +988,10 @@ cr_status cr_attn_kv4(int dtype, const void* q, int64_t q_row, int64_t q_head, i
     const Heads x{"q", q, q_row, q_head, Hq};
     if ((s = check_heads(x, T, cache->dim)) != CR_OK) return s;
     if ((s = check_kv4_call(cache, table, width, lens, cu)) != CR_OK) return s;
-    if (!y || !ws) return fail(CR_ERR_NULL, "y or workspace is NULL");
+    const size_t need = cr::attn_kv4_workspace(T, Hq, cache->heads, cache->dim, cache->page, width, B);
+    if (!y || (!ws && need)) return fail(CR_ERR_NULL, "y or workspace is NULL");
     if (!aligned16(y) || !aligned16(ws)) return fail(CR_ERR_ALIGN, "y or workspace not 16-byte aligned");
     if ((s = check_apart(x, T, cache->dim, y, (size_t)T * Hq * cache->dim * 2)) != CR_OK) return s;
-    const size_t need = cr_attn_kv4_workspace_bytes(T, Hq, cache, width, B);
     if (ws_bytes < need) return fail(CR_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", ws_bytes, need);
     if ((s = check_device()) != CR_OK) return s;
     cr::AttnArgs a{};

@@ -59,61 +59,183 @@ struct AppendArgs {
     int64_t row[2], head[2];     // their strides in values
 };
 
-// One wave a token, head and K or V.
-template <class T, int D>
-__global__ void k_kv4_append(AppendArgs a) {
-    constexpr int N = D / 64;
-    __shared__ uint8_t code[D];
-    const int t = blockIdx.x, h = blockIdx.y, which = blockIdx.z, lane = threadIdx.x, d = lane * N;
-    int b = 0;
-    Kv4Seq s = {};
-    for (; b < a.c.B; ++b) {
-        s = kv4_seq(a.c, b);
-        if (t >= s.first && t < s.first + s.rows) break;
+// Sums over the lanes up to each, by DPP (row_shr 1, 2, 4, 8, row_bcast 15, 31).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int dpp_or_zero(int v) { return __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false); }
+template <class F>
+__device__ __forceinline__ int wave_scan(int v, F add) {
+    v = add(v, dpp_or_zero<0x111, 0xF>(v));
+    v = add(v, dpp_or_zero<0x112, 0xF>(v));
+    v = add(v, dpp_or_zero<0x114, 0xF>(v));
+    v = add(v, dpp_or_zero<0x118, 0xF>(v));
+    v = add(v, dpp_or_zero<0x142, 0xA>(v));
+    return add(v, dpp_or_zero<0x143, 0xC>(v));
+}
+__device__ __forceinline__ int add_ints(int a, int b) { return a + b; }
+__device__ __forceinline__ int add_floats(int a, int b) { return __float_as_int(__int_as_float(a) + __int_as_float(b)); }
+
+// 16 rows of the cache (of one page) that take new tokens: rows r0 up to r1 of
+// the call's are positions pos0 and on, all in the 16 from pos0 & ~15.
+struct AppendWork {
+    int b, r0, r1, pos0;
+};
+__device__ __forceinline__ bool append_work(const Kv4& c, int index, AppendWork* w) {
+    const int lane = threadIdx.x & 63;
+    for (int b0 = 0; b0 < c.B; b0 += 64) {
+        const Kv4Seq s = kv4_seq(c, min(b0 + lane, c.B - 1));
+        // rows that come before token 0 are left out
+        const int rows = b0 + lane < c.B ? min(s.rows, s.tokens) : 0, from = s.tokens - rows;
+        const int n = rows > 0 ? (s.tokens - 1) / 16 - from / 16 + 1 : 0;
+        const int upto = wave_scan(n, add_ints);
+        const uint64_t after = __ballot(upto > index);
+        if (after) {
+            const int l = __builtin_ctzll(after);
+            auto of = [&](int v) { return __builtin_amdgcn_readlane(v, l); };
+            const int first = of(from), end = of(s.tokens), row = of(s.first + s.rows - rows);
+            const int block = first / 16 + index - of(upto - n), lo = max(first, block * 16), hi = min(end, block * 16 + 16);
+            w->b = b0 + l;
+            w->pos0 = lo;
+            w->r0 = row + (lo - first);
+            w->r1 = w->r0 + (hi - lo);
+            return true;
+        }
+        index -= __builtin_amdgcn_readlane(upto, 63);
     }
-    if (b == a.c.B) return;
-    const int pos = s.tokens - s.rows + (t - s.first);
-    if (pos < 0) return;
-    const int page = kv4_page(a.c, b, pos);
+    return false;
+}
+
+// One wave 16 rows of the cache, a head, K or V; lane 4 t + p holds token t's
+// d = 32 s + 8 p + 0..7: the strides of the rotation are among j (1, 2, 4),
+// among the four lanes (8, 16), among s (32 ..); K's bytes of a lane lie side
+// by side, V's go through LDS to have the 16 tokens of a pair of d side by side.
+// 1220 tokens, 8 heads of 128, rotated: TIME1; bound by the two launches' worth
+// of loads that wait for each other, not by the bytes.
+template <class T, int D, int NG>
+__global__ __launch_bounds__(256) void k_kv4_append(AppendArgs a) {
+    constexpr int KS = D / 32, SPG = KS / NG;
+    __shared__ __align__(16) uint8_t pairs[4][8 * D];
+    const int lane = threadIdx.x & 63, wave = wave_of_block(), t = lane >> 2, p = lane & 3;
+    const int hw = blockIdx.x * 4 + wave;
+    if (hw >= 2 * a.c.heads) return;
+    const int which = hw >= a.c.heads, h = hw - which * a.c.heads;
+    AppendWork w;
+    if (!append_work(a.c, blockIdx.y + blockIdx.z * gridDim.y, &w)) return;
+    const int page = kv4_page(a.c, w.b, w.pos0);
     if (page < 0) return;
-    const uint16_t* p = a.x[which] + t * a.row[which] + h * a.head[which];
-    float x[N];
+    // lanes of rows that take no token repeat the first's or the last's
+    const int base = w.pos0 & ~15, r = min(max(w.r0 + base + t - w.pos0, w.r0), w.r1 - 1);
+    const bool mine = base + t >= w.pos0 && base + t < w.pos0 + (w.r1 - w.r0);
+    const uint16_t* src = a.x[which] + r * a.row[which] + h * a.head[which] + 8 * p;
+    float x[KS][8];
 #pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = T::to_f32(p[d + i]);
-    if (a.c.rotate) rotate_head<D>(x);
-    float lo = 0.0f, hi = 0.0f;
-    int bad = 0;
+    for (int s = 0; s < KS; ++s) w4g_values<T>(src + 32 * s, x[s]);
+    if (a.c.rotate) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        lo = fminf(lo, x[i]);
-        hi = fmaxf(hi, x[i]);
-        bad |= !w4g_finite(x[i]);
+        for (int s = 0; s < KS; ++s) {
+#pragma unroll
+            for (int m = 1; m < 8; m <<= 1)
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if ((j & m) == 0) {
+                        const float u = x[s][j], v = x[s][j + m];
+                        x[s][j] = u + v;
+                        x[s][j + m] = u - v;
+                    }
+            rotate_lanes<1>(x[s], lane);
+            rotate_lanes<2>(x[s], lane);
+        }
+#pragma unroll
+        for (int m = 1; m < KS; m <<= 1)
+#pragma unroll
+            for (int s = 0; s < KS; ++s)
+                if ((s & m) == 0)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float u = x[s][j], v = x[s + m][j];
+                        x[s][j] = u + v;
+                        x[s + m][j] = u - v;
+                    }
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[s][j] *= kv4_norm<D>();
     }
-    for (int m = 1; m < a.c.group / N; m <<= 1) {
-        lo = fminf(lo, __shfl_xor(lo, m));
-        hi = fmaxf(hi, __shfl_xor(hi, m));
-        bad |= __shfl_xor(bad, m);
-    }
-    const uint32_t sb = bad ? kKv4Nan : (__float_as_uint(hi / 15.0f - lo / 15.0f) + 8) & ~15u;
-    const float sc = __uint_as_float(sb);
-    const float z = sc > 0.0f ? fminf(fmaxf(rintf(-lo / sc), 0.0f), 15.0f) : 0.0f;
+    uint32_t word[NG], code[KS];   // code: d + 2 j in bits 4 j, d + 2 j + 1 in bits 16 + 4 j
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-        code[d + i] = sc > 0.0f ? (uint8_t)fminf(fmaxf(rintf(x[i] / sc) + z, 0.0f), 15.0f) : 0;
-    __syncthreads();
-    const int row = pos & ((1 << a.c.page_log2) - 1);
-    uint8_t* out = a.c.codes + kv4_codes_at(a.c, page, which, h);
-    for (int k = lane; k < D / 2; k += 64) {
-        if (which == 0) {
-            const int dw = k >> 2, at = 32 * (dw % (D / 32)) + 8 * (dw / (D / 32)), half = (k >> 1) & 1, j = 2 * (k & 1);
-            out[kv4_k_byte(D, row, 0) + k] = code[at + 2 * j + half] | code[at + 2 * j + 2 + half] << 4;
-        } else {
-            const int at = 32 * (k >> 4) + (k & 15);
-            out[kv4_v_byte(D, row, k)] = code[at] | code[at + 16] << 4;
+    for (int n = 0; n < NG; ++n) {
+        float lo = 0.0f, hi = 0.0f, big = 0.0f;
+#pragma unroll
+        for (int s = n * SPG; s < (n + 1) * SPG; ++s)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                lo = fminf(lo, x[s][j]);
+                hi = fmaxf(hi, x[s][j]);
+                big += x[s][j] - x[s][j];   // NaN from the first infinity or NaN on
+            }
+        lo = fminf(lo, lane_xor<1>(lo));
+        lo = fminf(lo, lane_xor<2>(lo));
+        hi = fmaxf(hi, lane_xor<1>(hi));
+        hi = fmaxf(hi, lane_xor<2>(hi));
+        big += lane_xor<1>(big);
+        big += lane_xor<2>(big);
+        const uint32_t sb = big != big ? kKv4Nan : (__float_as_uint(hi / 15.0f - lo / 15.0f) + 8) & ~15u;
+        const float sc = __uint_as_float(sb);
+        const float z = sc > 0.0f ? fminf(fmaxf(rintf(-lo / sc), 0.0f), 15.0f) : 0.0f;
+        word[n] = sb | (uint32_t)z;
+#pragma unroll
+        for (int s = n * SPG; s < (n + 1) * SPG; ++s) {
+            code[s] = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float q = sc > 0.0f ? fminf(fmaxf(rintf(x[s][j] / sc) + z, 0.0f), 15.0f) : 0.0f;
+                code[s] |= (uint32_t)q << (4 * (j >> 1) + 16 * (j & 1));
+            }
         }
     }
-    if (d % a.c.group == 0)
-        a.c.scales[kv4_scales_at(a.c, page, which, h) + row * (D / a.c.group) + d / a.c.group] = sb | (uint32_t)z;
+    const int row = (base + t) & ((1 << a.c.page_log2) - 1);
+    if (mine) {
+        uint32_t* to = a.c.scales + kv4_scales_at(a.c, page, which, h) + row * NG;
+#pragma unroll
+        for (int n = 0; n < NG; ++n)
+            if ((n & 3) == p) to[n] = word[n];
+    }
+    uint8_t* codes = a.c.codes + kv4_codes_at(a.c, page, which, h);
+    if (which == 0) {
+        if (mine) {
+            uint32_t* to = reinterpret_cast<uint32_t*>(codes + kv4_k_byte(D, row, p * KS));
+            if constexpr (KS == 2) *reinterpret_cast<uint2*>(to) = uint2{code[0], code[1]};
+            else
+#pragma unroll
+                for (int s = 0; s < KS; s += 4)
+                    *reinterpret_cast<u32x4*>(to + s) = u32x4{code[s], code[s + 1], code[s + 2], code[s + 3]};
+        }
+        return;
+    }
+    // pair 16 s + 8 p + j (p < 2): d = 32 s + 8 p + j, and that of lane p + 2
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+        const uint32_t other = (uint32_t)__float_as_int(lane_xor<2>(__uint_as_float(code[s])));
+        if (p < 2)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int sh = 4 * (j >> 1) + 16 * (j & 1);
+                pairs[wave][(16 * s + 8 * p + j) * 16 + t] = (uint8_t)((code[s] >> sh & 15u) | (other >> sh & 15u) << 4);
+            }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    const int row0 = base & ((1 << a.c.page_log2) - 1), from = w.pos0 - base, to = from + (w.r1 - w.r0);
+#pragma unroll
+    for (int i = 0; i < (D / 2 + 63) / 64; ++i) {
+        const int pair = 64 * i + lane;
+        if (pair >= D / 2) break;
+        uint8_t* out = codes + kv4_v_byte(D, row0, pair);
+        const uint8_t* in = &pairs[wave][pair * 16];
+        if (to - from == 16) *reinterpret_cast<u32x4*>(out) = *reinterpret_cast<const u32x4*>(in);
+        else
+            for (int x = from; x < to; ++x) out[x] = in[x];   // the others' bytes are theirs
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -143,21 +265,6 @@ constexpr int max_tiles() { return D == 64 ? 3 : D == 128 ? 2 : 1; }
 struct Kv4Work {
     int b, first, rows, tokens, tile, chunk, chunks, span, slot;
 };
-// Sums over the lanes up to each, by DPP (row_shr 1, 2, 4, 8, row_bcast 15, 31).
-template <int CTRL, int ROWS>
-__device__ __forceinline__ int dpp_or_zero(int v) { return __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false); }
-template <class F>
-__device__ __forceinline__ int wave_scan(int v, F add) {
-    v = add(v, dpp_or_zero<0x111, 0xF>(v));
-    v = add(v, dpp_or_zero<0x112, 0xF>(v));
-    v = add(v, dpp_or_zero<0x114, 0xF>(v));
-    v = add(v, dpp_or_zero<0x118, 0xF>(v));
-    v = add(v, dpp_or_zero<0x142, 0xA>(v));
-    return add(v, dpp_or_zero<0x143, 0xC>(v));
-}
-__device__ __forceinline__ int add_ints(int a, int b) { return a + b; }
-__device__ __forceinline__ int add_floats(int a, int b) { return __float_as_int(__int_as_float(a) + __int_as_float(b)); }
-
 // The work of block `index` of `slots` (by_tile: of tile group `index`, its
 // chunk 0).  Every wave counts for itself, 64 sequences at a time.
 //   `fill` blocks of a head run at once.  A block's start and end cost as much
@@ -758,11 +865,27 @@ __global__ __launch_bounds__(64 * kJoinWaves) void k_attn_kv4_join(Kv4 c, AttnAr
     }
 }
 
+// f(head's size, groups of a head), as constants.
 template <class F>
-void by_dim(int D, F f) {
-    if (D == 64) f(std::integral_constant<int, 64>());
-    if (D == 128) f(std::integral_constant<int, 128>());
-    if (D == 256) f(std::integral_constant<int, 256>());
+void by_form(const Kv4& c, F f) {
+    const auto groups = [&](auto d, auto n) {
+        if (c.dim == d && c.dim / c.group == n) f(d, n);
+    };
+    const std::integral_constant<int, 64> d64;
+    const std::integral_constant<int, 128> d128;
+    const std::integral_constant<int, 256> d256;
+    const std::integral_constant<int, 1> n1;
+    const std::integral_constant<int, 2> n2;
+    const std::integral_constant<int, 4> n4;
+    const std::integral_constant<int, 8> n8;
+    groups(d64, n1);
+    groups(d64, n2);
+    groups(d128, n1);
+    groups(d128, n2);
+    groups(d128, n4);
+    groups(d256, n2);
+    groups(d256, n4);
+    groups(d256, n8);
 }
 
 }  // namespace
@@ -770,10 +893,13 @@ void by_dim(int D, F f) {
 hipError_t launch_kv4_append(bool fp16, const uint16_t* k, int64_t k_row, int64_t k_head, const uint16_t* v,
                              int64_t v_row, int64_t v_head, const Kv4& c, hipStream_t st) {
     const AppendArgs a{c, {k, v}, {k_row, v_row}, {k_head, v_head}};
-    const dim3 grid(c.T, c.heads, 2);
-    by_dim(c.dim, [&](auto d) {
-        if (fp16) k_kv4_append<Fp16, d><<<grid, 64, 0, st>>>(a);
-        else k_kv4_append<Bf16, d><<<grid, 64, 0, st>>>(a);
+    // groups of 16 rows that B sequences' T tokens can lie in
+    const int64_t n = ((int64_t)c.T + 30 * (int64_t)(c.B < c.T ? c.B : c.T)) / 16;
+    const int y = (int)(n < 32768 ? n : 32768);
+    const dim3 grid((2 * c.heads + 3) / 4, y, (unsigned)((n + y - 1) / y));
+    by_form(c, [&](auto d, auto ng) {
+        if (fp16) k_kv4_append<Fp16, d, ng><<<grid, 256, 0, st>>>(a);
+        else k_kv4_append<Bf16, d, ng><<<grid, 256, 0, st>>>(a);
     });
     return hipGetLastError();
 }
@@ -841,32 +967,24 @@ size_t attn_kv4_workspace(int T, int Hq, int heads, int dim, int page, int width
 hipError_t launch_attn_kv4(const AttnArgs& a, const Kv4& c, void* ws, hipStream_t st) {
     const Grid g = attn_kv4_grid(c.T, a.Hq / c.heads, c.heads, c.dim, 1 << c.page_log2, c.width, c.B);
     hipError_t e = hipErrorInvalidValue;
-    by_dim(c.dim, [&](auto d) {
-        auto groups = [&](auto ng) {
-            auto tiles = [&](auto rt) {
-                if constexpr (rt <= max_tiles<d>()) {
-                    if (g.tiles != rt) return;
-                    const auto run = [&](auto waves) {
-                        e = a.fp16 ? run_attn_kv4<Fp16, d, ng, rt, waves>(a, c, g, (float*)ws, st)
-                                   : run_attn_kv4<Bf16, d, ng, rt, waves>(a, c, g, (float*)ws, st);
-                    };
-                    // (a head of 256 takes the registers of two waves)
-                    if constexpr (d < 256 && rt == 1) {
-                        if (g.slots == 0) return run(std::integral_constant<int, 8>());
-                    }
-                    run(std::integral_constant<int, 4>());
+    by_form(c, [&](auto d, auto ng) {
+        const auto tiles = [&](auto rt) {
+            if constexpr (rt <= max_tiles<d>()) {
+                if (g.tiles != rt) return;
+                const auto run = [&](auto waves) {
+                    e = a.fp16 ? run_attn_kv4<Fp16, d, ng, rt, waves>(a, c, g, (float*)ws, st)
+                               : run_attn_kv4<Bf16, d, ng, rt, waves>(a, c, g, (float*)ws, st);
+                };
+                // (a head of 256 takes the registers of two waves)
+                if constexpr (d < 256 && rt == 1) {
+                    if (g.slots == 0) return run(std::integral_constant<int, 8>());
                 }
-            };
-            if (c.dim / c.group != ng) return;
-            tiles(std::integral_constant<int, 1>());
-            tiles(std::integral_constant<int, 2>());
-            tiles(std::integral_constant<int, 3>());
+                run(std::integral_constant<int, 4>());
+            }
         };
-        constexpr int D = d;
-        if constexpr (D <= 128) groups(std::integral_constant<int, 1>());
-        groups(std::integral_constant<int, 2>());
-        if constexpr (D >= 128) groups(std::integral_constant<int, 4>());
-        if constexpr (D == 256) groups(std::integral_constant<int, 8>());
+        tiles(std::integral_constant<int, 1>());
+        tiles(std::integral_constant<int, 2>());
+        tiles(std::integral_constant<int, 3>());
     });
     return e;
 }

@@ -100,10 +100,10 @@ def test_kv4_refusals(L):
                           SHAPE: [dict(k_row=1 << 24)]}.items():
         for c in cases:
             assert append(L, **c) == status, c
-    for status, cases in {NULL: [dict(q=None), dict(y=None), dict(ws=None)],
+    for status, cases in {NULL: [dict(q=None), dict(y=None), dict(ws=None, width=100)],
                           ALIGN: [dict(q=ODD), dict(y=ODD), dict(ws=ODD), dict(q_row=4), dict(q_head=-8)],
                           SHAPE: [dict(Hq=3), dict(Hq=0), dict(scale=NAN), dict(y=P)],
-                          WORKSPACE: [dict(ws_bytes=0), dict(ws_bytes=255)]}.items():
+                          WORKSPACE: [dict(ws_bytes=0, width=100), dict(ws_bytes=256, width=100)]}.items():
         for c in cases:
             assert attend(L, **c) == status, c
     assert L.cr_attn_kv4(0, P, 512, 128, 3, 4, None, P, 4, P, P, 1, 0.1, FAR, P, 1 << 30, None) == NULL
