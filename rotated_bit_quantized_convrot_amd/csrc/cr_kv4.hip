@@ -20,12 +20,13 @@ constexpr float kv4_norm() { return D == 64 ? 0.125f : D == 128 ? 0.088388347648
 
 template <int M, int N>
 __device__ __forceinline__ void rotate_lanes(float (&x)[N], int lane) {
+    const float c = lane & M ? -1.0f : 1.0f;   // x + p, or p - x: one rounding either way
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         float p;
         if constexpr (M == 32) p = __shfl_xor(x[i], 32);
         else p = lane_xor<M>(x[i]);
-        x[i] = (lane & M) ? p - x[i] : x[i] + p;
+        x[i] = __builtin_fmaf(x[i], c, p);
     }
 }
 
@@ -163,33 +164,49 @@ __global__ __launch_bounds__(256) void k_kv4_append(AppendArgs a) {
     uint32_t word[NG], code[KS];   // code: d + 2 j in bits 4 j, d + 2 j + 1 in bits 16 + 4 j
 #pragma unroll
     for (int n = 0; n < NG; ++n) {
-        float lo = 0.0f, hi = 0.0f, big = 0.0f;
+        float lo = 0.0f, hi = 0.0f, bad = 0.0f;
 #pragma unroll
         for (int s = n * SPG; s < (n + 1) * SPG; ++s)
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 lo = fminf(lo, x[s][j]);
                 hi = fmaxf(hi, x[s][j]);
-                big += x[s][j] - x[s][j];   // NaN from the first infinity or NaN on
+                bad = __builtin_fmaf(x[s][j], 0.0f, bad);   // NaN from the first infinity or NaN on
             }
         lo = fminf(lo, lane_xor<1>(lo));
         lo = fminf(lo, lane_xor<2>(lo));
         hi = fmaxf(hi, lane_xor<1>(hi));
         hi = fmaxf(hi, lane_xor<2>(hi));
-        big += lane_xor<1>(big);
-        big += lane_xor<2>(big);
-        const uint32_t sb = big != big ? kKv4Nan : (__float_as_uint(hi / 15.0f - lo / 15.0f) + 8) & ~15u;
+        bad += lane_xor<1>(bad);
+        bad += lane_xor<2>(bad);
+        const uint32_t sb = bad != bad ? kKv4Nan : (__float_as_uint(hi / 15.0f - lo / 15.0f) + 8) & ~15u;
         const float sc = __uint_as_float(sb);
-        const float z = sc > 0.0f ? fminf(fmaxf(rintf(-lo / sc), 0.0f), 15.0f) : 0.0f;
+        // x / s by a reciprocal and one exact correction: the same float32 as the division's.  With r = x inv off
+        // x / s by e, at most 1.5 of its last places, x - r s is exact (s has 20 bits) and r + (x - r s) inv off x / s
+        // by 2^-24 e at most, 2^-46 of it; and x / s, of 24 bits by 20, is no nearer than 2^-45 of itself to where the
+        // rounding turns.  The products stay normal where the scale is between 2^-100 and 2^100 (the others divide; a
+        // quotient under 1/2 is 0 either way).  With 0 for the reciprocal, a scale of 0 or NaN gives codes of 0.
+        const float inv = sc > 0.0f ? 1.0f / sc : 0.0f;
+        const float z = fminf(fmaxf(rintf(sc > 0.0f ? -lo / sc : 0.0f), 0.0f), 15.0f);
         word[n] = sb | (uint32_t)z;
+        const bool divide = __any(sc > 0x1p100f || (sc > 0.0f && sc < 0x1p-100f));
 #pragma unroll
         for (int s = n * SPG; s < (n + 1) * SPG; ++s) {
+            float q[8];
+            if (divide) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) q[j] = sc > 0.0f ? x[s][j] / sc : 0.0f;
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float r = x[s][j] * inv;
+                    q[j] = __builtin_fmaf(__builtin_fmaf(-r, sc, x[s][j]), inv, r);
+                }
+            }
             code[s] = 0;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float q = sc > 0.0f ? fminf(fmaxf(rintf(x[s][j] / sc) + z, 0.0f), 15.0f) : 0.0f;
-                code[s] |= (uint32_t)q << (4 * (j >> 1) + 16 * (j & 1));
-            }
+            for (int j = 0; j < 8; ++j)
+                code[s] |= (uint32_t)fminf(fmaxf(rintf(q[j]) + z, 0.0f), 15.0f) << (4 * (j >> 1) + 16 * (j & 1));
         }
     }
     const int row = (base + t) & ((1 << a.c.page_log2) - 1);
@@ -215,12 +232,15 @@ __global__ __launch_bounds__(256) void k_kv4_append(AppendArgs a) {
 #pragma unroll
     for (int s = 0; s < KS; ++s) {
         const uint32_t other = (uint32_t)__float_as_int(lane_xor<2>(__uint_as_float(code[s])));
-        if (p < 2)
+        // bytes of j = 0, 4, 1, 5 and 2, 6, 3, 7
+        const uint32_t u = (code[s] & 0x0F0F0F0Fu) | (other & 0x0F0F0F0Fu) << 4;
+        const uint32_t v = (code[s] >> 4 & 0x0F0F0F0Fu) | (other & 0xF0F0F0F0u);
+        if (p < 2) {
+            uint8_t* to = &pairs[wave][(16 * s + 8 * p) * 16 + t];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int sh = 4 * (j >> 1) + 16 * (j & 1);
-                pairs[wave][(16 * s + 8 * p + j) * 16 + t] = (uint8_t)((code[s] >> sh & 15u) | (other >> sh & 15u) << 4);
-            }
+            for (int j = 0; j < 8; ++j)
+                to[16 * j] = (uint8_t)(((j & 2) ? v : u) >> (8 * (j >> 2) + 16 * (j & 1)));
+        }
     }
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
