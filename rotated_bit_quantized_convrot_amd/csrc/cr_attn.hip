@@ -93,36 +93,34 @@ struct Tile {
 template <int BM>
 __device__ __forceinline__ bool find_tile(const int32_t* cu, int B, int T, int t, Tile* out) {
     const int lane = threadIdx.x & 63;
-    int total = 0;
-    for (int b0 = 0; b0 < B; b0 += 64) {
+    auto rows_of = [&](int b0, int* first) {
         const int b = min(b0 + lane, B - 1);
-        const int first = min(max(cu[b], 0), T), len = min(max(cu[b + 1], first), T) - first;
-        int n = b0 + lane < B ? (len + BM - 1) / BM : 0;
-#pragma unroll
-        for (int m = 1; m < 64; m <<= 1) n += __shfl_xor(n, m);
-        total += n;
+        *first = min(max(cu[b], 0), T);
+        return b0 + lane < B ? min(max(cu[b + 1], *first), T) - *first : 0;
+    };
+    int first0;
+    const int len0 = rows_of(0, &first0);
+    int total = __builtin_amdgcn_readlane(wave_scan((len0 + BM - 1) / BM, add_ints), 63);
+    for (int b0 = 64; b0 < B; b0 += 64) {
+        int first;
+        const int len = rows_of(b0, &first);
+        total += __builtin_amdgcn_readlane(wave_scan((len + BM - 1) / BM, add_ints), 63);
     }
     int left = total - 1 - t;   // tiles before this one
     if (left < 0) return false;
     for (int b0 = 0; b0 < B; b0 += 64) {
-        const int b = min(b0 + lane, B - 1);
-        const int first = min(max(cu[b], 0), T), len = min(max(cu[b + 1], first), T) - first;
-        const int n = b0 + lane < B ? (len + BM - 1) / BM : 0;
-        int upto = n;
-#pragma unroll
-        for (int m = 1; m < 64; m <<= 1) {
-            const int p = __shfl_up(upto, m);
-            if (lane >= m) upto += p;
-        }
+        int first = first0, len = len0;
+        if (b0 > 0) len = rows_of(b0, &first);
+        const int n = (len + BM - 1) / BM, upto = wave_scan(n, add_ints);
         const uint64_t after = __ballot(upto > left);
         if (after) {
             const int l = __builtin_ctzll(after);
-            out->first = __builtin_amdgcn_readfirstlane(__shfl(first, l));
-            out->len = __builtin_amdgcn_readfirstlane(__shfl(len, l));
-            out->row = __builtin_amdgcn_readfirstlane((left - __shfl(upto - n, l)) * BM);
+            out->first = __builtin_amdgcn_readlane(first, l);
+            out->len = __builtin_amdgcn_readlane(len, l);
+            out->row = (left - __builtin_amdgcn_readlane(upto - n, l)) * BM;
             return true;
         }
-        left -= __shfl(upto, 63);
+        left -= __builtin_amdgcn_readlane(upto, 63);
     }
     return false;
 }
@@ -134,6 +132,16 @@ template <int D, bool V>
 __device__ __forceinline__ int swizzle(int r) {
     constexpr int rows = D >= 128 ? 1 : 128 / D;   // rows in 256 bytes
     return V ? ((r / rows) & (rows > 1 ? 1 : 3)) * 4 : (r / rows) & (rows > 1 ? 7 : 15);
+}
+
+// Bytes of an output row in LDS; of a block: two buffers of K and V for each
+// half of the waves, later its rows.
+template <int D>
+constexpr int out_row() { return 2 * D + 16; }
+template <int D, int NW, int BN, int KG>
+constexpr int lds_bytes() {
+    constexpr int tiles = KG * 4 * BN * D * 2, rows = NW * 32 * out_row<D>();
+    return tiles > rows ? tiles : rows;
 }
 
 // One block: BM = 32 NW rows of one head, a wave 32 of them, over tiles of BN
@@ -308,7 +316,7 @@ __global__ __launch_bounds__(64 * NW * KG, D == 256 ? 1 : 2) void k_attn_prompt(
             stat[64] = sum;
         }
         __syncthreads();
-        if (kg == 1) return;
+        if (kg == 0) {
         const float other = stat[0], up = fmaxf(top, other);
         // a half that has seen no key has sums of 0, or NaN
         const float f0 = top == up || top == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(top - up);
@@ -320,8 +328,10 @@ __global__ __launch_bounds__(64 * NW * KG, D == 256 ? 1 : 2) void k_attn_prompt(
 #pragma unroll
             for (int x = 0; x < 4; ++x) o[i / 4][i % 4 * 4 + x] = o[i / 4][i % 4 * 4 + x] * f0 + v[x] * f1;
         }
+        }
     }
-    if (row0 >= t.len) return;
+    __syncthreads();   // where the rows go, the last tiles or the other half's sums were read
+    if (kg == 1 || row0 >= t.len) return;
     const float inv = 1.0f / sum;
     bool bad = false;
     float y[DT][16];
@@ -334,17 +344,30 @@ __global__ __launch_bounds__(64 * NW * KG, D == 256 ? 1 : 2) void k_attn_prompt(
         }
     const uint64_t wrong = __ballot(bad);
     const uint32_t again = (uint32_t)(wrong | wrong >> 32);   // rows that are infinite or NaN somewhere
-    uint16_t* out = a.y + ((int64_t)(t.first + row) * a.Hq + h) * D + 4 * (lane >> 5);
-    if (row < t.len && !(again >> (lane & 31) & 1)) {
+    // whole rows to memory: by way of LDS, each wave in a place of its own, 16 bytes between its rows (stored as
+    // they lie, 8 bytes a lane, 32 rows a store, they took 2 us)
+    constexpr int kRow = out_row<D>();
+    char* mine_out = lds + wave * 32 * kRow;
 #pragma unroll
-        for (int dt = 0; dt < DT; ++dt)
+    for (int dt = 0; dt < DT; ++dt)
 #pragma unroll
-            for (int i = 0; i < 16; i += 4) {
-                uint2 w;
-                w.x = pack2(T(), y[dt][i], y[dt][i + 1]);
-                w.y = pack2(T(), y[dt][i + 2], y[dt][i + 3]);
-                *reinterpret_cast<uint2*>(out + 32 * dt + 2 * i) = w;
-            }
+        for (int i = 0; i < 16; i += 4) {
+            uint2 w;
+            w.x = pack2(T(), y[dt][i], y[dt][i + 1]);
+            w.y = pack2(T(), y[dt][i + 2], y[dt][i + 3]);
+            *reinterpret_cast<uint2*>(mine_out + (lane & 31) * kRow + 8 * (lane >> 5) + 64 * dt + 4 * i) = w;
+        }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    uint16_t* out = a.y + ((int64_t)(t.first + row0) * a.Hq + h) * D;
+    const int rows = min(32, t.len - row0);
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) {
+        const int r = (i * 64 + lane) / (D / 8), ch = (i * 64 + lane) % (D / 8);
+        if (r < rows && !(again >> r & 1))
+            *reinterpret_cast<u32x4*>(out + (int64_t)r * a.Hq * D + 8 * ch) =
+                *reinterpret_cast<const u32x4*>(mine_out + r * kRow + 16 * ch);
     }
     // A weight of 0 times an infinity or a NaN of a key that the row does not see
     // made some of these: once more, without that key.
@@ -358,7 +381,7 @@ __global__ __launch_bounds__(64 * NW * KG, D == 256 ? 1 : 2) void k_attn_prompt(
 
 template <class T, int D, int NW, int BN, int KG>
 hipError_t launch(const AttnArgs& a, hipStream_t st) {
-    constexpr int BM = 32 * NW, lds = KG * 4 * BN * D * 2;
+    constexpr int BM = 32 * NW, lds = lds_bytes<D, NW, BN, KG>();
     static_assert(KG == 1 || NW * (D / 32 * 4096 + 512) <= lds, "the second half's sums fit");
     static std::atomic<uint64_t> done{0};
     if (lds > 65536) {

@@ -60,21 +60,6 @@ struct AppendArgs {
     int64_t row[2], head[2];     // their strides in values
 };
 
-// Sums over the lanes up to each, by DPP (row_shr 1, 2, 4, 8, row_bcast 15, 31).
-template <int CTRL, int ROWS>
-__device__ __forceinline__ int dpp_or_zero(int v) { return __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false); }
-template <class F>
-__device__ __forceinline__ int wave_scan(int v, F add) {
-    v = add(v, dpp_or_zero<0x111, 0xF>(v));
-    v = add(v, dpp_or_zero<0x112, 0xF>(v));
-    v = add(v, dpp_or_zero<0x114, 0xF>(v));
-    v = add(v, dpp_or_zero<0x118, 0xF>(v));
-    v = add(v, dpp_or_zero<0x142, 0xA>(v));
-    return add(v, dpp_or_zero<0x143, 0xC>(v));
-}
-__device__ __forceinline__ int add_ints(int a, int b) { return a + b; }
-__device__ __forceinline__ int add_floats(int a, int b) { return __float_as_int(__int_as_float(a) + __int_as_float(b)); }
-
 // 16 rows of the cache (of one page) that take new tokens: rows r0 up to r1 of
 // the call's are positions pos0 and on, all in the 16 from pos0 & ~15.
 struct AppendWork {
