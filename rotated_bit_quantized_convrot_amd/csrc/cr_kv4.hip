@@ -291,14 +291,17 @@ __device__ __forceinline__ bool kv4_work(const Kv4& c, int G, int slots, int fil
             total += __int_as_float(__builtin_amdgcn_readlane(wave_scan(__float_as_int((float)n * (float)s.tokens), add_floats), 63));
         }
         const int n = lane < c.B ? groups_of(first) : 0;
-        for (int f = 8; f <= 16; f += f < 10 ? 1 : f < 12 ? 2 : 4) {   // 8, 9, 10, 12, 16 eighths
-            const float e = fminf(total * (float)f / (8.0f * (float)fill), 1073741824.0f);
-            // (the sum is rounded: a little more than it where that could cost a slot)
-            span = ((int)(f == 16 ? e * 1.0001f + 1.0f : e) + kMinSpan - 1) / kMinSpan * kMinSpan;
-            span = max(span, kMinSpan);
-            if (c.B > 64) continue;
-            if (__builtin_amdgcn_readlane(wave_scan(n * max((first.tokens + span - 1) / span, 1), add_ints), 63) <= fill) break;
+        // in units of kMinSpan: fill's share, and twice it, with which at most fill / 2 blocks more than groups are
+        // needed (the sum is rounded: a little more than it)
+        const float e = fminf(total / (kMinSpan * (float)fill), 2097152.0f);
+        int lo = max((int)e, 1), hi = (int)(2.0f * e * 1.0001f) + 1;
+        while (c.B <= 64 && lo < hi) {   // (more sequences: as they are)
+            const int mid = (lo + hi) / 2;
+            span = mid * kMinSpan;
+            if (__builtin_amdgcn_readlane(wave_scan(n * max((first.tokens + span - 1) / span, 1), add_ints), 63) <= fill) hi = mid;
+            else lo = mid + 1;
         }
+        span = hi * kMinSpan;
     }
     int at = 0, slot = 0;
     for (int b0 = 0; b0 < c.B; b0 += 64) {
