@@ -406,7 +406,10 @@ cr_status cr_moe_w4g(int dtype, const void* x, int M, int K, const void* router,
  * cu[b+1] of int32 cu [B+1] on the device, which must not decrease; an empty
  * sequence has none.  Rows before cu[0] and from cu[B] on are not read, and
  * their outputs are left as they were.
- * Scores are scale * q . k, held in float32 with the softmax's sums. */
+ * Scores are scale * q . k (|scale| <= CR_MAX_SCALE), held in float32 with the
+ * softmax's sums; weights may be up to 2^8 times their share until the sums are
+ * divided. */
+#define CR_MAX_SCALE 1e30f
 #define CR_MAX_HEADS 1024
 #define CR_MAX_SEQS 65536
 
@@ -470,7 +473,11 @@ cr_status cr_kv4_append(int dtype, const void* k, int64_t k_row, int64_t k_head,
 /* Attention of a call's rows (q, already in the cache: cr_kv4_append comes
  * first) over the cache: row i of a sequence's n sees its tokens up to
  * lens[b] - n + i.  A row that sees none gives zeros.  With the cache's
- * rotation q is rotated and the output turned back.
+ * rotation q is rotated and the output turned back.  q and the weights times
+ * V's scales go to the products in 16 bits and more (two bf16 each); a token of
+ * NaN reaches the rows that see it.  Meant for a token or a few a sequence: up
+ * to 48, 32 or 16 rows (tokens times Hq / heads; dim 64, 128, 256) read the
+ * cache once, more read it again.
  *   ws / ws_bytes: at least cr_attn_kv4_workspace_bytes(...); calls that can
  *   run at the same time need a workspace each.  Nothing is kept in it.  Where
  *   the size is 256 (a table of up to 1024 tokens) none is used: ws may be NULL.

@@ -415,7 +415,7 @@ cr_status check_attn(int dtype, int T, int Hq, int Hkv, int D, int B, float scal
     if (D != 64 && D != 128 && D != 256) return fail(CR_ERR_SHAPE, "head of %d (need 64, 128 or 256)", D);
     if (Hq < 1 || Hq > CR_MAX_HEADS || Hkv < 1 || Hq % Hkv)
         return fail(CR_ERR_SHAPE, "%d heads on %d (need a multiple, up to %d)", Hq, Hkv, CR_MAX_HEADS);
-    if (!(scale - scale == 0.0f)) return fail(CR_ERR_SHAPE, "scale is not finite");
+    if (!(scale >= -CR_MAX_SCALE && scale <= CR_MAX_SCALE)) return fail(CR_ERR_SHAPE, "scale %g (need up to %g)", scale, CR_MAX_SCALE);
     return CR_OK;
 }
 cr_status check_kv4(const cr_kv4* c) {

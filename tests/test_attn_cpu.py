@@ -53,7 +53,7 @@ def test_prompt_refusals(L):
     for status, cases in {
         KIND: [dict(dtype=2), dict(dtype=-1)],
         SHAPE: [dict(T=-1), dict(T=(1 << 20) + 1), dict(D=96), dict(D=0), dict(Hq=3), dict(Hkv=0), dict(Hq=0),
-                dict(Hq=2048, Hkv=1024), dict(B=-1), dict(B=65537), dict(scale=NAN), dict(scale=INF), dict(scale=-INF),
+                dict(Hq=2048, Hkv=1024), dict(B=-1), dict(B=65537), dict(scale=NAN), dict(scale=INF), dict(scale=-INF), dict(scale=2e30), dict(scale=-2e30),
                 dict(q_row=1 << 24), dict(k_head=1 << 41),
                 dict(y=P), dict(y=ctypes.c_void_p((1 << 20) + 512 * 2 * 9 + 512 * 2 - 16)),
                 dict(y=ctypes.c_void_p((1 << 20) - 10 * 512 * 2 + 16))],

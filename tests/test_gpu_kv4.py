@@ -187,9 +187,51 @@ def test_append_views():
 @pytest.mark.parametrize("dtype", DT)
 @pytest.mark.parametrize("D,group", FORMS)
 @pytest.mark.parametrize("rotate", [True, False])
-def test_decode_forms(dtype, D, group, rotate):
-    s = Setup([37, 1, 300, 64], 2, D, group, 64, rotate, DT[dtype], seed=D + group).fill()
+@pytest.mark.parametrize("spare", [2, 40])   # tables of up to 1024 tokens, and longer ones: one span, or several
+def test_decode_forms(dtype, D, group, rotate, spare):
+    s = Setup([37, 1, 600, 64], 2, D, group, 64, rotate, DT[dtype], seed=D + group, spare=spare).fill()
     s.check([1, 1, 1, 1], 6)
+
+
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("D,group", FORMS)
+@pytest.mark.parametrize("rotate", [True, False])
+@pytest.mark.parametrize("new,Hq,spare", [([4, 4], 10, 2), ([7, 7], 10, 40), ([30, 2], 6, 40)])
+def test_chunk_forms(dtype, D, group, rotate, new, Hq, spare):
+    """Several tiles of rows: 20, 35 and 48 rows a key head on average, in
+    blocks of one to three tiles."""
+    s = Setup([700, 90], 2, D, group, 64, rotate, DT[dtype], seed=D + group, spare=spare).fill()
+    s.check(new, Hq)
+
+
+@pytest.mark.parametrize("H,Hq", [(1, 4), (8, 8), (3, 6)])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("lens", [[5000, 3, 700, 2600, 1, 0, 513], [257] * 70 + [9000], [1, 2, 3], [20000], [4096] * 9])
+def test_spans(H, Hq, D, lens):
+    """Ragged contexts in spans over the chip: more and fewer sequences than 64,
+    than the blocks that run at once; joined, or whole in tables that are wide."""
+    s = Setup(lens, H, D, 64, 128, True, torch.bfloat16, seed=H + D, spare=30).fill()
+    s.check([min(1, n) for n in lens], Hq)
+
+
+def test_two_workspaces_at_once():
+    """Two calls on two streams, a workspace each."""
+    s = Setup([3000, 100, 1500], 2, 128, 64, 64, True, torch.bfloat16, seed=20).fill()
+    t = Setup([2000, 1800], 2, 64, 32, 16, False, torch.float16, seed=21).fill()
+    q, p = s.queries([1, 1, 1], 8), t.queries([2, 1], 8)
+    args = [(q, s, ints([0, 1, 2, 3])), (p, t, ints([0, 2, 3]))]
+    lens = [ints(s.lens), ints(t.lens)]
+    want = [crp.attn_kv4(x, c.cache, c.table, n, cu).clone() for (x, c, cu), n in zip(args, lens)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for turn in range(10):
+        for i, ((x, c, cu), n) in enumerate(zip(args, lens)):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(crp.attn_kv4(x, c.cache, c.table, n, cu))
+    torch.cuda.synchronize()
+    for g, w in zip(got, want):
+        assert all(torch.equal(y, w) for y in g)
 
 
 @pytest.mark.parametrize("n", [1, 2, 15, 16, 17, 31, 33, 63, 64, 65, 127, 128, 129, 255, 256, 257, 511, 512, 513, 1000,
