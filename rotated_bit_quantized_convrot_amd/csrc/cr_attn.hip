@@ -156,6 +156,7 @@ template <class T, int D, int NW, int BN, int KG>
 __global__ __launch_bounds__(64 * NW * KG, D == 256 ? 1 : 2) void k_attn_prompt(AttnArgs a) {
     constexpr int BM = 32 * NW, KS = D / 16, DT = D / 32, MT = BN / 32, PS = BN / 16;
     constexpr int kTile = BN * D * 2, kLoads = kTile / 1024 / NW;   // bytes of a K or V tile; 1 KiB loads of a wave
+    constexpr bool MEET = KG == 2 && NW == 2;
     constexpr float kMove = 8.0f;   // the maximum follows when weights would pass 2^8
     // fp16 weights: 2^6 at the maximum, so that fewer fall below its normal range
     constexpr float kBias = std::is_same_v<T, Fp16> ? 6.0f : 0.0f;
@@ -218,6 +219,21 @@ __global__ __launch_bounds__(64 * NW * KG, D == 256 ? 1 : 2) void k_attn_prompt(
             if (a.scale < 0.0f) qv[s] ^= 0x80008000u;   // the sign goes to q
         }
     }
+    // Halves of two waves do not wait for each other: each has a count of its waves that have come to a turn (a
+    // barrier of the whole block: 600 tokens of 32 heads 16.9 us, this 15.7; D = 256 ragged 59.7 and 56.6; with halves
+    // of four waves it is the slower one, 1220 tokens 24.6 and 25.5).
+    __shared__ uint32_t came[2];
+    if constexpr (MEET) {
+        if (threadIdx.x < 2) came[threadIdx.x] = 0;
+        __syncthreads();
+    }
+    auto meet = [&](int turn) {
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // what this wave asked LDS for has been read
+        if (lane == 0) __hip_atomic_fetch_add(&came[kg], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+        const uint32_t all = (uint32_t)(turn + 1) * NW;
+        while (__builtin_amdgcn_readfirstlane(__hip_atomic_load(&came[kg], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP)) < all) {}
+        asm volatile("" ::: "memory");
+    };
     f32x16 o[DT] = {};
     // a scale of 0 would make NaN of the scores that are masked; all weights are 1 with this one too
     const float c = a.scale == 0.0f ? 1e-30f : fabsf(a.scale) * 1.4426950408889634f;
@@ -226,7 +242,8 @@ __global__ __launch_bounds__(64 * NW * KG, D == 256 ? 1 : 2) void k_attn_prompt(
     for (int turn = 0; turn * KG < tiles; ++turn) {
         const int j = turn * KG + kg;
         w4g_wait();
-        w4g_barrier();
+        if constexpr (MEET) meet(turn);
+        else w4g_barrier();
         if (j + KG < tiles) load(j + KG, (turn + 1) & 1);
         if (j * BN >= mine) continue;
         const char* kt = mem + (turn & 1) * 2 * kTile;
@@ -394,22 +411,43 @@ hipError_t launch(const AttnArgs& a, hipStream_t st) {
     k_attn_prompt<T, D, NW, BN, KG><<<dim3(a.Hq, y, (unsigned)((tiles + y - 1) / y)), 64 * NW * KG, lds, st>>>(a);
     return hipGetLastError();
 }
-// Blocks of 128 rows fill the 256 CUs twice, or the keys are split over two
-// halves of a block's waves, or its rows are 64 as well (D = 256, one wave a
-// SIMD: 64 rows and two halves, or 128).  Few blocks: what a block takes is
-// what the call takes.  Many: 64 rows load each key twice as often.  us, 128
-// rows / 128 rows in halves / 64 rows in halves, causal, one sequence:
-//   D = 128, 32 heads: 300 tokens (96 blocks) 11.8 / 12.6 / 10.6,
-//     600 (160) 18.6 / 17.1 / 16.9, 1220 (320) 31 / 27 / 39, 2500 (640) 67 / 78 / 107
-//   D = 64, 16 heads: 1220 tokens (160 blocks) 22.7 / 17.8 / 15.4
-//   D = 256, 16 heads: 300 tokens (48 blocks) 21.6 / - / 17.9, 8 heads: 16384 (1024) 1455 / - / 1780
+// What a block takes, by the number of blocks of 128 rows and the sequences'
+// mean length (rows of a block / keys of a tile / halves of the waves on the
+// keys).  Few blocks: what a block takes is what the call takes, so that 64 rows
+// and two halves are best, then 128 and two halves; many: 128 rows load each
+// key half as often; sequences shorter than a block leave most of it empty.
+// us a call, causal, one sequence or as said:
+//                                             128/64/1  128/64/2  64/64/2  64/32/2  64/32/1
+//   D = 128, 32 heads: 300 tokens  (96 blocks)    10.7      11.0     10.1     10.2     12.0
+//     600 (160)                                   17.1      15.6     15.7     15.2     18.4
+//     1220 (320)                                  30.1      24.4     35.9     26.6     34.5
+//     2500 (640)                                  63.9      73.0     95.5     77.9     73.7
+//     20 of 220 (1408)                            32.5      48.0     73.2     44.9     31.1
+//     40 of 60 (1216)                             19.0      37.5     37.1     21.4     16.1
+//   D = 64, 16 heads: 600 (80)                    11.9      10.3      9.2      9.8     12.9
+//     1220 (160)                                  19.7      15.7     14.6     16.0     23.2
+//     2500 (320)                                  36.2      28.6     25.9     29.5     43.7
+//     5000 (640)                                  75.9      67.7     78.6     70.9     87.7
+//   D = 64, 14 heads: 20 from 0 to 903 (616)      20.9      20.4     21.6     17.6     20.9
+//     20 of 220 (616)                             12.9      14.5     17.5     13.2     11.1
+//     8 of 1000 (924)                             31.8      33.3     39.1     35.0     32.2
+//   D = 64, 32 heads: 64 of 60 (1984)             13.4      23.0     23.4     14.8     11.0
+// D = 256 (one wave a SIMD), 128/32/1 and 64/32/2: 16 heads, 300 tokens (48
+// blocks) 21.2 / 17.5; 8 heads, 2741 (192) 91 / 57, 16384 (1024) 1410 / 1660.
 template <class T, int D>
 hipError_t launch_by_size(const AttnArgs& a, hipStream_t st) {
     const int64_t blocks = ((int64_t)a.T / 128 + (a.B + 1) / 2) * a.Hq;   // half a tile lost a sequence
-    if constexpr (D == 256) return blocks <= 448 ? launch<T, D, 2, 32, 2>(a, st) : launch<T, D, 4, 32, 1>(a, st);
-    else if (blocks <= 192) return launch<T, D, 2, 64, 2>(a, st);
-    else if (blocks <= 448) return launch<T, D, 4, 64, 2>(a, st);
-    else return launch<T, D, 4, 64, 1>(a, st);
+    const int mean = a.T / a.B;
+    if constexpr (D == 256) {
+        return blocks <= 448 ? launch<T, D, 2, 32, 2>(a, st) : launch<T, D, 4, 32, 1>(a, st);
+    } else {
+        if (blocks <= (D == 64 ? 352 : 192)) return launch<T, D, 2, 64, 2>(a, st);
+        if constexpr (D == 64) {
+            if (blocks <= 704 && mean < 512) return launch<T, D, 2, 32, 2>(a, st);
+        }
+        if (blocks <= (D == 64 ? 704 : 448)) return launch<T, D, 4, 64, 2>(a, st);
+        return mean <= 128 ? launch<T, D, 2, 32, 1>(a, st) : launch<T, D, 4, 64, 1>(a, st);
+    }
 }
 template <class T>
 hipError_t launch_by_dim(const AttnArgs& a, hipStream_t st) {
