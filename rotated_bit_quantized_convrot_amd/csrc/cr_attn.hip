@@ -156,7 +156,7 @@ template <class T, int D, int NW, int BN, int KG>
 __global__ __launch_bounds__(64 * NW * KG, D == 256 ? 1 : 2) void k_attn_prompt(AttnArgs a) {
     constexpr int BM = 32 * NW, KS = D / 16, DT = D / 32, MT = BN / 32, PS = BN / 16;
     constexpr int kTile = BN * D * 2, kLoads = kTile / 1024 / NW;   // bytes of a K or V tile; 1 KiB loads of a wave
-    constexpr bool MEET = KG == 2 && NW == 2;
+    constexpr bool MEET = KG == 2 && NW == 2, BETWEEN = NW == 4;
     constexpr float kMove = 8.0f;   // the maximum follows when weights would pass 2^8
     // fp16 weights: 2^6 at the maximum, so that fewer fall below its normal range
     constexpr float kBias = std::is_same_v<T, Fp16> ? 6.0f : 0.0f;
@@ -244,8 +244,24 @@ __global__ __launch_bounds__(64 * NW * KG, D == 256 ? 1 : 2) void k_attn_prompt(
         w4g_wait();
         if constexpr (MEET) meet(turn);
         else w4g_barrier();
-        if (j + KG < tiles) load(j + KG, (turn + 1) & 1);
-        if (j * BN >= mine) continue;
+        // The next tile's loads.  Blocks of four waves of rows send them between the products, where the wait of one
+        // load for another (64 bytes a clock) is hidden: two pictures 225.6 -> 219.1 us, 2500 tokens 64.5 -> 62.5; the
+        // others (ragged D = 256 56.7 and 57.4, 20 fp16 prompts 17.4 and 17.7 so) at once.  (Between the products
+        // there is no question whether there is a next tile: past the last it comes once more, to where nothing is read.)
+        const int next = min(j + KG, tiles - 1) * BN;
+        if (keys - next < BN) offsets(t.len - next < BN ? t.len - next : BN);
+        const v4i k_next = rows_at(k, a.k_row, next), v_next = rows_at(v, a.v_row, next);
+        const uint32_t to = __builtin_amdgcn_readfirstlane(lds0 + ((turn + 1) & 1) * 2 * kTile + wave * kLoads * 1024);
+        auto piece = [&](int i) {
+            if (i < kLoads) w4g_x_to_lds(k_next, k_off[i], to + i * 1024);
+            else w4g_x_to_lds(v_next, v_off[i - kLoads], to + kTile + (i - kLoads) * 1024);
+        };
+        const bool sees = j * BN < mine;
+        if ((!BETWEEN || !sees) && j + KG < tiles) {
+#pragma unroll
+            for (int i = 0; i < 2 * kLoads; ++i) piece(i);
+        }
+        if (!sees) continue;
         const char* kt = mem + (turn & 1) * 2 * kTile;
         const char* vt = kt + kTile;
         f32x16 s[MT];
@@ -258,6 +274,10 @@ __global__ __launch_bounds__(64 * NW * KG, D == 256 ? 1 : 2) void k_attn_prompt(
                 const int r = 32 * mt + (lane & 31);
                 s[mt] = mfma32(T(), *reinterpret_cast<const u32x4*>(kt + r * (2 * D) + ((2 * ks + (lane >> 5)) ^ swizzle<D, false>(r)) * 16),
                                qv[ks], s[mt]);
+                if (BETWEEN && mt == MT - 1) {
+#pragma unroll
+                    for (int i = ks * 2 * kLoads / KS; i < (ks + 1) * 2 * kLoads / KS; ++i) piece(i);
+                }
             }
         // this lane's score i of part mt: key j BN + 32 mt + 8 (i / 4) + 4 (lane / 32) + i % 4
         if (j * BN + BN > (a.causal ? min(row0 + 1, t.len) : t.len)) {
@@ -319,6 +339,7 @@ __global__ __launch_bounds__(64 * NW * KG, D == 256 ? 1 : 2) void k_attn_prompt(
         }
     }
 
+    w4g_wait();   // the last loads are in before LDS is used for something else
     sum += __shfl_xor(sum, 32);
     if constexpr (KG == 2) {
         // sums as they lie in the registers: lane by lane, 16 bytes each
