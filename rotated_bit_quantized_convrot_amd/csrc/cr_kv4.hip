@@ -7,6 +7,7 @@
 //   lo = min(0, min x'), hi = max(0, max x'), s = hi / 15 - lo / 15 to the
 //   nearest float32 whose low four bits are 0, z = clamp(rint(-lo / s), 0, 15),
 //   c = clamp(rint(x' / s) + z, 0, 15); both 0 where s = 0.
+#include <numeric>
 #include <type_traits>
 
 #include "cr_w4g.h"
@@ -278,10 +279,10 @@ struct Kv4Work {
 // at once, up to twice fill's share; then at most fill / 2 blocks more than
 // tile groups are needed, which is what the grid has.  A sequence's spans are
 // equal.  slots = 0: one span takes everything.
-template <int RT>
+template <int R>
 __device__ __forceinline__ bool kv4_work(const Kv4& c, int G, int slots, int fill, bool by_tile, int index, Kv4Work* w) {
     const int lane = threadIdx.x & 63;
-    auto groups_of = [&](const Kv4Seq& s) { return (s.rows * G + 16 * RT - 1) / (16 * RT); };   // rows * G <= 2^30
+    auto groups_of = [&](const Kv4Seq& s) { return (s.rows * G + R - 1) / R; };   // rows * G <= 2^30
     const Kv4Seq first = kv4_seq(c, min(lane, c.B - 1));
     int span = 0x40000000;
     if (slots > 0) {
@@ -338,10 +339,10 @@ __device__ __forceinline__ bool kv4_work(const Kv4& c, int G, int slots, int fil
     return false;
 }
 
-// Partial results of a slot: sums [16 RT][D], then the maxima and the sums of
-// weights [16 RT] each.
-template <int D, int RT>
-constexpr size_t part_words() { return 16 * RT * (D + 2); }
+// Partial results of a slot: sums [R][D], then the maxima and the sums of
+// weights [R] each, R the rows of a block.
+template <int D, int R>
+constexpr size_t part_words() { return R * (D + 2); }
 
 // Four operand pairs of a dword of codes: 1 + c / 16 in bf16.
 // The constants come in registers: as literals they would cost an instruction
@@ -374,8 +375,8 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t* hi, uint32_t*
 // Floats of a row in LDS, so that 16 rows' 16 bytes hit all banks; of the block.
 template <int D>
 constexpr int lds_row() { return D + 4; }
-template <int D, int W>
-constexpr int lds_words() { return W * 16 * lds_row<D>(); }
+template <int D, int W, int TR>
+constexpr int lds_words() { return W * TR * lds_row<D>(); }
 
 // A step's scales s and 1 + z / 16 (of V: the operand, in its order of tokens).
 template <int NG>
@@ -400,21 +401,26 @@ __device__ __forceinline__ void kv4_finish(float (&x)[D / 64], float total, int 
     for (int i = 0; i < D / 64; ++i) y[lane * (D / 64) + i] = T::from_f32(x[i]);
 }
 
-// LO: q needs its second part (rotated, or fp16's 11 bits).
-template <class T, int D, int NG, int RT, bool LO, int W>
+// RT tiles of TR rows.  TR = 16: a column of the products a row, and a second
+// product where q has a second part (LO: rotated, or fp16's 11 bits) and for the
+// weights' second part.  TR = 8: columns 8 and on take the second parts of rows
+// 0 to 7, half the products (131072 tokens, 4 heads a
+// key head: 37.6 -> 36.1 us, 32 ragged sequences 67.2 -> 64.3).
+template <class T, int D, int NG, int RT, int TR, bool LO, int W>
 __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_attn_kv4(Kv4 c, AttnArgs a, int slots, int fill, float* parts) {
-    constexpr int KS = D / 32, SPG = KS / NG, DT = D / 16, DPG = DT / NG;
+    constexpr int KS = D / 32, SPG = KS / NG, DT = D / 16, DPG = DT / NG, R = TR * RT;
+    constexpr bool HALF = TR == 8;
     constexpr float kMove = 8.0f;   // the maximum follows when weights would pass 2^8
     constexpr int kRow = lds_row<D>(), DEPTH = RT == 1 && (D == 64 || (D == 128 && NG <= 2)) ? 2 : 1;
     // the waves' scales of a step; then their sums of a tile
     extern __shared__ __align__(16) uint32_t lds[];
-    static_assert(W * sizeof(Stage<NG>) <= 4 * lds_words<D, W>(), "a step's scales fit where the sums go");
+    static_assert(W * sizeof(Stage<NG>) <= 4 * lds_words<D, W, TR>(), "a step's scales fit where the sums go");
     float* lds_o = reinterpret_cast<float*>(lds);
     __shared__ float lds_top[W][16], lds_sum[W][16];
     const int lane = threadIdx.x & 63, wave = wave_of_block(), col = lane & 15, quad = lane >> 4;
     const int g = blockIdx.x, G = a.Hq / c.heads;
     Kv4Work w;
-    if (!kv4_work<RT>(c, G, slots, fill, false, blockIdx.y + blockIdx.z * gridDim.y, &w)) return;
+    if (!kv4_work<R>(c, G, slots, fill, false, blockIdx.y + blockIdx.z * gridDim.y, &w)) return;
     const int begin = w.chunk * w.span, end = min(begin + w.span, w.tokens);
 
     // page of the 16 tokens from `pos` on, -1 past the end
@@ -466,11 +472,11 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_attn_kv4(Kv4 c, At
     int next_k = page_at(pos + DEPTH * kStride + 16 * (col >> 2)), next_v = page_at(pos + DEPTH * kStride + 16 * quad);
     // rows of the tiles: what they see, and q
     int seen[RT];
-    u32x4 qh[RT][KS], ql[RT][LO ? KS : 1];
+    u32x4 qh[RT][KS], ql[RT][LO && !HALF ? KS : 1];
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
         // a column past the last row repeats it
-        const int r = min((w.tile * RT + t) * 16 + col, w.rows * G - 1), i = r / G, h = g * G + r % G;
+        const int r = min((w.tile * RT + t) * TR + (HALF ? col & 7 : col), w.rows * G - 1), i = r / G, h = g * G + r % G;
         seen[t] = w.tokens - w.rows + i + 1;
         const uint16_t* p = a.q + (w.first + i) * a.q_row + h * a.q_head + 8 * quad;
 #pragma unroll
@@ -545,9 +551,10 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_attn_kv4(Kv4 c, At
             for (int j = 0; j < 4; ++j) {
                 uint32_t hi, lo;
                 split2(x[s][2 * j], x[s][2 * j + 1], &hi, &lo);
+                if (HALF && col >= 8) hi = lo;
                 qh[t][s][j] = hi;
                 float v = bf16_lo(hi) + bf16_hi(hi);
-                if constexpr (LO) {
+                if constexpr (LO && !HALF) {
                     ql[t][s][j] = lo;
                     v += bf16_lo(lo) + bf16_hi(lo);
                 }
@@ -616,7 +623,7 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_attn_kv4(Kv4 c, At
 #pragma unroll
                     for (int t = 0; t < RT; ++t) {
                         acc[t] = Bf16::mfma(op, qh[t][k], acc[t]);
-                        if constexpr (LO) acc[t] = Bf16::mfma(op, ql[t][k], acc[t]);
+                        if constexpr (LO && !HALF) acc[t] = Bf16::mfma(op, ql[t][k], acc[t]);
                     }
                 }
 #pragma unroll
@@ -627,6 +634,12 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_attn_kv4(Kv4 c, At
                         s[t][4 * x + i] = n == 0 ? sc[i] * d : __builtin_fmaf(sc[i], d, s[t][4 * x + i]);
                     }
             }
+        }
+        if constexpr (HALF) {
+#pragma unroll
+            for (int t = 0; t < RT; ++t)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) s[t][i] += lane_xor<8>(s[t][i]);   // the parts' scores together, in both
         }
         // a later step's K while this one's weights and V are at work
         const int page = pv[at], ahead = pos + DEPTH * kStride;
@@ -709,7 +722,7 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_attn_kv4(Kv4 c, At
                         const float x0 = s[t][8 * u + t0] * s0, x1 = s[t][8 * u + t1] * s1;
                         uint32_t h, l;
                         split2(x0, x1, &h, &l);
-                        hi[t][j] = h;
+                        hi[t][j] = HALF && col >= 8 ? l : h;
                         lo[t][j] = l;
                     }
                 }
@@ -720,7 +733,7 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_attn_kv4(Kv4 c, At
 #pragma unroll
                 for (int t = 0; t < RT; ++t) {
                     zp[t][n] = Bf16::mfma(zo, hi[t], zp[t][n]);
-                    zp[t][n] = Bf16::mfma(zo, lo[t], zp[t][n]);
+                    if constexpr (!HALF) zp[t][n] = Bf16::mfma(zo, lo[t], zp[t][n]);
                 }
 #pragma unroll
                 for (int d = n * DPG; d < (n + 1) * DPG; ++d) {
@@ -729,7 +742,7 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_attn_kv4(Kv4 c, At
 #pragma unroll
                     for (int t = 0; t < RT; ++t) {
                         o[t][d] = Bf16::mfma(op, hi[t], o[t][d]);
-                        o[t][d] = Bf16::mfma(op, lo[t], o[t][d]);
+                        if constexpr (!HALF) o[t][d] = Bf16::mfma(op, lo[t], o[t][d]);
                     }
                 }
             }
@@ -749,7 +762,7 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_attn_kv4(Kv4 c, At
 
     // the waves' results joined: rows of the tile, wave by wave
     const bool whole = w.chunks == 1;
-    float* part = parts + ((size_t)g * slots + w.slot) * part_words<D, RT>();
+    float* part = parts + ((size_t)g * slots + w.slot) * part_words<D, R>();
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
         sum[t] += __shfl_xor(sum[t], 16);
@@ -767,10 +780,14 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_attn_kv4(Kv4 c, At
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 v[i] = poison[t] >> (d / DPG) & 1 ? __uint_as_float(kKv4Nan) : 16.0f * (o[t][d][i] - zp[t][d / DPG][i]);
-            *reinterpret_cast<f32x4*>(lds_o + (wave * 16 + col) * kRow + 16 * d + 4 * quad) = v;
+            if constexpr (HALF) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] += lane_xor<8>(v[i]);
+            }
+            if (!HALF || col < 8) *reinterpret_cast<f32x4*>(lds_o + (wave * TR + col) * kRow + 16 * d + 4 * quad) = v;
         }
         __syncthreads();
-        const int r0 = (w.tile * RT + t) * 16, n = min(16, w.rows * G - r0);
+        const int r0 = (w.tile * RT + t) * TR, n = min(TR, w.rows * G - r0);
         for (int r = wave; r < n; r += W) {
             float m = lds_top[0][r], total = 0.0f, x[D / 64] = {};
 #pragma unroll
@@ -783,18 +800,18 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_attn_kv4(Kv4 c, At
                 total = __builtin_fmaf(f, lds_sum[k][r], total);
 #pragma unroll
                 for (int i = 0; i < D / 64; ++i)
-                    x[i] = __builtin_fmaf(f, lds_o[(k * 16 + r) * kRow + lane * (D / 64) + i], x[i]);
+                    x[i] = __builtin_fmaf(f, lds_o[(k * TR + r) * kRow + lane * (D / 64) + i], x[i]);
             }
             if (whole) {
                 const int i0 = (r0 + r) / G, h = g * G + (r0 + r) % G;
                 kv4_finish<T, D>(x, total, c.rotate, a.y + ((int64_t)(w.first + i0) * a.Hq + h) * D);
             } else {
-                float* p = part + (16 * t + r) * D + lane * (D / 64);
+                float* p = part + (TR * t + r) * D + lane * (D / 64);
 #pragma unroll
                 for (int i = 0; i < D / 64; ++i) p[i] = x[i];
                 if (lane == 0) {
-                    part[16 * RT * D + 16 * t + r] = m;
-                    part[16 * RT * (D + 1) + 16 * t + r] = total;
+                    part[R * D + TR * t + r] = m;
+                    part[R * (D + 1) + TR * t + r] = total;
                 }
             }
         }
@@ -804,16 +821,16 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_attn_kv4(Kv4 c, At
 // The slots of a tile group's spans joined: a block a row, its waves every
 // fourth span, 16 at a time, so that few loads wait for each other.
 constexpr int kJoinWaves = 4;
-template <class T, int D, int RT>
+template <class T, int D, int R>
 __global__ __launch_bounds__(64 * kJoinWaves) void k_attn_kv4_join(Kv4 c, AttnArgs a, int slots, int fill, int row_blocks,
                                                                    const float* parts) {
-    constexpr int N = D / 64, R = 16 * RT, W = kJoinWaves;
-    constexpr size_t P = part_words<D, RT>();
+    constexpr int N = D / 64, W = kJoinWaves;
+    constexpr size_t P = part_words<D, R>();
     __shared__ float lds_x[W][D], lds_sum[W], lds_top[W];
     const int lane = threadIdx.x & 63, wave = wave_of_block();
     const int g = blockIdx.x / row_blocks, G = a.Hq / c.heads;
     Kv4Work w;
-    if (!kv4_work<RT>(c, G, slots, fill, true, blockIdx.y + blockIdx.z * gridDim.y, &w) || w.chunks == 1) return;
+    if (!kv4_work<R>(c, G, slots, fill, true, blockIdx.y + blockIdx.z * gridDim.y, &w) || w.chunks == 1) return;
     const int r0 = w.tile * R, n = min(R, w.rows * G - r0);
     const float* part = parts + ((size_t)g * slots + w.slot) * P;
     for (int r = blockIdx.x % row_blocks; r < n; r += row_blocks) {
@@ -924,14 +941,17 @@ namespace {
 // turns of them.
 constexpr int kOneSpan = 1024;
 struct Grid {
-    int tiles, groups, slots, fill;
+    int tiles, rows, groups, slots, fill;   // rows: of a tile
 };
 Grid attn_kv4_grid(int T, int G, int heads, int dim, int page, int width, int B) {
     Grid g;
     const int most = dim == 64 ? max_tiles<64>() : dim == 128 ? max_tiles<128>() : max_tiles<256>();
     const int64_t rows = ((int64_t)T * G + B - 1) / B;   // of a sequence, on average
+    g.rows = rows <= 8 ? 8 : 16;
     g.tiles = rows > 16 * most ? most : (int)(rows + 15) / 16;
-    g.groups = (int)(((int64_t)T * G + (int64_t)(B < T ? B : T) * (16 * g.tiles - 1)) / (16 * g.tiles));
+    const int R = g.rows * g.tiles;
+    // a sequence's rows are a multiple of G: the last group of each lacks at most R - gcd(G, R)
+    g.groups = (int)(((int64_t)T * G + (int64_t)(B < T ? B : T) * (R - std::gcd(G, R))) / R);
     g.slots = g.fill = 0;
     if ((int64_t)width * page > kOneSpan) {
         g.fill = (dim == 256 ? 256 : 512) / heads;
@@ -940,15 +960,15 @@ Grid attn_kv4_grid(int T, int G, int heads, int dim, int page, int width, int B)
     }
     return g;
 }
-size_t part_bytes(int dim, int tiles) { return (size_t)16 * tiles * (dim + 2) * 4; }
+size_t part_bytes(int dim, int rows) { return (size_t)rows * (dim + 2) * 4; }
 
-template <class T, int D, int NG, int RT, int W>
+template <class T, int D, int NG, int RT, int TR, int W>
 hipError_t run_attn_kv4(const AttnArgs& a, const Kv4& c, const Grid& g, float* ws, hipStream_t st) {
     const auto grid = [&](int n, int x) {
         const int y = n < 32768 ? n : 32768;
         return dim3(x, y, (n + y - 1) / y);
     };
-    constexpr int lds = 4 * lds_words<D, W>();
+    constexpr int R = TR * RT, lds = 4 * lds_words<D, W, TR>();
     hipError_t e = hipSuccess;
     const auto go = [&](auto kernel, std::atomic<uint64_t>& done) {
         if (lds > 65536 && (e = opt_in_lds(reinterpret_cast<const void*>(kernel), lds, done)) != hipSuccess) return;
@@ -956,16 +976,16 @@ hipError_t run_attn_kv4(const AttnArgs& a, const Kv4& c, const Grid& g, float* w
         e = hipGetLastError();
     };
     static std::atomic<uint64_t> done[2];
-    if (c.rotate || a.fp16) go(k_attn_kv4<T, D, NG, RT, true, W>, done[0]);
-    else go(k_attn_kv4<T, D, NG, RT, false, W>, done[1]);
+    if (TR == 8 || c.rotate || a.fp16) go(k_attn_kv4<T, D, NG, RT, TR, true, W>, done[0]);
+    else if constexpr (TR == 16) go(k_attn_kv4<T, D, NG, RT, TR, false, W>, done[1]);
     if (e != hipSuccess || g.slots == 0) return e;
     // as many blocks as a group has rows on average, while there are few groups: some 1024 in all.  us a call, a block
     // a row / 1024 / 512: 64 sequences of 4000 tokens (joins nothing) 82 / 79.5 / 78.7, 4 of 8 new tokens 35 / 35 /
     // 37.6, 2 of 200 145 / 126 / 125
     const int64_t rows = ((int64_t)c.T * (a.Hq / c.heads) + g.groups - 1) / g.groups;
     const int64_t most = 1024 / ((int64_t)g.groups * c.heads) + 1;
-    const int row_blocks = (int)(rows < 16 * RT ? (rows < most ? rows : most) : (16 * RT < most ? 16 * RT : most));
-    k_attn_kv4_join<T, D, RT><<<grid(g.groups, c.heads * row_blocks), 64 * kJoinWaves, 0, st>>>(c, a, g.slots, g.fill, row_blocks, ws);
+    const int row_blocks = (int)(rows < R ? (rows < most ? rows : most) : (R < most ? R : most));
+    k_attn_kv4_join<T, D, R><<<grid(g.groups, c.heads * row_blocks), 64 * kJoinWaves, 0, st>>>(c, a, g.slots, g.fill, row_blocks, ws);
     return hipGetLastError();
 }
 
@@ -974,19 +994,19 @@ hipError_t run_attn_kv4(const AttnArgs& a, const Kv4& c, const Grid& g, float* w
 size_t attn_kv4_workspace(int T, int Hq, int heads, int dim, int page, int width, int B) {
     if (T == 0 || B == 0) return 0;
     const Grid g = attn_kv4_grid(T, Hq / heads, heads, dim, page, width, B);
-    return (size_t)g.slots * heads * part_bytes(dim, g.tiles);
+    return (size_t)g.slots * heads * part_bytes(dim, g.rows * g.tiles);
 }
 
 hipError_t launch_attn_kv4(const AttnArgs& a, const Kv4& c, void* ws, hipStream_t st) {
     const Grid g = attn_kv4_grid(c.T, a.Hq / c.heads, c.heads, c.dim, 1 << c.page_log2, c.width, c.B);
     hipError_t e = hipErrorInvalidValue;
     by_form(c, [&](auto d, auto ng) {
-        const auto tiles = [&](auto rt) {
+        const auto tiles = [&](auto rt, auto rows) {
             if constexpr (rt <= max_tiles<d>()) {
-                if (g.tiles != rt) return;
+                if (g.tiles != rt || g.rows != rows) return;
                 const auto run = [&](auto waves) {
-                    e = a.fp16 ? run_attn_kv4<Fp16, d, ng, rt, waves>(a, c, g, (float*)ws, st)
-                               : run_attn_kv4<Bf16, d, ng, rt, waves>(a, c, g, (float*)ws, st);
+                    e = a.fp16 ? run_attn_kv4<Fp16, d, ng, rt, rows, waves>(a, c, g, (float*)ws, st)
+                               : run_attn_kv4<Bf16, d, ng, rt, rows, waves>(a, c, g, (float*)ws, st);
                 };
                 // (a head of 256 takes the registers of two waves)
                 if constexpr (d < 256 && rt == 1) {
@@ -995,9 +1015,11 @@ hipError_t launch_attn_kv4(const AttnArgs& a, const Kv4& c, void* ws, hipStream_
                 run(std::integral_constant<int, 4>());
             }
         };
-        tiles(std::integral_constant<int, 1>());
-        tiles(std::integral_constant<int, 2>());
-        tiles(std::integral_constant<int, 3>());
+        const std::integral_constant<int, 16> sixteen;
+        tiles(std::integral_constant<int, 1>(), std::integral_constant<int, 8>());
+        tiles(std::integral_constant<int, 1>(), sixteen);
+        tiles(std::integral_constant<int, 2>(), sixteen);
+        tiles(std::integral_constant<int, 3>(), sixteen);
     });
     return e;
 }

@@ -341,8 +341,9 @@ def test_rows_outside_the_sequences():
     out = torch.full_like(q, 7.0)
     y = crp.attn_kv4(q, s.cache, s.table, ints(s.lens), ints([2, 3, 6]), out=out)
     assert y is out and (out[:2] == 7).all() and (out[6:] == 7).all()
-    want = crp.attn_kv4(q[2:6].contiguous(), s.cache, s.table, ints(s.lens), ints([0, 1, 4]))
-    assert torch.equal(out[2:6], want)
+    # (bits may differ from a call of other sizes: how rows are tiled goes by T)
+    want, tol = s.reference(q[2:6], [1, 3])
+    assert (np.abs(out[2:6].double().cpu().numpy() - want) <= tol).all()
 
 
 def test_a_long_cache():
