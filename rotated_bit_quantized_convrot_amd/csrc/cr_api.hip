@@ -973,7 +973,7 @@ cr_status cr_kv4_append(int dtype, const void* k, int64_t k_row, int64_t k_head,
 size_t cr_attn_kv4_workspace_bytes(int T, int Hq, const cr_kv4* cache, int width, int B) {
     if (check_kv4(cache) != CR_OK) return 0;
     if (check_attn(CR_BF16, T, Hq, cache->heads, cache->dim, B, 1.0f) != CR_OK || check_width(width) != CR_OK) return 0;
-    const size_t n = cr::attn_kv4_workspace(T, Hq, cache->heads, cache->dim, cache->page, width, B);
+    const size_t n = cr::attn_kv4_workspace(T, Hq, cache->heads, cache->dim, cache->group, cache->page, width, B);
     return n < 256 ? 256 : n;
 }
 
@@ -988,7 +988,7 @@ cr_status cr_attn_kv4(int dtype, const void* q, int64_t q_row, int64_t q_head, i
     const Heads x{"q", q, q_row, q_head, Hq};
     if ((s = check_heads(x, T, cache->dim)) != CR_OK) return s;
     if ((s = check_kv4_call(cache, table, width, lens, cu)) != CR_OK) return s;
-    const size_t need = cr::attn_kv4_workspace(T, Hq, cache->heads, cache->dim, cache->page, width, B);
+    const size_t need = cr::attn_kv4_workspace(T, Hq, cache->heads, cache->dim, cache->group, cache->page, width, B);
     if (!y || (!ws && need)) return fail(CR_ERR_NULL, "y or workspace is NULL");
     if (!aligned16(y) || !aligned16(ws)) return fail(CR_ERR_ALIGN, "y or workspace not 16-byte aligned");
     if ((s = check_apart(x, T, cache->dim, y, (size_t)T * Hq * cache->dim * 2)) != CR_OK) return s;

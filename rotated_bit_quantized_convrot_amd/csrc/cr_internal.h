@@ -156,7 +156,7 @@ hipError_t launch_attn_prompt(const AttnArgs& a, hipStream_t st);
 // types, q, Hq, scale and y).
 hipError_t launch_kv4_append(bool fp16, const uint16_t* k, int64_t k_row, int64_t k_head, const uint16_t* v,
                              int64_t v_row, int64_t v_head, const Kv4& c, hipStream_t st);
-size_t attn_kv4_workspace(int T, int Hq, int heads, int dim, int page, int width, int B);
+size_t attn_kv4_workspace(int T, int Hq, int heads, int dim, int group, int page, int width, int B);
 hipError_t launch_attn_kv4(const AttnArgs& a, const Kv4& c, void* ws, hipStream_t st);
 
 struct GemmArgs {

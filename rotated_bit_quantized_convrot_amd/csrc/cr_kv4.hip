@@ -276,9 +276,14 @@ struct Kv4Work {
 // chunk 0).  Every wave counts for itself, 64 sequences at a time.
 //   `fill` blocks of a head run at once.  A block's start and end cost as much
 // as some 500 tokens, so the spans are the shortest with which all blocks run
-// at once, up to twice fill's share; then at most fill / 2 blocks more than
-// tile groups are needed, which is what the grid has.  A sequence's spans are
-// equal.  slots = 0: one span takes everything.
+// at once, up to twice fill's share.  Where that leaves them unlike (spans
+// beyond 1.25 shares, the longest sequence beyond 1.25 times the mean) and a
+// share is 2048 tokens and more, the spans are half a share and the blocks
+// follow each other, at most 2 fill more than tile groups, which is what the
+// grid has.  us, at once / half shares: 64 sequences of up to 30000 tokens
+// 259 / 238, 100 of up to 6000 119.9 / 109.7; where both rules are off, 64 of
+// 4000 77.2 / 82.7, 64 of 2048 39.3 / 47.4.  A sequence's spans are equal.
+// slots = 0: one span takes everything.
 template <int R>
 __device__ __forceinline__ bool kv4_work(const Kv4& c, int G, int slots, int fill, bool by_tile, int index, Kv4Work* w) {
     const int lane = threadIdx.x & 63;
@@ -287,22 +292,26 @@ __device__ __forceinline__ bool kv4_work(const Kv4& c, int G, int slots, int fil
     int span = 0x40000000;
     if (slots > 0) {
         float total = 0.0f;   // of tokens, group by group
+        int top = 0, groups = 0;   // the longest sequence; tile groups
         for (int b0 = 0; b0 < c.B; b0 += 64) {
             const Kv4Seq s = b0 == 0 ? first : kv4_seq(c, min(b0 + lane, c.B - 1));
             const int n = b0 + lane < c.B ? groups_of(s) : 0;
             total += __int_as_float(__builtin_amdgcn_readlane(wave_scan(__float_as_int((float)n * (float)s.tokens), add_floats), 63));
+            top = max(top, __builtin_amdgcn_readlane(wave_scan(n > 0 ? s.tokens : 0, [](int x, int y) { return max(x, y); }), 63));
+            groups += __builtin_amdgcn_readlane(wave_scan(n, add_ints), 63);
         }
         const int n = lane < c.B ? groups_of(first) : 0;
         // in units of kMinSpan: fill's share, and twice it, with which at most fill / 2 blocks more than groups are
         // needed (the sum is rounded: a little more than it)
         const float e = fminf(total / (kMinSpan * (float)fill), 2097152.0f);
         int lo = max((int)e, 1), hi = (int)(2.0f * e * 1.0001f) + 1;
-        while (c.B <= 64 && lo < hi) {   // (more sequences: as they are)
+        while (c.B <= 64 && lo < hi) {
             const int mid = (lo + hi) / 2;
             span = mid * kMinSpan;
             if (__builtin_amdgcn_readlane(wave_scan(n * max((first.tokens + span - 1) / span, 1), add_ints), 63) <= fill) hi = mid;
             else lo = mid + 1;
         }
+        if (e >= 2048.0f / kMinSpan && (float)hi > 1.25f * e && (float)top * (float)groups > 1.25f * total) hi = (int)(0.5f * e) + 1;
         span = hi * kMinSpan;
     }
     int at = 0, slot = 0;
@@ -401,17 +410,29 @@ __device__ __forceinline__ void kv4_finish(float (&x)[D / 64], float total, int 
     for (int i = 0; i < D / 64; ++i) y[lane * (D / 64) + i] = T::from_f32(x[i]);
 }
 
+// Blocks of four waves that a CU holds, by their registers (three: 168 a lane;
+// more key groups or 16 rows of them spill).
+constexpr int blocks_a_cu(int dim, int groups, int rows) { return dim == 256 ? 1 : rows == 8 && dim * groups <= 256 ? 3 : 2; }
+
 // RT tiles of TR rows.  TR = 16: a column of the products a row, and a second
 // product where q has a second part (LO: rotated, or fp16's 11 bits) and for the
 // weights' second part.  TR = 8: columns 8 and on take the second parts of rows
 // 0 to 7, half the products (131072 tokens, 4 heads a
 // key head: 37.6 -> 36.1 us, 32 ragged sequences 67.2 -> 64.3).
+//   The bytes bound it where the cache is long: 131072 tokens of 8 key heads of
+// 128 are 142.6 MB, 30.2 us at a large copy's 4.7 TB/s; 5.4 to 5.9 TB/s while all
+// blocks read, and some 8 us before that (lengths, table, q's rotation, the first
+// loads, each after the other).  Short calls are these waits.
+//   Steps of loads in flight a wave: with three blocks a CU one is enough at
+// D = 128 (1 / 2 / 3 steps, two blocks: 39.8 / 40.2 / 40.5); D = 64 has the
+// registers for two (three blocks: 139).
 template <class T, int D, int NG, int RT, int TR, bool LO, int W>
-__global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_attn_kv4(Kv4 c, AttnArgs a, int slots, int fill, float* parts) {
+__global__ __launch_bounds__(64 * W, W == 4 ? blocks_a_cu(D, NG, TR) : D == 256 ? 1 : 2) void k_attn_kv4(Kv4 c, AttnArgs a, int slots,
+                                                                                              int fill, float* parts) {
     constexpr int KS = D / 32, SPG = KS / NG, DT = D / 16, DPG = DT / NG, R = TR * RT;
     constexpr bool HALF = TR == 8;
     constexpr float kMove = 8.0f;   // the maximum follows when weights would pass 2^8
-    constexpr int kRow = lds_row<D>(), DEPTH = RT == 1 && (D == 64 || (D == 128 && NG <= 2)) ? 2 : 1;
+    constexpr int kRow = lds_row<D>(), DEPTH = RT == 1 && D == 64 ? 2 : 1;
     // the waves' scales of a step; then their sums of a tile
     extern __shared__ __align__(16) uint32_t lds[];
     static_assert(W * sizeof(Stage<NG>) <= 4 * lds_words<D, W, TR>(), "a step's scales fit where the sums go");
@@ -934,16 +955,15 @@ hipError_t launch_kv4_append(bool fp16, const uint16_t* k, int64_t k_row, int64_
 namespace {
 
 // Rows a block takes, in tiles of 16; the tile groups that there can be; the
-// blocks of a head that the chip runs at once (two a CU, one where a wave takes
-// the registers of two) and those that the grid has; none where no sequence is
-// worth a second span.
+// blocks of a head that the chip is to run at once and those that the grid has;
+// none where no sequence is worth a second span.
 // Tokens up to which one block takes a sequence, with twice the waves: two
 // turns of them.
 constexpr int kOneSpan = 1024;
 struct Grid {
     int tiles, rows, groups, slots, fill;   // rows: of a tile
 };
-Grid attn_kv4_grid(int T, int G, int heads, int dim, int page, int width, int B) {
+Grid attn_kv4_grid(int T, int G, int heads, int dim, int scales, int page, int width, int B) {
     Grid g;
     const int most = dim == 64 ? max_tiles<64>() : dim == 128 ? max_tiles<128>() : max_tiles<256>();
     const int64_t rows = ((int64_t)T * G + B - 1) / B;   // of a sequence, on average
@@ -954,9 +974,12 @@ Grid attn_kv4_grid(int T, int G, int heads, int dim, int page, int width, int B)
     g.groups = (int)(((int64_t)T * G + (int64_t)(B < T ? B : T) * (R - std::gcd(G, R))) / R);
     g.slots = g.fill = 0;
     if ((int64_t)width * page > kOneSpan) {
-        g.fill = (dim == 256 ? 256 : 512) / heads;
+        // A sequence or two are even by themselves: two blocks a CU do with fewer starts.  us, 2 / 3 blocks: 131072
+        // tokens 40.0 / 40.7, 20000 and 3000 14.0 / 14.5; 3 ragged sequences 19.5 / 19.4, 32 70.6 / 56.4, 64 97.1 / 72.7
+        const int blocks = blocks_a_cu(dim, scales, g.rows);
+        g.fill = 256 * (B < 3 && blocks > 2 ? 2 : blocks) / heads;
         if (g.fill < 1) g.fill = 1;
-        g.slots = g.fill / 2 + g.groups + 1 > g.fill ? g.fill / 2 + g.groups + 1 : g.fill;
+        g.slots = 2 * g.fill + g.groups + 1;
     }
     return g;
 }
@@ -991,14 +1014,14 @@ hipError_t run_attn_kv4(const AttnArgs& a, const Kv4& c, const Grid& g, float* w
 
 }  // namespace
 
-size_t attn_kv4_workspace(int T, int Hq, int heads, int dim, int page, int width, int B) {
+size_t attn_kv4_workspace(int T, int Hq, int heads, int dim, int group, int page, int width, int B) {
     if (T == 0 || B == 0) return 0;
-    const Grid g = attn_kv4_grid(T, Hq / heads, heads, dim, page, width, B);
+    const Grid g = attn_kv4_grid(T, Hq / heads, heads, dim, dim / group, page, width, B);
     return (size_t)g.slots * heads * part_bytes(dim, g.rows * g.tiles);
 }
 
 hipError_t launch_attn_kv4(const AttnArgs& a, const Kv4& c, void* ws, hipStream_t st) {
-    const Grid g = attn_kv4_grid(c.T, a.Hq / c.heads, c.heads, c.dim, 1 << c.page_log2, c.width, c.B);
+    const Grid g = attn_kv4_grid(c.T, a.Hq / c.heads, c.heads, c.dim, c.dim / c.group, 1 << c.page_log2, c.width, c.B);
     hipError_t e = hipErrorInvalidValue;
     by_form(c, [&](auto d, auto ng) {
         const auto tiles = [&](auto rt, auto rows) {

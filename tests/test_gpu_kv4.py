@@ -214,6 +214,25 @@ def test_spans(H, Hq, D, lens):
     s.check([min(1, n) for n in lens], Hq)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("lens", [[20000, 300, 4000, 2, 900, 6000], [400] * 68 + [9000, 3], [9000] * 4])
+def test_uneven_spans(D, lens):
+    """Many key heads leave few blocks a head, whose shares are long: uneven
+    sequences in spans that follow each other, even ones as they are."""
+    H = 64
+    s = Setup(lens, H, D, 64, 128, True, torch.bfloat16, seed=D, spare=30)
+    few = s.k[:, :2].contiguous(), s.v[:, :2].contiguous()
+    s.k, s.v = (x.repeat(1, H // 2, 1) for x in few)
+    s.fill()
+    new = [1] * len(lens)
+    q = s.queries(new, 4)
+    got = s.attend(q.repeat(1, H // 2, 1), new)
+    s.k, s.v = few
+    y, tol = s.reference(q, new)
+    assert (np.abs(got[:, :4].double().cpu().numpy() - y) / tol).max() <= 1
+    assert torch.equal(got, got[:, :4].repeat(1, H // 2, 1))
+
+
 def test_two_workspaces_at_once():
     """Two calls on two streams, a workspace each."""
     s = Setup([3000, 100, 1500], 2, 128, 64, 64, True, torch.bfloat16, seed=20).fill()
