@@ -263,6 +263,7 @@ __global__ __launch_bounds__(256) void k_kv4_append(AppendArgs a) {
 // values of 8 bits each, in bf16's range whatever T.
 constexpr int kStep = 64;
 constexpr int kMinSpan = 4 * kStep;
+constexpr float kMostSpan = 2097152.0f;   // kMinSpans: twice of it hold the longest sequence, 2^30 tokens
 
 template <int D>
 constexpr int max_tiles() { return D == 64 ? 3 : D == 128 ? 2 : 1; }
@@ -303,7 +304,7 @@ __device__ __forceinline__ bool kv4_work(const Kv4& c, int G, int slots, int fil
         const int n = lane < c.B ? groups_of(first) : 0;
         // in units of kMinSpan: fill's share, and twice it, with which at most fill / 2 blocks more than groups are
         // needed (the sum is rounded: a little more than it)
-        const float e = fminf(total / (kMinSpan * (float)fill), 2097152.0f);
+        const float e = fminf(total / (kMinSpan * (float)fill), kMostSpan);
         int lo = max((int)e, 1), hi = (int)(2.0f * e * 1.0001f) + 1;
         while (c.B <= 64 && lo < hi) {
             const int mid = (lo + hi) / 2;
@@ -311,7 +312,8 @@ __device__ __forceinline__ bool kv4_work(const Kv4& c, int G, int slots, int fil
             if (__builtin_amdgcn_readlane(wave_scan(n * max((first.tokens + span - 1) / span, 1), add_ints), 63) <= fill) hi = mid;
             else lo = mid + 1;
         }
-        if (e >= 2048.0f / kMinSpan && (float)hi > 1.25f * e && (float)top * (float)groups > 1.25f * total) hi = (int)(0.5f * e) + 1;
+        if (e >= 2048.0f / kMinSpan && e < kMostSpan && (float)hi > 1.25f * e && (float)top * (float)groups > 1.25f * total)
+            hi = (int)(0.5f * e) + 1;
         span = hi * kMinSpan;
     }
     int at = 0, slot = 0;
