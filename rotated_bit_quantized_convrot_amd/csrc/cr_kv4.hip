@@ -7,6 +7,7 @@
 //   lo = min(0, min x'), hi = max(0, max x'), s = hi / 15 - lo / 15 to the
 //   nearest float32 whose low four bits are 0, z = clamp(rint(-lo / s), 0, 15),
 //   c = clamp(rint(x' / s) + z, 0, 15); both 0 where s = 0.
+#include <algorithm>
 #include <numeric>
 #include <type_traits>
 
@@ -275,7 +276,7 @@ struct Kv4Work {
 };
 // The work of block `index` of `slots` (by_tile: of tile group `index`, its
 // chunk 0).  Every wave counts for itself, 64 sequences at a time.
-//   `fill` blocks of a head run at once.  A block's start and end cost as much
+//   `fill` blocks of a head run at once (`few` where that is enough).  A block's start and end cost as much
 // as some 500 tokens, so the spans are the shortest with which all blocks run
 // at once, up to twice fill's share.  Where that leaves them unlike (spans
 // beyond 1.25 shares, the longest sequence beyond 1.25 times the mean) and a
@@ -286,7 +287,7 @@ struct Kv4Work {
 // 4000 77.2 / 82.7, 64 of 2048 39.3 / 47.4.  A sequence's spans are equal.
 // slots = 0: one span takes everything.
 template <int R>
-__device__ __forceinline__ bool kv4_work(const Kv4& c, int G, int slots, int fill, bool by_tile, int index, Kv4Work* w) {
+__device__ __forceinline__ bool kv4_work(const Kv4& c, int G, int slots, int fill, int few, bool by_tile, int index, Kv4Work* w) {
     const int lane = threadIdx.x & 63;
     auto groups_of = [&](const Kv4Seq& s) { return (s.rows * G + R - 1) / R; };   // rows * G <= 2^30
     const Kv4Seq first = kv4_seq(c, min(lane, c.B - 1));
@@ -301,6 +302,11 @@ __device__ __forceinline__ bool kv4_work(const Kv4& c, int G, int slots, int fil
             top = max(top, __builtin_amdgcn_readlane(wave_scan(n > 0 ? s.tokens : 0, [](int x, int y) { return max(x, y); }), 63));
             groups += __builtin_amdgcn_readlane(wave_scan(n, add_ints), 63);
         }
+        // A sequence or two are even by themselves: two blocks a CU do, with fewer starts, up to shares of some 2200
+        // tokens.  us, 2 / 3 blocks: 20000 and 3000 tokens 14.0 / 14.5, 100000 33.2 / 33.9, 131072 40.3 / 40.8, 160000
+        // 49.2 / 48.2, 250000 71.2 / 68.6, 500000 125 / 119; 3 ragged sequences 19.5 / 19.4, 32 70.6 / 56.4, 64 97.1 /
+        // 72.7
+        if (c.B < 3 && total < 2200.0f * (float)few) fill = few;
         const int n = lane < c.B ? groups_of(first) : 0;
         // in units of kMinSpan: fill's share, and twice it, with which at most fill / 2 blocks more than groups are
         // needed (the sum is rounded: a little more than it)
@@ -430,7 +436,7 @@ constexpr int blocks_a_cu(int dim, int groups, int rows) { return dim == 256 ? 1
 // registers for two (three blocks: 139).
 template <class T, int D, int NG, int RT, int TR, bool LO, int W>
 __global__ __launch_bounds__(64 * W, W == 4 ? blocks_a_cu(D, NG, TR) : D == 256 ? 1 : 2) void k_attn_kv4(Kv4 c, AttnArgs a, int slots,
-                                                                                              int fill, float* parts) {
+                                                                                              int fill, int few, float* parts) {
     constexpr int KS = D / 32, SPG = KS / NG, DT = D / 16, DPG = DT / NG, R = TR * RT;
     constexpr bool HALF = TR == 8;
     constexpr float kMove = 8.0f;   // the maximum follows when weights would pass 2^8
@@ -443,7 +449,7 @@ __global__ __launch_bounds__(64 * W, W == 4 ? blocks_a_cu(D, NG, TR) : D == 256 
     const int lane = threadIdx.x & 63, wave = wave_of_block(), col = lane & 15, quad = lane >> 4;
     const int g = blockIdx.x, G = a.Hq / c.heads;
     Kv4Work w;
-    if (!kv4_work<R>(c, G, slots, fill, false, blockIdx.y + blockIdx.z * gridDim.y, &w)) return;
+    if (!kv4_work<R>(c, G, slots, fill, few, false, blockIdx.y + blockIdx.z * gridDim.y, &w)) return;
     const int begin = w.chunk * w.span, end = min(begin + w.span, w.tokens);
 
     // page of the 16 tokens from `pos` on, -1 past the end
@@ -845,7 +851,7 @@ __global__ __launch_bounds__(64 * W, W == 4 ? blocks_a_cu(D, NG, TR) : D == 256 
 // fourth span, 16 at a time, so that few loads wait for each other.
 constexpr int kJoinWaves = 4;
 template <class T, int D, int R>
-__global__ __launch_bounds__(64 * kJoinWaves) void k_attn_kv4_join(Kv4 c, AttnArgs a, int slots, int fill, int row_blocks,
+__global__ __launch_bounds__(64 * kJoinWaves) void k_attn_kv4_join(Kv4 c, AttnArgs a, int slots, int fill, int few, int row_blocks,
                                                                    const float* parts) {
     constexpr int N = D / 64, W = kJoinWaves;
     constexpr size_t P = part_words<D, R>();
@@ -853,7 +859,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void k_attn_kv4_join(Kv4 c, AttnAr
     const int lane = threadIdx.x & 63, wave = wave_of_block();
     const int g = blockIdx.x / row_blocks, G = a.Hq / c.heads;
     Kv4Work w;
-    if (!kv4_work<R>(c, G, slots, fill, true, blockIdx.y + blockIdx.z * gridDim.y, &w) || w.chunks == 1) return;
+    if (!kv4_work<R>(c, G, slots, fill, few, true, blockIdx.y + blockIdx.z * gridDim.y, &w) || w.chunks == 1) return;
     const int r0 = w.tile * R, n = min(R, w.rows * G - r0);
     const float* part = parts + ((size_t)g * slots + w.slot) * P;
     for (int r = blockIdx.x % row_blocks; r < n; r += row_blocks) {
@@ -957,13 +963,14 @@ hipError_t launch_kv4_append(bool fp16, const uint16_t* k, int64_t k_row, int64_
 namespace {
 
 // Rows a block takes, in tiles of 16; the tile groups that there can be; the
-// blocks of a head that the chip is to run at once and those that the grid has;
+// blocks of a head that the chip runs at once, two a CU at most (few) or all
+// (fill), and those that the grid has;
 // none where no sequence is worth a second span.
 // Tokens up to which one block takes a sequence, with twice the waves: two
 // turns of them.
 constexpr int kOneSpan = 1024;
 struct Grid {
-    int tiles, rows, groups, slots, fill;   // rows: of a tile
+    int tiles, rows, groups, slots, fill, few;   // rows: of a tile
 };
 Grid attn_kv4_grid(int T, int G, int heads, int dim, int scales, int page, int width, int B) {
     Grid g;
@@ -974,13 +981,11 @@ Grid attn_kv4_grid(int T, int G, int heads, int dim, int scales, int page, int w
     const int R = g.rows * g.tiles;
     // a sequence's rows are a multiple of G: the last group of each lacks at most R - gcd(G, R)
     g.groups = (int)(((int64_t)T * G + (int64_t)(B < T ? B : T) * (R - std::gcd(G, R))) / R);
-    g.slots = g.fill = 0;
+    g.slots = g.fill = g.few = 0;
     if ((int64_t)width * page > kOneSpan) {
-        // A sequence or two are even by themselves: two blocks a CU do with fewer starts.  us, 2 / 3 blocks: 131072
-        // tokens 40.0 / 40.7, 20000 and 3000 14.0 / 14.5; 3 ragged sequences 19.5 / 19.4, 32 70.6 / 56.4, 64 97.1 / 72.7
         const int blocks = blocks_a_cu(dim, scales, g.rows);
-        g.fill = 256 * (B < 3 && blocks > 2 ? 2 : blocks) / heads;
-        if (g.fill < 1) g.fill = 1;
+        g.fill = std::max(256 * blocks / heads, 1);
+        g.few = std::max(256 * std::min(blocks, 2) / heads, 1);
         g.slots = 2 * g.fill + g.groups + 1;
     }
     return g;
@@ -997,7 +1002,7 @@ hipError_t run_attn_kv4(const AttnArgs& a, const Kv4& c, const Grid& g, float* w
     hipError_t e = hipSuccess;
     const auto go = [&](auto kernel, std::atomic<uint64_t>& done) {
         if (lds > 65536 && (e = opt_in_lds(reinterpret_cast<const void*>(kernel), lds, done)) != hipSuccess) return;
-        kernel<<<grid(g.slots ? g.slots : g.groups, c.heads), 64 * W, lds, st>>>(c, a, g.slots, g.fill, ws);
+        kernel<<<grid(g.slots ? g.slots : g.groups, c.heads), 64 * W, lds, st>>>(c, a, g.slots, g.fill, g.few, ws);
         e = hipGetLastError();
     };
     static std::atomic<uint64_t> done[2];
@@ -1010,7 +1015,7 @@ hipError_t run_attn_kv4(const AttnArgs& a, const Kv4& c, const Grid& g, float* w
     const int64_t rows = ((int64_t)c.T * (a.Hq / c.heads) + g.groups - 1) / g.groups;
     const int64_t most = 1024 / ((int64_t)g.groups * c.heads) + 1;
     const int row_blocks = (int)(rows < R ? (rows < most ? rows : most) : (R < most ? R : most));
-    k_attn_kv4_join<T, D, R><<<grid(g.groups, c.heads * row_blocks), 64 * kJoinWaves, 0, st>>>(c, a, g.slots, g.fill, row_blocks, ws);
+    k_attn_kv4_join<T, D, R><<<grid(g.groups, c.heads * row_blocks), 64 * kJoinWaves, 0, st>>>(c, a, g.slots, g.fill, g.few, row_blocks, ws);
     return hipGetLastError();
 }
 
