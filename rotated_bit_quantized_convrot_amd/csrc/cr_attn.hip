@@ -61,7 +61,8 @@ __device__ __forceinline__ void attn_row(const uint16_t* q, const uint16_t* k, i
 #pragma unroll
         for (int x = 1; x < 64; x <<= 1) m = fmaxf(m, __shfl_xor(m, x));
         const float up = fmaxf(top, m), f = top == up ? 1.0f : expf(top - up);
-        const float p = lane < n ? expf(s - up) : 0.0f;
+        // keys of a score of -infinity weigh nothing, also where there has been no other yet
+        const float p = up > -__builtin_inff() ? (lane < n ? expf(s - up) : 0.0f) : s == s ? 0.0f : s;
         float all = p;
 #pragma unroll
         for (int x = 1; x < 64; x <<= 1) all += __shfl_xor(all, x);
@@ -317,7 +318,7 @@ __global__ __launch_bounds__(64 * NW * KG, D == 256 ? 1 : 2) void k_attn_prompt(
                 for (int i = 0; i < 16; ++i) o[dt][i] *= f;
         }
         u32x4 p[PS];
-        const float off = kBias - top;
+        const float off = top == -__builtin_inff() ? 0.0f : kBias - top;   // a row whose keys have all scored -infinity
 #pragma unroll
         for (int ps = 0; ps < PS; ++ps) {
             float e[8];

@@ -1,0 +1,77 @@
+"""GPU: attention over prompts at the ends of the types' ranges: keys that
+score minus infinity, a scale of 0, scores and values as large as the types
+hold, against the definition in 64 bits."""
+import numpy as np
+import pytest
+import torch
+
+import rotated_bit_quantized_convrot_amd as crp
+
+from . import _attn_ref as R
+
+pytestmark = pytest.mark.gpu
+DT = {"bf16": torch.bfloat16, "fp16": torch.float16}
+# (lengths, query heads): every way of splitting rows and keys over blocks and waves, for heads of 64, 128 and 256
+WAYS = [([300], 4), ([300], 128), ([300], 240), ([600], 100), ([100] * 12, 128)]
+
+
+def make(lens, D, dtype=torch.bfloat16, seed=0):
+    """q [T, 4, D], k and v [T, 2, D]."""
+    gen = torch.Generator().manual_seed(seed)
+    return (torch.randn((sum(lens), h, D), generator=gen).to(dtype).cuda() for h in (4, 2, 2))
+
+
+def attend(q, k, v, lens, heads, causal, scale=None):
+    """The call with every query head `heads` / 4 times, which all give the
+    same: y [T, 4, D]."""
+    cu = torch.tensor([0] + list(np.cumsum(lens)), dtype=torch.int32).cuda()
+    y = crp.attn_prompt(q.repeat_interleave(heads // 4, 1), k, v, cu, causal=causal, scale=scale)
+    y = y.view(q.shape[0], 4, heads // 4, -1)
+    assert torch.equal(y.view(torch.int16), y[:, :, :1].expand_as(y).contiguous().view(torch.int16))
+    return y[:, :, 0].double().cpu().numpy()
+
+
+def reference(q, k, v, seen, scale, dtype, score_error=None):
+    """One sequence whose row r sees the first seen[r] of the keys: y and the
+    tolerance, which _attn_ref.prompt derives, with its error of the scores or
+    this one."""
+    q, k, v = (t.double().cpu().numpy() for t in (q, k, v))
+    y, tol = np.zeros(q.shape), np.zeros(q.shape)
+    half = torch.finfo(dtype).eps / 2
+    for h in range(q.shape[1]):
+        y[:, h], (A, ds, span, n, total) = R.attend(q[:, h], k[:, h // 2], v[:, h // 2], seen, scale)
+        e = 2 * ((ds if score_error is None else score_error) + 4 * R.U * (span + 1) + 2 * n * R.U)
+        tol[:, h] = (half + e)[:, None] * A + half * np.abs(y[:, h]) * (1 + 1e-3) + 2.0 ** -126
+        if dtype == torch.float16:
+            tol[:, h] += (n * 2.0 ** -25 / total)[:, None] * np.abs(v).max() + 2.0 ** -25
+    return y, tol
+
+
+def pieces(lens):
+    at = 0
+    for n in lens:
+        yield slice(at, at + n), n
+        at += n
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("lens,heads", WAYS)
+@pytest.mark.parametrize("at,bad", [(0, 64), (0, 65), (0, 128), (64, 64)])
+def test_keys_that_score_minus_infinity(D, causal, lens, heads, at, bad):
+    """An infinite channel of some keys next to each other, against the sign of
+    q: weights of 0, a softmax over the others, NaN where there is no other."""
+    if at + bad >= lens[0]:
+        at, bad = 0, lens[0] - 2
+    q, k, v = make(lens, D, seed=D + bad)
+    q[..., 5] = -q[..., 5].abs().clamp(min=0.25)
+    for one, n in pieces(lens):
+        k[one][at:at + bad, :, 5] = float("inf")
+    got = attend(q, k, v, lens, heads, causal)
+    for one, n in pieces(lens):
+        i = np.arange(n) if causal else np.full(n, n - 1)
+        seen = np.minimum(i + 1, at) + np.maximum(i + 1 - at - bad, 0)
+        rest = torch.cat((k[one][:at], k[one][at + bad:])), torch.cat((v[one][:at], v[one][at + bad:]))
+        want, tol = reference(q[one], *rest, seen, D ** -0.5, torch.bfloat16)
+        assert np.isnan(got[one][seen == 0]).all()
+        assert (np.abs(got[one] - want) <= tol)[seen > 0].all()
