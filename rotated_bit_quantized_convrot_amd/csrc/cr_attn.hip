@@ -36,6 +36,13 @@ __device__ __forceinline__ float add2(Fp16, uint32_t p, float sum) {
     return __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2, p), __builtin_bit_cast(f16x2, 0x3C003C00u), sum, false);
 }
 
+// Two values of 0 times: a scale of 0 goes to q, whose infinities and NaN it turns into NaN.
+template <class T>
+__device__ __forceinline__ uint32_t none_of(uint32_t v) {
+    constexpr uint32_t top = std::is_same_v<T, Fp16> ? 0x7C00u : 0x7F80u;
+    return ((v & top) == top ? 0x7FFFu : 0u) | ((v >> 16 & top) == top ? 0x7FFF0000u : 0u);
+}
+
 // One row by one wave, without matrix cores: only what the row sees is touched.
 // A lane takes a key of 64, then d = l D / 64 and on.  Ends when every value
 // is NaN.
@@ -54,7 +61,7 @@ __device__ __forceinline__ void attn_row(const uint16_t* q, const uint16_t* k, i
             w4g_values<T>(q + d, x);
             w4g_values<T>(kr + d, w);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) s = __builtin_fmaf(x[i], w[i], s);
+            for (int i = 0; i < 8; ++i) s = __builtin_fmaf(scale == 0.0f ? x[i] * 0.0f : x[i], w[i], s);
         }
         s = lane < n ? s * scale : -__builtin_inff();
         float m = s;
@@ -227,9 +234,12 @@ __global__ __launch_bounds__(64 * NW * KG, D == 256 ? 1 : 2) void k_attn_prompt(
     {
         const uint16_t* p = q + (int64_t)min(row, t.len - 1) * a.q_row + 8 * (lane >> 5);
 #pragma unroll
-        for (int s = 0; s < KS; ++s) {
-            qv[s] = *reinterpret_cast<const u32x4*>(p + 16 * s);
-            if (a.scale < 0.0f) qv[s] ^= 0x80008000u;   // the sign goes to q
+        for (int s = 0; s < KS; ++s) qv[s] = *reinterpret_cast<const u32x4*>(p + 16 * s);
+        if (!(a.scale > 0.0f)) {   // the sign goes to q, and 0
+#pragma unroll
+            for (int s = 0; s < KS; ++s)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) qv[s][j] = a.scale < 0.0f ? qv[s][j] ^ 0x80008000u : none_of<T>(qv[s][j]);
         }
     }
     // Halves of two waves do not wait for each other: each has a count of its waves that have come to a turn (a
@@ -248,8 +258,8 @@ __global__ __launch_bounds__(64 * NW * KG, D == 256 ? 1 : 2) void k_attn_prompt(
         asm volatile("" ::: "memory");
     };
     f32x16 o[DT] = {};
-    // a scale of 0 would make NaN of the scores that are masked; all weights are 1 with this one too
-    const float c = a.scale == 0.0f ? 1e-30f : fabsf(a.scale) * 1.4426950408889634f;
+    // (a scale of 0 is in q, and would make NaN of the scores that are masked)
+    const float c = a.scale == 0.0f ? 1.0f : fabsf(a.scale) * 1.4426950408889634f;
     float top = -__builtin_inff(), sum = 0.0f;   // of the scores times c; this lane's keys
 
     for (int turn = 0; turn * KG < tiles; ++turn) {

@@ -545,6 +545,10 @@ __global__ __launch_bounds__(64 * W, W == 4 ? blocks_a_cu(D, NG, TR) : D == 256 
                 x[s][2 * j] = T::to_f32(qh[t][s][j] & 0xFFFFu);
                 x[s][2 * j + 1] = T::to_f32(qh[t][s][j] >> 16);
             }
+            if (a.scale == 0.0f) {   // goes to q, whose infinities and NaN it turns into NaN
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[s][j] *= 0.0f;
+            }
         }
         if (LO && c.rotate) {
             u32x4 part[2][KS];
@@ -604,8 +608,8 @@ __global__ __launch_bounds__(64 * W, W == 4 ? blocks_a_cu(D, NG, TR) : D == 256 
         top[t] = -__builtin_inff();
         sum[t] = 0.0f;
     }
-    // masked scores become -infinity times cs; a scale of 0 would make NaN of them, and 1e-30 gives equal weights too
-    const float cs = 16.0f * (a.scale == 0.0f ? 1e-30f : fabsf(a.scale) * 1.4426950408889634f);
+    // masked scores become -infinity times cs; a scale of 0, which would make NaN of them, is in q
+    const float cs = 16.0f * (a.scale == 0.0f ? 1.0f : fabsf(a.scale) * 1.4426950408889634f);
 
     Stage<NG>& stage = reinterpret_cast<Stage<NG>*>(lds)[wave];
     auto step = [&](auto slot) {

@@ -75,3 +75,26 @@ def test_keys_that_score_minus_infinity(D, causal, lens, heads, at, bad):
         want, tol = reference(q[one], *rest, seen, D ** -0.5, torch.bfloat16)
         assert np.isnan(got[one][seen == 0]).all()
         assert (np.abs(got[one] - want) <= tol)[seen > 0].all()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("lens,heads", WAYS)
+@pytest.mark.parametrize("size", [1e15, 2.0 ** 63])
+def test_a_scale_of_0(D, causal, lens, heads, size):
+    """The mean of the values, however large q and k are (at 2^63 their
+    products pass float32); a row of q with an infinity gives NaN."""
+    q, k, v = make(lens, D, seed=D)
+    q, k = ((x.float() * size).to(torch.bfloat16) for x in (q, k))
+    q[7, 1, 3], q[9, 2, 4] = float("inf"), float("nan")
+    got = attend(q, k, v, lens, heads, causal, scale=0.0)
+    assert np.isnan(got[7, 1]).all() and np.isnan(got[9, 2]).all()
+    got[7, 1] = got[9, 2] = 0
+    q, k = q.nan_to_num(0, 0, 0), k
+    for one, n in pieces(lens):
+        seen = np.arange(1, n + 1) if causal else np.full(n, n)
+        want, tol = reference(q[one], k[one], v[one], seen, 0.0, torch.bfloat16)
+        off = np.abs(got[one] - want) <= tol
+        if one.start == 0:
+            off[7, 1] = off[9, 2] = True
+        assert off.all()

@@ -1,0 +1,76 @@
+"""GPU: attention over the 4-bit cache at the ends of the types' ranges: signs
+and sizes of the scale, scores, queries and values as large as the types
+hold, against the definition in 64 bits."""
+import numpy as np
+import pytest
+import torch
+
+import rotated_bit_quantized_convrot_amd as crp
+
+from . import _attn_ref as R
+from .test_gpu_kv4 import Setup, ints, starts
+
+pytestmark = pytest.mark.gpu
+DT = {"bf16": torch.bfloat16, "fp16": torch.float16}
+# (lengths, new tokens, query heads of 2 key heads, pages of a table beyond what is needed): one span or several, tiles of
+# 8 rows, of 16, and two or three of those
+WAYS = [([300, 37], [1, 1], 6, 2), ([3000, 500], [1, 1], 6, 40), ([300, 90], [3, 3], 10, 2), ([2500, 90], [3, 3], 10, 40),
+        ([700, 90], [7, 7], 10, 40)]
+
+
+def reference(s, q, new, scale, score_error=None):
+    """Setup.reference; with `score_error` in the place of the scores' error
+    that it derives."""
+    if score_error is None:
+        # its bound is written for scales that are not negative: the sign to q
+        return s.reference(-q if scale < 0 else q, new, abs(scale))
+    y, tol = np.zeros(q.shape), np.zeros(q.shape)
+    a, c = starts(new), starts(s.lens)
+    rot = R.hadamard(s.D) if s.rotate else np.eye(s.D)
+    kv = [(R.values(*w, s.group), (w[0] + 16.0) * (w[1] & np.uint32(0xFFFFFFF0)).view(np.float32).astype(float).repeat(s.group, -1))
+          for w in (R.encode(s.k, s.group, s.rotate), R.encode(s.v, s.group, s.rotate))]
+    (k, _), (v, v_big) = kv
+    x = q.double().cpu().numpy()
+    for b, n in enumerate(s.lens):
+        rows, one = slice(a[b], a[b + 1]), slice(c[b], c[b + 1])
+        seen = np.clip(n - new[b] + 1 + np.arange(new[b]), 0, n)
+        for h in range(x.shape[1]):
+            g = h // (x.shape[1] // s.H)
+            o, (A, _, span, m, total) = R.attend(x[rows, h] @ rot, k[one, g], v[one, g], seen, scale)
+            big = R.attend(x[rows, h] @ rot, k[one, g], v_big[one, g], seen, scale)[0]
+            e = 2 * (score_error + 4 * R.U * (span + 1) + 2 * m * R.U) + 2.0 ** -17
+            off = e[:, None] * A + 2 * (m + 4)[:, None] * R.U * big
+            y[rows, h] = o @ rot
+            tol[rows, h] = (off @ np.abs(rot) + 20 * R.U * np.abs(o) @ np.abs(rot) +
+                            torch.finfo(s.dtype).eps / 2 * np.abs(y[rows, h]) * (1 + 1e-3) + 2.0 ** -25)
+    return y, tol
+
+
+@pytest.mark.parametrize("rotate", [True, False])
+@pytest.mark.parametrize("D,group", [(64, 64), (128, 32), (256, 64)])
+@pytest.mark.parametrize("lens,new,Hq,spare", WAYS)
+@pytest.mark.parametrize("scale", [-0.1, 0.0])
+def test_signs_of_the_scale(rotate, D, group, lens, new, Hq, spare, scale):
+    s = Setup(lens, 2, D, group, 64, rotate, torch.bfloat16, seed=D, spare=spare).fill()
+    q = s.queries(new, Hq)
+    y, tol = reference(s, q, new, scale)
+    assert (np.abs(s.attend(q, new, scale=scale).double().cpu().numpy() - y) <= tol).all()
+
+
+@pytest.mark.parametrize("rotate", [True, False])
+@pytest.mark.parametrize("lens,new,Hq,spare", WAYS)
+@pytest.mark.parametrize("size", [1e15, 2.0 ** 63])
+def test_a_scale_of_0(rotate, lens, new, Hq, spare, size):
+    """The mean of the values, however large q and k are (at 2^63 their
+    products pass float32); a row of q with an infinity gives NaN."""
+    s = Setup(lens, 2, 128, 64, 64, rotate, torch.bfloat16, seed=3, spare=spare)
+    s.k *= size
+    s.fill()
+    q = (s.queries(new, Hq).float() * size).to(torch.bfloat16)
+    want, tol = reference(s, q, new, 0.0)
+    q[0, 1, 3], q[1, 2, 4] = float("inf"), float("nan")
+    got = s.attend(q, new, scale=0.0).double().cpu().numpy()
+    assert np.isnan(got[0, 1]).all() and np.isnan(got[1, 2]).all()
+    off = np.abs(got - want) <= tol
+    off[0, 1] = off[1, 2] = True
+    assert off.all()
