@@ -440,6 +440,8 @@ __global__ __launch_bounds__(64 * W, W == 4 ? blocks_a_cu(D, NG, TR) : D == 256 
     constexpr int KS = D / 32, SPG = KS / NG, DT = D / 16, DPG = DT / NG, R = TR * RT;
     constexpr bool HALF = TR == 8;
     constexpr float kMove = 8.0f;   // the maximum follows when weights would pass 2^8
+    // From here on the maximum's own rounding shows in the exponents (by 2^-4 at 2^20, by 128 at 2^32).
+    constexpr float kFar = 1048576.0f;
     constexpr int kRow = lds_row<D>(), DEPTH = RT == 1 && D == 64 ? 2 : 1;
     // the waves' scales of a step; then their sums of a tile
     extern __shared__ __align__(16) uint32_t lds[];
@@ -603,8 +605,10 @@ __global__ __launch_bounds__(64 * W, W == 4 ? blocks_a_cu(D, NG, TR) : D == 256 
     f32x4 o[RT][DT] = {}, zp[RT][NG] = {};   // zp: sums of weights times 1 + z / 16
     uint32_t poison[RT] = {};                // bit n: group n of V is NaN
     float top[RT], sum[RT];
+    bool far[RT];   // of some row of the tile: a maximum beyond kFar, or none yet
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
+        far[t] = true;
         top[t] = -__builtin_inff();
         sum[t] = 0.0f;
     }
@@ -718,16 +722,26 @@ __global__ __launch_bounds__(64 * W, W == 4 ? blocks_a_cu(D, NG, TR) : D == 256 
                 m = fmaxf(m, __shfl_xor(m, 32));
                 const float up = fmaxf(top[t], m), f = top[t] == up ? 1.0f : __builtin_amdgcn_exp2f(top[t] - up);
                 top[t] = up;
+                far[t] = __any(!(fabsf(up) <= kFar));
                 sum[t] *= f;
 #pragma unroll
                 for (int d = 0; d < DT; ++d) o[t][d] *= f;
 #pragma unroll
                 for (int n = 0; n < NG; ++n) zp[t][n] *= f;
             }
-            const float off = top[t] == -__builtin_inff() ? 0.0f : -top[t];   // a row that has seen nothing yet
+            float c1 = cs, off = -top[t];
+            if (far[t]) {
+                // The product is rounded as the maximum's was, so that the maximum's own exponent is 0; unrounded it
+                // would be up to half of the maximum's last place.
+                const float base = top[t] == -__builtin_inff() ? 0.0f : top[t];   // a row that has seen nothing yet
+#pragma unroll
+                for (int i = 0; i < 16; ++i) s[t][i] = s[t][i] * cs - base;
+                c1 = 1.0f;
+                off = 0.0f;
+            }
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                s[t][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][i], cs, off));
+                s[t][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][i], c1, off));
                 sum[t] += s[t][i];
             }
         }

@@ -98,3 +98,29 @@ def test_a_scale_of_0(D, causal, lens, heads, size):
         if one.start == 0:
             off[7, 1] = off[9, 2] = True
         assert off.all()
+
+
+@pytest.mark.parametrize("dtype,D", [("fp16", 64), ("bf16", 128), ("fp16", 128), ("bf16", 256)])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("lens,heads", WAYS)
+@pytest.mark.parametrize("size", [2.0 ** 11, 2.0 ** 24, 2.0 ** 32, 1e30])
+def test_scores_as_large_as_float32_holds(dtype, D, causal, lens, heads, size):
+    """Rows whose weight goes to one key, or to some with the same score: q and
+    k along one direction, where float32 has the scores exactly."""
+    dt = DT[dtype]
+    q, k, v = make(lens, D, dt, seed=D)
+    gen = torch.Generator().manual_seed(D)
+    u = torch.randint(0, 2, (D,), generator=gen).mul(2).sub(1).float().cuda()
+    sign = torch.randint(0, 2, q.shape[:2], generator=gen).mul(2).sub(1).float()
+    q = ((1 + torch.rand(q.shape[:2], generator=gen)) * sign).cuda()[..., None].mul(u).to(dt)
+    r = (2 * torch.rand(k.shape[:2], generator=gen) - 1).cuda()
+    k = r[..., None].mul(u).to(dt)
+    scale = size / D
+    got = attend(q, k, v, lens, heads, causal, scale=scale)
+    for one, n in pieces(lens):
+        seen = np.arange(1, n + 1) if causal else np.full(n, n)
+        # scale and log2 e are rounded once more each, and their product with a score of up to twice `size`; from 2^20
+        # on keys of other scores have no weight, and equal ones the same error
+        ds = 6 * R.U * size if size < 2.0 ** 20 else 0.0
+        want, tol = reference(q[one], k[one], v[one], seen, float(np.float32(scale)), dt, ds)
+        assert (np.abs(got[one] - want) <= tol).all()

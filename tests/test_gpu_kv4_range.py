@@ -74,3 +74,25 @@ def test_a_scale_of_0(rotate, lens, new, Hq, spare, size):
     off = np.abs(got - want) <= tol
     off[0, 1] = off[1, 2] = True
     assert off.all()
+
+
+@pytest.mark.parametrize("rotate", [True, False])
+@pytest.mark.parametrize("dtype,D,group", [("fp16", 64, 32), ("bf16", 128, 128), ("bf16", 256, 64)])
+@pytest.mark.parametrize("lens,new,Hq,spare", WAYS)
+@pytest.mark.parametrize("size", [2.0 ** 11, 2.0 ** 24, 2.0 ** 32, 1e30])
+def test_scores_as_large_as_float32_holds(dtype, rotate, D, group, lens, new, Hq, spare, size):
+    """Rows whose weight goes to one token, or to some with the same codes: q
+    and k along one direction, which the rotation turns into one channel."""
+    s = Setup(lens, 2, D, group, 64, rotate, DT[dtype], seed=D, spare=spare)
+    r = 2 * torch.rand(s.k.shape[:2], generator=s.gen) - 1
+    s.k.copy_(r[..., None].expand(*s.k.shape))
+    s.fill()
+    q = 1 + torch.rand((sum(new), Hq), generator=s.gen)
+    q[:, ::2] *= -1
+    q = q[..., None].expand(-1, -1, D).to(s.dtype).cuda()
+    scale = size / D
+    # Scores of up to twice `size` (a little more after rounding): scale and log2 e are rounded once each, q (2^-17), the
+    # sums and three products; from 2^20 on tokens of other scores have no weight, and equal ones the same error.
+    ds = 2.1 * size * (2.0 ** -17 + (31 * (D + 4) + 8) * R.U) if size < 2.0 ** 20 else 0.0
+    y, tol = reference(s, q, new, float(np.float32(scale)), ds)
+    assert (np.abs(s.attend(q, new, scale=scale).double().cpu().numpy() - y) <= tol).all()
