@@ -44,8 +44,8 @@ __device__ __forceinline__ uint32_t none_of(uint32_t v) {
 }
 
 // One row by one wave, without matrix cores: only what the row sees is touched.
-// A lane takes a key of 64, then d = l D / 64 and on.  Ends when every value
-// is NaN.
+// A lane takes a key of 64, then d = l D / 64 and on.  o holds the average so
+// far, which is no larger than v is.  Ends when every value is NaN.
 template <class T, int D>
 __device__ __forceinline__ void attn_row(const uint16_t* q, const uint16_t* k, int64_t k_row, const uint16_t* v, int64_t v_row,
                               int keys, float scale, uint16_t* y) {
@@ -73,24 +73,30 @@ __device__ __forceinline__ void attn_row(const uint16_t* q, const uint16_t* k, i
         float all = p;
 #pragma unroll
         for (int x = 1; x < 64; x <<= 1) all += __shfl_xor(all, x);
-        sum = sum * f + all;
+        const float total = sum * f + all, inv = total == 0.0f ? 0.0f : 1.0f / total, keep = sum * f * inv;
+        sum = total;
         top = up;
         bool open = false;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            o[i] *= f;
+            if (!(fabsf(o[i]) == __builtin_inff())) o[i] *= keep;
             open |= o[i] == o[i];
         }
         if (!__any(open)) break;
+        // what an infinity is multiplied with: a weight that is 0 in float32 alone is none of the definition's
+        const float share = p * inv, some = s > -__builtin_inff() ? fmaxf(share, 1e-30f) : share;
         for (int j = 0; j < n; ++j) {
-            const float w = __shfl(p, j);
+            const float w = __shfl(share, j), w_inf = __shfl(some, j);
             const uint16_t* vr = v + (int64_t)(j0 + j) * v_row + lane * N;
 #pragma unroll
-            for (int i = 0; i < N; ++i) o[i] = __builtin_fmaf(w, T::to_f32(vr[i]), o[i]);
+            for (int i = 0; i < N; ++i) {
+                const float x = T::to_f32(vr[i]);
+                o[i] = __builtin_fmaf(fabsf(x) == __builtin_inff() ? w_inf : w, x, o[i]);
+            }
         }
     }
 #pragma unroll
-    for (int i = 0; i < N; ++i) y[lane * N + i] = T::from_f32(o[i] / sum);
+    for (int i = 0; i < N; ++i) y[lane * N + i] = T::from_f32(sum == 0.0f ? __builtin_nanf("") : o[i]);
 }
 
 // The sequence and the tile of BM rows in it that tile `t` from the end is:

@@ -124,3 +124,40 @@ def test_scores_as_large_as_float32_holds(dtype, D, causal, lens, heads, size):
         ds = 6 * R.U * size if size < 2.0 ** 20 else 0.0
         want, tol = reference(q[one], k[one], v[one], seen, float(np.float32(scale)), dt, ds)
         assert (np.abs(got[one] - want) <= tol).all()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("lens,heads", WAYS)
+@pytest.mark.parametrize("sign", [False, True])
+def test_values_as_large_as_the_type_holds(D, causal, lens, heads, sign):
+    """Averages of v close to bf16's largest number, of one sign or of both, next
+    to channels of ordinary size."""
+    q, k, v = make(lens, D, seed=D)
+    v[..., ::2] = (v[..., ::2].float().abs().clamp(0, 1).mul(0.25).add(0.75) * torch.finfo(torch.bfloat16).max *
+                   (v[..., ::2].float().sign() if sign else 1)).to(torch.bfloat16)
+    v[1, 0, 0] = v[0, 0, 0] = 2e38
+    assert v.isfinite().all()
+    got = attend(q, k, v, lens, heads, causal)
+    for one, n in pieces(lens):
+        seen = np.arange(1, n + 1) if causal else np.full(n, n)
+        want, tol = reference(q[one], k[one], v[one], seen, D ** -0.5, torch.bfloat16)
+        assert (np.abs(got[one] - want) <= tol).all()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_infinite_values_of_keys_of_little_weight(D):
+    """exp underflows in float32, not in the definition: a weight that is not 0
+    times infinity is infinity; with a score of -infinity it is 0, and NaN."""
+    q, k, v = make([200], D, seed=1)
+    q[..., 5], k[..., 5] = 1.0, 0.0
+    k[60, 0, 5] = -200 * D ** 0.5
+    k[70, 1, 5] = float("-inf")
+    v[60, 0, 9] = v[70, 1, 9] = float("inf")
+    got = attend(q, k, v, [200], 4, True)
+    assert np.isposinf(got[60:, :2, 9]).all() and np.isnan(got[70:, 2:, 9]).all()
+    v[60, 0, 9] = v[70, 1, 9] = 0
+    want, tol = reference(q, k.nan_to_num(0, 0, -200 * D ** 0.5), v, np.arange(1, 201), D ** -0.5, torch.bfloat16)
+    clean = np.ones(got.shape, bool)
+    clean[60:, :2, 9] = clean[70:, 2:, 9] = False
+    assert (np.abs(got - want) <= tol)[clean].all()
