@@ -732,10 +732,12 @@ __global__ __launch_bounds__(64 * W, W == 4 ? blocks_a_cu(D, NG, TR) : D == 256 
             float c1 = cs, off = -top[t];
             if (far[t]) {
                 // The product is rounded as the maximum's was, so that the maximum's own exponent is 0; unrounded it
-                // would be up to half of the maximum's last place.
+                // would be up to half of the maximum's last place.  The tile's other rows are not: their bits are
+                // theirs alone.
                 const float base = top[t] == -__builtin_inff() ? 0.0f : top[t];   // a row that has seen nothing yet
+                const bool own = fabsf(base) > kFar;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) s[t][i] = s[t][i] * cs - base;
+                for (int i = 0; i < 16; ++i) s[t][i] = own ? s[t][i] * cs - base : __builtin_fmaf(s[t][i], cs, -base);
                 c1 = 1.0f;
                 off = 0.0f;
             }

@@ -96,3 +96,13 @@ def test_scores_as_large_as_float32_holds(dtype, rotate, D, group, lens, new, Hq
     ds = 2.1 * size * (2.0 ** -17 + (31 * (D + 4) + 8) * R.U) if size < 2.0 ** 20 else 0.0
     y, tol = reference(s, q, new, float(np.float32(scale)), ds)
     assert (np.abs(s.attend(q, new, scale=scale).double().cpu().numpy() - y) <= tol).all()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("seed", range(4))
+def test_rows_that_see_nothing_change_no_bit_of_others(D, seed):
+    s = Setup([40], 2, D, 32, 64, True, torch.float16, seed=seed).fill()
+    q = s.queries([47], 4)
+    want = crp.attn_kv4(q[7:], s.cache, s.table, ints([40]), ints([0, 40]))
+    got = crp.attn_kv4(q, s.cache, s.table, ints([40]), ints([0, 47]))
+    assert (got[:7] == 0).all() and torch.equal(got[7:], want)
