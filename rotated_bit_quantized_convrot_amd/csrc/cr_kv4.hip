@@ -356,8 +356,11 @@ __device__ __forceinline__ bool kv4_work(const Kv4& c, int G, int slots, int fil
     return false;
 }
 
-// Partial results of a slot: sums [R][D], then the maxima and the sums of
+// Partial results of a slot: averages [R][D], then the maxima and the sums of
 // weights [R] each, R the rows of a block.
+//   Averages, in LDS too, carry 2^-8, so that neither a code's offset nor
+// turning them back passes float32 where the output does not.
+constexpr float kPart = 1.0f / 256.0f;
 template <int D, int R>
 constexpr size_t part_words() { return R * (D + 2); }
 
@@ -407,15 +410,18 @@ struct Words {
     uint32_t w[N];
 };
 
-// y = sums over the sum of weights, turned back; 0 for a row that saw nothing.
+// 1 / x to a unit in the last place (sums of weights are 0 or some 1 and more),
+// or 0: where all weights are 0, as those of a row that saw nothing, averages
+// are.
+__device__ __forceinline__ float reciprocal_or_0(float x) { return x == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(x); }
+
+// y = the average, turned back.
 template <class T, int D>
-__device__ __forceinline__ void kv4_finish(float (&x)[D / 64], float total, int rotate, uint16_t* y) {
+__device__ __forceinline__ void kv4_finish(float (&x)[D / 64], int rotate, uint16_t* y) {
     const int lane = threadIdx.x & 63;
-#pragma unroll
-    for (int i = 0; i < D / 64; ++i) x[i] = total == 0.0f ? 0.0f : x[i] / total;
     if (rotate) rotate_head<D>(x);
 #pragma unroll
-    for (int i = 0; i < D / 64; ++i) y[lane * (D / 64) + i] = T::from_f32(x[i]);
+    for (int i = 0; i < D / 64; ++i) y[lane * (D / 64) + i] = T::from_f32(x[i] * (1.0f / kPart));
 }
 
 // Blocks of four waves that a CU holds, by their registers (three: 168 a lane;
@@ -604,6 +610,11 @@ __global__ __launch_bounds__(64 * W, W == 4 ? blocks_a_cu(D, NG, TR) : D == 256 
 
     f32x4 o[RT][DT] = {}, zp[RT][NG] = {};   // zp: sums of weights times 1 + z / 16
     uint32_t poison[RT] = {};                // bit n: group n of V is NaN
+    // bit n: group n of V has had a scale beyond kLarge, and its scales and sums carry kShrink from then on: below it
+    // 2^30 tokens' sums, of weights of up to 2^8, stay under 2^120
+    uint32_t shrunk = 0;
+    constexpr uint32_t kLarge = 0x67800000u;   // 2^80
+    constexpr float kShrink = 0x1p-64f;
     float top[RT], sum[RT];
     bool far[RT];   // of some row of the tile: a maximum beyond kFar, or none yet
 #pragma unroll
@@ -629,9 +640,24 @@ __global__ __launch_bounds__(64 * W, W == 4 ? blocks_a_cu(D, NG, TR) : D == 256 
                 const uint32_t k = there ? kw[at].w[n] : 0, v = there ? vw[at].w[n] : 0;
                 stage.ks[n][lane] = __uint_as_float(k & ~15u);
                 stage.kz[n][lane] = __uint_as_float((k & 15u) << 19 | 0x3F800000u);
-                const bool nan = (v & 0x7F800000u) == 0x7F800000u;
-                nans[n] = __ballot(nan);
-                stage.vs[n][lane] = nan ? 0.0f : __uint_as_float(v & ~15u);
+                float scale = __uint_as_float(v & ~15u);
+                nans[n] = __ballot(v >= kLarge);
+                if (nans[n] != 0 || (shrunk >> n & 1)) {
+                    const bool nan = (v & 0x7F800000u) == 0x7F800000u;
+                    const uint64_t large = nans[n];
+                    nans[n] = __ballot(nan);
+                    if (!(shrunk >> n & 1) && (large & ~nans[n]) != 0) {
+                        shrunk |= 1u << n;
+#pragma unroll
+                        for (int t = 0; t < RT; ++t) {
+                            zp[t][n] *= kShrink;
+#pragma unroll
+                            for (int d = n * DPG; d < (n + 1) * DPG; ++d) o[t][d] *= kShrink;
+                        }
+                    }
+                    scale = nan ? 0.0f : shrunk >> n & 1 ? scale * kShrink : scale;
+                }
+                stage.vs[n][lane] = scale;
                 stage.vz[n][place] = (uint16_t)((v & 15u) << 3 | 0x3F80u);
             }
             __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
@@ -818,6 +844,7 @@ __global__ __launch_bounds__(64 * W, W == 4 ? blocks_a_cu(D, NG, TR) : D == 256 
         sum[t] += __shfl_xor(sum[t], 32);
         poison[t] |= __shfl_xor(poison[t], 16);
         poison[t] |= __shfl_xor(poison[t], 32);
+        const float share = 16.0f * kPart * reciprocal_or_0(sum[t]);
         __syncthreads();   // the words, or the last tile's rows, were read
         if (quad == 0) {
             lds_top[wave][col] = top[t];
@@ -828,7 +855,8 @@ __global__ __launch_bounds__(64 * W, W == 4 ? blocks_a_cu(D, NG, TR) : D == 256 
             f32x4 v;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                v[i] = poison[t] >> (d / DPG) & 1 ? __uint_as_float(kKv4Nan) : 16.0f * (o[t][d][i] - zp[t][d / DPG][i]);
+                v[i] = poison[t] >> (d / DPG) & 1 ? __uint_as_float(kKv4Nan)
+                                                  : (shrunk >> (d / DPG) & 1 ? share / kShrink : share) * (o[t][d][i] - zp[t][d / DPG][i]);
             if constexpr (HALF) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) v[i] += lane_xor<8>(v[i]);
@@ -838,22 +866,25 @@ __global__ __launch_bounds__(64 * W, W == 4 ? blocks_a_cu(D, NG, TR) : D == 256 
         __syncthreads();
         const int r0 = (w.tile * RT + t) * TR, n = min(TR, w.rows * G - r0);
         for (int r = wave; r < n; r += W) {
-            float m = lds_top[0][r], total = 0.0f, x[D / 64] = {};
+            float m = lds_top[0][r], total = 0.0f, x[D / 64] = {}, of[W];
 #pragma unroll
             for (int k = 1; k < W; ++k) m = fmaxf(m, lds_top[k][r]);
 #pragma unroll
             for (int k = 0; k < W; ++k) {
-                // a wave that has seen nothing has sums of 0, or NaN
-                const float f = lds_top[k][r] == m || lds_top[k][r] == -__builtin_inff()
-                                    ? 1.0f : __builtin_amdgcn_exp2f(lds_top[k][r] - m);
-                total = __builtin_fmaf(f, lds_sum[k][r], total);
+                // a wave that has seen nothing has a sum of 0, or NaN
+                of[k] = lds_sum[k][r] * (lds_top[k][r] == m || lds_top[k][r] == -__builtin_inff()
+                                             ? 1.0f : __builtin_amdgcn_exp2f(lds_top[k][r] - m));
+                total += of[k];
+            }
+            const float inv = reciprocal_or_0(total);
+#pragma unroll
+            for (int k = 0; k < W; ++k)
 #pragma unroll
                 for (int i = 0; i < D / 64; ++i)
-                    x[i] = __builtin_fmaf(f, lds_o[(k * TR + r) * kRow + lane * (D / 64) + i], x[i]);
-            }
+                    x[i] = __builtin_fmaf(of[k] * inv, lds_o[(k * TR + r) * kRow + lane * (D / 64) + i], x[i]);
             if (whole) {
                 const int i0 = (r0 + r) / G, h = g * G + (r0 + r) % G;
-                kv4_finish<T, D>(x, total, c.rotate, a.y + ((int64_t)(w.first + i0) * a.Hq + h) * D);
+                kv4_finish<T, D>(x, c.rotate, a.y + ((int64_t)(w.first + i0) * a.Hq + h) * D);
             } else {
                 float* p = part + (TR * t + r) * D + lane * (D / 64);
 #pragma unroll
@@ -897,20 +928,21 @@ __global__ __launch_bounds__(64 * kJoinWaves) void k_attn_kv4_join(Kv4 c, AttnAr
 #pragma unroll
             for (int i = 1; i < 16; i <<= 1) up = fmaxf(up, __shfl_xor(up, i));
             up = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(up)));
-            // sums of a span that saw nothing are 0, or NaN
+            // the sum of a span that saw nothing is 0, or NaN
             const float f = top == up || top == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(top - up);
-            const float f0 = m == up || m == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(m - up);
+            const float before = total * (m == up || m == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(m - up));
+            const float of = lane < some ? f * sum : 0.0f;
             m = up;
-            total *= f0;
+            total = before + __int_as_float(__builtin_amdgcn_readlane(wave_scan(__float_as_int(of), add_floats), 63));
+            const float inv = reciprocal_or_0(total), share = of * inv;
 #pragma unroll
-            for (int d = 0; d < N; ++d) x[d] *= f0;
+            for (int d = 0; d < N; ++d) x[d] *= before * inv;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 if (i >= some) continue;
-                const float fi = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(f), i));
-                total = __builtin_fmaf(fi, __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(sum), i)), total);
+                const float si = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(share), i));
 #pragma unroll
-                for (int d = 0; d < N; ++d) x[d] = __builtin_fmaf(fi, y[i][d], x[d]);
+                for (int d = 0; d < N; ++d) x[d] = __builtin_fmaf(si, y[i][d], x[d]);
             }
         }
 #pragma unroll
@@ -924,18 +956,22 @@ __global__ __launch_bounds__(64 * kJoinWaves) void k_attn_kv4_join(Kv4 c, AttnAr
             float up = m;
 #pragma unroll
             for (int k = 1; k < W; ++k) up = fmaxf(up, lds_top[k]);
+            float of[W];
             total = 0.0f;
+#pragma unroll
+            for (int k = 0; k < W; ++k) {
+                of[k] = lds_sum[k] * (lds_top[k] == up || lds_top[k] == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(lds_top[k] - up));
+                total += of[k];
+            }
+            const float inv = reciprocal_or_0(total);
 #pragma unroll
             for (int d = 0; d < N; ++d) x[d] = 0.0f;
 #pragma unroll
-            for (int k = 0; k < W; ++k) {
-                const float f = lds_top[k] == up || lds_top[k] == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(lds_top[k] - up);
-                total = __builtin_fmaf(f, lds_sum[k], total);
+            for (int k = 0; k < W; ++k)
 #pragma unroll
-                for (int d = 0; d < N; ++d) x[d] = __builtin_fmaf(f, lds_x[k][lane * N + d], x[d]);
-            }
+                for (int d = 0; d < N; ++d) x[d] = __builtin_fmaf(of[k] * inv, lds_x[k][lane * N + d], x[d]);
             const int i0 = (r0 + r) / G, h = g * G + (r0 + r) % G;
-            kv4_finish<T, D>(x, total, c.rotate, a.y + ((int64_t)(w.first + i0) * a.Hq + h) * D);
+            kv4_finish<T, D>(x, c.rotate, a.y + ((int64_t)(w.first + i0) * a.Hq + h) * D);
         }
         __syncthreads();
     }

@@ -106,3 +106,68 @@ def test_rows_that_see_nothing_change_no_bit_of_others(D, seed):
     want = crp.attn_kv4(q[7:], s.cache, s.table, ints([40]), ints([0, 40]))
     got = crp.attn_kv4(q, s.cache, s.table, ints([40]), ints([0, 47]))
     assert (got[:7] == 0).all() and torch.equal(got[7:], want)
+
+
+def large_values(s, size):
+    s.v.copy_((s.v.float().sign() * (0.5 + 0.5 * torch.rand(s.v.shape, generator=s.gen).cuda()) * size).to(torch.bfloat16))
+    assert s.v.isfinite().all()
+
+
+@pytest.mark.parametrize("D,group", [(64, 32), (128, 32), (128, 128), (256, 64)])
+@pytest.mark.parametrize("lens,new,Hq,spare", WAYS)
+@pytest.mark.parametrize("size", [2.0 ** 79, 2.0 ** 84, 2.0 ** 127])
+def test_values_as_large_as_the_type_holds(D, group, lens, new, Hq, spare, size):
+    """Without a rotation: values of up to 2^127; where there are several groups
+    one of them holds ordinary ones, which lose nothing."""
+    s = Setup(lens, 2, D, group, 64, False, torch.bfloat16, seed=D + group, spare=spare)
+    plain = s.v.clone()
+    large_values(s, size)
+    s.v[:, 0] = s.v[:, 0].abs()   # of one sign: the average is as large
+    if D > group:
+        s.v[..., group:2 * group] = plain[..., group:2 * group]
+    s.fill()
+    s.check(new, Hq, gain=0.5)
+
+
+@pytest.mark.parametrize("D,group", [(64, 32), (128, 64), (256, 128)])
+@pytest.mark.parametrize("lens,new,Hq,spare", WAYS)
+def test_large_values_late(D, group, lens, new, Hq, spare):
+    """Ordinary tokens, then some of up to 2^120: the sums before them count for
+    nothing next to them, and where a group has none they are as they were."""
+    s = Setup(lens, 2, D, group, 64, False, torch.bfloat16, seed=D, spare=spare)
+    at = starts(s.lens)
+    for b, n in enumerate(s.lens):
+        s.v[at[b] + n // 2:at[b] + n // 2 + 3, :, :group] *= 2.0 ** 120
+    s.fill()
+    s.check(new, Hq)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("lens,new,Hq,spare", WAYS)
+@pytest.mark.parametrize("spike", [False, True])
+def test_large_values_rotated(D, lens, new, Hq, spare, spike):
+    """Values whose rotation float32 holds: all of up to 2^127 / dim, or one of
+    2^127 a head."""
+    s = Setup(lens, 2, D, 64, 64, True, torch.bfloat16, seed=D, spare=spare)
+    if spike:
+        s.v[:] = 0
+        s.v[..., 17] = 2.0 ** 127
+    else:
+        large_values(s, 2.0 ** 127 / D)
+    s.fill()
+    s.check(new, Hq)
+
+
+def test_a_bad_token_among_large_values():
+    """A group of NaN beside groups of large values: only its channels, only the
+    rows that see it."""
+    s = Setup([2000, 100], 2, 128, 64, 64, False, torch.bfloat16, seed=4, spare=40)
+    large_values(s, 2.0 ** 126)
+    s.fill()
+    q = s.queries([6, 1], 4)
+    want, tol = reference(s, q, [6, 1], 128 ** -0.5)
+    s.v[1997, 1, 70] = float("inf")
+    y = s.fill().attend(q, [6, 1]).double().cpu().numpy()
+    bad = np.zeros(y.shape, bool)
+    bad[3:6, 2:, 64:] = True
+    assert np.array_equal(np.isnan(y), bad) and (np.abs(y - want) <= tol)[~bad].all()
