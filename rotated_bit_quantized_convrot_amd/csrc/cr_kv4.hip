@@ -257,11 +257,14 @@ __global__ __launch_bounds__(256) void k_kv4_append(AppendArgs a) {
 //                    tokens 16 (lane / 16) + 0..15
 //   O^T = V^T P^T    the weights are the second operand as they lie; V is laid
 //                    out so that a lane's 16 bytes are these tokens of two d
-// The operands hold 1 + c / 16, the code put into the mantissa of 1.0 (two
-// instructions a pair); what that adds, (1 + z / 16) sum q and
-// (1 + z / 16) sum p, is known and taken off in float32.
+// The operands hold u (1 + c / 16), the code put into the mantissa of
+// u = 2^-10 (two instructions a pair); what that adds, (1 + z / 16) u sum q and
+// u (1 + z / 16) sum p, is known and taken off in float32.  With 1 for u the
+// sums of a head of 256 would pass float32 from q of some 2^118 on.
 // q (rotated: float32) and the weights times V's scales go in as two bf16
 // values of 8 bits each, in bf16's range whatever T.
+constexpr uint32_t kUnitBf16 = 0x3A80u;
+constexpr float kUnit = 0x1p-10f;
 constexpr int kStep = 64;
 constexpr int kMinSpan = 4 * kStep;
 constexpr float kMostSpan = 2097152.0f;   // kMinSpans: twice of it hold the longest sequence, 2^30 tokens
@@ -364,11 +367,11 @@ constexpr float kPart = 1.0f / 256.0f;
 template <int D, int R>
 constexpr size_t part_words() { return R * (D + 2); }
 
-// Four operand pairs of a dword of codes: 1 + c / 16 in bf16.
+// Four operand pairs of a dword of codes: u (1 + c / 16) in bf16.
 // The constants come in registers: as literals they would cost an instruction
 // more a pair.
 struct Mantissa {
-    uint32_t mask = 0x00780078u, one = 0x3F803F80u;
+    uint32_t mask = 0x00780078u, one = kUnitBf16 * 0x10001u;
     __device__ __forceinline__ uint32_t operator()(uint32_t w) const { return (w & mask) | one; }
 };
 __device__ __forceinline__ Mantissa mantissa() {
@@ -398,7 +401,8 @@ constexpr int lds_row() { return D + 4; }
 template <int D, int W, int TR>
 constexpr int lds_words() { return W * TR * lds_row<D>(); }
 
-// A step's scales s and 1 + z / 16 (of V: the operand, in its order of tokens).
+// A step's scales s and 1 + z / 16 (of V: the operand, u (1 + z / 16), in its
+// order of tokens).
 template <int NG>
 struct Stage {
     float ks[NG][kStep], kz[NG][kStep], vs[NG][kStep];
@@ -527,14 +531,14 @@ __global__ __launch_bounds__(64 * W, W == 4 ? blocks_a_cu(D, NG, TR) : D == 256 
         }
     // The Hadamard matrix as an operand: (-1)^popcount(d & d'), row m of tile u for d' = 32 (u / 2) + 8 (m / 4) +
     // 4 (u % 2) + m % 4, so that a lane's results are the d' = 32 s + 8 quad + 0..7 that it needs; here the bits of
-    // d = 8 quad + j and of d' below 32.
+    // d = 8 quad + j and of d' below 32.  Times 2^-4, so that no sum passes float32 where its turned value does not.
     u32x4 hadamard[2];
     if (LO && c.rotate) {
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                uint32_t v = 0x3F803F80u;
+                uint32_t v = 0x3D803D80u;
 #pragma unroll
                 for (int x = 0; x < 2; ++x)
                     v ^= (uint32_t)((__popc((2 * j + x) & (4 * u + (col & 3))) ^ __popc(quad & (col >> 2))) & 1) << (15 + 16 * x);
@@ -580,10 +584,10 @@ __global__ __launch_bounds__(64 * W, W == 4 ? blocks_a_cu(D, NG, TR) : D == 256 
                     if constexpr (std::is_same_v<T, Fp16>) acc = Bf16::mfma(sign, part[1][s], acc);
                 }
 #pragma unroll
-                for (int j = 0; j < 4; ++j) x[u / 2][4 * (u % 2) + j] = acc[j] * kv4_norm<D>();
+                for (int j = 0; j < 4; ++j) x[u / 2][4 * (u % 2) + j] = acc[j] * (16.0f * kv4_norm<D>());
             }
         }
-        // the sums of what the operands hold, group by group
+        // u times the sums of what the operands hold, group by group
 #pragma unroll
         for (int n = 0; n < NG; ++n) qs[t][n] = 0.0f;
 #pragma unroll
@@ -594,10 +598,10 @@ __global__ __launch_bounds__(64 * W, W == 4 ? blocks_a_cu(D, NG, TR) : D == 256 
                 split2(x[s][2 * j], x[s][2 * j + 1], &hi, &lo);
                 if (HALF && col >= 8) hi = lo;
                 qh[t][s][j] = hi;
-                float v = bf16_lo(hi) + bf16_hi(hi);
+                float v = kUnit * bf16_lo(hi) + kUnit * bf16_hi(hi);
                 if constexpr (LO && !HALF) {
                     ql[t][s][j] = lo;
-                    v += bf16_lo(lo) + bf16_hi(lo);
+                    v += kUnit * bf16_lo(lo) + kUnit * bf16_hi(lo);
                 }
                 qs[t][s / SPG] += v;
             }
@@ -608,10 +612,10 @@ __global__ __launch_bounds__(64 * W, W == 4 ? blocks_a_cu(D, NG, TR) : D == 256 
         }
     }
 
-    f32x4 o[RT][DT] = {}, zp[RT][NG] = {};   // zp: sums of weights times 1 + z / 16
+    f32x4 o[RT][DT] = {}, zp[RT][NG] = {};   // zp: sums of weights times u (1 + z / 16)
     uint32_t poison[RT] = {};                // bit n: group n of V is NaN
     // bit n: group n of V has had a scale beyond kLarge, and its scales and sums carry kShrink from then on: below it
-    // 2^30 tokens' sums, of weights of up to 2^8, stay under 2^120
+    // 2^30 tokens' sums, of weights of up to 2^8, stay under 2^110
     uint32_t shrunk = 0;
     constexpr uint32_t kLarge = 0x67800000u;   // 2^80
     constexpr float kShrink = 0x1p-64f;
@@ -624,7 +628,7 @@ __global__ __launch_bounds__(64 * W, W == 4 ? blocks_a_cu(D, NG, TR) : D == 256 
         sum[t] = 0.0f;
     }
     // masked scores become -infinity times cs; a scale of 0, which would make NaN of them, is in q
-    const float cs = 16.0f * (a.scale == 0.0f ? 1.0f : fabsf(a.scale) * 1.4426950408889634f);
+    const float cs = 16.0f / kUnit * (a.scale == 0.0f ? 1.0f : fabsf(a.scale) * 1.4426950408889634f);
 
     Stage<NG>& stage = reinterpret_cast<Stage<NG>*>(lds)[wave];
     auto step = [&](auto slot) {
@@ -658,7 +662,7 @@ __global__ __launch_bounds__(64 * W, W == 4 ? blocks_a_cu(D, NG, TR) : D == 256 
                     scale = nan ? 0.0f : shrunk >> n & 1 ? scale * kShrink : scale;
                 }
                 stage.vs[n][lane] = scale;
-                stage.vz[n][place] = (uint16_t)((v & 15u) << 3 | 0x3F80u);
+                stage.vz[n][place] = (uint16_t)((v & 15u) << 3 | kUnitBf16);
             }
             __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
             __builtin_amdgcn_wave_barrier();
@@ -783,7 +787,7 @@ __global__ __launch_bounds__(64 * W, W == 4 ? blocks_a_cu(D, NG, TR) : D == 256 
 #pragma unroll
                         for (int i = 0; i < 8; ++i) asm volatile("" : "+v"(s[t][8 * u + i]));
                 }
-                // weights times scales, in V's order of tokens, and the operand 1 + z / 16
+                // weights times scales, in V's order of tokens, and the operand u (1 + z / 16)
                 const f32x4 sc[2] = {*reinterpret_cast<const f32x4*>(&stage.vs[n][16 * quad + 8 * u]),
                                      *reinterpret_cast<const f32x4*>(&stage.vs[n][16 * quad + 8 * u + 4])};
                 const u32x4 zo = *reinterpret_cast<const u32x4*>(&stage.vz[n][16 * quad + 8 * u]);
@@ -844,7 +848,7 @@ __global__ __launch_bounds__(64 * W, W == 4 ? blocks_a_cu(D, NG, TR) : D == 256 
         sum[t] += __shfl_xor(sum[t], 32);
         poison[t] |= __shfl_xor(poison[t], 16);
         poison[t] |= __shfl_xor(poison[t], 32);
-        const float share = 16.0f * kPart * reciprocal_or_0(sum[t]);
+        const float share = 16.0f / kUnit * kPart * reciprocal_or_0(sum[t]);
         __syncthreads();   // the words, or the last tile's rows, were read
         if (quad == 0) {
             lds_top[wave][col] = top[t];

@@ -171,3 +171,19 @@ def test_a_bad_token_among_large_values():
     bad = np.zeros(y.shape, bool)
     bad[3:6, 2:, 64:] = True
     assert np.array_equal(np.isnan(y), bad) and (np.abs(y - want) <= tol)[~bad].all()
+
+
+@pytest.mark.parametrize("rotate", [True, False])
+@pytest.mark.parametrize("D,group", [(64, 32), (128, 128), (256, 64)])
+@pytest.mark.parametrize("lens,new,Hq,spare", WAYS)
+@pytest.mark.parametrize("size", [2.0 ** 111, 2.0 ** 125])
+def test_queries_as_large_as_the_type_holds(rotate, D, group, lens, new, Hq, spare, size):
+    """Large q against small k: scores of ordinary size."""
+    s = Setup(lens, 2, D, group, 64, rotate, torch.bfloat16, seed=D, spare=spare)
+    s.k *= 2.0 ** -60
+    s.fill()
+    q = s.queries(new, Hq).float().clamp(-4, 4).mul(size / 4).to(torch.bfloat16)
+    assert q.isfinite().all()
+    scale = 4 * D ** -0.5 * 2.0 ** 60 / size
+    y, tol = reference(s, q, new, scale)
+    assert (np.abs(s.attend(q, new, scale=scale).double().cpu().numpy() - y) <= tol).all()
