@@ -399,8 +399,10 @@ cr_status cr_moe_w4g(int dtype, const void* x, int M, int K, const void* router,
  * D = 64, 128 or 256 side by side, token t's head h at t * row + h * head
  * values from the pointer (strides: not negative, multiples of 8, so that a
  * projection's fused output can be taken apart without a copy).  Outputs are
- * contiguous [T,Hq,D] and must not overlap an input (CR_ERR_SHAPE).  Query
- * head h reads key / value head h / (Hq / Hkv) (Hq a multiple of Hkv, 1 <= Hq
+ * contiguous [T,Hq,D].  What a call writes (y, the used part of a workspace,
+ * a cache by cr_kv4_append) must not overlap what it reads, the arrays of
+ * lengths and pages among that, nor each other (CR_ERR_SHAPE).  Query head h
+ * reads key / value head h / (Hq / Hkv) (Hq a multiple of Hkv, 1 <= Hq
  * <= CR_MAX_HEADS).
  * T rows hold B sequences (0 <= B <= CR_MAX_SEQS), sequence b rows cu[b] up to
  * cu[b+1] of int32 cu [B+1] on the device, which must not decrease; an empty

@@ -6,6 +6,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 #include <atomic>
 #include <mutex>
 
@@ -403,8 +404,16 @@ cr_status check_heads(const Heads& x, int T, int D) {
         return fail(CR_ERR_SHAPE, "%s: stride beyond the limit", x.name);
     return CR_OK;
 }
-cr_status check_apart(const Heads& x, int T, int D, const void* y, size_t y_bytes) {
-    if (overlap(x.p, (size_t)span(x, T, D) * 2, y, y_bytes)) return fail(CR_ERR_SHAPE, "y overlaps %s", x.name);
+// Some of a call's memory.
+struct Part {
+    const char* name;
+    const void* p;
+    size_t bytes;
+};
+Part part(const Heads& x, int T, int D) { return {x.name, x.p, (size_t)span(x, T, D) * 2}; }
+cr_status check_apart(const Part& out, std::initializer_list<Part> others) {
+    for (const Part& x : others)
+        if (overlap(x.p, x.bytes, out.p, out.bytes)) return fail(CR_ERR_SHAPE, "%s overlaps %s", out.name, x.name);
     return CR_OK;
 }
 cr_status check_attn(int dtype, int T, int Hq, int Hkv, int D, int B, float scale) {
@@ -443,6 +452,8 @@ cr_status check_width(int width) {
     if (width < 1 || width > CR_MAX_DIM) return fail(CR_ERR_SHAPE, "bad table width=%d", width);
     return CR_OK;
 }
+size_t codes_bytes(const cr_kv4* c) { return (size_t)c->pages * 2 * c->heads * c->page * (c->dim / 2); }
+size_t scales_bytes(const cr_kv4* c) { return (size_t)c->pages * 2 * c->heads * c->page * (c->dim / c->group) * 4; }
 cr::Kv4 kv4_of(const cr_kv4* c, const int32_t* table, int width, const int32_t* lens, const int32_t* cu, int B, int T) {
     cr::Kv4 k{};
     k.codes = static_cast<uint8_t*>(c->codes); k.scales = static_cast<uint32_t*>(c->scales);
@@ -929,8 +940,9 @@ cr_status cr_attn_prompt(int dtype, const void* q, int64_t q_row, int64_t q_head
     if (!cu || !y) return fail(CR_ERR_NULL, "cu or y is NULL");
     if (!aligned4(cu)) return fail(CR_ERR_ALIGN, "cu not 4-byte aligned");
     if (!aligned16(y)) return fail(CR_ERR_ALIGN, "y not 16-byte aligned");
-    for (const Heads& x : in)
-        if ((s = check_apart(x, T, D, y, (size_t)T * Hq * D * 2)) != CR_OK) return s;
+    if ((s = check_apart({"y", y, (size_t)T * Hq * D * 2}, {part(in[0], T, D), part(in[1], T, D), part(in[2], T, D),
+                                                           {"cu", cu, (size_t)(B + 1) * 4}})) != CR_OK)
+        return s;
     if ((s = check_device()) != CR_OK) return s;
     cr::AttnArgs a{};
     a.fp16 = dtype == CR_FP16; a.causal = causal != 0;
@@ -942,13 +954,11 @@ cr_status cr_attn_prompt(int dtype, const void* q, int64_t q_row, int64_t q_head
 }
 
 size_t cr_kv4_codes_bytes(const cr_kv4* c) {
-    if (check_kv4(c) != CR_OK) return 0;
-    return (size_t)c->pages * 2 * c->heads * c->page * (c->dim / 2);
+    return check_kv4(c) == CR_OK ? codes_bytes(c) : 0;
 }
 
 size_t cr_kv4_scales_bytes(const cr_kv4* c) {
-    if (check_kv4(c) != CR_OK) return 0;
-    return (size_t)c->pages * 2 * c->heads * c->page * (c->dim / c->group) * 4;
+    return check_kv4(c) == CR_OK ? scales_bytes(c) : 0;
 }
 
 cr_status cr_kv4_append(int dtype, const void* k, int64_t k_row, int64_t k_head, const void* v, int64_t v_row,
@@ -963,6 +973,13 @@ cr_status cr_kv4_append(int dtype, const void* k, int64_t k_row, int64_t k_head,
     for (const Heads& x : in)
         if ((s = check_heads(x, T, cache->dim)) != CR_OK) return s;
     if ((s = check_kv4_call(cache, table, width, lens, cu)) != CR_OK) return s;
+    const Part codes{"the cache's codes", cache->codes, codes_bytes(cache)};
+    const Part scales{"the cache's scales", cache->scales, scales_bytes(cache)};
+    for (const Part& out : {codes, scales})
+        if ((s = check_apart(out, {part(in[0], T, cache->dim), part(in[1], T, cache->dim), {"table", table, (size_t)B * width * 4},
+                                   {"lens", lens, (size_t)B * 4}, {"cu", cu, (size_t)(B + 1) * 4}})) != CR_OK)
+            return s;
+    if ((s = check_apart(codes, {scales})) != CR_OK) return s;
     if ((s = check_device()) != CR_OK) return s;
     return launch_err(cr::launch_kv4_append(dtype == CR_FP16, static_cast<const uint16_t*>(k), k_row, k_head,
                                             static_cast<const uint16_t*>(v), v_row, v_head,
@@ -991,8 +1008,14 @@ cr_status cr_attn_kv4(int dtype, const void* q, int64_t q_row, int64_t q_head, i
     const size_t need = cr::attn_kv4_workspace(T, Hq, cache->heads, cache->dim, cache->group, cache->page, width, B);
     if (!y || (!ws && need)) return fail(CR_ERR_NULL, "y or workspace is NULL");
     if (!aligned16(y) || !aligned16(ws)) return fail(CR_ERR_ALIGN, "y or workspace not 16-byte aligned");
-    if ((s = check_apart(x, T, cache->dim, y, (size_t)T * Hq * cache->dim * 2)) != CR_OK) return s;
+    const std::initializer_list<Part> in = {part(x, T, cache->dim), {"the cache's codes", cache->codes, codes_bytes(cache)},
+                                            {"the cache's scales", cache->scales, scales_bytes(cache)},
+                                            {"table", table, (size_t)B * width * 4}, {"lens", lens, (size_t)B * 4},
+                                            {"cu", cu, (size_t)(B + 1) * 4}};
+    const Part out{"y", y, (size_t)T * Hq * cache->dim * 2}, work{"the workspace", ws, need};
+    if ((s = check_apart(out, in)) != CR_OK) return s;
     if (ws_bytes < need) return fail(CR_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", ws_bytes, need);
+    if (need && ((s = check_apart(work, in)) != CR_OK || (s = check_apart(work, {out})) != CR_OK)) return s;
     if ((s = check_device()) != CR_OK) return s;
     cr::AttnArgs a{};
     a.fp16 = dtype == CR_FP16;
