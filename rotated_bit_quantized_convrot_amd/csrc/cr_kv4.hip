@@ -364,6 +364,9 @@ __device__ __forceinline__ bool kv4_work(const Kv4& c, int G, int slots, int fil
 //   Averages, in LDS too, carry 2^-8, so that neither a code's offset nor
 // turning them back passes float32 where the output does not.
 constexpr float kPart = 1.0f / 256.0f;
+// The maximum of a row whose tokens have all scored -infinity; that of a row
+// that has seen none is -infinity.
+constexpr float kNoScore = -3.402823466e38f;
 template <int D, int R>
 constexpr size_t part_words() { return R * (D + 2); }
 
@@ -419,10 +422,14 @@ struct Words {
 // are.
 __device__ __forceinline__ float reciprocal_or_0(float x) { return x == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(x); }
 
-// y = the average, turned back.
+// y = the average, turned back; NaN where there are scores but no weight.
 template <class T, int D>
-__device__ __forceinline__ void kv4_finish(float (&x)[D / 64], int rotate, uint16_t* y) {
+__device__ __forceinline__ void kv4_finish(float (&x)[D / 64], float top, float total, int rotate, uint16_t* y) {
     const int lane = threadIdx.x & 63;
+    if (total == 0.0f && top > -__builtin_inff()) {
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) x[i] = __uint_as_float(kKv4Nan);
+    }
     if (rotate) rotate_head<D>(x);
 #pragma unroll
     for (int i = 0; i < D / 64; ++i) y[lane * (D / 64) + i] = T::from_f32(x[i] * (1.0f / kPart));
@@ -614,6 +621,7 @@ __global__ __launch_bounds__(64 * W, W == 4 ? blocks_a_cu(D, NG, TR) : D == 256 
 
     f32x4 o[RT][DT] = {}, zp[RT][NG] = {};   // zp: sums of weights times u (1 + z / 16)
     uint32_t poison[RT] = {};                // bit n: group n of V is NaN
+    constexpr uint32_t kSeen = 1u << 31;     // a token has scored -infinity where there was no other
     // bit n: group n of V has had a scale beyond kLarge, and its scales and sums carry kShrink from then on: below it
     // 2^30 tokens' sums, of weights of up to 2^8, stay under 2^110
     uint32_t shrunk = 0;
@@ -766,6 +774,7 @@ __global__ __launch_bounds__(64 * W, W == 4 ? blocks_a_cu(D, NG, TR) : D == 256 
                 // theirs alone.
                 const float base = top[t] == -__builtin_inff() ? 0.0f : top[t];   // a row that has seen nothing yet
                 const bool own = fabsf(base) > kFar;
+                if (lim[t] > 0 && top[t] == -__builtin_inff()) poison[t] |= kSeen;
 #pragma unroll
                 for (int i = 0; i < 16; ++i) s[t][i] = own ? s[t][i] * cs - base : __builtin_fmaf(s[t][i], cs, -base);
                 c1 = 1.0f;
@@ -851,7 +860,7 @@ __global__ __launch_bounds__(64 * W, W == 4 ? blocks_a_cu(D, NG, TR) : D == 256 
         const float share = 16.0f / kUnit * kPart * reciprocal_or_0(sum[t]);
         __syncthreads();   // the words, or the last tile's rows, were read
         if (quad == 0) {
-            lds_top[wave][col] = top[t];
+            lds_top[wave][col] = top[t] == -__builtin_inff() && (poison[t] & kSeen) ? kNoScore : top[t];
             lds_sum[wave][col] = sum[t];
         }
 #pragma unroll
@@ -888,7 +897,7 @@ __global__ __launch_bounds__(64 * W, W == 4 ? blocks_a_cu(D, NG, TR) : D == 256 
                     x[i] = __builtin_fmaf(of[k] * inv, lds_o[(k * TR + r) * kRow + lane * (D / 64) + i], x[i]);
             if (whole) {
                 const int i0 = (r0 + r) / G, h = g * G + (r0 + r) % G;
-                kv4_finish<T, D>(x, c.rotate, a.y + ((int64_t)(w.first + i0) * a.Hq + h) * D);
+                kv4_finish<T, D>(x, m, total, c.rotate, a.y + ((int64_t)(w.first + i0) * a.Hq + h) * D);
             } else {
                 float* p = part + (TR * t + r) * D + lane * (D / 64);
 #pragma unroll
@@ -975,7 +984,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void k_attn_kv4_join(Kv4 c, AttnAr
 #pragma unroll
                 for (int d = 0; d < N; ++d) x[d] = __builtin_fmaf(of[k] * inv, lds_x[k][lane * N + d], x[d]);
             const int i0 = (r0 + r) / G, h = g * G + (r0 + r) % G;
-            kv4_finish<T, D>(x, c.rotate, a.y + ((int64_t)(w.first + i0) * a.Hq + h) * D);
+            kv4_finish<T, D>(x, up, total, c.rotate, a.y + ((int64_t)(w.first + i0) * a.Hq + h) * D);
         }
         __syncthreads();
     }

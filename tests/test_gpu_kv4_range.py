@@ -187,3 +187,26 @@ def test_queries_as_large_as_the_type_holds(rotate, D, group, lens, new, Hq, spa
     scale = 4 * D ** -0.5 * 2.0 ** 60 / size
     y, tol = reference(s, q, new, scale)
     assert (np.abs(s.attend(q, new, scale=scale).double().cpu().numpy() - y) <= tol).all()
+
+
+@pytest.mark.parametrize("rotate", [True, False])
+@pytest.mark.parametrize("D,group", [(64, 32), (128, 128), (256, 64)])
+@pytest.mark.parametrize("lens,new,Hq,spare", WAYS)
+@pytest.mark.parametrize("others", [0, 1, 20, 85])
+def test_scores_below_what_float32_holds(rotate, D, group, lens, new, Hq, spare, others):
+    """Tokens whose scores are -infinity weigh nothing beside others; a row
+    that sees no other gives NaN, not what a row gives that sees no token."""
+    s = Setup(lens, 2, D, group, 64, rotate, torch.bfloat16, seed=D, spare=spare)
+    s.k[:] = -2.0 ** 100
+    at = starts(s.lens)
+    others = min(others, min(lens) - 1)
+    for b in range(len(lens)):
+        s.k[at[b]:at[b] + others:2], s.k[at[b + 1] - others:at[b + 1]] = 0, 0
+    s.fill()
+    q = torch.full((sum(new), Hq, D), 2.0 ** 100, dtype=torch.bfloat16, device="cuda")
+    got = s.attend(q, new).double().cpu().numpy()
+    if others == 0:
+        assert np.isnan(got).all()
+    else:
+        y, tol = reference(s, q, new, D ** -0.5, 0.0)
+        assert (np.abs(got - y) <= tol).all()
