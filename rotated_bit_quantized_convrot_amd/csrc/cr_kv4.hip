@@ -281,7 +281,9 @@ struct Kv4Work {
 // chunk 0).  Every wave counts for itself, 64 sequences at a time.
 //   `fill` blocks of a head run at once (`few` where that is enough).  A block's start and end cost as much
 // as some 500 tokens, so the spans are the shortest with which all blocks run
-// at once, up to twice fill's share.  Where that leaves them unlike (spans
+// at once, up to twice fill's share; of more than 64 sequences, which the lanes
+// do not count at once, they are twice fill's share (us, 64 and 66 of 4000
+// tokens: one key head 20.1 and 22.7, two 27.9 and 33.4).  Where that leaves them unlike (spans
 // beyond 1.25 shares, the longest sequence beyond 1.25 times the mean) and a
 // share is 2048 tokens and more, the spans are half a share and the blocks
 // follow each other, at most 2 fill more than tile groups, which is what the
@@ -450,7 +452,12 @@ constexpr int blocks_a_cu(int dim, int groups, int rows) { return dim == 256 ? 1
 // loads, each after the other).  Short calls are these waits.
 //   Steps of loads in flight a wave: with three blocks a CU one is enough at
 // D = 128 (1 / 2 / 3 steps, two blocks: 39.8 / 40.2 / 40.5); D = 64 has the
-// registers for two (three blocks: 139).
+// registers for two (three blocks: 142).
+//   Two and three tiles of several groups do not fit into 256 registers: they
+// keep 120 and 228 bytes a lane in scratch memory at D = 64 (three tiles, groups
+// of 32, LO false and true), 0 and 44, 68 and 208, 232 and 484 at D = 128 (two
+// tiles, groups of 128, 64, 32); a tile of 16 rows 132 at D = 256 with LO and
+// groups of 32.
 template <class T, int D, int NG, int RT, int TR, bool LO, int W>
 __global__ __launch_bounds__(64 * W, W == 4 ? blocks_a_cu(D, NG, TR) : D == 256 ? 1 : 2) void k_attn_kv4(Kv4 c, AttnArgs a, int slots,
                                                                                               int fill, int few, float* parts) {
@@ -625,7 +632,7 @@ __global__ __launch_bounds__(64 * W, W == 4 ? blocks_a_cu(D, NG, TR) : D == 256 
     // bit n: group n of V has had a scale beyond kLarge, and its scales and sums carry kShrink from then on: below it
     // 2^30 tokens' sums, of weights of up to 2^8, stay under 2^110
     uint32_t shrunk = 0;
-    constexpr uint32_t kLarge = 0x67800000u;   // 2^80
+    constexpr uint32_t kLarge = 0x67800000u, kInfinity = 0x7F800000u;   // 2^80
     constexpr float kShrink = 0x1p-64f;
     float top[RT], sum[RT];
     bool far[RT];   // of some row of the tile: a maximum beyond kFar, or none yet
@@ -643,22 +650,27 @@ __global__ __launch_bounds__(64 * W, W == 4 ? blocks_a_cu(D, NG, TR) : D == 256 
         constexpr int at = slot;
         // scales and 1 + z / 16 through LDS: a token's own lane has them, its 16 lanes need them; of tokens that are
         // not there, zeros
-        uint64_t nans[NG];   // tokens whose V is NaN
+        uint64_t odd;   // tokens with a V of NaN or beyond kLarge
         {
             const bool there = pos + lane < end && pv[at] >= 0;
             const int place = (lane & ~7) | (lane & 4) | (lane & 1) << 1 | (lane >> 1 & 1);   // 0 2, 1 3, 4 6, 5 7
+            uint32_t most = 0;
 #pragma unroll
             for (int n = 0; n < NG; ++n) {
                 const uint32_t k = there ? kw[at].w[n] : 0, v = there ? vw[at].w[n] : 0;
                 stage.ks[n][lane] = __uint_as_float(k & ~15u);
                 stage.kz[n][lane] = __uint_as_float((k & 15u) << 19 | 0x3F800000u);
-                float scale = __uint_as_float(v & ~15u);
-                nans[n] = __ballot(v >= kLarge);
-                if (nans[n] != 0 || (shrunk >> n & 1)) {
-                    const bool nan = (v & 0x7F800000u) == 0x7F800000u;
-                    const uint64_t large = nans[n];
-                    nans[n] = __ballot(nan);
-                    if (!(shrunk >> n & 1) && (large & ~nans[n]) != 0) {
+                stage.vs[n][lane] = __uint_as_float(v & ~15u);
+                stage.vz[n][place] = (uint16_t)((v & 15u) << 3 | kUnitBf16);
+                most = max(most, v);
+            }
+            odd = __ballot(most >= kLarge);
+            if (odd != 0 || shrunk != 0) {
+#pragma unroll
+                for (int n = 0; n < NG; ++n) {
+                    const uint32_t v = there ? vw[at].w[n] : 0;
+                    const bool nan = v >= kInfinity;
+                    if (!(shrunk >> n & 1) && __any(v >= kLarge && !nan)) {
                         shrunk |= 1u << n;
 #pragma unroll
                         for (int t = 0; t < RT; ++t) {
@@ -667,10 +679,8 @@ __global__ __launch_bounds__(64 * W, W == 4 ? blocks_a_cu(D, NG, TR) : D == 256 
                             for (int d = n * DPG; d < (n + 1) * DPG; ++d) o[t][d] *= kShrink;
                         }
                     }
-                    scale = nan ? 0.0f : shrunk >> n & 1 ? scale * kShrink : scale;
+                    stage.vs[n][lane] = nan ? 0.0f : __uint_as_float(v & ~15u) * (shrunk >> n & 1 ? kShrink : 1.0f);
                 }
-                stage.vs[n][lane] = scale;
-                stage.vz[n][place] = (uint16_t)((v & 15u) << 3 | kUnitBf16);
             }
             __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
             __builtin_amdgcn_wave_barrier();
@@ -741,14 +751,15 @@ __global__ __launch_bounds__(64 * W, W == 4 ? blocks_a_cu(D, NG, TR) : D == 256 
         }
         // rows that see a token whose V is NaN: their sums are made NaN at the end (0 times it would reach the others)
 #pragma unroll
-        for (int n = 0; n < NG; ++n)
-            if (nans[n] != 0) {
+        for (int n = 0; n < NG; ++n) {
+            if (odd == 0) break;
+            const uint64_t nans = __ballot(pos + lane < end && page >= 0 && vw[at].w[n] >= kInfinity);
 #pragma unroll
-                for (int t = 0; t < RT; ++t) {
-                    const uint32_t visible = lim[t] >= 16 ? 0xFFFFu : lim[t] > 0 ? (1u << lim[t]) - 1 : 0u;
-                    if ((uint32_t)(nans[n] >> (16 * quad)) & visible) poison[t] |= 1u << n;
-                }
+            for (int t = 0; t < RT; ++t) {
+                const uint32_t visible = lim[t] >= 16 ? 0xFFFFu : lim[t] > 0 ? (1u << lim[t]) - 1 : 0u;
+                if ((uint32_t)(nans >> (16 * quad)) & visible) poison[t] |= 1u << n;
             }
+        }
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
             float m = s[t][0];
