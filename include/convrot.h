@@ -408,9 +408,11 @@ cr_status cr_moe_w4g(int dtype, const void* x, int M, int K, const void* router,
  * cu[b+1] of int32 cu [B+1] on the device, which must not decrease; an empty
  * sequence has none.  Rows before cu[0] and from cu[B] on are not read, and
  * their outputs are left as they were.
- * Scores are scale * q . k (|scale| <= CR_MAX_SCALE), held in float32 with the
- * softmax's sums; weights may be up to 2^8 times their share until the sums are
- * divided. */
+ * Scores are scale * q . k (|scale| <= CR_MAX_SCALE), held in float32 as q . k
+ * is and the softmax's sums are; beyond float32 they are infinite.  A key that
+ * scores -infinity weighs nothing, a row whose keys all do gives NaN, and a
+ * scale of 0 weighs all alike (NaN where q is not finite).  Averages of finite
+ * values stay finite. */
 #define CR_MAX_SCALE 1e30f
 #define CR_MAX_HEADS 1024
 #define CR_MAX_SEQS 65536
@@ -436,7 +438,8 @@ cr_status cr_attn_prompt(int dtype, const void* q, int64_t q_row, int64_t q_head
  *     z = clamp(rint(-lo / s), 0, 15), c = clamp(rint(x' / s) + z, 0, 15)
  *     (both 0 where s = 0)
  * and stands for x' = s (c - z).  A group that holds an infinity or a NaN
- * stands for NaN.
+ * stands for NaN (so may all of a head to be rotated whose values pass
+ * 2^128 / dim: the butterflies' sums are float32).
  *   codes   [pages][K, V][heads][page * dim / 2] bytes, 16-byte aligned
  *     K     token r of a page at r * dim / 2; its dword i * dim / 32 + s holds
  *           d = 32 s + 8 i + 0..7: d + 2 j in bits 4 j, d + 2 j + 1 in bits
@@ -477,9 +480,12 @@ cr_status cr_kv4_append(int dtype, const void* k, int64_t k_row, int64_t k_head,
  * lens[b] - n + i.  A row that sees none gives zeros.  With the cache's
  * rotation q is rotated and the output turned back.  q and the weights times
  * V's scales go to the products in 16 bits and more (two bf16 each); a token of
- * NaN reaches the rows that see it.  Meant for a token or a few a sequence: up
- * to 48, 32 or 16 rows (tokens times Hq / heads; dim 64, 128, 256) read the
- * cache once, more read it again.
+ * NaN reaches the rows that see it.  Where a group of V has scales beyond 2^80,
+ * its values under some 2^-50 may be lost, in other tokens too.
+ * Meant for a token or a few a sequence: 8, 16, 32 or 48 rows (tokens times
+ * Hq / heads; up to 48 for dim 64, 32 for 128, 16 for 256) read the cache once,
+ * as many as the call's sequences have on average; those that have more read it
+ * again for each such number.
  *   ws / ws_bytes: at least cr_attn_kv4_workspace_bytes(...); calls that can
  *   run at the same time need a workspace each.  Nothing is kept in it.  Where
  *   the size is 256 (a table of up to 1024 tokens) none is used: ws may be NULL.

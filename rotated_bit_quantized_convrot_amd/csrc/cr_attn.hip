@@ -482,6 +482,12 @@ hipError_t launch(const AttnArgs& a, hipStream_t st) {
 //     20 of 220 (616)                             12.9      14.5     17.5     13.2     11.1
 //     8 of 1000 (924)                             31.8      33.3     39.1     35.0     32.2
 //   D = 64, 32 heads: 64 of 60 (1984)             13.4      23.0     23.4     14.8     11.0
+// The host knows T and B, not the lengths.  Where short sequences of heads of 64
+// leave some blocks (up to 704), 64/32/2 loses less on like lengths than it
+// gains on unlike ones, 14 heads, 64/32/2 and 64/32/1: 30 of 100 9.4 and 8.7, 30
+// from 0 to 200 9.6 and 9.2; 20 of 220 13.1 and 11.2, from 0 to 440 12.5 and
+// 13.4, from 0 to 900 17.5 and 20.6; 10 of 400 13.7 and 13.5, from 0 to 800 17.1
+// and 18.9; 12 from 0 to 600 15.1 and 16.5.
 // D = 256 (one wave a SIMD), 128/32/1 and 64/32/2: 16 heads, 300 tokens (48
 // blocks) 21.2 / 17.5; 8 heads, 2741 (192) 91 / 57, 16384 (1024) 1410 / 1660.
 template <class T, int D>
